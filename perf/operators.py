@@ -343,7 +343,7 @@ def _own_fork(s, c):
 def _own_retire(s, c):
     import w4a16_group_quantised_gb300 as w
     table, lens, ref = s["table"].clone(), s["lens"].clone(), s["ref"].clone()
-    w.w4a16_kv_free(table, lens, ref, s["ended"], c["page"])
+    w.w4a16_kv_free(table, lens, ref, s["ended"])
     w.w4a16_kv_trim(table, lens, ref, c["page"], window=c["window"], sinks=c["sinks"])
     w.w4a16_kv_compact(_own_cache(w, s), table, ref)
     return {"table": table, "lens": lens, "ref": ref, **_codes(s)}
