@@ -402,6 +402,146 @@ int w4a16_version(void);
  * next w4a16_gemm call with W4A16_ERR_ARG. */
 int w4a16_debug_set_config(int which, const int *vals, int n);
 
+/* ------------------------------------------------------------------------
+ * Paged 8-bit key/value cache: what runs between a decoder layer's qkv and
+ * output projections, and between its steps.  The pages the rest of this
+ * header cites stop at the linear layers; these are library additions for
+ * programs that run whole layers on them.
+ *
+ * A cached value is code * scale: codes in 8 bits, one fp32 scale for each
+ * page (a block of page_size tokens) and kv head.  Position p of sequence b
+ * is slot p % page_size of page block_table[b, p / page_size].
+ *
+ * Everything the lengths decide is read on the device, so that a captured
+ * call may be replayed with other lengths.  What only the device can see is
+ * checked there: a page id outside [0, n_pages) where a page is needed, a
+ * length past the table's width, q_starts that leave [0, n_tokens] or fall.
+ * Such a token or key is left out, nothing out of range is touched, and the
+ * status word reads W4A16_ERR_ARG.
+ *
+ * These kernels wait for the kernel before them on the stream before they
+ * read or write anything.  Like every entry point they neither allocate nor
+ * synchronise; scratch is the caller's and needs no initialisation. */
+typedef enum {
+    W4A16_KV_INT8 = 0,       /* int8, -127..127                                */
+    W4A16_KV_E4M3 = 1        /* 8-bit float: 4 exponent, 3 fraction bits, +-448 */
+} w4a16_kv_dtype_t;
+
+/* Smallest scale the append stores (that of a block of zeros): 2^-60.  Every
+ * scale of a page in use must be positive; a block whose values are not
+ * finite gets a scale that is not, and attention that sees it gives NaN. */
+#define W4A16_KV_SCALE_MIN 8.673617379884035e-19f
+
+typedef struct {
+    void *k, *v;                /* codes: k[page * page_stride + head * head_stride + token * token_stride + d] */
+    float *k_scale, *v_scale;   /* [n_pages, n_kv_heads], contiguous                       */
+    int n_pages, page_size;     /* page_size 16, 32, 64 or 128                             */
+    int n_kv_heads, head_dim;   /* head_dim 64 or 128                                      */
+    long long page_stride, head_stride, token_stride;   /* bytes, multiples of 16; k and v alike */
+    int kv_dtype;               /* w4a16_kv_dtype_t                                        */
+} w4a16_kv_cache_t;
+
+/* The sequences of a call.  Sequence b brings q_starts[b+1] - q_starts[b]
+ * tokens (0 is fine), rows q_starts[b].. of the call's token tensors: its
+ * newest, at positions kv_lens[b] - that many .. kv_lens[b] - 1.  All on the
+ * device. */
+typedef struct {
+    const int32_t *block_table; /* [n_seqs, max_blocks]; entries no token needs may hold anything */
+    const int32_t *kv_lens;     /* [n_seqs], the call's own tokens included                       */
+    const int32_t *q_starts;    /* [n_seqs + 1], from 0, non-decreasing                           */
+    int n_seqs, max_blocks;
+    int n_tokens;               /* rows of the token tensors, q_starts[n_seqs]                    */
+} w4a16_kv_batch_t;
+
+/* Quantise the batch's new keys and values into their pages.  k_new, v_new:
+ * [n_tokens, n_kv_heads, head_dim] of dtype, 16-byte aligned, rows k_stride
+ * and v_stride elements apart (multiples of 8; views of a merged qkv output
+ * will do).  For each page and kv head touched, with amax the largest new
+ * |x| and s_old the scale of the tokens already there (0 without any):
+ *     s = max(s_old, amax / 127 (int8) or / 448 (e4m3), W4A16_KV_SCALE_MIN)
+ *     code = RN(x * RN(1 / s)), ties to even, saturated
+ * all in fp32.  When s > s_old the older codes of the block are rounded
+ * again, code = RN((code * s_old) * RN(1 / s)); otherwise they stay.  No
+ * other slot changes.  Appending the same tokens again changes nothing.  No
+ * two sequences of the batch may append to the same page. */
+int w4a16_kv_append(const w4a16_kv_cache_t *cache, const void *k_new, long long k_stride, const void *v_new,
+                    long long v_stride, const w4a16_kv_batch_t *batch, w4a16_dtype_t dtype,
+                    w4a16_stream_t stream);
+
+/* Read the batch's tokens back: k_out, v_out [n_tokens, n_kv_heads,
+ * head_dim], RN_dtype(code * scale).  For any other consumer of the cache. */
+int w4a16_kv_read(const w4a16_kv_cache_t *cache, const w4a16_kv_batch_t *batch, void *k_out, void *v_out,
+                  w4a16_dtype_t dtype, w4a16_stream_t stream);
+
+/* Attention of the batch's tokens over the cache, their own keys included
+ * (append first).  q: [n_tokens, n_heads, head_dim] of dtype, rows q_stride
+ * elements apart; query head a reads kv head a / (n_heads / n_kv_heads).  A
+ * token at position i sees key j when
+ *     j <= i  and  (window == 0  or  i - j < window  or  j < sinks)
+ * and out[t, a] = sum_j softmax_j(scale * q . k_j) v_j, [n_tokens, n_heads,
+ * head_dim] contiguous, rounded once into dtype from fp32.  lse (optional):
+ * [n_tokens, n_heads] fp32, log sum_j exp(scale * q . k_j).  A token that
+ * sees no key gets zeros and -inf.  Pages that no token of a sequence sees
+ * are never read, so their table entries may be -1 (w4a16_kv_trim).
+ * max_q_len: the most tokens that one sequence brings.  It picks kernels
+ * only: the result holds whatever it is.
+ * workspace: w4a16_kv_attention_workspace bytes, 16-byte aligned, not shared
+ * with a call that may run at the same time. */
+int w4a16_kv_attention(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
+                       const w4a16_kv_batch_t *batch, int max_q_len, float scale, int window, int sinks,
+                       void *out, float *lse_or_null, w4a16_dtype_t dtype, void *workspace,
+                       long long workspace_bytes, w4a16_stream_t stream);
+
+/* The bytes w4a16_kv_attention needs on the current device for these sizes,
+ * whatever the lengths. */
+int w4a16_kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
+                                 long long *bytes);
+
+/* Page pool.  refcount[p] counts the block-table entries that name page p; a
+ * page with count 0 is free.  The caller sets the count when it hands a page
+ * to one sequence; these keep it after that.
+ *
+ * Copy pages: for i < n, page dst[i] becomes page src[i] (codes and scales).
+ * A pair with a negative id is skipped.  No dst may be named twice or be a
+ * src of another pair. */
+int w4a16_kv_copy_pages(const w4a16_kv_cache_t *cache, const int32_t *src, const int32_t *dst, int n,
+                        w4a16_stream_t stream);
+
+/* Fork: row children[i] of the tables becomes a continuation of row
+ * parents[i].  The full pages are shared (their counts go up); a last page
+ * that is not full is copied into a free one: the children that need one
+ * take the free pages in ascending order, child by child.  Without enough of
+ * them the children that get none are left empty (row -1, length 0) and the
+ * status word reads W4A16_ERR_ARG.  What a child's row named before is not
+ * freed.  No row may be a child twice, or both a parent and a child.
+ * workspace: w4a16_kv_pool_workspace bytes. */
+int w4a16_kv_fork(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *kv_lens, int n_seqs,
+                  int max_blocks, int32_t *refcount, const int32_t *parents, const int32_t *children, int n,
+                  void *workspace, long long workspace_bytes, w4a16_stream_t stream);
+
+/* Free sequences: every page that rows seqs[0..n) name loses one count, the
+ * rows become -1 and their lengths 0. */
+int w4a16_kv_free(int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount,
+                  int n_pages, const int32_t *seqs, int n, w4a16_stream_t stream);
+
+/* Trim: in every row, pages whose positions all lie in [sinks, kv_len -
+ * window + 1) lose one count and their entries become -1: with this window no
+ * later token sees them.  window == 0 trims nothing. */
+int w4a16_kv_trim(int32_t *block_table, const int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount,
+                  int n_pages, int page_size, int window, int sinks, w4a16_stream_t stream);
+
+/* Compact: with m pages in use, the pages in use at m and above move, in
+ * ascending order, into the free pages below m, in ascending order; counts
+ * and every table entry follow.  n_live (optional, device) receives m.  Pages
+ * at m and above keep their old codes.
+ * workspace: w4a16_kv_pool_workspace bytes. */
+int w4a16_kv_compact(const w4a16_kv_cache_t *cache, int32_t *block_table, int n_seqs, int max_blocks,
+                     int32_t *refcount, int32_t *n_live_or_null, void *workspace, long long workspace_bytes,
+                     w4a16_stream_t stream);
+
+/* Scratch bytes of w4a16_kv_fork and w4a16_kv_compact for a pool of n_pages. */
+int w4a16_kv_pool_workspace(int n_pages, long long *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,6 +5,9 @@ K as [N, K/8], per-group scales [N, K/G] (G in {32, 64, 128}), symmetric
 (bias 8) or asymmetric weights (zero points packed 8 per int32 along N as
 [N/8, K/G]), fp32 accumulation.
 
+Beside it, for whole decoder layers: a paged key/value cache in 8 bits (kv.py:
+append, attention with an optional window and sinks, page operators).
+
 The compute path is the C-ABI shared library ``libw4a16.so`` built from
 ``csrc/`` (hand-written CUDA for sm_103a); ``binding`` marshals torch tensors
 into it.  Nothing here falls back to a CPU or PyTorch implementation: if the
@@ -34,4 +37,17 @@ from .binding import (  # noqa: F401
     w4a16_pack,
     w4a16_pack_zeros,
     w4a16_select_path,
+)
+from .kv import (  # noqa: F401
+    KVCache,
+    w4a16_kv_append,
+    w4a16_kv_attention,
+    w4a16_kv_attention_workspace,
+    w4a16_kv_compact,
+    w4a16_kv_copy_pages,
+    w4a16_kv_fork,
+    w4a16_kv_free,
+    w4a16_kv_pool_workspace,
+    w4a16_kv_read,
+    w4a16_kv_trim,
 )

@@ -54,7 +54,7 @@ def load_library():
                 f"{path} is missing: build it with w4a16_group_quantised_gb300.build.build()"
                 + (" (variant='trace')" if path.endswith("_trace.so") else ""))
         lib = ctypes.CDLL(path)
-        P, I, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+        P, I, L, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
         sig = {
             "w4a16_pack": [P, I, I, P, P],
             "w4a16_pack_zeros": [P, I, I, P, P],
@@ -80,6 +80,16 @@ def load_library():
             "w4a16_debug_set_config": [I, P, I],
             "w4a16_debug_prefill_plan": [I, I, I, I, I, P, P],
             "w4a16_debug_decode_trace": [P, P],
+            "w4a16_kv_append": [P, P, L, P, L, P, I, P],
+            "w4a16_kv_read": [P, P, P, P, I, P],
+            "w4a16_kv_attention": [P, L, I, P, P, I, F, I, I, P, P, I, P, L, P],
+            "w4a16_kv_attention_workspace": [I, I, I, I, I, P],
+            "w4a16_kv_copy_pages": [P, P, P, I, P],
+            "w4a16_kv_fork": [P, P, P, I, I, P, P, P, I, P, L, P],
+            "w4a16_kv_free": [P, P, I, I, P, I, P, I, P],
+            "w4a16_kv_trim": [P, P, I, I, P, I, I, I, I, P],
+            "w4a16_kv_compact": [P, P, I, I, P, P, P, L, P],
+            "w4a16_kv_pool_workspace": [I, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)

@@ -479,6 +479,10 @@ bool pdl_enabled() {
     return g_pdl != 0;
 }
 
+int device_info(const DeviceInfo **out) { return get_device(out); }
+
+void log_kernel_selection(const char *line) { log_selection(line); }
+
 bool pdl_for_stream(cudaStream_t s) {
     const bool on = pdl_enabled();
     return take_weights_written(s) ? false : on;

@@ -85,6 +85,57 @@ cudaError_t launch_decode_sk(const GemmArgs &a, int ns, const DeviceInfo &dev, f
 // smaller launch lower it under a graph node captured with a larger one.
 cudaError_t raise_smem_cap(const void *func, size_t need);
 
+// ---- paged 8-bit key/value cache (kv_append.cu, kv_attention.cu, kv_pages.cu; entry points in kv_api.cu)
+struct KvCache {
+    uint8_t *k, *v;                       // codes: [page][head][token][dim] by these strides, dims contiguous
+    float *k_scale, *v_scale;             // [n_pages, n_kv_heads]
+    long long page_stride, head_stride, token_stride;   // bytes
+    int n_pages, page_shift;              // pages of 1 << page_shift tokens
+    int n_kv_heads, head_dim;
+    int kv_dtype;                         // 0 int8, 1 e4m3
+};
+struct KvBatch {
+    const int *block_table, *kv_lens, *q_starts;
+    int n_seqs, max_blocks, n_tokens;
+};
+struct KvAttentionArgs {
+    const void *q;
+    long long q_stride;                   // elements between rows of q
+    int n_heads, max_q_len, window, sinks;
+    float scale;
+    void *out;
+    float *lse;                           // or null
+    int dtype;                            // 0 fp16, 1 bf16
+    void *workspace;
+};
+cudaError_t launch_kv_append(const KvCache &c, const KvBatch &b, const void *k_new, long long k_stride,
+                             const void *v_new, long long v_stride, int dtype, const DeviceInfo &dev, cudaStream_t s,
+                             bool pdl);
+cudaError_t launch_kv_read(const KvCache &c, const KvBatch &b, void *k_out, void *v_out, int dtype,
+                           const DeviceInfo &dev, cudaStream_t s, bool pdl);
+cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, const DeviceInfo &dev,
+                                cudaStream_t s, bool pdl);
+long long kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
+                                 const DeviceInfo &dev);
+cudaError_t launch_kv_copy_pages(const KvCache &c, const int *src, const int *dst, int n, const DeviceInfo &dev,
+                                 cudaStream_t s, bool pdl);
+cudaError_t launch_kv_fork(const KvCache &c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
+                           const int *parents, const int *children, int n, void *workspace, const DeviceInfo &dev,
+                           cudaStream_t s, bool pdl);
+cudaError_t launch_kv_free(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
+                           const int *seqs, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl);
+cudaError_t launch_kv_trim(int *table, const int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
+                           int page_size, int window, int sinks, const DeviceInfo &dev, cudaStream_t s, bool pdl);
+cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_blocks, int *refcount, int *n_live,
+                              void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
+long long kv_pool_workspace(int n_pages);
+
+// ---- api.cu helpers used by kv_api.cu: the current device's state (W4A16_OK
+// or an error), the early-launch switch, the kernel-selection log
+int device_info(const DeviceInfo **out);
+bool pdl_enabled();
+void log_kernel_selection(const char *line);
+
 // ---- api.cu helpers used by noalloc.cu
 int validate_gemm_args(const void *x, int M, int K, const int32_t *qw, const void *scales, const int32_t *qz,
                        int G, int N, const void *out, int dtype);
