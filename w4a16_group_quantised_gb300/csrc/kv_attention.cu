@@ -13,7 +13,7 @@
 // Bound by the cache read: 256 B a key and kv head (head dim 128) against
 // rows * 512 multiply-adds.  So the design is about bytes in flight and even
 // shares, not about matrix instructions:
-//  * The work is a line of steps of 16 keys: sequence by sequence, kv head by
+//  * The work is a line of steps of one or two blocks of 16 keys: sequence by sequence, kv head by
 //    kv head, row tile by row tile, every step of the keys that the sequence's
 //    new tokens see.  Lengths are read here, so each CTA sums the line's
 //    length up itself, takes an equal piece of it, and its warps take equal
@@ -44,10 +44,10 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kStep = 16;                 // keys of a step
-constexpr int kMaxSeqs = 1024;            // sequences of a launch
-constexpr int kShort = 16;                // tiles of up to so many steps stay in one CTA
-constexpr int kLeast = 4;                 // fewest steps worth a CTA
+constexpr int kBlock = 16;                // keys of a block: one TMA box of K, one of V, within one page
+constexpr int kMaxSeqs = 512;             // sequences of a launch
+constexpr int kShort = 256 / kBlock;      // tiles of up to so many blocks stay in one CTA
+constexpr int kLeast = 2;                 // fewest steps worth a CTA
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
 constexpr float kHead = 14.0f;            // ... and a moved reference puts the largest at 2^kHead
@@ -64,31 +64,43 @@ struct FewParams {
     int *status;
 };
 
-// Steps of the keys that new tokens of a sequence see: [0, sink_steps) and
-// [first_step, ...), `steps` in all, one at least.
+// Blocks of the keys that new tokens of a sequence see: [0, sink) and
+// [first, ...), `blocks` in all, one at least.
 struct Span {
-    int steps, sink_steps, first_step;
+    int blocks, sink, first;
+    template <int BPS>
+    __device__ __forceinline__ int steps() const { return (blocks + BPS - 1) / BPS; }
 };
 __device__ __forceinline__ Span span_of(int n, int len, int window, int sinks) {
     Span s;
     const int lo = window > 0 ? max(0, len - n + 1 - window) : 0;
-    s.first_step = lo / kStep;
-    s.sink_steps = (min(sinks, lo) + kStep - 1) / kStep;
-    if (s.sink_steps >= s.first_step) s.sink_steps = s.first_step;
-    s.steps = max(s.sink_steps + (len + kStep - 1) / kStep - s.first_step, 1);
+    s.first = lo / kBlock;
+    s.sink = min((min(sinks, lo) + kBlock - 1) / kBlock, s.first);
+    s.blocks = max(s.sink + (len + kBlock - 1) / kBlock - s.first, 1);
     return s;
 }
+
+// a / b for a of a line's length: nearly always within 32 bits, where division is cheap
+__device__ __forceinline__ int line_div(long long a, int b) {
+    return a >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
+}
+
+// A tile of which warps hold parts: steps [begin, end) of the CTA's line, and its rows.
+struct Shared {
+    int has, first_warp, begin, end, q0, n, head, row;
+};
 
 template <int D, int NR, int NW, int NS>
 struct FewSmem {
     static constexpr int kRows = 8 * NR;
-    static constexpr int kStage = 2 * kStep * D;                   // K then V
+    static constexpr int kStage = 2 * kBlock * D;                  // K then V
     static constexpr int kPart = kRows * (D + 2);                  // floats: rows of out, then (M, l) of each row
     static constexpr int kPark = NW * NS * kStage;                 // a warp's first piece, if another began it
     static constexpr int kSeq = kPark + NW * kPart * 4;            // int4 {q0, n, len, row tiles}
     static constexpr int kPre = kSeq + kMaxSeqs * 16;              // line position of each sequence
     static constexpr int kBars = kPre + (kMaxSeqs + 1) * 8;
-    static constexpr int kMisc = kBars + NW * NS * 8;
+    static constexpr int kShared = kBars + NW * NS * 8;            // tiles that warps share: the CTA's first, then by warp
+    static constexpr int kMisc = kShared + (NW + 1) * 32;
     static constexpr int kEnd = kMisc + (NW + 3) * 8 + 1024;       // 1024: slack to align the base
     static_assert(NS * kStage >= kPart * 4, "the last piece is parked in the ring");
 };
@@ -105,6 +117,10 @@ __device__ __forceinline__ float ex2(float v) {
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -128,21 +144,21 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t
     }
 }
 
-// What a step needs, held by the lane that looked it up.
+// What a block needs, held by the lane that looked it up.
 struct Meta {
     int page, where;       // page or -1; first token within the page | kv head << 8
-    int pos;               // position of the first key (past every query for a page that is not there)
-    int tile;              // where on the CTA's line its tile begins (below 0: in an earlier CTA)
-    float ks, lv, iv;      // key scale, log2 and reciprocal of the value scale
+    int pos;               // position of the first key (past every query for a block that is not there)
+    float ks, vs;          // scales
 };
 
-template <int KT, int D, int NR, int NW, int NS>
+template <int KT, int D, int NR, int BPS, int NW, int NS>
 __global__ void __launch_bounds__(32 * NW, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const FewParams p) {
     using L = FewSmem<D, NR, NW, NS>;
     constexpr int ROWS = L::kRows;
     constexpr int KS = D / 16;                                     // k-steps of S, and 16-dim tiles of out
+    constexpr int LOOK = 32 / BPS;                                 // steps looked up at once, a block a lane
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);    // swizzled tiles need it
@@ -151,6 +167,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     int &s_abort = *reinterpret_cast<int *>(s_cut + 2), &s_last = *(&s_abort + 1);
     int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
     long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
+    Shared *shared = reinterpret_cast<Shared *>(smem + L::kShared);
     const uint32_t ring = smem_u32(smem) + warp * NS * L::kStage;
     const uint32_t bars = smem_u32(smem + L::kBars) + warp * NS * 8;
     const int Hk = p.c.n_kv_heads, group = p.a.n_heads / Hk, B = p.b.n_seqs;
@@ -161,6 +178,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         tma_prefetch_desc(&tm_v);
     }
     if (lane < NS) mbar_init(bars + lane * 8, 1);
+    if (tid <= NW) shared[tid].has = 0;
     fence_mbar_init();
     kv_begin();
 
@@ -174,7 +192,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const int rows = s.n * group;
             const int tiles = p.row_limit > 0 && rows > p.row_limit ? 0 : (rows + ROWS - 1) / ROWS;
             seqs[i] = make_int4(s.q0, s.n, s.len, tiles);
-            v = (long long)tiles * Hk * span_of(s.n, s.len, p.a.window, p.a.sinks).steps;
+            v = (long long)tiles * Hk * span_of(s.n, s.len, p.a.window, p.a.sinks).template steps<BPS>();
         }
         long long inc = v;
 #pragma unroll
@@ -186,13 +204,14 @@ __global__ void __launch_bounds__(32 * NW, 1)
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
         long long ahead = total;
+#pragma unroll
         for (int w = 0; w < NW; ++w) {
-            ahead += w < warp ? s_scan[w] : 0;
-            total += s_scan[w];
+            const long long x = s_scan[w];
+            ahead += w < warp ? x : 0;
+            total += x;
         }
         if (i < B) pre[i] = ahead + inc - v;
     }
-    if (tid == 0) pre[B] = total;
     __syncthreads();
     if (total == 0) return;
 
@@ -207,46 +226,48 @@ __global__ void __launch_bounds__(32 * NW, 1)
         return lo;
     };
     const long long ctas = min((long long)gridDim.x, (total + kLeast - 1) / kLeast);
-    // where CTA i begins: an equal share, moved back to the tile's start in a short tile
-    auto cut = [&](long long i) {
-        const long long raw = i * total / ctas;
-        if (raw <= 0 || raw >= total) return raw;
-        const int b = find(raw);
-        const int4 s = seqs[b];
-        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).steps;
-        return steps > kShort ? raw : raw - (raw - pre[b]) % steps;
-    };
     if (blockIdx.x >= ctas) return;
-    if (tid < 2) s_cut[tid] = cut((long long)blockIdx.x + tid);
+    // where CTA i begins: an equal share, moved back to the tile's start in a short tile
+    if (tid < 2) {
+        long long at = ((long long)blockIdx.x + tid) * total / ctas;
+        if (at > 0 && at < total) {
+            const int b = find(at);
+            const int4 s = seqs[b];
+            const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
+            const long long rem = at - pre[b];
+            const int steps = sp.template steps<BPS>();
+            if (sp.blocks <= kShort) at -= rem - (long long)line_div(rem, steps) * steps;
+        }
+        s_cut[tid] = at;
+    }
     __syncthreads();
-    const long long c0 = s_cut[0], c1 = s_cut[1];
-    if (c0 >= c1) return;
-    const int mine = (int)(c1 - c0);
+    const long long c0 = s_cut[0];
+    const int mine = (int)(s_cut[1] - c0);
+    if (mine <= 0) return;
     const int w0 = (int)((long long)mine * warp / NW), w1 = (int)((long long)mine * (warp + 1) / NW);
 
-    // ---- 32 steps looked up at once, one a lane
+    // ---- blocks looked up a lane each: those of LOOK steps
     auto look_up = [&](int at) {
         Meta m;
-        m.page = -1, m.where = 0, m.pos = 0x7fffff00, m.tile = -1, m.ks = 0.0f, m.lv = 0.0f, m.iv = 0.0f;
+        m.page = -1, m.where = 0, m.pos = 0x7fffff00, m.ks = 0.0f, m.vs = 1.0f;
+        at += lane / BPS;
         if (at < w1) {
             const long long line = c0 + at;
             const int b = find(line);
             const int4 s = seqs[b];
             const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
             const long long rem = line - pre[b];
-            const int tile = (int)(rem / sp.steps), st = (int)(rem - (long long)tile * sp.steps);
-            const int head = tile / s.w;
-            const int blk = st < sp.sink_steps ? st : sp.first_step + st - sp.sink_steps;
-            m.tile = at - st;
-            m.where = (blk * kStep & ((1 << p.c.page_shift) - 1)) | head << 8;
-            if (blk * kStep < s.z) m.page = kv_page(p.c, p.b, b, blk * kStep >> p.c.page_shift, p.status);
+            const int steps = sp.template steps<BPS>(), tile = line_div(rem, steps);
+            const int st = (int)(rem - (long long)tile * steps), nth = st * BPS + lane % BPS;
+            const int head = (int)((unsigned)tile / (unsigned)s.w);
+            const int blk = nth < sp.sink ? nth : sp.first + nth - sp.sink;
+            m.where = (blk * kBlock & ((1 << p.c.page_shift) - 1)) | head << 8;
+            if (blk * kBlock < s.z) m.page = kv_page(p.c, p.b, b, blk * kBlock >> p.c.page_shift, p.status);
             if (m.page >= 0) {
-                m.pos = blk * kStep;
+                m.pos = blk * kBlock;
                 const long long i = (long long)m.page * Hk + head;
                 m.ks = __ldg(p.c.k_scale + i);
-                const float vs = __ldg(p.c.v_scale + i);
-                m.lv = __log2f(vs);
-                m.iv = 1.0f / vs;
+                m.vs = __ldg(p.c.v_scale + i);
             }
         }
         return m;
@@ -258,23 +279,15 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const int tok = where & 255, head = where >> 8;
             const int x = p.token_first ? head : tok, y = p.token_first ? tok : head;
             tma_load_4d(dst, &tm_k, bar, 0, x, y, page);
-            tma_load_4d(dst + kStep * D, &tm_v, bar, 0, x, y, page);
+            tma_load_4d(dst + kBlock * D, &tm_v, bar, 0, x, y, page);
         }
     };
-
-    Meta cur = look_up(w0 + lane), nxt = cur;
-    int fetched = w0;                                              // steps issued so far
-    for (; fetched < min(w0 + NS, w1); ++fetched) {
-        const int l = fetched - w0;
-        issue(l, __shfl_sync(0xffffffffu, cur.page, l), __shfl_sync(0xffffffffu, cur.where, l));
-    }
-    nxt = look_up(w0 + 32 + lane);
 
     // ---- the running tile
     uint32_t q[NR][KS][2];
     float o[NR][KS][4], ref[NR][2], sum[NR][2], fac[NR][2];
     int row_pos[NR][2];                                            // position of each row's token; -1: no such row
-    int tile = -1, tile_q0 = 0, tile_n = 0, tile_row = 0, tile_head = 0, min_pos = 0, max_pos = 0;
+    int tile = -1, tile_end = 0, tile_q0 = 0, tile_n = 0, tile_row = 0, tile_head = 0, min_pos = 0, max_pos = 0;
 
     auto row_of = [&](int nr, int e) { return nr * 8 + 2 * t + e; };
     // token row and query head of a row of the tile; false past the last
@@ -284,34 +297,49 @@ __global__ void __launch_bounds__(32 * NW, 1)
         at = (long long)(tile_q0 + r / group) * p.a.n_heads + tile_head * group + r % group;
         return true;
     };
-    auto start_tile = [&](int at) {
+    uint4 raw[NR][KS / 4][2];                                      // a row's 16-byte pieces before conversion
+    auto load_rows = [&](int at) {
         const long long line = c0 + at;
         const int b = find(line);
         const int4 s = seqs[b];
-        const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
-        const int idx = (int)((line - pre[b]) / sp.steps);
-        tile_head = idx / s.w;
-        tile_row = idx % s.w * ROWS;
+        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).template steps<BPS>();
+        const long long rem = line - pre[b];
+        const int idx = line_div(rem, steps);
+        tile = at - (int)(rem - (long long)idx * steps);
+        tile_end = tile + steps;
+        tile_head = (int)((unsigned)idx / (unsigned)s.w);
+        tile_row = (idx - tile_head * s.w) * ROWS;
         tile_q0 = s.x, tile_n = s.y;
         const int first = s.z - s.y;
         min_pos = first + tile_row / group;
         max_pos = first + min(tile_row + ROWS - 1, s.y * group - 1) / group;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            // row g's dims as B: for a lane's chunk t (and t + 4), four words of four dims each
-            float x[KS][4];
-            float top = 0.0f;
             const int r = tile_row + nr * 8 + g;
             const bool has = r < s.y * group;
             const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(s.x + r / group) * p.a.q_stride +
                                   (tile_head * group + r % group) * D;
 #pragma unroll
+            for (int j = 0; j < KS / 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    raw[nr][j][i] = has ? ldg_nc_v4(src + (t + 4 * j) * 16 + 8 * i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rr = tile_row + row_of(nr, e);
+                row_pos[nr][e] = rr < s.y * group ? first + rr / group : -1;
+            }
+        }
+    };
+    auto start_tile = [&]() {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            // row g's dims as B: for a lane's chunk t (and t + 4), four words of four dims each
+            float x[KS][4];
+            float top = 0.0f;
+#pragma unroll
             for (int j = 0; j < KS / 4; ++j) {
-                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (has) {
-                    v[0] = ldg_nc_v4(src + (t + 4 * j) * 16);
-                    v[1] = ldg_nc_v4(src + (t + 4 * j) * 16 + 8);
-                }
+                const uint4 *v = raw[nr][j];
                 const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -338,8 +366,6 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 fac[nr][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
-                const int rr = tile_row + row_of(nr, e);
-                row_pos[nr][e] = rr < s.y * group ? first + rr / group : -1;
                 ref[nr][e] = kRefStart;
                 sum[nr][e] = 0.0f;
             }
@@ -348,11 +374,25 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[nr][k][i] = 0.0f;
         }
-        tile = at;
     };
-    // dims of out that o[.][k][0..1] (i = 0) and o[.][k][2..3] (i = 1) hold: a lane has D / 8 in a row
-    // from g * D / 8 on, k and i counting them.
-    auto sum_rows = [&]() {
+    auto store_row = [&](long long at, int d0, const float *v, int count, float l, float m) {
+        const float r = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
+#pragma unroll
+        for (int i = 0; i < count; i += 4) {
+            uint2 w;
+            if (p.a.dtype == 0) {
+                w.x = pack_half2(v[i] * r, v[i + 1] * r), w.y = pack_half2(v[i + 2] * r, v[i + 3] * r);
+            } else {
+                w.x = pack_bf162(v[i] * r, v[i + 1] * r), w.y = pack_bf162(v[i + 2] * r, v[i + 3] * r);
+            }
+            *reinterpret_cast<uint2 *>(dst + i) = w;
+        }
+        if (p.a.lse && d0 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    };
+    // The tile's part of this warp: to the output when `whole`, else to `park`.
+    // o[.][k][0..1] and o[.][k][2..3] are dims g * D / 8 + 2 k and that plus 1.
+    auto finish_tile = [&](bool whole, float *park) {
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -360,38 +400,14 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 sum[nr][e] += __shfl_xor_sync(0xffffffffu, sum[nr][e], 4);
                 sum[nr][e] += __shfl_xor_sync(0xffffffffu, sum[nr][e], 8);
                 sum[nr][e] += __shfl_xor_sync(0xffffffffu, sum[nr][e], 16);
-            }
-    };
-    auto store_row = [&](long long at, int d0, const float *v, int count, float l, float m) {
-        const float r = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
-        for (int i = 0; i < count; i += 4) {
-            uint2 w;
-            if (p.a.dtype == 0) {
-                w.x = (uint32_t)kv_to_act<0>(v[i] * r) | (uint32_t)kv_to_act<0>(v[i + 1] * r) << 16;
-                w.y = (uint32_t)kv_to_act<0>(v[i + 2] * r) | (uint32_t)kv_to_act<0>(v[i + 3] * r) << 16;
-            } else {
-                w.x = (uint32_t)kv_to_act<1>(v[i] * r) | (uint32_t)kv_to_act<1>(v[i + 1] * r) << 16;
-                w.y = (uint32_t)kv_to_act<1>(v[i + 2] * r) | (uint32_t)kv_to_act<1>(v[i + 3] * r) << 16;
-            }
-            *reinterpret_cast<uint2 *>(dst + i) = w;
-        }
-        if (p.a.lse && d0 == 0) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
-    };
-    // The tile's part of this warp: to the output when `whole`, else to `park`.
-    auto finish_tile = [&](bool whole, float *park) {
-        sum_rows();
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
                 float v[2 * KS];
 #pragma unroll
                 for (int k = 0; k < KS; ++k) v[2 * k] = o[nr][k][e], v[2 * k + 1] = o[nr][k][2 + e];
                 const int row = row_of(nr, e);
+                long long at;
+                if (!place(row, at)) continue;
                 if (whole) {
-                    long long at;
-                    if (place(row, at)) store_row(at, g * 2 * KS, v, 2 * KS, sum[nr][e], ref[nr][e]);
+                    store_row(at, g * 2 * KS, v, 2 * KS, sum[nr][e], ref[nr][e]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2)
@@ -407,6 +423,18 @@ __global__ void __launch_bounds__(32 * NW, 1)
     float *first_part = reinterpret_cast<float *>(smem + L::kPark) + warp * L::kPart;
     float *last_part = reinterpret_cast<float *>(smem + warp * NS * L::kStage);
 
+    // ---- first copies, first rows
+    Meta cur = look_up(w0), nxt = cur;
+    const int blocks = (w1 - w0) * BPS;                            // the warp's blocks, two a step or one
+    int fetched = min(NS, blocks);                                 // blocks issued so far
+    for (int i = 0; i < fetched; ++i)
+        issue(i, __shfl_sync(0xffffffffu, cur.page, i), __shfl_sync(0xffffffffu, cur.where, i));
+    if (w0 < w1) {
+        load_rows(w0);
+        start_tile();
+    }
+    if (w0 + LOOK < w1) nxt = look_up(w0 + LOOK);
+
     // ---- steps
     // K rows as A: row g is key tau(g), row g + 8 key 8 + tau(g), an order in which eight lanes' 16-byte
     // chunks hit eight different bank groups of the swizzled tile.  P^T then has keys (tau(2t), tau(2t + 1))
@@ -417,269 +445,284 @@ __global__ void __launch_bounds__(32 * NW, 1)
     const int flip = D == 128 ? g & 1 : (g >> 1) & 1;
     const uint32_t sel_lo = flip ? 0x1504 : 0x5140, sel_hi = flip ? 0x3726 : 0x7362;
     bool failed = false;
-    int phase = 0, stage = 0;
+    int phase = 0, stage = 0;                                      // of the next block to consume
     for (int at = w0; at < w1; ++at) {
-        const int l = (at - w0) & 31;
+        const int l = (at - w0) % LOOK;
         if (l == 0 && at != w0) {
             cur = nxt;
-            nxt = look_up(at + 32 + lane);
+            if (at + LOOK < w1) nxt = look_up(at + LOOK);
         }
-        const int m_tile = __shfl_sync(0xffffffffu, cur.tile, l);
-        const int pos = __shfl_sync(0xffffffffu, cur.pos, l);
-        const float ks = __shfl_sync(0xffffffffu, cur.ks, l);
-        const float lv = __shfl_sync(0xffffffffu, cur.lv, l);
-        const float iv = __shfl_sync(0xffffffffu, cur.iv, l);
-        if (at == w0 || m_tile != tile) {
-            if (at != w0) finish_tile(tile >= w0, first_part);
-            start_tile(at);
-            tile = m_tile;
+        if (at == tile_end) {
+            finish_tile(tile >= w0, first_part);
+            load_rows(at);
+            start_tile();
         }
-        if (!mbar_wait_bounded(bars + stage * 8, phase, p.status, &s_abort)) {
-            failed = true;
-            break;
+        float s[BPS][NR][4], iv[BPS];
+        int pos[BPS], st[BPS];
+        bool edge[BPS];
+#pragma unroll
+        for (int b = 0; b < BPS; ++b) {
+            st[b] = stage;
+            if (!mbar_wait_bounded(bars + stage * 8, phase, p.status, &s_abort)) failed = true;
+            if (++stage == NS) stage = 0, phase ^= 1;
         }
-        const uint32_t kb = ring + stage * L::kStage, vb = kb + kStep * D;
-        float s[NR][4];
+        if (failed) break;
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
+        for (int b = 0; b < BPS; ++b) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nr][i] = 0.0f;
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int j = 0; j < KS / 4; ++j) {
-            const int chunk = t + 4 * j;
-            const int sw = D == 128 ? chunk ^ (tau & 7) : chunk ^ ((tau >> 1) & 3);
-            const uint4 a = lds128(kb + tau * D + sw * 16), b = lds128(kb + (tau + 8) * D + sw * 16);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+                for (int i = 0; i < 4; ++i) s[b][nr][i] = 0.0f;
+            const uint32_t kb = ring + st[b] * L::kStage;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t a0, a1, a2, a3;
-                codes_to_half<KT>(aw[w], a0, a2);
-                codes_to_half<KT>(bw[w], a1, a3);
+            for (int j = 0; j < KS / 4; ++j) {
+                const int chunk = t + 4 * j;
+                const int sw = D == 128 ? chunk ^ (tau & 7) : chunk ^ ((tau >> 1) & 3);
+                const uint4 x = lds128(kb + tau * D + sw * 16), y = lds128(kb + (tau + 8) * D + sw * 16);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-                    mma16816<0>(s[nr], a0, a1, a2, a3, q[nr][4 * j + w][0], q[nr][4 * j + w][1]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    codes_to_half<KT>(xw[w], a0, a2);
+                    codes_to_half<KT>(yw[w], a1, a3);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+                        mma16816<0>(s[b][nr], a0, a1, a2, a3, q[nr][4 * j + w][0], q[nr][4 * j + w][1]);
+                }
             }
         }
         // x_j + log2(vs); keys a row does not see get -inf
-        const bool edge = pos + kStep - 1 > min_pos ||
-                          (p.a.window > 0 && pos <= max_pos - p.a.window && pos + kStep > p.a.sinks);
+        float top[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) top[nr][0] = top[nr][1] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < BPS; ++b) {
+            const int from = l * BPS + b;
+            pos[b] = __shfl_sync(0xffffffffu, cur.pos, from);
+            const float ks = __shfl_sync(0xffffffffu, cur.ks, from), vs = __shfl_sync(0xffffffffu, cur.vs, from);
+            const float lv = __log2f(vs);
+            iv[b] = __fdividef(1.0f, vs);
+            edge[b] = pos[b] + kBlock - 1 > min_pos ||
+                      (p.a.window > 0 && pos[b] <= max_pos - p.a.window && pos[b] + kBlock > p.a.sinks);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[b][nr][i] = fmaf(s[b][nr][i], fac[nr][i & 1] * ks, lv);
+                if (edge[b])
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = pos[b] + tau + 8 * (i >> 1), r = row_pos[nr][i & 1];
+                        const bool see = j <= r && (p.a.window == 0 || r - j < p.a.window || j < p.a.sinks);
+                        if (!see) s[b][nr][i] = -INFINITY;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[nr][i & 1] = fmaxf(top[nr][i & 1], s[b][nr][i]);
+            }
+        }
         bool over = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = i & 1;
-                s[nr][i] = fmaf(s[nr][i], fac[nr][e] * ks, lv);
-                if (edge) {
-                    const int j = pos + tau + 8 * (i >> 1), r = row_pos[nr][e];
-                    const bool see = j <= r && (p.a.window == 0 || r - j < p.a.window || j < p.a.sinks);
-                    if (!see) s[nr][i] = -INFINITY;
-                }
-                over |= s[nr][i] - ref[nr][e] > kTop;
-            }
+            over |= top[nr][0] - ref[nr][0] > kTop || top[nr][1] - ref[nr][1] > kTop;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float top = fmaxf(s[nr][e], s[nr][2 + e]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    if (top - ref[nr][e] > kHead) {
-                        const float f = ex2(ref[nr][e] - (top - kHead));
-                        ref[nr][e] = top - kHead;
+                    float m = top[nr][e];
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                    if (m - ref[nr][e] > kHead) {
+                        const float f = ex2(ref[nr][e] - (m - kHead));
+                        ref[nr][e] = m - kHead;
                         sum[nr][e] *= f;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) o[nr][k][e] *= f, o[nr][k][2 + e] *= f;
                     }
                 }
         }
-        uint32_t pt[NR][2];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = ex2(s[nr][i] - ref[nr][i & 1]);
-            sum[nr][0] = fmaf(w[0] + w[2], iv, sum[nr][0]);
-            sum[nr][1] = fmaf(w[1] + w[3], iv, sum[nr][1]);
-            pt[nr][0] = movmatrix(pack_half2(w[0], w[1]));
-            pt[nr][1] = movmatrix(pack_half2(w[2], w[3]));
-        }
-        // V^T as A: byte i of a lane's chunk g is dim g * D / 8 + i
-        uint32_t vw[4][D / 32];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
-            if (D == 128) {
-                const uint4 v = lds128(vb + key * D + (g ^ (key & 7)) * 16);
-                vw[r][0] = v.x, vw[r][1] = v.y, vw[r][D / 32 - 2] = v.z, vw[r][D / 32 - 1] = v.w;
-            } else {
-                const uint2 v = lds64(vb + key * D + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
-                vw[r][0] = v.x, vw[r][1] = v.y;
-            }
-        }
-        if (edge && KT == kKvE4m3) {
-            // bytes of keys no row sees may be NaN codes; their weight of 0 would not hide them
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = pos + ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
-                if (j > max_pos)
-#pragma unroll
-                    for (int w = 0; w < D / 32; ++w) vw[r][w] = 0;
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-            uint32_t a[4][2];                                      // [dim of the word][keys 0/1 or 8/9]
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t x = vw[2 * h][w], y = vw[2 * h + 1][w];
-                codes_to_half<KT>(__byte_perm(x, y, sel_lo), a[0][h], a[1][h]);
-                codes_to_half<KT>(__byte_perm(x, y, sel_hi), a[2][h], a[3][h]);
-            }
+        for (int b = 0; b < BPS; ++b) {
+            uint32_t pt[NR][2];
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
-                mma16816<0>(o[nr][2 * w], a[0][0], a[1][0], a[0][1], a[1][1], pt[nr][0], pt[nr][1]);
-                mma16816<0>(o[nr][2 * w + 1], a[2][0], a[3][0], a[2][1], a[3][1], pt[nr][0], pt[nr][1]);
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = ex2(s[b][nr][i] - ref[nr][i & 1]);
+                sum[nr][0] = fmaf(w[0] + w[2], iv[b], sum[nr][0]);
+                sum[nr][1] = fmaf(w[1] + w[3], iv[b], sum[nr][1]);
+                pt[nr][0] = movmatrix(pack_half2(w[0], w[1]));
+                pt[nr][1] = movmatrix(pack_half2(w[2], w[3]));
+            }
+            // V^T as A: byte i of a lane's chunk g is dim g * D / 8 + i
+            const uint32_t vb = ring + st[b] * L::kStage + kBlock * D;
+            uint32_t vw[4][D / 32];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
+                if (D == 128) {
+                    const uint4 v = lds128(vb + key * D + (g ^ (key & 7)) * 16);
+                    vw[r][0] = v.x, vw[r][1] = v.y, vw[r][D / 32 - 2] = v.z, vw[r][D / 32 - 1] = v.w;
+                } else {
+                    const uint2 v = lds64(vb + key * D + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
+                    vw[r][0] = v.x, vw[r][1] = v.y;
+                }
+            }
+            if (KT == kKvE4m3 && edge[b]) {
+                // bytes of keys no row sees may be NaN codes; their weight of 0 would not hide them
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = pos[b] + ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
+                    if (j > max_pos)
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) vw[r][w] = 0;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+                uint32_t a[4][2];                                  // [dim of the word][keys 2t, 2t + 1 or those + 8]
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = vw[2 * h][w], y = vw[2 * h + 1][w];
+                    codes_to_half<KT>(__byte_perm(x, y, sel_lo), a[0][h], a[1][h]);
+                    codes_to_half<KT>(__byte_perm(x, y, sel_hi), a[2][h], a[3][h]);
+                }
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    mma16816<0>(o[nr][2 * w], a[0][0], a[1][0], a[0][1], a[1][1], pt[nr][0], pt[nr][1]);
+                    mma16816<0>(o[nr][2 * w + 1], a[2][0], a[3][0], a[2][1], a[3][1], pt[nr][0], pt[nr][1]);
+                }
             }
         }
         __syncwarp();
-        if (fetched < w1) {
-            const int f = (fetched - w0) & 31;
-            const bool ahead = ((fetched - w0) ^ (at - w0)) >= 32;
-            const int page = __shfl_sync(0xffffffffu, ahead ? nxt.page : cur.page, f);
-            const int where = __shfl_sync(0xffffffffu, ahead ? nxt.where : cur.where, f);
+        if (fetched < blocks) {
             if (lane == 0) fence_proxy_async_smem();
-            issue(stage, page, where);
-            ++fetched;
+            // the blocks just freed: `fetched` counts blocks, LOOK * BPS = 32 of them a look-up
+            const bool ahead = fetched / 32 != (at - w0) / LOOK;
+#pragma unroll
+            for (int b = 0; b < BPS; ++b) {
+                // with an odd ring the two blocks of a step may belong to different look-ups
+                const int f = fetched + b;
+                const bool far = BPS == 1 ? ahead : f / 32 != (at - w0) / LOOK;
+                const int page = __shfl_sync(0xffffffffu, far ? nxt.page : cur.page, f & 31);
+                const int where = __shfl_sync(0xffffffffu, far ? nxt.where : cur.where, f & 31);
+                if (f < blocks) issue(st[b], page, where);
+            }
+            fetched += BPS;
         }
-        if (++stage == NS) stage = 0, phase ^= 1;
     }
     if (failed) {
         // leave with no copy in flight
-        for (int at = fetched - w0 - NS; at < fetched - w0; ++at)
-            if (at >= 0) mbar_wait_bounded(bars + at % NS * 8, (at / NS) & 1, p.status, &s_abort);
-    }
-    // the piece still held: whole when its tile begins here and ends here
-    if (w0 < w1 && !failed) {
-        const long long line = c0 + w1;
-        const int b = find(line - 1);
-        const int4 s = seqs[b];
-        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).steps;
-        const bool ends = (line - pre[b]) % steps == 0;
-        if (tile >= w0 && ends) {
+        for (int i = max(0, min(fetched, blocks) - NS); i < min(fetched, blocks); ++i)
+            mbar_wait_bounded(bars + i % NS * 8, (i / NS) & 1, p.status, &s_abort);
+    } else if (w0 < w1) {
+        // the piece still held: whole when its tile begins here and ends here
+        if (tile >= w0 && tile_end <= w1) {
             finish_tile(true, nullptr);
-        } else if (tile < w0) {
-            finish_tile(false, first_part);                        // began before this warp: ends or goes on
         } else {
             __syncwarp();
-            finish_tile(false, last_part);                         // begins here, goes on
+            finish_tile(false, tile < w0 ? first_part : last_part);
+        }
+        if (lane == 0) {
+            // the warp that holds a tile's first part in this CTA says so
+            if (tile >= w0 && tile_end > w1) shared[1 + warp] = Shared{1, warp, tile, tile_end, tile_q0, tile_n, tile_head, tile_row};
+        }
+    }
+    // a tile that an earlier CTA began: the CTA's first step is in it
+    if (tid == 0) {
+        const int b = find(c0);
+        const int4 s = seqs[b];
+        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).template steps<BPS>();
+        const long long rem = c0 - pre[b];
+        const int idx = line_div(rem, steps), begin = (int)((long long)idx * steps - rem);
+        if (begin < 0) {
+            const int head = (int)((unsigned)idx / (unsigned)s.w);
+            shared[0] = Shared{1, 0, begin, begin + steps, s.x, s.y, head, (idx - head * s.w) * ROWS};
         }
     }
     __syncthreads();
     if (s_abort) return;
 
-    // ---- tiles that more than one warp holds a part of
-    // The CTA's tiles in order: one that began earlier (or at c0), then each that a warp begins and does
-    // not end.  All threads sum the parts of one tile, in warp order.
-    for (int w = 0; w < NW; ++w) {
-        // a tile whose first part in this CTA is warp w's
-        const int a0 = (int)((long long)mine * w / NW), a1 = (int)((long long)mine * (w + 1) / NW);
-        if (a0 >= a1) continue;
-        for (int which = 0; which < 2; ++which) {
-            // which = 0: the tile at the CTA's first step, if it began in an earlier CTA; 1: the tile at the
-            // warp's last step, if it begins in this warp and goes on after it
-            if (which == 0 && a0 != 0) continue;
-            const int probe = which == 0 ? 0 : a1 - 1;
-            const int b = find(c0 + probe);
-            const int4 s = seqs[b];
-            const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).steps;
-            const long long begin = c0 + probe - (c0 + probe - pre[b]) % steps, end = begin + steps;
-            if (which == 0 ? begin >= c0 : (begin < c0 + a0 || end <= c0 + a1)) continue;
-            // its parts: warp w's, then the first parts of the warps after it up to the tile's end
-            tile_q0 = s.x, tile_n = s.y;
-            const int idx = (int)((begin - pre[b]) / steps);
-            tile_head = idx / s.w, tile_row = idx % s.w * ROWS;
-            const bool whole = begin >= c0 && end <= c1;
-            const int slot = which == 0 ? 0 : 1;
-            float *dst = p.parts + ((long long)blockIdx.x * 2 + slot) * L::kPart;
-            const int rows = min(ROWS, s.y * group - tile_row);
-            for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
-                const int row = i / (D / 4), d = i % (D / 4) * 4;
-                float m = kRefStart;
-                for (int v = w; v < NW; ++v) {
-                    const long long v0 = c0 + (long long)mine * v / NW;
-                    const long long v1 = c0 + (long long)mine * (v + 1) / NW;
-                    if (v0 >= v1) continue;
-                    if (v0 >= end) break;
-                    const float *part = v == w && which == 1
-                                            ? reinterpret_cast<const float *>(smem + v * NS * L::kStage)
-                                            : reinterpret_cast<const float *>(smem + L::kPark) + v * L::kPart;
-                    m = fmaxf(m, part[ROWS * D + 2 * row]);
-                }
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-                for (int v = w; v < NW; ++v) {
-                    const long long v0 = c0 + (long long)mine * v / NW;
-                    const long long v1 = c0 + (long long)mine * (v + 1) / NW;
-                    if (v0 >= v1) continue;
-                    if (v0 >= end) break;
-                    const float *part = v == w && which == 1
-                                            ? reinterpret_cast<const float *>(smem + v * NS * L::kStage)
-                                            : reinterpret_cast<const float *>(smem + L::kPark) + v * L::kPart;
-                    const float f = ex2(part[ROWS * D + 2 * row] - m);
-                    const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
-                    l = fmaf(part[ROWS * D + 2 * row + 1], f, l);
-                    acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-                    acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
-                }
-                if (whole) {
-                    long long at;
-                    if (place(row, at)) store_row(at, d, acc, 4, l, m);
-                } else {
-                    *reinterpret_cast<float4 *>(dst + row * D + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    if (d == 0) dst[ROWS * D + 2 * row] = m, dst[ROWS * D + 2 * row + 1] = l;
-                }
+    // ---- tiles that more than one warp holds a part of: all threads sum the parts of one, in warp order
+    for (int r = 0; r <= NW; ++r) {
+        const Shared sh = shared[r];
+        if (!sh.has) continue;
+        tile_q0 = sh.q0, tile_n = sh.n, tile_head = sh.head, tile_row = sh.row;
+        const bool whole = sh.begin >= 0 && sh.end <= mine;
+        const int rows = min(ROWS, sh.n * group - sh.row);
+        float *dst = p.parts + ((long long)blockIdx.x * 2 + (r > 0)) * L::kPart;
+        // parts: the first warp's (its last one when the tile begins there), then the first ones of the
+        // warps after it up to the tile's end
+        auto part_of = [&](int v) -> const float * {
+            const int v0 = (int)((long long)mine * v / NW), v1 = (int)((long long)mine * (v + 1) / NW);
+            if (v0 >= v1 || v0 >= sh.end) return nullptr;
+            return r > 0 && v == sh.first_warp ? reinterpret_cast<const float *>(smem + v * NS * L::kStage)
+                                               : reinterpret_cast<const float *>(smem + L::kPark) + v * L::kPart;
+        };
+        for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            float m = kRefStart;
+            for (int v = sh.first_warp; v < NW; ++v) {
+                const float *part = part_of(v);
+                if (part) m = fmaxf(m, part[ROWS * D + 2 * row]);
             }
-            if (whole) continue;
-            // ---- a tile that CTAs from..to share: the last of them to come sums it
-            const int from = (int)(((begin + 1) * ctas + total - 1) / total - 1);
-            const int to = (int)((end * ctas + total - 1) / total - 1);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                unsigned long long *tk = p.tickets + from, old = *tk, seen;
-                unsigned long long put;
-                do {
-                    seen = old;
-                    const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
-                    put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
-                    old = atomicCAS(tk, seen, put);
-                } while (old != seen);
-                __threadfence();
-                s_last = put == 0;
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+            for (int v = sh.first_warp; v < NW; ++v) {
+                const float *part = part_of(v);
+                if (!part) continue;
+                const float f = ex2(part[ROWS * D + 2 * row] - m);
+                const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
+                l = fmaf(part[ROWS * D + 2 * row + 1], f, l);
+                acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+                acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
             }
-            __syncthreads();
-            if (!s_last) continue;
-            for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
-                const int row = i / (D / 4), d = i % (D / 4) * 4;
-                float m = kRefStart;
-                // CTA `from` holds its part in slot 1, the others in slot 0
-                for (int c = from; c <= to; ++c)
-                    m = fmaxf(m, __ldcg(p.parts + ((long long)c * 2 + (c == from)) * L::kPart + ROWS * D + 2 * row));
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-#pragma unroll 4
-                for (int c = from; c <= to; ++c) {
-                    const float *part = p.parts + ((long long)c * 2 + (c == from)) * L::kPart;
-                    const float f = ex2(__ldcg(part + ROWS * D + 2 * row) - m);
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + row * D + d));
-                    l = fmaf(__ldcg(part + ROWS * D + 2 * row + 1), f, l);
-                    acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-                    acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
-                }
+            if (whole) {
                 long long at;
                 if (place(row, at)) store_row(at, d, acc, 4, l, m);
+            } else {
+                __stcg(reinterpret_cast<float4 *>(dst + row * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
+                if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + ROWS * D + 2 * row), make_float2(m, l));
             }
+        }
+        if (whole) continue;
+        // ---- a tile that CTAs from..to share: the last of them to come sums it
+        const long long begin = c0 + sh.begin, end = c0 + sh.end;
+        const int from = (int)(((begin + 1) * ctas + total - 1) / total - 1);
+        const int to = (int)((end * ctas + total - 1) / total - 1);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
+            do {
+                seen = old;
+                const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
+                put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
+                old = atomicCAS(tk, seen, put);
+            } while (old != seen);
+            __threadfence();
+            s_last = put == 0;
+        }
+        __syncthreads();
+        if (!s_last) continue;
+        // CTA `from` holds its part in slot 1, the others in slot 0
+        auto slot = [&](int c) { return p.parts + ((long long)c * 2 + (c == from)) * L::kPart; };
+        for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            float m = kRefStart;
+#pragma unroll 8
+            for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(slot(c) + ROWS * D + 2 * row));
+            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+#pragma unroll 8
+            for (int c = from; c <= to; ++c) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot(c) + ROWS * D + 2 * row));
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot(c) + row * D + d));
+                const float f = ex2(ml.x - m);
+                l = fmaf(ml.y, f, l);
+                acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+                acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
+            }
+            long long at;
+            if (place(row, at)) store_row(at, d, acc, 4, l, m);
         }
     }
 }
@@ -708,16 +751,16 @@ cudaError_t encode_codes(const DeviceInfo &dev, const KvCache &c, void *base, in
     }
     const CUresult r = reinterpret_cast<EncodeTiledFn>(dev.encode_tiled)(
         out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-        c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int KT, int D, int NR, int NW, int NS>
+template <int KT, int D, int NR, int BPS, int NW, int NS>
 cudaError_t launch_few(const FewParams &p, const CUtensorMap &k, const CUtensorMap &v, int grid, cudaStream_t s,
                        bool pdl) {
     using L = FewSmem<D, NR, NW, NS>;
-    auto kern = few_rows_kernel<KT, D, NR, NW, NS>;
+    auto kern = few_rows_kernel<KT, D, NR, BPS, NW, NS>;
     const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(kern), L::kEnd);
     if (e != cudaSuccess) return e;
     return kv_launch(kern, dim3(grid), dim3(32 * NW), L::kEnd, s, pdl, k, v, p);
@@ -732,8 +775,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     const int group = a.n_heads / c.n_kv_heads;
     const bool token_first = c.n_kv_heads > 1 && c.head_stride < c.token_stride;
     CUtensorMap k, v;
-    cudaError_t e = encode_codes(dev, c, c.k, kStep, token_first, &k);
-    if (e == cudaSuccess) e = encode_codes(dev, c, c.v, kStep, token_first, &v);
+    cudaError_t e = encode_codes(dev, c, c.k, kBlock, token_first, &k);
+    if (e == cudaSuccess) e = encode_codes(dev, c, c.v, kBlock, token_first, &v);
     if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> launches{0x5ca1ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
@@ -750,10 +793,10 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         const int grid = dev.sm_count;
         const bool few = (long long)a.max_q_len * group <= 8;
 #define W4A16_FEW(KT)                                                                          \
-    e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 8, 5>(p, k, v, grid, s, pdl)         \
-                                 : launch_few<KT, 128, 2, 8, 4>(p, k, v, grid, s, pdl))        \
-                          : (few ? launch_few<KT, 64, 1, 8, 10>(p, k, v, grid, s, pdl)         \
-                                 : launch_few<KT, 64, 2, 8, 8>(p, k, v, grid, s, pdl))
+    e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 2, 8, 5>(p, k, v, grid, s, pdl)         \
+                                 : launch_few<KT, 128, 2, 1, 8, 4>(p, k, v, grid, s, pdl))        \
+                          : (few ? launch_few<KT, 64, 1, 2, 8, 10>(p, k, v, grid, s, pdl)         \
+                                 : launch_few<KT, 64, 2, 1, 8, 8>(p, k, v, grid, s, pdl))
         if (c.kv_dtype == kKvInt8) W4A16_FEW(kKvInt8);
         else W4A16_FEW(kKvE4m3);
 #undef W4A16_FEW
