@@ -48,6 +48,7 @@ constexpr int kBlock = 16;                // keys of a block: one TMA box of K, 
 constexpr int kMaxSeqs = 512;             // sequences of a launch
 constexpr int kShort = 256 / kBlock;      // tiles of up to so many blocks stay in one CTA
 constexpr int kLeast = 2;                 // fewest steps worth a CTA
+constexpr int kTileCost = 2;              // blocks that the start and end of a tile count for in the shares
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
 constexpr float kHead = 14.0f;            // ... and a moved reference puts the largest at 2^kHead
@@ -98,10 +99,11 @@ struct FewSmem {
     static constexpr int kPark = NW * NS * kStage;                 // a warp's first piece, if another began it
     static constexpr int kSeq = kPark + NW * kPart * 4;            // int4 {q0, n, len, row tiles}
     static constexpr int kPre = kSeq + kMaxSeqs * 16;              // line position of each sequence
-    static constexpr int kBars = kPre + (kMaxSeqs + 1) * 8;
+    static constexpr int kTiles = kPre + kMaxSeqs * 8;             // tiles of the sequences before each
+    static constexpr int kBars = kTiles + kMaxSeqs * 4;
     static constexpr int kShared = kBars + NW * NS * 8;            // tiles that warps share: the CTA's first, then by warp
     static constexpr int kMisc = kShared + (NW + 1) * 32;
-    static constexpr int kEnd = kMisc + (NW + 3) * 8 + 1024;       // 1024: slack to align the base
+    static constexpr int kEnd = kMisc + (2 * NW + 1) * 8 + 32 + 1024;       // 1024: slack to align the base
     static_assert(NS * kStage >= kPart * 4, "the last piece is parked in the ring");
 };
 
@@ -164,9 +166,11 @@ __global__ void __launch_bounds__(32 * NW, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);    // swizzled tiles need it
     // no static shared memory: the launch may ask for all of an SM's
     long long *s_scan = reinterpret_cast<long long *>(smem + L::kMisc), *s_cut = s_scan + NW;
-    int &s_abort = *reinterpret_cast<int *>(s_cut + 2), &s_last = *(&s_abort + 1);
+    int &s_abort = *reinterpret_cast<int *>(s_cut + NW + 1);
+    int *s_out = &s_abort + 1, *s_from = s_out + 2, *s_to = s_from + 2;      // tiles shared with other CTAs
     int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
     long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
+    int *tiles_before = reinterpret_cast<int *>(smem + L::kTiles);
     Shared *shared = reinterpret_cast<Shared *>(smem + L::kShared);
     const uint32_t ring = smem_u32(smem) + warp * NS * L::kStage;
     const uint32_t bars = smem_u32(smem + L::kBars) + warp * NS * 8;
@@ -174,6 +178,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
 
     if (tid == 0) {
         s_abort = 0;
+        s_out[0] = s_out[1] = -1;
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
@@ -182,71 +187,100 @@ __global__ void __launch_bounds__(32 * NW, 1)
     fence_mbar_init();
     kv_begin();
 
-    // ---- the line: each sequence's steps, summed up
-    long long total = 0;
+    // ---- the line: each sequence's steps and tiles, summed up
+    constexpr int COST = (kTileCost + BPS - 1) / BPS;
+    long long total = 0;                                           // steps, and COST a tile
+    int tiles_all = 0;
     for (int base = 0; base < B; base += 32 * NW) {
         const int i = base + tid;
         long long v = 0;
+        int tiles = 0;
         if (i < B) {
             const KvSeq s = kv_sequence(p.b, p.c.page_shift, i, p.status);
             const int rows = s.n * group;
-            const int tiles = p.row_limit > 0 && rows > p.row_limit ? 0 : (rows + ROWS - 1) / ROWS;
-            seqs[i] = make_int4(s.q0, s.n, s.len, tiles);
-            v = (long long)tiles * Hk * span_of(s.n, s.len, p.a.window, p.a.sinks).template steps<BPS>();
+            const int row_tiles = p.row_limit > 0 && rows > p.row_limit ? 0 : (rows + ROWS - 1) / ROWS;
+            seqs[i] = make_int4(s.q0, s.n, s.len, row_tiles);
+            tiles = row_tiles * Hk;
+            v = (long long)tiles * (span_of(s.n, s.len, p.a.window, p.a.sinks).template steps<BPS>() + COST);
         }
         long long inc = v;
+        int inc_tiles = tiles;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
+            const long long x = __shfl_up_sync(0xffffffffu, inc, d);
+            const int y = __shfl_up_sync(0xffffffffu, inc_tiles, d);
+            if (lane >= d) inc += x, inc_tiles += y;
         }
         __syncthreads();
-        if (lane == 31) s_scan[warp] = inc;
+        if (lane == 31) s_scan[warp] = inc, s_cut[warp] = inc_tiles;
         __syncthreads();
         long long ahead = total;
+        int tiles_ahead = tiles_all;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const long long x = s_scan[w];
+            const int y = (int)s_cut[w];
             ahead += w < warp ? x : 0;
+            tiles_ahead += w < warp ? y : 0;
             total += x;
+            tiles_all += y;
         }
-        if (i < B) pre[i] = ahead + inc - v;
+        if (i < B) {
+            tiles_before[i] = tiles_ahead + inc_tiles - tiles;
+            pre[i] = ahead + inc - v - (long long)tiles_before[i] * COST;
+        }
     }
     __syncthreads();
     if (total == 0) return;
 
-    // the sequence of a position of the line
-    auto find = [&](long long at) {
+    // the sequence of a position of the line: of steps alone (cost = 0), or with the tiles' cost
+    auto find = [&](long long at, int cost = 0) {
         int lo = 0, hi = B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (pre[mid] <= at) lo = mid;
+            if (pre[mid] + (long long)tiles_before[mid] * cost <= at) lo = mid;
             else hi = mid - 1;
         }
         return lo;
     };
-    const long long ctas = min((long long)gridDim.x, (total + kLeast - 1) / kLeast);
+    const long long ctas = min((long long)gridDim.x, (total + kLeast + COST - 1) / (kLeast + COST));
     if (blockIdx.x >= ctas) return;
-    // where CTA i begins: an equal share, moved back to the tile's start in a short tile
-    if (tid < 2) {
-        long long at = ((long long)blockIdx.x + tid) * total / ctas;
-        if (at > 0 && at < total) {
-            const int b = find(at);
-            const int4 s = seqs[b];
-            const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
-            const long long rem = at - pre[b];
-            const int steps = sp.template steps<BPS>();
-            if (sp.blocks <= kShort) at -= rem - (long long)line_div(rem, steps) * steps;
+    // The step where an equal share of the work begins: `at` steps and tiles' costs into the line.  In a
+    // short tile, when `snap`, the tile's first; *moved is where that is with the costs.
+    auto step_of = [&](long long at, bool snap, long long &moved) {
+        moved = at;
+        const int b = find(at, COST);
+        const int4 s = seqs[b];
+        const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
+        const int steps = sp.template steps<BPS>();
+        const long long rem = at - pre[b] - (long long)tiles_before[b] * COST;
+        const int idx = line_div(rem, steps + COST);
+        int st = (int)(rem - (long long)idx * (steps + COST));
+        if (snap && sp.blocks <= kShort) {
+            moved -= st;
+            st = 0;
         }
-        s_cut[tid] = at;
+        // past the last tile of a sequence that has any, the next one's first step
+        return pre[b] + (long long)idx * steps + min(max(st - COST, 0), steps);
+    };
+    if (warp == 0) {
+        long long v = ((long long)blockIdx.x + min(lane, 1)) * total / ctas, moved;
+        const long long end = step_of(v, true, moved);
+        const long long v0 = __shfl_sync(0xffffffffu, moved, 0), v1 = __shfl_sync(0xffffffffu, moved, 1);
+        const long long c0 = __shfl_sync(0xffffffffu, end, 0), c1 = __shfl_sync(0xffffffffu, end, 1);
+        if (lane <= NW) {
+            const long long mid = step_of(v0 + (v1 - v0) * lane / NW, false, moved);
+            s_cut[lane] = lane == 0 ? c0 : lane == NW ? c1 : min(max(mid, c0), c1);
+        }
     }
     __syncthreads();
     const long long c0 = s_cut[0];
-    const int mine = (int)(s_cut[1] - c0);
+    const int mine = (int)(s_cut[NW] - c0);
     if (mine <= 0) return;
-    const int w0 = (int)((long long)mine * warp / NW), w1 = (int)((long long)mine * (warp + 1) / NW);
+    auto warp_start = [&](int w) { return (int)(s_cut[w] - c0); };
+    const int w0 = warp_start(warp), w1 = warp_start(warp + 1);
 
-    // ---- blocks looked up a lane each: those of LOOK steps
+    // ---- blocks looked up a lane each, those of LOOK steps: first the page id, then, once it is here, the scales
     auto look_up = [&](int at) {
         Meta m;
         m.page = -1, m.where = 0, m.pos = 0x7fffff00, m.ks = 0.0f, m.vs = 1.0f;
@@ -258,19 +292,27 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
             const long long rem = line - pre[b];
             const int steps = sp.template steps<BPS>(), tile = line_div(rem, steps);
-            const int st = (int)(rem - (long long)tile * steps), nth = st * BPS + lane % BPS;
+            const int nth = (int)(rem - (long long)tile * steps) * BPS + lane % BPS;
             const int head = (int)((unsigned)tile / (unsigned)s.w);
             const int blk = nth < sp.sink ? nth : sp.first + nth - sp.sink;
             m.where = (blk * kBlock & ((1 << p.c.page_shift) - 1)) | head << 8;
-            if (blk * kBlock < s.z) m.page = kv_page(p.c, p.b, b, blk * kBlock >> p.c.page_shift, p.status);
-            if (m.page >= 0) {
+            if (blk * kBlock < s.z) {
                 m.pos = blk * kBlock;
-                const long long i = (long long)m.page * Hk + head;
-                m.ks = __ldg(p.c.k_scale + i);
-                m.vs = __ldg(p.c.v_scale + i);
+                m.page = p.b.block_table[(long long)b * p.b.max_blocks + (blk * kBlock >> p.c.page_shift)];
             }
         }
         return m;
+    };
+    auto look_up_scales = [&](Meta &m) {
+        if (m.pos == 0x7fffff00) return;
+        if (m.page < 0 || m.page >= p.c.n_pages) {
+            kv_report(p.status);
+            m.page = -1, m.pos = 0x7fffff00;
+            return;
+        }
+        const long long i = (long long)m.page * Hk + (m.where >> 8);
+        m.ks = __ldg(p.c.k_scale + i);
+        m.vs = __ldg(p.c.v_scale + i);
     };
     auto issue = [&](int stage, int page, int where) {
         if (lane == 0) {
@@ -284,54 +326,59 @@ __global__ void __launch_bounds__(32 * NW, 1)
     };
 
     // ---- the running tile
+    struct Tile {
+        int begin, end;                                            // on the CTA's line
+        int q0, n, row, head;                                      // the sequence's rows, the tile's first row, its kv head
+        int first;                                                 // position of the sequence's first new token
+    };
     uint32_t q[NR][KS][2];
     float o[NR][KS][4], ref[NR][2], sum[NR][2], fac[NR][2];
-    int row_pos[NR][2];                                            // position of each row's token; -1: no such row
-    int tile = -1, tile_end = 0, tile_q0 = 0, tile_n = 0, tile_row = 0, tile_head = 0, min_pos = 0, max_pos = 0;
+    int row_pos[NR][2], min_pos = 0, max_pos = 0;                  // position of each row's token; -1: no such row
+    Tile tile = {}, next = {};
+    uint4 raw[NR][KS / 4][2];                                      // rows of a tile to come, before conversion
 
     auto row_of = [&](int nr, int e) { return nr * 8 + 2 * t + e; };
-    // token row and query head of a row of the tile; false past the last
-    auto place = [&](int row, long long &at) {
-        const int r = tile_row + row;
-        if (r >= tile_n * group) return false;
-        at = (long long)(tile_q0 + r / group) * p.a.n_heads + tile_head * group + r % group;
+    auto divide = [](int x, int y) { return (int)((unsigned)x / (unsigned)y); };
+    // token row and query head of a row of a tile; false past the last
+    auto place = [&](const Tile &tl, int row, long long &at) {
+        const int r = tl.row + row;
+        if (r >= tl.n * group) return false;
+        const int tok = divide(r, group);
+        at = (long long)(tl.q0 + tok) * p.a.n_heads + tl.head * group + r - tok * group;
         return true;
     };
-    uint4 raw[NR][KS / 4][2];                                      // a row's 16-byte pieces before conversion
     auto load_rows = [&](int at) {
+        Tile tl;
         const long long line = c0 + at;
         const int b = find(line);
         const int4 s = seqs[b];
         const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).template steps<BPS>();
         const long long rem = line - pre[b];
         const int idx = line_div(rem, steps);
-        tile = at - (int)(rem - (long long)idx * steps);
-        tile_end = tile + steps;
-        tile_head = (int)((unsigned)idx / (unsigned)s.w);
-        tile_row = (idx - tile_head * s.w) * ROWS;
-        tile_q0 = s.x, tile_n = s.y;
-        const int first = s.z - s.y;
-        min_pos = first + tile_row / group;
-        max_pos = first + min(tile_row + ROWS - 1, s.y * group - 1) / group;
+        tl.begin = at - (int)(rem - (long long)idx * steps);
+        tl.end = tl.begin + steps;
+        tl.head = divide(idx, s.w);
+        tl.row = (idx - tl.head * s.w) * ROWS;
+        tl.q0 = s.x, tl.n = s.y;
+        tl.first = s.z - s.y;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            const int r = tile_row + nr * 8 + g;
+            const int r = tl.row + nr * 8 + g, tok = divide(r, group);
             const bool has = r < s.y * group;
-            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(s.x + r / group) * p.a.q_stride +
-                                  (tile_head * group + r % group) * D;
+            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(s.x + tok) * p.a.q_stride +
+                                  (tl.head * group + r - tok * group) * D;
 #pragma unroll
             for (int j = 0; j < KS / 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     raw[nr][j][i] = has ? ldg_nc_v4(src + (t + 4 * j) * 16 + 8 * i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int rr = tile_row + row_of(nr, e);
-                row_pos[nr][e] = rr < s.y * group ? first + rr / group : -1;
-            }
         }
+        return tl;
     };
-    auto start_tile = [&]() {
+    auto start_tile = [&](const Tile &tl) {
+        tile = tl;
+        min_pos = tl.first + divide(tl.row, group);
+        max_pos = tl.first + divide(min(tl.row + ROWS, tl.n * group) - 1, group);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             // row g's dims as B: for a lane's chunk t (and t + 4), four words of four dims each
@@ -366,6 +413,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 fac[nr][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
+                const int rr = tl.row + row_of(nr, e);
+                row_pos[nr][e] = rr < tl.n * group ? tl.first + divide(rr, group) : -1;
                 ref[nr][e] = kRefStart;
                 sum[nr][e] = 0.0f;
             }
@@ -405,7 +454,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 for (int k = 0; k < KS; ++k) v[2 * k] = o[nr][k][e], v[2 * k + 1] = o[nr][k][2 + e];
                 const int row = row_of(nr, e);
                 long long at;
-                if (!place(row, at)) continue;
+                if (!place(tile, row, at)) continue;
                 if (whole) {
                     store_row(at, g * 2 * KS, v, 2 * KS, sum[nr][e], ref[nr][e]);
                 } else {
@@ -423,17 +472,15 @@ __global__ void __launch_bounds__(32 * NW, 1)
     float *first_part = reinterpret_cast<float *>(smem + L::kPark) + warp * L::kPart;
     float *last_part = reinterpret_cast<float *>(smem + warp * NS * L::kStage);
 
-    // ---- first copies, first rows
+    // ---- first copies, first rows: every load on its way before one is waited for
     Meta cur = look_up(w0), nxt = cur;
+    if (w0 < w1) next = load_rows(w0);
+    look_up_scales(cur);
     const int blocks = (w1 - w0) * BPS;                            // the warp's blocks, two a step or one
     int fetched = min(NS, blocks);                                 // blocks issued so far
     for (int i = 0; i < fetched; ++i)
         issue(i, __shfl_sync(0xffffffffu, cur.page, i), __shfl_sync(0xffffffffu, cur.where, i));
-    if (w0 < w1) {
-        load_rows(w0);
-        start_tile();
-    }
-    if (w0 + LOOK < w1) nxt = look_up(w0 + LOOK);
+    if (w0 < w1) start_tile(next);
 
     // ---- steps
     // K rows as A: row g is key tau(g), row g + 8 key 8 + tau(g), an order in which eight lanes' 16-byte
@@ -448,15 +495,16 @@ __global__ void __launch_bounds__(32 * NW, 1)
     int phase = 0, stage = 0;                                      // of the next block to consume
     for (int at = w0; at < w1; ++at) {
         const int l = (at - w0) % LOOK;
-        if (l == 0 && at != w0) {
-            cur = nxt;
-            if (at + LOOK < w1) nxt = look_up(at + LOOK);
+        // the next blocks' page ids and scales, a few steps apart so that neither is waited for
+        if (l == 0 && at != w0) cur = nxt;
+        if (l == 1 && at - 1 + LOOK < w1) nxt = look_up(at - 1 + LOOK);
+        if (l == LOOK / 4 && at - l + LOOK < w1) look_up_scales(nxt);
+        if (at == tile.end) {
+            finish_tile(tile.begin >= w0, first_part);
+            if (NR > 1) next = load_rows(at);
+            start_tile(next);
         }
-        if (at == tile_end) {
-            finish_tile(tile >= w0, first_part);
-            load_rows(at);
-            start_tile();
-        }
+        if (NR == 1 && at + 1 == tile.end && at + 1 < w1) next = load_rows(at + 1);
         float s[BPS][NR][4], iv[BPS];
         int pos[BPS], st[BPS];
         bool edge[BPS];
@@ -617,16 +665,16 @@ __global__ void __launch_bounds__(32 * NW, 1)
             mbar_wait_bounded(bars + i % NS * 8, (i / NS) & 1, p.status, &s_abort);
     } else if (w0 < w1) {
         // the piece still held: whole when its tile begins here and ends here
-        if (tile >= w0 && tile_end <= w1) {
+        if (tile.begin >= w0 && tile.end <= w1) {
             finish_tile(true, nullptr);
         } else {
             __syncwarp();
-            finish_tile(false, tile < w0 ? first_part : last_part);
+            finish_tile(false, tile.begin < w0 ? first_part : last_part);
         }
-        if (lane == 0) {
-            // the warp that holds a tile's first part in this CTA says so
-            if (tile >= w0 && tile_end > w1) shared[1 + warp] = Shared{1, warp, tile, tile_end, tile_q0, tile_n, tile_head, tile_row};
-        }
+        // the warp that holds a tile's first part in this CTA says so
+        const bool leads = tile.begin >= w0 && tile.end > w1;
+        if (lane == 0 && leads) shared[1 + warp] = Shared{1, warp, tile.begin, tile.end, tile.q0, tile.n, tile.head, tile.row};
+        if (lane == 0 && leads && tile.end > mine) s_out[1] = 1 + warp;
     }
     // a tile that an earlier CTA began: the CTA's first step is in it
     if (tid == 0) {
@@ -636,62 +684,67 @@ __global__ void __launch_bounds__(32 * NW, 1)
         const long long rem = c0 - pre[b];
         const int idx = line_div(rem, steps), begin = (int)((long long)idx * steps - rem);
         if (begin < 0) {
-            const int head = (int)((unsigned)idx / (unsigned)s.w);
+            const int head = divide(idx, s.w);
             shared[0] = Shared{1, 0, begin, begin + steps, s.x, s.y, head, (idx - head * s.w) * ROWS};
+            s_out[0] = 0;
         }
     }
     __syncthreads();
     if (s_abort) return;
 
-    // ---- tiles that more than one warp holds a part of: all threads sum the parts of one, in warp order
-    for (int r = 0; r <= NW; ++r) {
-        const Shared sh = shared[r];
-        if (!sh.has) continue;
-        tile_q0 = sh.q0, tile_n = sh.n, tile_head = sh.head, tile_row = sh.row;
-        const bool whole = sh.begin >= 0 && sh.end <= mine;
-        const int rows = min(ROWS, sh.n * group - sh.row);
-        float *dst = p.parts + ((long long)blockIdx.x * 2 + (r > 0)) * L::kPart;
-        // parts: the first warp's (its last one when the tile begins there), then the first ones of the
-        // warps after it up to the tile's end
-        auto part_of = [&](int v) -> const float * {
-            const int v0 = (int)((long long)mine * v / NW), v1 = (int)((long long)mine * (v + 1) / NW);
-            if (v0 >= v1 || v0 >= sh.end) return nullptr;
-            return r > 0 && v == sh.first_warp ? reinterpret_cast<const float *>(smem + v * NS * L::kStage)
-                                               : reinterpret_cast<const float *>(smem + L::kPark) + v * L::kPart;
-        };
-        for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
-            const int row = i / (D / 4), d = i % (D / 4) * 4;
-            float m = kRefStart;
-            for (int v = sh.first_warp; v < NW; ++v) {
-                const float *part = part_of(v);
-                if (part) m = fmaxf(m, part[ROWS * D + 2 * row]);
-            }
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-            for (int v = sh.first_warp; v < NW; ++v) {
-                const float *part = part_of(v);
-                if (!part) continue;
-                const float f = ex2(part[ROWS * D + 2 * row] - m);
-                const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
-                l = fmaf(part[ROWS * D + 2 * row + 1], f, l);
-                acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-                acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
-            }
-            if (whole) {
-                long long at;
-                if (place(row, at)) store_row(at, d, acc, 4, l, m);
-            } else {
-                __stcg(reinterpret_cast<float4 *>(dst + row * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
-                if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + ROWS * D + 2 * row), make_float2(m, l));
-            }
+    // ---- tiles that more than one warp holds a part of, summed in warp order
+    // Parts of a shared tile: the first warp's (its last piece when the tile begins there), then the first
+    // pieces of the warps after it up to the tile's end.  Row `row`, dims d..d + 3.
+    auto sum_parts = [&](const Shared &sh, bool leads, int row, int d, float (&acc)[4], float &l, float &m) {
+        const float *part = leads ? reinterpret_cast<const float *>(smem + sh.first_warp * NS * L::kStage)
+                                  : reinterpret_cast<const float *>(smem + L::kPark) + sh.first_warp * L::kPart;
+        m = kRefStart, l = 0.0f;
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+        for (int v = sh.first_warp; v < NW; ++v) {
+            const int v0 = warp_start(v), v1 = warp_start(v + 1);
+            if (v0 >= sh.end) break;
+            if (v > sh.first_warp) part = reinterpret_cast<const float *>(smem + L::kPark) + v * L::kPart;
+            if (v0 >= v1) continue;
+            const float2 ml = *reinterpret_cast<const float2 *>(part + ROWS * D + 2 * row);
+            const float4 x = *reinterpret_cast<const float4 *>(part + row * D + d);
+            const float to = fmaxf(m, ml.x), f = ex2(m - to), w = ex2(ml.x - to);
+            m = to;
+            l = fmaf(ml.y, w, l * f);
+            acc[0] = fmaf(x.x, w, acc[0] * f), acc[1] = fmaf(x.y, w, acc[1] * f);
+            acc[2] = fmaf(x.z, w, acc[2] * f), acc[3] = fmaf(x.w, w, acc[3] * f);
         }
-        if (whole) continue;
-        // ---- a tile that CTAs from..to share: the last of them to come sums it
-        const long long begin = c0 + sh.begin, end = c0 + sh.end;
-        const int from = (int)(((begin + 1) * ctas + total - 1) / total - 1);
-        const int to = (int)((end * ctas + total - 1) / total - 1);
+    };
+    // Those that leave the CTA first: at its start and at its end, into slots 0 and 1 of the workspace, by all threads.
+    bool out[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        out[i] = s_out[i] >= 0;
+        if (!out[i]) continue;
+        const Shared sh = shared[s_out[i]];
+        const int rows = min(ROWS, sh.n * group - sh.row);
+        float *dst = p.parts + ((long long)blockIdx.x * 2 + i) * L::kPart;
+        for (int k = tid; k < rows * (D / 4); k += 32 * NW) {
+            const int row = k / (D / 4), d = k % (D / 4) * 4;
+            float acc[4], l, m;
+            sum_parts(sh, i == 1, row, d, acc, l, m);
+            __stcg(reinterpret_cast<float4 *>(dst + row * D + d), make_float4(acc[0], acc[1], acc[2], acc[3]));
+            if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + ROWS * D + 2 * row), make_float2(m, l));
+        }
+    }
+    if (out[0] || out[1]) {
         __threadfence();
         __syncthreads();
-        if (tid == 0) {
+        // tickets: which CTAs share the tile follows from where it begins and ends
+        if (tid < 2 && out[tid]) {
+            const Shared sh = shared[s_out[tid]];
+            // with the costs, the tile begins and ends at
+            const int b = find(c0 + sh.begin);
+            const int idx = line_div(c0 + sh.begin - pre[b], sh.end - sh.begin);
+            const long long begin = c0 + sh.begin + (long long)(tiles_before[b] + idx) * COST;
+            const long long end = begin + sh.end - sh.begin + COST;
+            // the last CTA whose share begins by the tile's first step, and by its last
+            const int from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
+            const int to = (int)((end * ctas + total - 1) / total - 1);
             unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
             do {
                 seen = old;
@@ -700,29 +753,67 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 old = atomicCAS(tk, seen, put);
             } while (old != seen);
             __threadfence();
-            s_last = put == 0;
+            s_from[tid] = put == 0 ? from : -1;
+            s_to[tid] = to;
         }
-        __syncthreads();
-        if (!s_last) continue;
+    }
+    // those within the CTA: each by the warp that holds the first part
+    {
+        const Shared sh = shared[1 + warp];
+        if (sh.has && sh.end <= mine) {
+            const int rows = min(ROWS, sh.n * group - sh.row);
+            for (int k = lane; k < rows * (D / 4); k += 32) {
+                const int row = k / (D / 4), d = k % (D / 4) * 4;
+                float acc[4], l, m;
+                sum_parts(sh, true, row, d, acc, l, m);
+                long long at;
+                if (place(tile, row, at)) store_row(at, d, acc, 4, l, m);
+            }
+        }
+    }
+    if (!out[0] && !out[1]) return;
+    __syncthreads();
+    // ---- a tile that CTAs from..to share: the last of them to come sums it
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (!out[i] || s_from[i] < 0) continue;
+        const int from = s_from[i], to = s_to[i];
+        const Shared sh = shared[s_out[i]];
+        const Tile tl = {sh.begin, sh.end, sh.q0, sh.n, sh.row, sh.head, 0};
+        const int rows = min(ROWS, sh.n * group - sh.row);
         // CTA `from` holds its part in slot 1, the others in slot 0
         auto slot = [&](int c) { return p.parts + ((long long)c * 2 + (c == from)) * L::kPart; };
-        for (int i = tid; i < rows * (D / 4); i += 32 * NW) {
-            const int row = i / (D / 4), d = i % (D / 4) * 4;
-            float m = kRefStart;
-#pragma unroll 8
-            for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(slot(c) + ROWS * D + 2 * row));
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-#pragma unroll 8
-            for (int c = from; c <= to; ++c) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot(c) + ROWS * D + 2 * row));
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(slot(c) + row * D + d));
-                const float f = ex2(ml.x - m);
-                l = fmaf(ml.y, f, l);
-                acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-                acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
+        for (int k = tid; k < rows * (D / 4); k += 32 * NW) {
+            const int row = k / (D / 4), d = k % (D / 4) * 4;
+            float m = kRefStart, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
+            // eight parts at a time: their loads are on their way together
+            for (int c = from; c <= to; c += 8) {
+                float2 ml[8];
+                float4 x[8];
+                float top = m;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float *part = slot(min(c + j, to));
+                    ml[j] = __ldcg(reinterpret_cast<const float2 *>(part + ROWS * D + 2 * row));
+                    x[j] = __ldcg(reinterpret_cast<const float4 *>(part + row * D + d));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, ml[j].x);
+                const float f = ex2(m - top);
+                m = top;
+                l *= f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] *= f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float w = c + j <= to ? ex2(ml[j].x - m) : 0.0f;
+                    l = fmaf(ml[j].y, w, l);
+                    acc[0] = fmaf(x[j].x, w, acc[0]), acc[1] = fmaf(x[j].y, w, acc[1]);
+                    acc[2] = fmaf(x[j].z, w, acc[2]), acc[3] = fmaf(x[j].w, w, acc[3]);
+                }
             }
             long long at;
-            if (place(row, at)) store_row(at, d, acc, 4, l, m);
+            if (place(tl, row, at)) store_row(at, d, acc, 4, l, m);
         }
     }
 }
