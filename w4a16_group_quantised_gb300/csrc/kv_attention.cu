@@ -13,14 +13,14 @@
 // Bound by the cache read: 256 B a key and kv head (head dim 128) against
 // rows * 512 multiply-adds.  So the design is about bytes in flight and even
 // shares, not about matrix instructions:
-//  * The work is a line of steps of one or two blocks of 16 keys: sequence by sequence, kv head by
+//  * The work is a line of steps of 32 keys or so: sequence by sequence, kv head by
 //    kv head, row tile by row tile, every step of the keys that the sequence's
 //    new tokens see.  Lengths are read here, so each CTA sums the line's
 //    length up itself, takes an equal piece of it, and its warps take equal
 //    pieces of that.  Ragged lengths, windows and few long sequences all
 //    spread over the whole GPU alike.
-//  * A warp is on its own: it owns a ring of stages, its first lane issues
-//    the two TMA boxes (16 keys of K, of V) of a step into it, all lanes
+//  * A warp is on its own: it owns a ring of stages, its first lane issues a
+//    TMA box (16 or 32 keys of K and of V, one page) into each, all lanes
 //    consume.  No barrier among warps until their pieces end.  Page ids and
 //    scales of 32 steps are looked up at once, one step a lane.
 //  * mma.sync m16n8k16 with the keys as A (16 keys x 16 dims) and the rows as
@@ -44,11 +44,10 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kBlock = 16;                // keys of a block: one TMA box of K, one of V, within one page
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kShort = 256 / kBlock;      // tiles of up to so many blocks stay in one CTA
+constexpr int kShort = 256;               // tiles of up to so many keys stay in one CTA
 constexpr int kLeast = 2;                 // fewest steps worth a CTA
-constexpr int kTileCost = 2;              // blocks that the start and end of a tile count for in the shares
+constexpr int kTileCost = 32;             // keys that the start and end of a tile count for in the shares
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
 constexpr float kHead = 14.0f;            // ... and a moved reference puts the largest at 2^kHead
@@ -58,26 +57,28 @@ struct FewParams {
     KvCache c;
     KvBatch b;
     int row_limit;                        // sequences with more rows a kv head than this are another kernel's (0: none)
-    int token_first;                      // tensor map dims are (dim, head, token, page), not (dim, token, head, page)
+    int token_first;                      // tensor map dims are (dim, head, token, page, K or V), not (dim, token, head, ...)
+    int merged;                           // one box brings K and V; else the second map brings V
+    int k_at, v_at;                       // where a stage holds K and V, in tiles
     float *parts;                         // [grid][2][ROWS][D + 2]
     unsigned long long *tickets;          // [grid]
     unsigned long long tag;
     int *status;
 };
 
-// Blocks of the keys that new tokens of a sequence see: [0, sink) and
-// [first, ...), `blocks` in all, one at least.
+// Blocks of KB keys that new tokens of a sequence see: [0, sink) and
+// [first, ...), `blocks` in all, one at least; BPS of them are a step.
 struct Span {
-    int blocks, sink, first;
-    template <int BPS>
-    __device__ __forceinline__ int steps() const { return (blocks + BPS - 1) / BPS; }
+    int blocks, sink, first, steps;
 };
+template <int KB, int BPS>
 __device__ __forceinline__ Span span_of(int n, int len, int window, int sinks) {
     Span s;
     const int lo = window > 0 ? max(0, len - n + 1 - window) : 0;
-    s.first = lo / kBlock;
-    s.sink = min((min(sinks, lo) + kBlock - 1) / kBlock, s.first);
-    s.blocks = max(s.sink + (len + kBlock - 1) / kBlock - s.first, 1);
+    s.first = lo / KB;
+    s.sink = min((min(sinks, lo) + KB - 1) / KB, s.first);
+    s.blocks = max(s.sink + (len + KB - 1) / KB - s.first, 1);
+    s.steps = (s.blocks + BPS - 1) / BPS;
     return s;
 }
 
@@ -91,10 +92,10 @@ struct Shared {
     int has, first_warp, begin, end, q0, n, head, row;
 };
 
-template <int D, int NR, int NW, int NS>
+template <int D, int NR, int KB, int NW, int NS>
 struct FewSmem {
     static constexpr int kRows = 8 * NR;
-    static constexpr int kStage = 2 * kBlock * D;                  // K then V
+    static constexpr int kStage = 2 * KB * D;                      // K and V of a block
     static constexpr int kPart = kRows * (D + 2);                  // floats: rows of out, then (M, l) of each row
     static constexpr int kPark = NW * NS * kStage;                 // a warp's first piece, if another began it
     static constexpr int kSeq = kPark + NW * kPart * 4;            // int4 {q0, n, len, row tiles}
@@ -153,11 +154,12 @@ struct Meta {
     float ks, vs;          // scales
 };
 
-template <int KT, int D, int NR, int BPS, int NW, int NS>
+template <int KT, int D, int NR, int KB, int BPS, int NW, int NS>
 __global__ void __launch_bounds__(32 * NW, 1)
     few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const FewParams p) {
-    using L = FewSmem<D, NR, NW, NS>;
+    using L = FewSmem<D, NR, KB, NW, NS>;
+    constexpr int SUB = KB / 16;                                   // 16-key tiles of a block
     constexpr int ROWS = L::kRows;
     constexpr int KS = D / 16;                                     // k-steps of S, and 16-dim tiles of out
     constexpr int LOOK = 32 / BPS;                                 // steps looked up at once, a block a lane
@@ -188,7 +190,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
     kv_begin();
 
     // ---- the line: each sequence's steps and tiles, summed up
-    constexpr int COST = (kTileCost + BPS - 1) / BPS;
+    constexpr int COST = (kTileCost + KB * BPS - 1) / (KB * BPS);
+    auto span = [&](int n, int len) { return span_of<KB, BPS>(n, len, p.a.window, p.a.sinks); };
     long long total = 0;                                           // steps, and COST a tile
     int tiles_all = 0;
     for (int base = 0; base < B; base += 32 * NW) {
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const int row_tiles = p.row_limit > 0 && rows > p.row_limit ? 0 : (rows + ROWS - 1) / ROWS;
             seqs[i] = make_int4(s.q0, s.n, s.len, row_tiles);
             tiles = row_tiles * Hk;
-            v = (long long)tiles * (span_of(s.n, s.len, p.a.window, p.a.sinks).template steps<BPS>() + COST);
+            v = (long long)tiles * (span(s.n, s.len).steps + COST);
         }
         long long inc = v;
         int inc_tiles = tiles;
@@ -251,12 +254,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
         moved = at;
         const int b = find(at, COST);
         const int4 s = seqs[b];
-        const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
-        const int steps = sp.template steps<BPS>();
+        const Span sp = span(s.y, s.z);
+        const int steps = sp.steps;
         const long long rem = at - pre[b] - (long long)tiles_before[b] * COST;
         const int idx = line_div(rem, steps + COST);
         int st = (int)(rem - (long long)idx * (steps + COST));
-        if (snap && sp.blocks <= kShort) {
+        if (snap && sp.blocks <= kShort / KB) {
             moved -= st;
             st = 0;
         }
@@ -289,16 +292,16 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const long long line = c0 + at;
             const int b = find(line);
             const int4 s = seqs[b];
-            const Span sp = span_of(s.y, s.z, p.a.window, p.a.sinks);
+            const Span sp = span(s.y, s.z);
             const long long rem = line - pre[b];
-            const int steps = sp.template steps<BPS>(), tile = line_div(rem, steps);
+            const int steps = sp.steps, tile = line_div(rem, steps);
             const int nth = (int)(rem - (long long)tile * steps) * BPS + lane % BPS;
             const int head = (int)((unsigned)tile / (unsigned)s.w);
             const int blk = nth < sp.sink ? nth : sp.first + nth - sp.sink;
-            m.where = (blk * kBlock & ((1 << p.c.page_shift) - 1)) | head << 8;
-            if (blk * kBlock < s.z) {
-                m.pos = blk * kBlock;
-                m.page = p.b.block_table[(long long)b * p.b.max_blocks + (blk * kBlock >> p.c.page_shift)];
+            m.where = (blk * KB & ((1 << p.c.page_shift) - 1)) | head << 8;
+            if (blk * KB < s.z) {
+                m.pos = blk * KB;
+                m.page = p.b.block_table[(long long)b * p.b.max_blocks + (blk * KB >> p.c.page_shift)];
             }
         }
         return m;
@@ -320,8 +323,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
             mbar_arrive_expect_tx(bar, L::kStage);
             const int tok = where & 255, head = where >> 8;
             const int x = p.token_first ? head : tok, y = p.token_first ? tok : head;
-            tma_load_4d(dst, &tm_k, bar, 0, x, y, page);
-            tma_load_4d(dst + kBlock * D, &tm_v, bar, 0, x, y, page);
+            tma_load_5d(dst, &tm_k, bar, 0, x, y, page, 0);
+            if (!p.merged) tma_load_5d(dst + KB * D, &tm_v, bar, 0, x, y, page, 0);
         }
     };
 
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         const long long line = c0 + at;
         const int b = find(line);
         const int4 s = seqs[b];
-        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).template steps<BPS>();
+        const int steps = span(s.y, s.z).steps;
         const long long rem = line - pre[b];
         const int idx = line_div(rem, steps);
         tl.begin = at - (int)(rem - (long long)idx * steps);
@@ -480,7 +483,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
     int fetched = min(NS, blocks);                                 // blocks issued so far
     for (int i = 0; i < fetched; ++i)
         issue(i, __shfl_sync(0xffffffffu, cur.page, i), __shfl_sync(0xffffffffu, cur.where, i));
-    if (w0 < w1) start_tile(next);
+    if (lane == 0 && w0 == 0 && w1 > 0 && next.begin < 0) {
+        // a tile that an earlier CTA began: this warp has its first part here
+        shared[0] = Shared{1, warp, next.begin, next.end, next.q0, next.n, next.head, next.row};
+        s_out[0] = 0;
+    }
+    tile.end = w0;
 
     // ---- steps
     // K rows as A: row g is key tau(g), row g + 8 key 8 + tau(g), an order in which eight lanes' 16-byte
@@ -493,19 +501,21 @@ __global__ void __launch_bounds__(32 * NW, 1)
     const uint32_t sel_lo = flip ? 0x1504 : 0x5140, sel_hi = flip ? 0x3726 : 0x7362;
     bool failed = false;
     int phase = 0, stage = 0;                                      // of the next block to consume
-    for (int at = w0; at < w1; ++at) {
+    const uint32_t k_row = ring + p.k_at * KB * D + tau * D, v_ring = ring + p.v_at * KB * D;
+    for (int at = w0;; ++at) {
         const int l = (at - w0) % LOOK;
         // the next blocks' page ids and scales, a few steps apart so that neither is waited for
         if (l == 0 && at != w0) cur = nxt;
         if (l == 1 && at - 1 + LOOK < w1) nxt = look_up(at - 1 + LOOK);
         if (l == LOOK / 4 && at - l + LOOK < w1) look_up_scales(nxt);
-        if (at == tile.end) {
-            finish_tile(tile.begin >= w0, first_part);
-            if (NR > 1) next = load_rows(at);
+        if (at == tile.end || at == w1) {
+            if (at > w0) finish_tile(tile.begin >= w0 && tile.end == at, tile.begin < w0 ? first_part : last_part);
+            if (at == w1) break;
+            if (NR > 1 && at > w0) next = load_rows(at);
             start_tile(next);
         }
         if (NR == 1 && at + 1 == tile.end && at + 1 < w1) next = load_rows(at + 1);
-        float s[BPS][NR][4], iv[BPS];
+        float s[BPS][SUB][NR][4], iv[BPS];
         int pos[BPS], st[BPS];
         bool edge[BPS];
 #pragma unroll
@@ -516,29 +526,31 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
         if (failed) break;
 #pragma unroll
-        for (int b = 0; b < BPS; ++b) {
+        for (int b = 0; b < BPS; ++b)
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+            for (int u = 0; u < SUB; ++u) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[b][nr][i] = 0.0f;
-            const uint32_t kb = ring + st[b] * L::kStage;
+                for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int j = 0; j < KS / 4; ++j) {
-                const int chunk = t + 4 * j;
-                const int sw = D == 128 ? chunk ^ (tau & 7) : chunk ^ ((tau >> 1) & 3);
-                const uint4 x = lds128(kb + tau * D + sw * 16), y = lds128(kb + (tau + 8) * D + sw * 16);
-                const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                    for (int i = 0; i < 4; ++i) s[b][u][nr][i] = 0.0f;
+                const uint32_t kb = k_row + st[b] * L::kStage + u * 16 * D;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t a0, a1, a2, a3;
-                    codes_to_half<KT>(xw[w], a0, a2);
-                    codes_to_half<KT>(yw[w], a1, a3);
+                for (int j = 0; j < KS / 4; ++j) {
+                    const int chunk = t + 4 * j;
+                    const int sw = D == 128 ? chunk ^ (tau & 7) : chunk ^ ((tau >> 1) & 3);
+                    const uint4 x = lds128(kb + sw * 16), y = lds128(kb + 8 * D + sw * 16);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
-                        mma16816<0>(s[b][nr], a0, a1, a2, a3, q[nr][4 * j + w][0], q[nr][4 * j + w][1]);
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t a0, a1, a2, a3;
+                        codes_to_half<KT>(xw[w], a0, a2);
+                        codes_to_half<KT>(yw[w], a1, a3);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+                            mma16816<0>(s[b][u][nr], a0, a1, a2, a3, q[nr][4 * j + w][0], q[nr][4 * j + w][1]);
+                    }
                 }
             }
-        }
         // x_j + log2(vs); keys a row does not see get -inf
         float top[NR][2];
 #pragma unroll
@@ -550,21 +562,28 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const float ks = __shfl_sync(0xffffffffu, cur.ks, from), vs = __shfl_sync(0xffffffffu, cur.vs, from);
             const float lv = __log2f(vs);
             iv[b] = __fdividef(1.0f, vs);
-            edge[b] = pos[b] + kBlock - 1 > min_pos ||
-                      (p.a.window > 0 && pos[b] <= max_pos - p.a.window && pos[b] + kBlock > p.a.sinks);
+            edge[b] = pos[b] + KB - 1 > min_pos ||
+                      (p.a.window > 0 && pos[b] <= max_pos - p.a.window && pos[b] + KB > p.a.sinks);
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
+                const float f0 = fac[nr][0] * ks, f1 = fac[nr][1] * ks;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[b][nr][i] = fmaf(s[b][nr][i], fac[nr][i & 1] * ks, lv);
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[b][u][nr][i] = fmaf(s[b][u][nr][i], i & 1 ? f1 : f0, lv);
                 if (edge[b])
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = pos[b] + tau + 8 * (i >> 1), r = row_pos[nr][i & 1];
-                        const bool see = j <= r && (p.a.window == 0 || r - j < p.a.window || j < p.a.sinks);
-                        if (!see) s[b][nr][i] = -INFINITY;
-                    }
+                    for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) top[nr][i & 1] = fmaxf(top[nr][i & 1], s[b][nr][i]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = pos[b] + u * 16 + tau + 8 * (i >> 1), r = row_pos[nr][i & 1];
+                            const bool see = j <= r && (p.a.window == 0 || r - j < p.a.window || j < p.a.sinks);
+                            if (!see) s[b][u][nr][i] = -INFINITY;
+                        }
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top[nr][i & 1] = fmaxf(top[nr][i & 1], s[b][u][nr][i]);
             }
         }
         bool over = false;
@@ -590,58 +609,60 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 }
         }
 #pragma unroll
-        for (int b = 0; b < BPS; ++b) {
-            uint32_t pt[NR][2];
+        for (int b = 0; b < BPS; ++b)
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = ex2(s[b][nr][i] - ref[nr][i & 1]);
-                sum[nr][0] = fmaf(w[0] + w[2], iv[b], sum[nr][0]);
-                sum[nr][1] = fmaf(w[1] + w[3], iv[b], sum[nr][1]);
-                pt[nr][0] = movmatrix(pack_half2(w[0], w[1]));
-                pt[nr][1] = movmatrix(pack_half2(w[2], w[3]));
-            }
-            // V^T as A: byte i of a lane's chunk g is dim g * D / 8 + i
-            const uint32_t vb = ring + st[b] * L::kStage + kBlock * D;
-            uint32_t vw[4][D / 32];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int key = ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
-                if (D == 128) {
-                    const uint4 v = lds128(vb + key * D + (g ^ (key & 7)) * 16);
-                    vw[r][0] = v.x, vw[r][1] = v.y, vw[r][D / 32 - 2] = v.z, vw[r][D / 32 - 1] = v.w;
-                } else {
-                    const uint2 v = lds64(vb + key * D + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
-                    vw[r][0] = v.x, vw[r][1] = v.y;
-                }
-            }
-            if (KT == kKvE4m3 && edge[b]) {
-                // bytes of keys no row sees may be NaN codes; their weight of 0 would not hide them
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = pos[b] + ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
-                    if (j > max_pos)
-#pragma unroll
-                        for (int w = 0; w < D / 32; ++w) vw[r][w] = 0;
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                uint32_t a[4][2];                                  // [dim of the word][keys 2t, 2t + 1 or those + 8]
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t x = vw[2 * h][w], y = vw[2 * h + 1][w];
-                    codes_to_half<KT>(__byte_perm(x, y, sel_lo), a[0][h], a[1][h]);
-                    codes_to_half<KT>(__byte_perm(x, y, sel_hi), a[2][h], a[3][h]);
-                }
+            for (int u = 0; u < SUB; ++u) {
+                uint32_t pt[NR][2];
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr) {
-                    mma16816<0>(o[nr][2 * w], a[0][0], a[1][0], a[0][1], a[1][1], pt[nr][0], pt[nr][1]);
-                    mma16816<0>(o[nr][2 * w + 1], a[2][0], a[3][0], a[2][1], a[3][1], pt[nr][0], pt[nr][1]);
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = ex2(s[b][u][nr][i] - ref[nr][i & 1]);
+                    sum[nr][0] = fmaf(w[0] + w[2], iv[b], sum[nr][0]);
+                    sum[nr][1] = fmaf(w[1] + w[3], iv[b], sum[nr][1]);
+                    pt[nr][0] = movmatrix(pack_half2(w[0], w[1]));
+                    pt[nr][1] = movmatrix(pack_half2(w[2], w[3]));
+                }
+                // V^T as A: byte i of a lane's chunk g is dim g * D / 8 + i
+                const uint32_t vb = v_ring + st[b] * L::kStage + u * 16 * D;
+                uint32_t vw[4][D / 32];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int key = ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
+                    if (D == 128) {
+                        const uint4 v = lds128(vb + key * D + (g ^ (key & 7)) * 16);
+                        vw[r][0] = v.x, vw[r][1] = v.y, vw[r][D / 32 - 2] = v.z, vw[r][D / 32 - 1] = v.w;
+                    } else {
+                        const uint2 v = lds64(vb + key * D + ((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
+                        vw[r][0] = v.x, vw[r][1] = v.y;
+                    }
+                }
+                if (KT == kKvE4m3 && edge[b]) {
+                    // bytes of keys no row sees may be NaN codes; their weight of 0 would not hide them
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = pos[b] + u * 16 + ((r & 1) != flip ? v_key1 : v_key0) + 8 * (r >> 1);
+                        if (j > max_pos)
+#pragma unroll
+                            for (int w = 0; w < D / 32; ++w) vw[r][w] = 0;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < D / 32; ++w) {
+                    uint32_t a[4][2];                              // [dim of the word][keys 2t, 2t + 1 or those + 8]
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = vw[2 * h][w], y = vw[2 * h + 1][w];
+                        codes_to_half<KT>(__byte_perm(x, y, sel_lo), a[0][h], a[1][h]);
+                        codes_to_half<KT>(__byte_perm(x, y, sel_hi), a[2][h], a[3][h]);
+                    }
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        mma16816<0>(o[nr][2 * w], a[0][0], a[1][0], a[0][1], a[1][1], pt[nr][0], pt[nr][1]);
+                        mma16816<0>(o[nr][2 * w + 1], a[2][0], a[3][0], a[2][1], a[3][1], pt[nr][0], pt[nr][1]);
+                    }
                 }
             }
-        }
         __syncwarp();
         if (fetched < blocks) {
             if (lane == 0) fence_proxy_async_smem();
@@ -663,31 +684,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
         // leave with no copy in flight
         for (int i = max(0, min(fetched, blocks) - NS); i < min(fetched, blocks); ++i)
             mbar_wait_bounded(bars + i % NS * 8, (i / NS) & 1, p.status, &s_abort);
-    } else if (w0 < w1) {
-        // the piece still held: whole when its tile begins here and ends here
-        if (tile.begin >= w0 && tile.end <= w1) {
-            finish_tile(true, nullptr);
-        } else {
-            __syncwarp();
-            finish_tile(false, tile.begin < w0 ? first_part : last_part);
-        }
+    } else if (lane == 0 && w0 < w1 && tile.begin >= w0 && tile.end > w1) {
         // the warp that holds a tile's first part in this CTA says so
-        const bool leads = tile.begin >= w0 && tile.end > w1;
-        if (lane == 0 && leads) shared[1 + warp] = Shared{1, warp, tile.begin, tile.end, tile.q0, tile.n, tile.head, tile.row};
-        if (lane == 0 && leads && tile.end > mine) s_out[1] = 1 + warp;
-    }
-    // a tile that an earlier CTA began: the CTA's first step is in it
-    if (tid == 0) {
-        const int b = find(c0);
-        const int4 s = seqs[b];
-        const int steps = span_of(s.y, s.z, p.a.window, p.a.sinks).template steps<BPS>();
-        const long long rem = c0 - pre[b];
-        const int idx = line_div(rem, steps), begin = (int)((long long)idx * steps - rem);
-        if (begin < 0) {
-            const int head = divide(idx, s.w);
-            shared[0] = Shared{1, 0, begin, begin + steps, s.x, s.y, head, (idx - head * s.w) * ROWS};
-            s_out[0] = 0;
-        }
+        shared[1 + warp] = Shared{1, warp, tile.begin, tile.end, tile.q0, tile.n, tile.head, tile.row};
+        if (tile.end > mine) s_out[1] = 1 + warp;
     }
     __syncthreads();
     if (s_abort) return;
@@ -732,7 +732,6 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
     }
     if (out[0] || out[1]) {
-        __threadfence();
         __syncthreads();
         // tickets: which CTAs share the tile follows from where it begins and ends
         if (tid < 2 && out[tid]) {
@@ -745,6 +744,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             // the last CTA whose share begins by the tile's first step, and by its last
             const int from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
             const int to = (int)((end * ctas + total - 1) / total - 1);
+            __threadfence();                                       // after the barrier: for the whole CTA's parts
             unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
             do {
                 seen = old;
@@ -822,36 +822,38 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// A map of codes whose boxes are `keys` tokens of one head of one page.  The
-// middle dimensions go by rising stride.
-cudaError_t encode_codes(const DeviceInfo &dev, const KvCache &c, void *base, int keys, bool token_first,
-                         CUtensorMap *out) {
+// A map of codes whose boxes are `keys` tokens of one head of one page, of one
+// tensor or (apart > 0: the bytes from it to the other) of K and V.  The
+// dimensions after the first go by rising stride.
+cudaError_t encode_codes(const DeviceInfo &dev, const KvCache &c, void *base, long long apart, int keys,
+                         bool token_first, CUtensorMap *out) {
     if (dev.encode_tiled == nullptr) return cudaErrorNotSupported;
     const cuuint64_t tokens = (cuuint64_t)1 << c.page_shift, heads = (cuuint64_t)c.n_kv_heads;
     // a dimension of one element has no stride of its own
     const cuuint64_t sh = c.n_kv_heads > 1 ? (cuuint64_t)c.head_stride : (cuuint64_t)c.token_stride << c.page_shift;
     const cuuint64_t sp = c.n_pages > 1 ? (cuuint64_t)c.page_stride : (cuuint64_t)c.token_stride << c.page_shift;
-    cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, tokens, heads, (cuuint64_t)c.n_pages};
-    cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, sh, sp};
-    cuuint32_t box[4] = {(cuuint32_t)c.head_dim, (cuuint32_t)keys, 1, 1};
-    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const cuuint32_t both = apart > 0 ? 2 : 1;
+    cuuint64_t dims[5] = {(cuuint64_t)c.head_dim, tokens, heads, (cuuint64_t)c.n_pages, both};
+    cuuint64_t strides[4] = {(cuuint64_t)c.token_stride, sh, sp, apart > 0 ? (cuuint64_t)apart : sp};
+    cuuint32_t box[5] = {(cuuint32_t)c.head_dim, (cuuint32_t)keys, 1, 1, both};
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
     if (token_first) {
         std::swap(dims[1], dims[2]);
         std::swap(strides[0], strides[1]);
         std::swap(box[1], box[2]);
     }
     const CUresult r = reinterpret_cast<EncodeTiledFn>(dev.encode_tiled)(
-        out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
         c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int KT, int D, int NR, int BPS, int NW, int NS>
+template <int KT, int D, int NR, int KB, int BPS, int NW, int NS>
 cudaError_t launch_few(const FewParams &p, const CUtensorMap &k, const CUtensorMap &v, int grid, cudaStream_t s,
                        bool pdl) {
-    using L = FewSmem<D, NR, NW, NS>;
-    auto kern = few_rows_kernel<KT, D, NR, BPS, NW, NS>;
+    using L = FewSmem<D, NR, KB, NW, NS>;
+    auto kern = few_rows_kernel<KT, D, NR, KB, BPS, NW, NS>;
     const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(kern), L::kEnd);
     if (e != cudaSuccess) return e;
     return kv_launch(kern, dim3(grid), dim3(32 * NW), L::kEnd, s, pdl, k, v, p);
@@ -865,10 +867,16 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
                                 cudaStream_t s, bool pdl) {
     const int group = a.n_heads / c.n_kv_heads;
     const bool token_first = c.n_kv_heads > 1 && c.head_stride < c.token_stride;
+    // blocks of 32 keys where a page holds them: half the boxes and look-ups
+    const int keys = c.page_shift >= 5 ? 32 : 16;
+    // one map over both tensors, from the lower one up, where their distance fits a stride
+    const long long apart = c.v - c.k, distance = apart < 0 ? -apart : apart;
+    const bool merged = distance < 1LL << 40;
     CUtensorMap k, v;
-    cudaError_t e = encode_codes(dev, c, c.k, kBlock, token_first, &k);
-    if (e == cudaSuccess) e = encode_codes(dev, c, c.v, kBlock, token_first, &v);
+    cudaError_t e = encode_codes(dev, c, merged && apart < 0 ? c.v : c.k, merged ? distance : 0, keys, token_first, &k);
+    if (e == cudaSuccess && !merged) e = encode_codes(dev, c, c.v, 0, keys, token_first, &v);
     if (e != cudaSuccess) return e;
+    if (merged) v = k;
     static std::atomic<unsigned long long> launches{0x5ca1ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;
@@ -876,20 +884,31 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         b.kv_lens += b0;
         b.q_starts += b0;
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
-        FewParams p{a, c, b, 0, token_first ? 1 : 0, nullptr, nullptr, 0, dev.status};
+        FewParams p{a, c, b, 0, token_first ? 1 : 0, merged ? 1 : 0, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,
+                    nullptr, nullptr, 0, dev.status};
         p.tickets = static_cast<unsigned long long *>(a.workspace);
         p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
         p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
         if (p.tag == 0) p.tag = 1;
         const int grid = dev.sm_count;
         const bool few = (long long)a.max_q_len * group <= 8;
-#define W4A16_FEW(KT)                                                                          \
-    e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 2, 8, 5>(p, k, v, grid, s, pdl)         \
-                                 : launch_few<KT, 128, 2, 1, 8, 4>(p, k, v, grid, s, pdl))        \
-                          : (few ? launch_few<KT, 64, 1, 2, 8, 10>(p, k, v, grid, s, pdl)         \
-                                 : launch_few<KT, 64, 2, 1, 8, 8>(p, k, v, grid, s, pdl))
-        if (c.kv_dtype == kKvInt8) W4A16_FEW(kKvInt8);
-        else W4A16_FEW(kKvE4m3);
+        // <codes, dims, 8-row tiles, keys a block, blocks a step, warps, ring stages>
+#define W4A16_FEW(KT)                                                                                              \
+    if (keys == 32)                                                                                                \
+        e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 32, 1, 8, 2>(p, k, v, grid, s, pdl)                  \
+                                     : launch_few<KT, 128, 2, 32, 1, 8, 2>(p, k, v, grid, s, pdl))                 \
+                              : (few ? launch_few<KT, 64, 1, 32, 2, 8, 5>(p, k, v, grid, s, pdl)                   \
+                                     : launch_few<KT, 64, 2, 32, 1, 8, 4>(p, k, v, grid, s, pdl));                 \
+    else                                                                                                           \
+        e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 16, 2, 8, 5>(p, k, v, grid, s, pdl)                  \
+                                     : launch_few<KT, 128, 2, 16, 1, 8, 4>(p, k, v, grid, s, pdl))                 \
+                              : (few ? launch_few<KT, 64, 1, 16, 2, 8, 10>(p, k, v, grid, s, pdl)                  \
+                                     : launch_few<KT, 64, 2, 16, 2, 8, 8>(p, k, v, grid, s, pdl))
+        if (c.kv_dtype == kKvInt8) {
+            W4A16_FEW(kKvInt8);
+        } else {
+            W4A16_FEW(kKvE4m3);
+        }
 #undef W4A16_FEW
         if (e != cudaSuccess) return e;
     }
