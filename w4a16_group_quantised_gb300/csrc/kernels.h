@@ -115,6 +115,10 @@ cudaError_t launch_kv_read(const KvCache &c, const KvBatch &b, void *k_out, void
                            const DeviceInfo &dev, cudaStream_t s, bool pdl);
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, const DeviceInfo &dev,
                                 cudaStream_t s, bool pdl);
+// sequences with more than row_limit rows (tokens * query heads of a kv head), in kv_attention_tc.cu
+cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, int row_limit,
+                                     const DeviceInfo &dev, cudaStream_t s, bool pdl);
+long long kv_attention_many_workspace(int head_dim, const DeviceInfo &dev);
 long long kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
                                  const DeviceInfo &dev);
 cudaError_t launch_kv_copy_pages(const KvCache &c, const int *src, const int *dst, int n, const DeviceInfo &dev,

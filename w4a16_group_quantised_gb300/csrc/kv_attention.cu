@@ -618,8 +618,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
                     float w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = ex2(s[b][u][nr][i] - ref[nr][i & 1]);
-                    sum[nr][0] = fmaf(w[0] + w[2], iv[b], sum[nr][0]);
-                    sum[nr][1] = fmaf(w[1] + w[3], iv[b], sum[nr][1]);
+                    // a block that the row does not see adds nothing, whatever its scale
+                    if (w[0] + w[2] != 0.0f) sum[nr][0] = fmaf(w[0] + w[2], iv[b], sum[nr][0]);
+                    if (w[1] + w[3] != 0.0f) sum[nr][1] = fmaf(w[1] + w[3], iv[b], sum[nr][1]);
                     pt[nr][0] = movmatrix(pack_half2(w[0], w[1]));
                     pt[nr][1] = movmatrix(pack_half2(w[2], w[3]));
                 }
@@ -877,6 +878,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     if (e == cudaSuccess && !merged) e = encode_codes(dev, c, c.v, 0, keys, token_first, &v);
     if (e != cudaSuccess) return e;
     if (merged) v = k;
+    // sequences with more rows than a tile of this kernel holds go to the tensor-core kernel
+    const bool many = (long long)a.max_q_len * group > kMostRows;
     static std::atomic<unsigned long long> launches{0x5ca1ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;
@@ -892,6 +895,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         if (p.tag == 0) p.tag = 1;
         const int grid = dev.sm_count;
         const bool few = (long long)a.max_q_len * group <= 8;
+        if (many) p.row_limit = kMostRows;
         // <codes, dims, 8-row tiles, keys a block, blocks a step, warps, ring stages>
 #define W4A16_FEW(KT)                                                                                              \
     if (keys == 32)                                                                                                \
@@ -912,10 +916,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
 #undef W4A16_FEW
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
+    return many ? launch_kv_attention_many(a, c, batch, kMostRows, dev, s, pdl) : cudaSuccess;
 }
 
-long long kv_attention_workspace(int, int, int head_dim, int, int, const DeviceInfo &dev) {
+long long kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int, int n_tokens, const DeviceInfo &dev) {
+    if ((long long)n_tokens * (n_heads / n_kv_heads) > kMostRows) return kv_attention_many_workspace(head_dim, dev);
     return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * kMostRows * (head_dim + 2) * 4;
 }
 

@@ -1,0 +1,842 @@
+// kv_attention_tc.cu -- attention of many query rows over the paged 8-bit
+// cache, on the 5th-generation tensor cores (tcgen05 + TMEM).
+//
+// The mathematics of kv_attention.cu: weights 2^e_j with e_j = x_j +
+// log2(vs_j) - M, M a reference of each row that moves only when some e_j
+// passes 15.9, so that the value scales stay out of the products and the
+// weights fit fp16.  The rows of a tile are the tokens of one sequence times
+// the query heads of one kv head, tokens outermost.
+//
+// A CTA works on tiles of 256 rows as two halves of 128, over 128 keys a
+// step.  Per step and half, S = Q K^T (128 x 128 x D) and out += P V (128 x D
+// x 128); TMEM holds S and out of both halves, and P as fp16 over the S it
+// came from, the A operand of the second product.
+//  * Warps 0-3 and 4-7: softmax of a half, a row a thread: no exchange among
+//    threads, out is rescaled in TMEM by the same thread in the rare step that
+//    moves M.  They also load the half's Q (scaled to fp16 by a power of two a
+//    row) and write its output.
+//  * Warps 8-11: codes to fp16 operands.  Global loads into registers a step
+//    ahead, exact conversion, 128-byte-swizzled stores: K is the K-major B
+//    operand of S, V the MN-major B operand of out, the same bytes row by row.
+//    The conversion is paid once for 256 rows.
+//  * Warp 12: one thread issues the MMAs.  While one half's softmax runs the
+//    tensor cores work on the other half's out += P V and next S.
+// Bound by the tensor cores (4 * 128 * 128 * D flops a step and half) with the
+// exponentials (128 * 128 a step and half) close behind.
+//
+// The work is cut as in kv_attention.cu: a line of all tiles' steps, each
+// causal tile with just the steps that its rows see, in equal shares; CTAs
+// that share a tile add their parts up through the workspace, in order.
+#include <algorithm>
+#include <atomic>
+
+#include "kv.cuh"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
+constexpr int kMaxSeqs = 512;             // sequences of a launch
+constexpr int kMaxPairs = 2048;           // (sequence, row tile) pairs of a launch
+constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
+constexpr int kCost = 1;                  // steps that a tile's start and end count for in the shares
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);   // whole warpgroups: the register split goes by them
+constexpr int kRegsSoft = 168, kRegsConv = 104, kRegsMma = 72; // 256, 128 and 128 threads: 65536 in all, the launch's 512 * 128
+constexpr float kRefStart = -3.402823466e38f, kTop = 15.9f, kHead = 14.0f;
+
+struct ManyParams {
+    KvAttentionArgs a;
+    KvCache c;
+    KvBatch b;
+    int row_limit;                        // sequences with up to so many rows a kv head are another kernel's
+    int pair_first;                       // this launch's pairs: [pair_first, pair_first + kMaxPairs)
+    float *parts;                         // [grid][2][D / 4 + 1][256] float4: out by dims, then (M, l)
+    unsigned long long *tickets;          // [grid]
+    unsigned long long tag;
+    int *status;
+};
+
+struct ManyTile {
+    int q0, n, first;                     // the sequence's rows, new tokens, position of the first
+    int pair, seq, len, head, row0, rows;
+    int steps, sink, block0;              // key blocks [0, sink) and from block0 on
+    int lo, hi;                           // its rows see positions below `sinks` and lo..hi
+    long long begin;                      // on the line
+};
+
+template <int D>
+struct ManySmem {
+    static constexpr int kBlockBytes = kKeys * 128;               // 128 rows of 64 fp16
+    static constexpr int kBlocks = D / 64;
+    static constexpr int kOperand = kBlocks * kBlockBytes;
+    static constexpr int kQ = 0;                                  // two halves
+    static constexpr int kK = kQ + 2 * kOperand;                  // two stages
+    static constexpr int kV = kK + 2 * kOperand;
+    static constexpr int kPre = kV + 2 * kOperand;                // line position of each pair, of one kv head
+    static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
+    static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
+    static constexpr int kScale = kPairSeq + kMaxPairs * 2;       // [4][8] float4 {ks, log2 vs, 1 / vs, -}
+    static constexpr int kBars = kScale + 4 * 8 * 16;
+    static constexpr int kMisc = kBars + 18 * 8;
+    static constexpr int kEnd = kMisc + 256 + 1024;               // 1024: slack to align the base
+};
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// two fp32 multiply-adds in one instruction
+__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 p, q, r, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+        "fma.rn.f32x2 s, p, q, r;\n\tmov.b64 {%0, %1}, s;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] . B[smem], kind::f16.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// A V tile as B: rows are keys (the contraction), 64 dims a 128-byte row,
+// 128-byte swizzle, the next 64 dims a block further.  MN-major: the leading
+// offset goes from 64 dims to the next, the stride offset from 8 keys to the
+// next.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block_bytes) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(block_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// Codes of a word as fp16 pairs (0, 1) and (2, 3), exactly (see kv_attention.cu).
+template <int KT>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if (KT == kKvInt8) {
+        w ^= 0x80808080u;
+        const uint32_t bias = 0x64806480u;
+        const uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 b = *reinterpret_cast<const __half2 *>(&bias);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&x), b);
+        const __half2 s = __hsub2(*reinterpret_cast<const __half2 *>(&y), b);
+        lo = *reinterpret_cast<const uint32_t *>(&r), hi = *reinterpret_cast<const uint32_t *>(&s);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    }
+}
+
+template <int KT, int D>
+__global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams p) {
+    using L = ManySmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int Hk = p.c.n_kv_heads, group = p.a.n_heads / Hk, B = p.b.n_seqs;
+    long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
+    int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
+    uint16_t *pair_seq = reinterpret_cast<uint16_t *>(smem + L::kPairSeq);
+    float4 *scales = reinterpret_cast<float4 *>(smem + L::kScale);
+    const uint32_t bars = smem_u32(smem + L::kBars);
+    int *misc = reinterpret_cast<int *>(smem + L::kMisc);
+    long long *s_cut = reinterpret_cast<long long *>(misc + 8);    // [2]
+    long long *s_scan = s_cut + 2;                                 // [kThreads / 32]
+    volatile int *abort_flag = misc;
+    // barriers: halves' S ready, P ready, out ready, Q ready; stages of K and V full and empty
+    auto s_full = [&](int i) { return bars + 8u * i; };
+    auto p_ready = [&](int i) { return bars + 8u * (2 + i); };
+    auto o_full = [&](int i) { return bars + 8u * (4 + i); };
+    auto q_full = [&](int i) { return bars + 8u * (6 + i); };
+    auto k_full = [&](int i) { return bars + 8u * (8 + i); };
+    auto k_empty = [&](int i) { return bars + 8u * (10 + i); };
+    auto v_full = [&](int i) { return bars + 8u * (12 + i); };
+    auto v_empty = [&](int i) { return bars + 8u * (14 + i); };
+    const uint32_t drain = bars + 8u * 16;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_ready(i), kHalfRows);
+            mbar_init(o_full(i), 1);
+            mbar_init(q_full(i), kHalfRows);
+            mbar_init(k_full(i), kConvWarps);
+            mbar_init(k_empty(i), 1);
+            mbar_init(v_full(i), kConvWarps);
+            mbar_init(v_empty(i), 1);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        misc[0] = 0;
+    }
+    kv_begin();
+
+    auto tile_of = [&](const int4 s, int b, int r) {
+        ManyTile t;
+        t.seq = b;
+        t.q0 = s.x, t.n = s.y, t.len = s.z, t.first = s.z - s.y;
+        t.row0 = r * kTileRows;
+        t.rows = min(kTileRows, s.y * group - t.row0);
+        const int lo_pos = t.first + t.row0 / group, hi_pos = t.first + (t.row0 + t.rows - 1) / group;
+        const int lo = p.a.window > 0 ? max(0, lo_pos + 1 - p.a.window) : 0;
+        t.lo = lo, t.hi = hi_pos;
+        t.block0 = lo / kKeys;
+        t.sink = min((min(p.a.sinks, lo) + kKeys - 1) / kKeys, t.block0);
+        t.steps = max(t.sink + (max(hi_pos + 1, 0) + kKeys - 1) / kKeys - t.block0, 1);
+        t.pair = t.head = 0;
+        t.begin = 0;
+        return t;
+    };
+    // Sum over the threads before this one, and of all; every thread calls.
+    auto scan = [&](long long v, long long &all) {
+        long long inc = v;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const long long x = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += x;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        long long ahead = 0;
+        all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const long long x = s_scan[w];
+            ahead += w < warp ? x : 0;
+            all += x;
+        }
+        return ahead + inc - v;
+    };
+
+    // ---- the line: pairs (sequence, row tile), then the steps of each, for one kv head
+    int pairs = 0;
+    for (int base = 0; base < B; base += kThreads) {
+        const int i = base + tid;
+        int4 s = make_int4(0, 0, 0, 0);
+        int mine = 0;
+        if (i < B) {
+            const KvSeq q = kv_sequence(p.b, p.c.page_shift, i, p.status);
+            const int rows = q.n * group;
+            mine = rows <= p.row_limit ? 0 : (rows + kTileRows - 1) / kTileRows;
+            s = make_int4(q.q0, q.n, q.len, 0);
+        }
+        long long all;
+        s.w = (int)scan(mine, all) + pairs - p.pair_first;         // within this launch's range
+        if (i < B) seqs[i] = s;
+        pairs += (int)all;
+    }
+    pairs = min(pairs - p.pair_first, kMaxPairs);
+    if (pairs <= 0) return;
+    __syncthreads();
+    long long total = 0;
+    for (int base = 0; base < pairs; base += kThreads) {
+        const int i = base + tid;
+        long long v = 0;
+        if (i < pairs) {
+            int lo = 0, hi = B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (seqs[mid].w <= i) lo = mid;
+                else hi = mid - 1;
+            }
+            pair_seq[i] = (uint16_t)lo;
+            v = tile_of(seqs[lo], lo, i - seqs[lo].w).steps + kCost;
+        }
+        long long all;
+        const long long at = scan(v, all) + total;
+        if (i < pairs) pre[i] = at;
+        total += all;
+    }
+    if (tid == 0) pre[pairs] = total;
+    total *= Hk;
+    __syncthreads();
+
+    auto tile_at = [&](int pair, int head) {
+        const int b = pair_seq[pair];
+        const int4 s = seqs[b];
+        ManyTile t = tile_of(s, b, pair - s.w);
+        t.pair = pair, t.head = head;
+        t.begin = pre[pair] * Hk + (long long)head * (t.steps + kCost);
+        return t;
+    };
+    auto pair_of = [&](long long at) {                             // the pair of a position of the line
+        int lo = 0, hi = pairs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pre[mid] * Hk <= at) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+    const long long ctas = min((long long)gridDim.x, (total + kCost) / (1 + kCost));
+    if (blockIdx.x >= ctas) return;
+    if (tid < 2) {
+        long long at = ((long long)blockIdx.x + tid) * total / ctas;
+        if (at > 0 && at < total) {
+            const int pair = pair_of(at);
+            const long long each = pre[pair + 1] - pre[pair], rem = at - pre[pair] * Hk;
+            if (each <= kShortSteps + kCost) at -= rem % each;
+        }
+        s_cut[tid] = at;
+    }
+    if (warp == kSoftWarps + kConvWarps) {
+        tmem_alloc(smem_u32(misc + 1), 512u);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const long long c0 = s_cut[0], c1 = s_cut[1];
+    const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+    // the tile at c0, and the walk from there
+    int pair = 0, head = 0;
+    if (c0 < c1) {
+        pair = pair_of(c0);
+        head = (int)((c0 - pre[pair] * Hk) / (pre[pair + 1] - pre[pair]));
+    }
+    // this CTA's steps of a tile
+    auto from_step = [&](const ManyTile &t) { return (int)min(max(c0 - t.begin - kCost, 0LL), (long long)t.steps); };
+    auto to_step = [&](const ManyTile &t) { return (int)min(max(c1 - t.begin - kCost, 0LL), (long long)t.steps); };
+    // The walk over this CTA's tiles, the same in every role.
+    struct Walk {
+        int pair, head;
+    };
+    auto next_tile = [&](Walk &w, ManyTile &t, int &s0, int &s1) {
+        while (w.pair < pairs) {
+            t = tile_at(w.pair, w.head);
+            if (t.begin >= c1) return false;
+            if (++w.head == Hk) w.head = 0, ++w.pair;
+            s0 = from_step(t), s1 = to_step(t);
+            if (s0 < s1) return true;
+        }
+        return false;
+    };
+    Walk walk = {pair, head};
+    auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
+
+    if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // ------------------------------------------------------------ softmax, Q, output
+        const int half = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
+        int s_phase = 0, o_phase = 0;
+        auto place = [&](const ManyTile &t, long long &at) {
+            const int row = half * kHalfRows + r;
+            if (row >= t.rows) return false;
+            const int x = t.row0 + row, tok = x / group;
+            at = (long long)(t.q0 + tok) * p.a.n_heads + t.head * group + x - tok * group;
+            return true;
+        };
+        float fac = 0.0f;
+        auto load_q = [&](const ManyTile &t) {
+            const int x = t.row0 + half * kHalfRows + r, tok = x / group;
+            const bool has = half * kHalfRows + r < t.rows;
+            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(t.q0 + tok) * p.a.q_stride +
+                                  (t.head * group + x - tok * group) * D;
+            uint4 v[D / 8];
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) v[i] = has ? ldg_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+            auto value = [&](uint32_t w, int e) {
+                const uint16_t h = (uint16_t)(w >> (16 * e));
+                return p.a.dtype == 0 ? kv_act<0>(h) : kv_act<1>(h);
+            };
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(value(w[j], 0)), fabsf(value(w[j], 1))));
+            }
+            // a power of two puts the row's largest value in [2^14, 2^15); a negative scale's sign goes along
+            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+            float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+            fac = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(p.a.scale) * 1.4426950408889634f;
+            if (p.a.scale < 0.0f) up = -up;
+            uint8_t *dst = smem + L::kQ + half * L::kOperand + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[j] = pack_half2(value(w[j], 0) * up, value(w[j], 1) * up);
+                *reinterpret_cast<uint4 *>(dst + (i >> 3) * L::kBlockBytes + (((i & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full(half));
+        };
+        auto store = [&](long long at, int d0, const float *v, int count, float inv) {
+            uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
+#pragma unroll
+            for (int i = 0; i < count; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = p.a.dtype == 0 ? pack_half2(v[i + 2 * j] * inv, v[i + 2 * j + 1] * inv)
+                                          : pack_bf162(v[i + 2 * j] * inv, v[i + 2 * j + 1] * inv);
+                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        };
+        int counter = 0;                                           // steps so far: the scales' ring position
+        bool ok = true;
+        auto load_next_q = [&]() {                                 // of the tile that comes next
+            Walk ahead = walk;
+            ManyTile t;
+            int s0, s1;
+            if (next_tile(ahead, t, s0, s1) && half * kHalfRows < t.rows) load_q(t);
+        };
+        load_next_q();
+        for (;;) {
+            ManyTile t;
+            int s0, s1;
+            if (!next_tile(walk, t, s0, s1)) break;
+            const bool runs = half * kHalfRows < t.rows;           // a tile of up to 128 rows is the first half's alone
+            const float my_fac = fac;
+            const Walk here = {t.pair, t.head};
+            const int sink_blocks = t.sink, block0 = t.block0 - t.sink;
+            const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
+            const int x = t.row0 + half * kHalfRows + r;
+            const bool exists = half * kHalfRows + r < t.rows;
+            const int pos = exists ? t.first + x / group : -1;
+            const int min_pos = t.first + (t.row0 + half * kHalfRows) / group;
+            const int max_pos = t.first + (min(t.row0 + half * kHalfRows + kHalfRows, t.row0 + t.rows) - 1) / group;
+            float ref = kRefStart, sum = 0.0f;
+            for (int st = s0; st < s1 && ok; ++st, ++counter) {
+                if (!runs) continue;
+                const int pos0 = (st < sink_blocks ? st : block0 + st) * kKeys;
+                const float4 *sc = scales + (counter & 3) * 8;
+                if (!mbar_wait_bounded(s_full(half), s_phase, p.status, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                s_phase ^= 1;
+                tc_fence_after();
+                const bool edge = pos0 + kKeys - 1 > min_pos ||
+                                  (p.a.window > 0 && pos0 <= max_pos - p.a.window && pos0 + kKeys > p.a.sinks);
+                const int hi = pos - pos0;                         // columns up to hi, and past lo or below sink
+                const int lo = p.a.window > 0 ? hi - p.a.window : -1, sink = p.a.sinks - pos0;
+                auto sees = [&](int c) { return c <= hi && (c > lo || c < sink); };
+                uint32_t pk[kKeys / 2];
+                float part;
+                for (;;) {
+                    float top = -INFINITY;
+                    part = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + c, v);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const float4 z = sc[c / 16 + g];
+                            const float f = my_fac * z.x, add = z.y - ref;
+                            float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const int k = g * 16 + i;
+                                float a, b;
+                                fma2(a, b, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, add);
+                                if (edge) {
+                                    if (!sees(c + k)) a = -INFINITY;
+                                    if (!sees(c + k + 1)) b = -INFINITY;
+                                }
+                                top = fmaxf(top, fmaxf(a, b));
+                                a = ex2(a), b = ex2(b);
+                                w0 += a, w1 += b;
+                                pk[(c + k) / 2] = pack_half2(a, b);
+                            }
+                            // a block that the row does not see adds nothing, whatever its scale
+                            if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, z.z, part);
+                        }
+                    }
+                    if (!__any_sync(0xffffffffu, top > kTop)) break;
+                    // the reference moves: the largest exponent afresh (from the start value it is not exact)
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(t_s + c, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float4 z = sc[c / 16 + k / 16];
+                            const float e = fmaf(__uint_as_float(v[k]), my_fac * z.x, z.y);
+                            if (!edge || sees(c + k)) m = fmaxf(m, e);
+                        }
+                    }
+                    const float to = m - ref > kHead ? m - kHead : ref;
+                    const float f = ex2(ref - to);
+                    ref = to;
+                    sum *= f;
+                    if (st > s0) {
+                        // out of the steps before is complete: this step's S was issued after it
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t v[32];
+                            tmem_ld32(t_o + c, v);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                            tmem_st32(t_o + c, v);
+                        }
+                    }
+                }
+                sum += part;
+                tmem_st32(t_s, pk);
+                tmem_st32(t_s + 32, pk + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(p_ready(half));
+            }
+            if (!ok) break;
+            // the next tile's rows while the last product runs
+            load_next_q();
+            if (!runs) continue;
+            if (!mbar_wait_bounded(o_full(half), o_phase, p.status, abort_flag)) break;
+            o_phase ^= 1;
+            tc_fence_after();
+            t = tile_at(here.pair, here.head);                     // afresh: kept out of the steps' registers
+            long long at = 0;
+            const bool has = place(t, at);
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(t_o + c, v);
+                    float f[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(v[k]);
+                    if (has) store(at, c, f, 32, inv);
+                }
+                if (has && p.a.lse)
+                    p.a.lse[at] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
+            } else {
+                // a tile that CTAs from..to share: each leaves its part, in slot 1 the first of them, in slot 0
+                // the others; the last of them to come adds them up
+                constexpr int kPartVecs = (D / 4 + 1) * kTileRows;
+                auto slot = [&](int c, bool first) { return reinterpret_cast<float4 *>(p.parts) + ((long long)c * 2 + first) * kPartVecs; };
+                const int row = half * kHalfRows + r;
+                float4 *dst = slot(blockIdx.x, opens);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(t_o + c, v);
+                    if (has)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            __stcg(dst + (c + k) / 4 * kTileRows + row,
+                                   make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
+                                               __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
+                }
+                if (has) __stcg(dst + D / 4 * kTileRows + row, make_float4(ref, sum, 0.0f, 0.0f));
+                const int threads = t.rows > kHalfRows ? 2 * kHalfRows : kHalfRows;
+                const int from = (int)(((t.begin + kCost + 1) * ctas + total - 1) / total - 1);
+                const int to = (int)(((t.begin + kCost + t.steps) * ctas + total - 1) / total - 1);
+                named_barrier_sync(threads == 256 ? 1 : 2, threads);
+                if (tid == 0) {
+                    __threadfence();
+                    unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
+                    do {
+                        seen = old;
+                        const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
+                        put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
+                        old = atomicCAS(tk, seen, put);
+                    } while (old != seen);
+                    __threadfence();
+                    misc[2] = put == 0;
+                }
+                named_barrier_sync(threads == 256 ? 1 : 2, threads);
+                const bool last = *reinterpret_cast<volatile int *>(misc + 2);
+                named_barrier_sync(threads == 256 ? 1 : 2, threads);      // misc[2] is read before it is written again
+                if (last && has) {
+                    float m = kRefStart, l = 0.0f;
+                    for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(slot(c, c == from) + D / 4 * kTileRows + row).x);
+                    for (int c = from; c <= to; ++c) {
+                        const float4 z = __ldcg(slot(c, c == from) + D / 4 * kTileRows + row);
+                        l = fmaf(z.y, ex2(z.x - m), l);
+                    }
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        float f[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) f[k] = 0.0f;
+                        for (int c = from; c <= to; ++c) {
+                            const float4 *src = slot(c, c == from) + row;
+                            const float w = ex2(__ldcg(src + D / 4 * kTileRows).x - m);
+#pragma unroll
+                            for (int k = 0; k < 32; k += 4) {
+                                const float4 z = __ldcg(src + (d + k) / 4 * kTileRows);
+                                f[k] = fmaf(z.x, w, f[k]), f[k + 1] = fmaf(z.y, w, f[k + 1]);
+                                f[k + 2] = fmaf(z.z, w, f[k + 2]), f[k + 3] = fmaf(z.w, w, f[k + 3]);
+                            }
+                        }
+                        store(at, d, f, 32, inv);
+                    }
+                    if (p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+                }
+            }
+            tc_fence_before();
+        }
+    } else if (warp < kSoftWarps + kConvWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+        // ------------------------------------------------------------ codes to operands
+        // A lane takes 16-byte piece `piece` of rows row0 + 4 i (head dim 128) or + 8 i (64): a warp's load
+        // covers whole rows, and eight lanes' stores hit eight different bank groups.
+        constexpr int ROWS = D == 128 ? 4 : 8;                     // rows of a warp's load
+        constexpr int LOADS = 32 / ROWS;                           // loads of a warp's 32 rows
+        const int w = warp - kSoftWarps;
+        const int piece = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
+        const int row_in = D == 128 ? (lane >> 2) & 3 : lane >> 2;
+        uint4 kraw[LOADS], vraw[LOADS];
+        int page[2];                                               // of the warp's two 16-key groups; -2: not needed
+        auto pages_of = [&](const ManyTile &t, int st) {
+            const int pos0 = block_of(t, st) * kKeys + w * 32;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int at = pos0 + 16 * g;
+                const bool needed = at <= t.hi && at < t.len && (at + 15 >= t.lo || at < p.a.sinks);
+                page[g] = needed ? p.b.block_table[(long long)t.seq * p.b.max_blocks + (at >> p.c.page_shift)] : -2;
+            }
+        };
+        auto check = [&]() {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if (page[g] != -2 && (page[g] < 0 || page[g] >= p.c.n_pages)) {
+                    kv_report(p.status);
+                    page[g] = -2;
+                }
+        };
+        auto load = [&](const uint8_t *base, const ManyTile &t, int st, uint4 (&raw)[LOADS]) {
+            const int pos0 = block_of(t, st) * kKeys + w * 32;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int row = row_in + ROWS * i, pos = pos0 + row, g = row >> 4;
+                const uint8_t *src = base + (long long)page[g] * p.c.page_stride + t.head * p.c.head_stride +
+                                     (pos & ((1 << p.c.page_shift) - 1)) * p.c.token_stride + piece * 16;
+                raw[i] = page[g] >= 0 && pos < t.len ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto convert = [&](const uint4 (&raw)[LOADS], uint8_t *tile) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const int row = w * 32 + row_in + ROWS * i;
+                uint32_t h[8];
+                codes_to_half<KT>(raw[i].x, h[0], h[1]);
+                codes_to_half<KT>(raw[i].y, h[2], h[3]);
+                codes_to_half<KT>(raw[i].z, h[4], h[5]);
+                codes_to_half<KT>(raw[i].w, h[6], h[7]);
+                uint8_t *dst = tile + (piece >> 2) * L::kBlockBytes + row * 128;
+                const int c = 2 * piece & 7;
+                *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+        };
+        float ks = 0.0f, vs = 0.0f;
+        bool there = false;
+        auto load_scales = [&](const ManyTile &t) {                // lanes 0 and 1: of the warp's two groups
+            there = lane < 2 && page[lane & 1] >= 0;
+            if (there) {
+                const long long i = (long long)page[lane & 1] * Hk + t.head;
+                ks = __ldg(p.c.k_scale + i);
+                vs = __ldg(p.c.v_scale + i);
+            }
+        };
+        ManyTile t;
+        int st = 0, s1 = 0;
+        bool more = next_tile(walk, t, st, s1);
+        if (more) {
+            pages_of(t, st);
+            check();
+            load(p.c.k, t, st, kraw);
+            load_scales(t);
+            load(p.c.v, t, st, vraw);
+        }
+        for (int counter = 0; more; ++counter) {
+            const int stg = counter & 1, ph = (counter >> 1) & 1;
+            // the next step's page ids, then its codes as soon as the registers are free
+            if (++st == s1) more = next_tile(walk, t, st, s1);
+            if (more) pages_of(t, st);
+            if (!mbar_wait_bounded(k_empty(stg), ph ^ 1, p.status, abort_flag)) break;
+            convert(kraw, smem + L::kK + stg * L::kOperand);
+            if (lane < 2)                                          // no page: weight 0 whatever the scores
+                scales[(counter & 3) * 8 + w * 2 + lane] =
+                    there ? make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f) : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(k_full(stg));
+            if (more) {
+                check();
+                load(p.c.k, t, st, kraw);
+                load_scales(t);
+            }
+            if (!mbar_wait_bounded(v_empty(stg), ph ^ 1, p.status, abort_flag)) break;
+            convert(vraw, smem + L::kV + stg * L::kOperand);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full(stg));
+            if (more) load(p.c.v, t, st, vraw);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    }
+    if (warp == kSoftWarps + kConvWarps && lane == 0) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint32_t idesc_s = make_idesc_f16(0, kHalfRows, kKeys);
+        const uint32_t idesc_o = make_idesc_f16(0, kHalfRows, D) | 1u << 16;      // V is MN-major
+        const uint32_t sm = smem_u32(smem);
+        int counter = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+        auto scores = [&](int half, int stg) {
+            const uint32_t a = sm + L::kQ + half * L::kOperand, b = sm + L::kK + stg * L::kOperand;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * L::kBlockBytes + (k & 3) * 32;
+                tc_mma_f16(tmem + half * 128, smem_desc_sw128(a + off), smem_desc_sw128(b + off), idesc_s, k > 0);
+            }
+            tc_commit(s_full(half));
+        };
+        auto output = [&](int half, int stg, bool fresh) {
+            const uint32_t b = sm + L::kV + stg * L::kOperand;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+                tc_mma_f16_ts(tmem + 256 + half * D, tmem + half * 128 + k * 8,
+                              desc_mn_sw128(b + k * 2048, L::kBlockBytes), idesc_o, !fresh || k > 0);
+        };
+        auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
+        auto run_tile = [&](const ManyTile &t, int s0, int s1) {
+            const int halves = t.rows > kHalfRows ? 2 : 1;
+            for (int st = s0; st < s1; ++st, ++counter) {
+                const int stg = counter & 1, ph = (counter >> 1) & 1;
+                if (st == s0) {
+                    if (!wait(k_full(stg), ph)) return false;
+                    for (int h = 0; h < halves; ++h) {
+                        if (!wait(q_full(h), q_phase[h])) return false;
+                        q_phase[h] ^= 1;
+                        tc_fence_after();
+                        scores(h, stg);
+                    }
+                    tc_commit(k_empty(stg));
+                }
+                const int nstg = (counter + 1) & 1, nph = ((counter + 1) >> 1) & 1;
+                for (int h = 0; h < halves; ++h) {
+                    if (!wait(p_ready(h), p_phase[h])) return false;
+                    p_phase[h] ^= 1;
+                    if (h == 0 && !wait(v_full(stg), ph)) return false;
+                    tc_fence_after();
+                    output(h, stg, st == s0);
+                    if (st + 1 == s1) tc_commit(o_full(h));
+                    if (h + 1 == halves) tc_commit(v_empty(stg));
+                    if (st + 1 < s1) {
+                        // MMAs run in the order they are issued: P is read before the next S replaces it
+                        if (h == 0 && !wait(k_full(nstg), nph)) return false;
+                        tc_fence_after();
+                        scores(h, nstg);
+                        if (h + 1 == halves) tc_commit(k_empty(nstg));
+                    }
+                }
+            }
+            return true;
+        };
+        ManyTile t;
+        int s0, s1;
+        while (next_tile(walk, t, s0, s1))
+            if (!run_tile(t, s0, s1)) {
+                // leave with no product in flight
+                tc_commit(drain);
+                for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
+                break;
+            }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps + kConvWarps) tmem_dealloc(tmem, 512u);
+}
+
+template <int KT, int D>
+cudaError_t launch(const ManyParams &p, int grid, cudaStream_t s, bool pdl) {
+    using L = ManySmem<D>;
+    auto kern = many_rows_kernel<KT, D>;
+    const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(kern), L::kEnd);
+    if (e != cudaSuccess) return e;
+    return kv_launch(kern, dim3(grid), dim3(kThreads), L::kEnd, s, pdl, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
+                                     const DeviceInfo &dev, cudaStream_t s, bool pdl) {
+    const int group = a.n_heads / c.n_kv_heads;
+    static std::atomic<unsigned long long> launches{0x7e57ab1e0000ull};
+    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
+        KvBatch b = batch;
+        b.block_table += (long long)b0 * b.max_blocks;
+        b.kv_lens += b0;
+        b.q_starts += b0;
+        b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
+        // as many pairs as these sequences can have at most
+        const long long pairs = (long long)b.n_tokens * group / kTileRows + b.n_seqs;
+        for (long long first = 0; first < pairs; first += kMaxPairs) {
+            ManyParams p{a, c, b, row_limit, (int)first, nullptr, nullptr, 0, dev.status};
+            p.tickets = static_cast<unsigned long long *>(a.workspace);
+            p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
+            p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
+            if (p.tag == 0) p.tag = 1;
+            const cudaError_t e =
+                c.kv_dtype == kKvInt8
+                    ? (c.head_dim == 128 ? launch<kKvInt8, 128>(p, dev.sm_count, s, pdl) : launch<kKvInt8, 64>(p, dev.sm_count, s, pdl))
+                    : (c.head_dim == 128 ? launch<kKvE4m3, 128>(p, dev.sm_count, s, pdl) : launch<kKvE4m3, 64>(p, dev.sm_count, s, pdl));
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+long long kv_attention_many_workspace(int head_dim, const DeviceInfo &dev) {
+    return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * (head_dim / 4 + 1) * kTileRows * 16;
+}
+
+}  // namespace w4a16
