@@ -41,8 +41,7 @@ constexpr int kMaxPairs = 2048;           // (sequence, row tile) pairs of a lau
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
 constexpr int kCost = 1;                  // steps that a tile's start and end count for in the shares
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);   // whole warpgroups: the register split goes by them
-constexpr int kRegsSoft = 168, kRegsConv = 104, kRegsMma = 72; // 256, 128 and 128 threads: 65536 in all, the launch's 512 * 128
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr float kRefStart = -3.402823466e38f, kTop = 15.9f, kHead = 14.0f;
 
 struct ManyParams {
@@ -115,7 +114,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
@@ -123,6 +122,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -359,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
 
     if (warp < kSoftWarps) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         // ------------------------------------------------------------ softmax, Q, output
         const int half = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -410,10 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             fence_proxy_async_smem();
             mbar_arrive(q_full(half));
         };
-        auto store = [&](long long at, int d0, const float *v, int count, float inv) {
+        auto store = [&](long long at, int d0, const float (&v)[32], float inv) {
             uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
 #pragma unroll
-            for (int i = 0; i < count; i += 8) {
+            for (int i = 0; i < 32; i += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -460,54 +466,32 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                                   (p.a.window > 0 && pos0 <= max_pos - p.a.window && pos0 + kKeys > p.a.sinks);
                 const int hi = pos - pos0;                         // columns up to hi, and past lo or below sink
                 const int lo = p.a.window > 0 ? hi - p.a.window : -1, sink = p.a.sinks - pos0;
-                auto sees = [&](int c) { return c <= hi && (c > lo || c < sink); };
-                uint32_t pk[kKeys / 2];
-                float part;
-                for (;;) {
-                    float top = -INFINITY;
-                    part = 0.0f;
+                // the columns of 32 from c on that the row sees, as bits
+                auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+                auto seen = [&](int c) { return below(hi + 1 - c) & (~below(lo + 1 - c) | below(sink - c)); };
+                // the largest exponent: of each 16 keys the largest score, the factor not being negative
+                float top = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(t_s + c, v);
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(t_s + c, v);
+                    if (edge) {
+                        const uint32_t bits = seen(c);
 #pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            const float4 z = sc[c / 16 + g];
-                            const float f = my_fac * z.x, add = z.y - ref;
-                            float w0 = 0.0f, w1 = 0.0f;
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const int k = g * 16 + i;
-                                float a, b;
-                                fma2(a, b, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, add);
-                                if (edge) {
-                                    if (!sees(c + k)) a = -INFINITY;
-                                    if (!sees(c + k + 1)) b = -INFINITY;
-                                }
-                                top = fmaxf(top, fmaxf(a, b));
-                                a = ex2(a), b = ex2(b);
-                                w0 += a, w1 += b;
-                                pk[(c + k) / 2] = pack_half2(a, b);
-                            }
-                            // a block that the row does not see adds nothing, whatever its scale
-                            if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, z.z, part);
-                        }
+                        for (int k = 0; k < 32; ++k)
+                            if (!(bits >> k & 1)) v[k] = 0xff800000u;
                     }
-                    if (!__any_sync(0xffffffffu, top > kTop)) break;
-                    // the reference moves: the largest exponent afresh (from the start value it is not exact)
-                    float m = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(t_s + c, v);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float4 z = sc[c / 16 + k / 16];
-                            const float e = fmaf(__uint_as_float(v[k]), my_fac * z.x, z.y);
-                            if (!edge || sees(c + k)) m = fmaxf(m, e);
-                        }
+                    for (int g = 0; g < 2; ++g) {
+                        const float4 z = sc[c / 16 + g];
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) m = fmaxf(m, __uint_as_float(v[g * 16 + k]));
+                        top = fmaxf(top, fmaf(m, my_fac * z.x, z.y));
                     }
-                    const float to = m - ref > kHead ? m - kHead : ref;
+                }
+                if (__any_sync(0xffffffffu, top - ref > kTop)) {
+                    const float to = top - ref > kTop ? top - kHead : ref;
                     const float f = ex2(ref - to);
                     ref = to;
                     sum *= f;
@@ -523,9 +507,36 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                         }
                     }
                 }
+                float part = 0.0f;
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t v[32], pk[16];
+                    tmem_ld32(t_s + c, v);
+                    const uint32_t bits = edge ? seen(c) : 0xffffffffu;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const float4 z = sc[c / 16 + g];
+                        const float f = my_fac * z.x, add = z.y - ref;
+                        float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const int k = g * 16 + i;
+                            float a, b;
+                            fma2(a, b, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, add);
+                            if (edge) {
+                                if (!(bits >> k & 1)) a = -INFINITY;
+                                if (!(bits >> (k + 1) & 1)) b = -INFINITY;
+                            }
+                            a = ex2(a), b = ex2(b);
+                            w0 += a, w1 += b;
+                            pk[k / 2] = pack_half2(a, b);
+                        }
+                        // a block that the row does not see adds nothing, whatever its scale
+                        if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, z.z, part);
+                    }
+                    tmem_st16(t_s + c / 2, pk);                    // over scores that have been read
+                }
                 sum += part;
-                tmem_st32(t_s, pk);
-                tmem_st32(t_s + 32, pk + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_ready(half));
@@ -549,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     float f[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(v[k]);
-                    if (has) store(at, c, f, 32, inv);
+                    if (has) store(at, c, f, inv);
                 }
                 if (has && p.a.lse)
                     p.a.lse[at] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
@@ -614,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                                 f[k + 2] = fmaf(z.z, w, f[k + 2]), f[k + 3] = fmaf(z.w, w, f[k + 3]);
                             }
                         }
-                        store(at, d, f, 32, inv);
+                        store(at, d, f, inv);
                     }
                     if (p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
                 }
@@ -622,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             tc_fence_before();
         }
     } else if (warp < kSoftWarps + kConvWarps) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
         // ------------------------------------------------------------ codes to operands
         // A lane takes 16-byte piece `piece` of rows row0 + 4 i (head dim 128) or + 8 i (64): a warp's load
         // covers whole rows, and eight lanes' stores hit eight different bank groups.
@@ -720,8 +730,6 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             if (lane == 0) mbar_arrive(v_full(stg));
             if (more) load(p.c.v, t, st, vraw);
         }
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     }
     if (warp == kSoftWarps + kConvWarps && lane == 0) {
         // ------------------------------------------------------------ MMA issuer
