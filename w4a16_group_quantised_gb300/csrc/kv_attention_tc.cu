@@ -114,6 +114,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
+// The load alone; its registers are good after tmem_ld_wait on them.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])::"memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -471,25 +491,37 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 auto seen = [&](int c) { return below(hi + 1 - c) & (~below(lo + 1 - c) | below(sink - c)); };
                 // the largest exponent: of each 16 keys the largest score, the factor not being negative
                 float top = -INFINITY;
+                uint32_t v[32], z[32];
+                tmem_ld32_start(t_s, v);
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 64) {
+                    tmem_ld32_start(t_s + c + 32, z);
+                    tmem_ld_wait(v);                               // both loads
+                    auto most = [&](uint32_t (&x)[32], int from) {
+                        if (edge) {
+                            const uint32_t bits = seen(from);
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(t_s + c, v);
-                    if (edge) {
-                        const uint32_t bits = seen(c);
+                            for (int k = 0; k < 32; ++k)
+                                if (!(bits >> k & 1)) x[k] = 0xff800000u;
+                        }
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (!(bits >> k & 1)) v[k] = 0xff800000u;
-                    }
+                        for (int g = 0; g < 2; ++g) {
+                            const float2 f = *reinterpret_cast<const float2 *>(sc + from / 16 + g);
+                            float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const float4 z = sc[c / 16 + g];
-                        float m = -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) m = fmaxf(m, __uint_as_float(v[g * 16 + k]));
-                        top = fmaxf(top, fmaf(m, my_fac * z.x, z.y));
-                    }
+                            for (int k = 0; k < 16; k += 2) {
+                                m0 = fmaxf(m0, __uint_as_float(x[g * 16 + k]));
+                                m1 = fmaxf(m1, __uint_as_float(x[g * 16 + k + 1]));
+                            }
+                            top = fmaxf(top, fmaf(fmaxf(m0, m1), my_fac * f.x, f.y));
+                        }
+                    };
+                    tmem_ld_wait(z);
+                    most(v, c);
+                    if (c + 64 < kKeys) tmem_ld32_start(t_s + c + 64, v);
+                    most(z, c + 32);
                 }
+                tmem_ld32_start(t_s, v);                           // ahead of the weights
                 if (__any_sync(0xffffffffu, top - ref > kTop)) {
                     const float to = top - ref > kTop ? top - kHead : ref;
                     const float f = ex2(ref - to);
@@ -499,30 +531,27 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                         // out of the steps before is complete: this step's S was issued after it
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
-                            uint32_t v[32];
-                            tmem_ld32(t_o + c, v);
+                            tmem_ld32(t_o + c, z);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                            tmem_st32(t_o + c, v);
+                            for (int k = 0; k < 32; ++k) z[k] = __float_as_uint(__uint_as_float(z[k]) * f);
+                            tmem_st32(t_o + c, z);
                         }
                     }
                 }
                 float part = 0.0f;
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    uint32_t v[32], pk[16];
-                    tmem_ld32(t_s + c, v);
-                    const uint32_t bits = edge ? seen(c) : 0xffffffffu;
+                auto weigh = [&](const uint32_t (&x)[32], int from) {
+                    uint32_t pk[16];
+                    const uint32_t bits = edge ? seen(from) : 0xffffffffu;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        const float4 z = sc[c / 16 + g];
-                        const float f = my_fac * z.x, add = z.y - ref;
+                        const float4 f4 = sc[from / 16 + g];
+                        const float f = my_fac * f4.x, add = f4.y - ref;
                         float w0 = 0.0f, w1 = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const int k = g * 16 + i;
                             float a, b;
-                            fma2(a, b, __uint_as_float(v[k]), __uint_as_float(v[k + 1]), f, add);
+                            fma2(a, b, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), f, add);
                             if (edge) {
                                 if (!(bits >> k & 1)) a = -INFINITY;
                                 if (!(bits >> (k + 1) & 1)) b = -INFINITY;
@@ -532,9 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                             pk[k / 2] = pack_half2(a, b);
                         }
                         // a block that the row does not see adds nothing, whatever its scale
-                        if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, z.z, part);
+                        if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, f4.z, part);
                     }
-                    tmem_st16(t_s + c / 2, pk);                    // over scores that have been read
+                    tmem_st16(t_s + from / 2, pk);                 // over scores that have been read
+                };
+#pragma unroll 1
+                for (int c = 0; c < kKeys; c += 64) {
+                    tmem_ld_wait(v);
+                    tmem_ld32_start(t_s + c + 32, z);
+                    weigh(v, c);
+                    tmem_ld_wait(z);
+                    if (c + 64 < kKeys) tmem_ld32_start(t_s + c + 64, v);
+                    weigh(z, c + 32);
                 }
                 sum += part;
                 tmem_wait_st();
