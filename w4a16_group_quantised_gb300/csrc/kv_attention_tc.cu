@@ -102,6 +102,19 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, flo
         : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
 
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
+        "mov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+// the largest of a value and two words of scores
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -154,14 +167,45 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] . B[smem], kind::f16.
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// A step's MMAs, issued by one elected lane of a converged warp, so that
+// descriptors and addresses stay in uniform registers: issued from a
+// diverged lane, each MMA cost three times its 32 cycles of arithmetic.
+// Descriptors are a low word (address, leading offset) and a constant high
+// word; 16 of the contraction's elements further is a constant step.
+//
+// S = Q K^T: 64 dims are four steps of 32 bytes in a 128-byte row; `far` is
+// the step to the next 64 dims.
+template <int BLOCKS>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc) {
+    static_assert(BLOCKS == 1 || BLOCKS == 2, "64 or 128 dims");
+#pragma unroll
+    for (int k = 0; k < 4 * BLOCKS; ++k) {
+        const uint32_t off = (k >> 2) * (kKeys * 128 / 16) + (k & 3) * 2;
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+            "r"(alo + off), "r"(blo + off), "r"(hi), "r"(idesc), "r"(k > 0 ? 1u : 0u)
+            : "memory");
+    }
+}
+// out (+)= P V: P in TMEM, 8 columns a step; 16 keys of V are 2048 bytes.
+__device__ __forceinline__ void mma_output(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc,
+                                           uint32_t accumulate) {
+#pragma unroll
+    for (int k = 0; k < kKeys / 16; ++k) {
+        asm volatile(
+            "{\n\t.reg .pred e, p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+            "r"(a + 8 * k), "r"(blo + 128 * k), "r"(hi), "r"(idesc), "r"(k > 0 ? 1u : accumulate)
+            : "memory");
+    }
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -509,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                             const float2 f = *reinterpret_cast<const float2 *>(sc + from / 16 + g);
                             float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                m0 = fmaxf(m0, __uint_as_float(x[g * 16 + k]));
-                                m1 = fmaxf(m1, __uint_as_float(x[g * 16 + k + 1]));
+                            for (int k = 0; k < 16; k += 4) {
+                                m0 = max3(m0, x[g * 16 + k], x[g * 16 + k + 1]);
+                                m1 = max3(m1, x[g * 16 + k + 2], x[g * 16 + k + 3]);
                             }
                             top = fmaxf(top, fmaf(fmaxf(m0, m1), my_fac * f.x, f.y));
                         }
@@ -557,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                                 if (!(bits >> (k + 1) & 1)) b = -INFINITY;
                             }
                             a = ex2(a), b = ex2(b);
-                            w0 += a, w1 += b;
+                            add2(w0, w1, a, b);
                             pk[k / 2] = pack_half2(a, b);
                         }
                         // a block that the row does not see adds nothing, whatever its scale
@@ -769,27 +813,22 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             if (more) load(p.c.v, t, st, vraw);
         }
     }
-    if (warp == kSoftWarps + kConvWarps && lane == 0) {
+    if (warp == kSoftWarps + kConvWarps) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc_s = make_idesc_f16(0, kHalfRows, kKeys);
         const uint32_t idesc_o = make_idesc_f16(0, kHalfRows, D) | 1u << 16;      // V is MN-major
         const uint32_t sm = smem_u32(smem);
+        const uint32_t k_desc = (uint32_t)smem_desc_sw128(0u), v_desc = (uint32_t)desc_mn_sw128(0u, L::kBlockBytes);
+        const uint32_t hi = (uint32_t)(smem_desc_sw128(0u) >> 32);
         int counter = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
         auto scores = [&](int half, int stg) {
-            const uint32_t a = sm + L::kQ + half * L::kOperand, b = sm + L::kK + stg * L::kOperand;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * L::kBlockBytes + (k & 3) * 32;
-                tc_mma_f16(tmem + half * 128, smem_desc_sw128(a + off), smem_desc_sw128(b + off), idesc_s, k > 0);
-            }
-            tc_commit(s_full(half));
+            mma_scores<L::kBlocks>(tmem + half * 128, k_desc + ((sm + L::kQ + half * L::kOperand) >> 4),
+                                   k_desc + ((sm + L::kK + stg * L::kOperand) >> 4), hi, idesc_s);
+            commit_elected(s_full(half));
         };
         auto output = [&](int half, int stg, bool fresh) {
-            const uint32_t b = sm + L::kV + stg * L::kOperand;
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                tc_mma_f16_ts(tmem + 256 + half * D, tmem + half * 128 + k * 8,
-                              desc_mn_sw128(b + k * 2048, L::kBlockBytes), idesc_o, !fresh || k > 0);
+            mma_output(tmem + 256 + half * D, tmem + half * 128, v_desc + ((sm + L::kV + stg * L::kOperand) >> 4), hi,
+                       idesc_o, fresh ? 0u : 1u);
         };
         auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
         auto run_tile = [&](const ManyTile &t, int s0, int s1) {
@@ -804,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                         tc_fence_after();
                         scores(h, stg);
                     }
-                    tc_commit(k_empty(stg));
+                    commit_elected(k_empty(stg));
                 }
                 const int nstg = (counter + 1) & 1, nph = ((counter + 1) >> 1) & 1;
                 for (int h = 0; h < halves; ++h) {
@@ -813,14 +852,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     if (h == 0 && !wait(v_full(stg), ph)) return false;
                     tc_fence_after();
                     output(h, stg, st == s0);
-                    if (st + 1 == s1) tc_commit(o_full(h));
-                    if (h + 1 == halves) tc_commit(v_empty(stg));
+                    if (st + 1 == s1) commit_elected(o_full(h));
+                    if (h + 1 == halves) commit_elected(v_empty(stg));
                     if (st + 1 < s1) {
                         // MMAs run in the order they are issued: P is read before the next S replaces it
                         if (h == 0 && !wait(k_full(nstg), nph)) return false;
                         tc_fence_after();
                         scores(h, nstg);
-                        if (h + 1 == halves) tc_commit(k_empty(nstg));
+                        if (h + 1 == halves) commit_elected(k_empty(nstg));
                     }
                 }
             }
@@ -828,13 +867,17 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         };
         ManyTile t;
         int s0, s1;
-        while (next_tile(walk, t, s0, s1))
+        while (next_tile(walk, t, s0, s1)) {
+            // the same in every lane, and known to be
+            t.rows = __reduce_max_sync(0xffffffffu, t.rows);
+            s0 = __reduce_max_sync(0xffffffffu, s0), s1 = __reduce_max_sync(0xffffffffu, s1);
             if (!run_tile(t, s0, s1)) {
                 // leave with no product in flight
-                tc_commit(drain);
+                commit_elected(drain);
                 for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
                 break;
             }
+        }
     }
     __syncwarp();
     tc_fence_before();
