@@ -29,6 +29,7 @@
 // that share a tile add their parts up through the workspace, in order.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv.cuh"
 
@@ -164,6 +165,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+// 32 bytes at a 32-byte boundary (else two halves)
+__device__ __forceinline__ void st_v8(void *dst, const uint32_t *w) {
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *(reinterpret_cast<uint4 *>(dst) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -443,54 +449,65 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             return true;
         };
         float fac = 0.0f;
+        // A warp loads its 32 rows together, two (head dim 128) or four rows a load, so that each load covers
+        // whole rows; a row's D / 8 lanes find its largest value.
         auto load_q = [&](const ManyTile &t) {
-            const int x = t.row0 + half * kHalfRows + r, tok = x / group;
-            const bool has = half * kHalfRows + r < t.rows;
-            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(t.q0 + tok) * p.a.q_stride +
-                                  (t.head * group + x - tok * group) * D;
-            uint4 v[D / 8];
-            float top = 0.0f;
+            constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
+            const int row = half * kHalfRows + r, x = t.row0 + row, tok = x / group;
+            const long long mine = row < t.rows ? (long long)(t.q0 + tok) * p.a.q_stride +
+                                                      (long long)(t.head * group + x - tok * group) * D
+                                                : -1;
+            const uint16_t *q = static_cast<const uint16_t *>(p.a.q);
+            const int sub = lane / LANES, piece = lane % LANES;
+            uint8_t *dst = smem + L::kQ + half * L::kOperand + (piece >> 3) * L::kBlockBytes;
+            constexpr int BATCH = 8;                               // loads on their way together
+            constexpr int ROUNDS = 32 / AT_ONCE;
+#pragma unroll 1
+            for (int i0 = 0; i0 < ROUNDS; i0 += BATCH) {
+                uint4 v[BATCH];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) v[i] = has ? ldg_nc_v4(src + 8 * i) : make_uint4(0, 0, 0, 0);
-            auto value = [&](uint32_t w, int e) {
-                const uint16_t h = (uint16_t)(w >> (16 * e));
-                return p.a.dtype == 0 ? kv_act<0>(h) : kv_act<1>(h);
-            };
+                for (int i = 0; i < BATCH; ++i) {
+                    const long long at = __shfl_sync(0xffffffffu, mine, (i0 + i) * AT_ONCE + sub);
+                    v[i] = at >= 0 ? ldg_nc_v4(q + at + piece * 8) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                for (int i = 0; i < BATCH; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    float f[8], top = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(value(w[j], 0)), fabsf(value(w[j], 1))));
-            }
-            // a power of two puts the row's largest value in [2^14, 2^15); a negative scale's sign goes along
-            const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-            float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-            fac = __uint_as_float((uint32_t)(ex - 14 + 127) << 23) * fabsf(p.a.scale) * 1.4426950408889634f;
-            if (p.a.scale < 0.0f) up = -up;
-            uint8_t *dst = smem + L::kQ + half * L::kOperand + r * 128;
+                    for (int j = 0; j < 8; ++j) {
+                        const uint16_t h = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+                        f[j] = p.a.dtype == 0 ? kv_act<0>(h) : kv_act<1>(h);
+                        top = fmaxf(top, fabsf(f[j]));
+                    }
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] = pack_half2(value(w[j], 0) * up, value(w[j], 1) * up);
-                *reinterpret_cast<uint4 *>(dst + (i >> 3) * L::kBlockBytes + (((i & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int d = 1; d < LANES; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    // a power of two puts the row's largest value in [2^14, 2^15); a negative scale's sign goes along
+                    const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+                    const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23 | (p.a.scale < 0.0f ? 0x80000000u : 0u));
+                    const int rr = (warp & 3) * 32 + (i0 + i) * AT_ONCE + sub;
+                    *reinterpret_cast<uint4 *>(dst + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4)) =
+                        make_uint4(pack_half2(f[0] * up, f[1] * up), pack_half2(f[2] * up, f[3] * up),
+                                   pack_half2(f[4] * up, f[5] * up), pack_half2(f[6] * up, f[7] * up));
+                    // to the lane whose row it is
+                    const int back = __shfl_sync(0xffffffffu, ex, (lane % AT_ONCE) * LANES);
+                    if (lane / AT_ONCE == i0 + i)
+                        fac = __uint_as_float((uint32_t)(back - 14 + 127) << 23) * fabsf(p.a.scale) * 1.4426950408889634f;
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full(half));
         };
         auto store = [&](long long at, int d0, const float (&v)[32], float inv) {
             uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+            for (int j = 0; j < 16; ++j)
+                w[j] = p.a.dtype == 0 ? pack_half2(v[2 * j] * inv, v[2 * j + 1] * inv)
+                                      : pack_bf162(v[2 * j] * inv, v[2 * j + 1] * inv);
+            // whole 32-byte sectors
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = p.a.dtype == 0 ? pack_half2(v[i + 2 * j] * inv, v[i + 2 * j + 1] * inv)
-                                          : pack_bf162(v[i + 2 * j] * inv, v[i + 2 * j + 1] * inv);
-                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 16; j += 8) st_v8(dst + 2 * j, &w[j]);
         };
         int counter = 0;                                           // steps so far: the scales' ring position
         bool ok = true;
@@ -533,6 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 // the columns of 32 from c on that the row sees, as bits
                 auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
                 auto seen = [&](int c) { return below(hi + 1 - c) & (~below(lo + 1 - c) | below(sink - c)); };
+                // two forms, with the mask and without
+                auto weights = [&](auto tag) {
+                constexpr bool EDGE = decltype(tag)::value;
                 // the largest exponent: of each 16 keys the largest score, the factor not being negative
                 float top = -INFINITY;
                 uint32_t v[32], z[32];
@@ -542,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     tmem_ld32_start(t_s + c + 32, z);
                     tmem_ld_wait(v);                               // both loads
                     auto most = [&](uint32_t (&x)[32], int from) {
-                        if (edge) {
+                        if (EDGE) {
                             const uint32_t bits = seen(from);
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
@@ -585,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 float part = 0.0f;
                 auto weigh = [&](const uint32_t (&x)[32], int from) {
                     uint32_t pk[16];
-                    const uint32_t bits = edge ? seen(from) : 0xffffffffu;
+                    const uint32_t bits = EDGE ? seen(from) : 0xffffffffu;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f4 = sc[from / 16 + g];
@@ -596,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                             const int k = g * 16 + i;
                             float a, b;
                             fma2(a, b, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), f, add);
-                            if (edge) {
+                            if (EDGE) {
                                 if (!(bits >> k & 1)) a = -INFINITY;
                                 if (!(bits >> (k + 1) & 1)) b = -INFINITY;
                             }
@@ -619,6 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     weigh(z, c + 32);
                 }
                 sum += part;
+                };
+                if (edge) weights(std::true_type{});
+                else weights(std::false_type{});
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(p_ready(half));
