@@ -38,11 +38,12 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kMaxPairs = 2048;           // (sequence, row tile) pairs of a launch
+constexpr int kMaxPairs = 1536;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
-constexpr int kCost = 1;                  // steps that a tile's start and end count for in the shares
+constexpr int kCost = 3;                  // steps that a tile's start and end count for in the shares
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 2);
+constexpr int kRing = 4;                  // tiles that the planner is ahead of the slowest role
 constexpr float kRefStart = -3.402823466e38f, kTop = 15.9f, kHead = 14.0f;
 
 struct ManyParams {
@@ -65,6 +66,12 @@ struct ManyTile {
     long long begin;                      // on the line
 };
 
+// A tile with this CTA's steps [s0, s1) of it; s1 == 0 ends the list.
+struct PlannedTile {
+    ManyTile t;
+    int s0, s1;
+};
+
 template <int D>
 struct ManySmem {
     static constexpr int kBlockBytes = kKeys * 128;               // 128 rows of 64 fp16
@@ -77,8 +84,9 @@ struct ManySmem {
     static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
     static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
     static constexpr int kScale = kPairSeq + kMaxPairs * 2;       // [4][8] float4 {ks, log2 vs, 1 / vs, -}
-    static constexpr int kBars = kScale + 4 * 8 * 16;
-    static constexpr int kMisc = kBars + 18 * 8;
+    static constexpr int kPlan = kScale + 4 * 8 * 16;
+    static constexpr int kBars = kPlan + kRing * (int)sizeof(PlannedTile);
+    static constexpr int kMisc = kBars + (18 + 2 * kRing) * 8;
     static constexpr int kEnd = kMisc + 256 + 1024;               // 1024: slack to align the base
 };
 
@@ -95,19 +103,22 @@ __device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-// two fp32 multiply-adds in one instruction
-__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
-    asm("{\n\t.reg .b64 p, q, r, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
-        "fma.rn.f32x2 s, p, q, r;\n\tmov.b64 {%0, %1}, s;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+// two fp32 numbers in a 64-bit register, and the arithmetic on such pairs
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
-
-__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tadd.rn.f32x2 p, p, q;\n\t"
-        "mov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b));
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 // the largest of a value and two words of scores
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
@@ -274,6 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     auto v_full = [&](int i) { return bars + 8u * (12 + i); };
     auto v_empty = [&](int i) { return bars + 8u * (14 + i); };
     const uint32_t drain = bars + 8u * 16;
+    auto plan_full = [&](int i) { return bars + 8u * (18 + i); };
+    auto plan_empty = [&](int i) { return bars + 8u * (18 + kRing + i); };
+    PlannedTile *plan = reinterpret_cast<PlannedTile *>(smem + L::kPlan);
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -287,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             mbar_init(v_empty(i), 1);
         }
         mbar_init(drain, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(plan_full(i), 1);
+            mbar_init(plan_empty(i), kSoftWarps + kConvWarps + 1);
+        }
         fence_mbar_init();
         misc[0] = 0;
     }
@@ -380,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         t.begin = pre[pair] * Hk + (long long)head * (t.steps + kCost);
         return t;
     };
-    auto pair_of = [&](long long at) {                             // the pair of a position of the line
+    auto find_pair = [&](long long at) {                           // the pair of a position of the line
         int lo = 0, hi = pairs - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -394,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     if (tid < 2) {
         long long at = ((long long)blockIdx.x + tid) * total / ctas;
         if (at > 0 && at < total) {
-            const int pair = pair_of(at);
+            const int pair = find_pair(at);
             const long long each = pre[pair + 1] - pre[pair], rem = at - pre[pair] * Hk;
             if (each <= kShortSteps + kCost) at -= rem % each;
         }
@@ -412,27 +430,20 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     // the tile at c0, and the walk from there
     int pair = 0, head = 0;
     if (c0 < c1) {
-        pair = pair_of(c0);
+        pair = find_pair(c0);
         head = (int)((c0 - pre[pair] * Hk) / (pre[pair + 1] - pre[pair]));
     }
-    // this CTA's steps of a tile
-    auto from_step = [&](const ManyTile &t) { return (int)min(max(c0 - t.begin - kCost, 0LL), (long long)t.steps); };
-    auto to_step = [&](const ManyTile &t) { return (int)min(max(c1 - t.begin - kCost, 0LL), (long long)t.steps); };
-    // The walk over this CTA's tiles, the same in every role.
-    struct Walk {
-        int pair, head;
+    // The list of this CTA's tiles, written by the planner ahead of the other roles.  open_tile waits for
+    // the idx-th (null: the end, or a wait that ran out), close_tile gives its place back.
+    auto open_tile = [&](int idx) -> const PlannedTile * {
+        if (!mbar_wait_bounded(plan_full(idx % kRing), (idx / kRing) & 1, p.status, abort_flag)) return nullptr;
+        const PlannedTile *t = plan + idx % kRing;
+        return t->s1 > 0 ? t : nullptr;
     };
-    auto next_tile = [&](Walk &w, ManyTile &t, int &s0, int &s1) {
-        while (w.pair < pairs) {
-            t = tile_at(w.pair, w.head);
-            if (t.begin >= c1) return false;
-            if (++w.head == Hk) w.head = 0, ++w.pair;
-            s0 = from_step(t), s1 = to_step(t);
-            if (s0 < s1) return true;
-        }
-        return false;
+    auto close_tile = [&](int idx) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(plan_empty(idx % kRing));
     };
-    Walk walk = {pair, head};
     auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
 
     if (warp < kSoftWarps) {
@@ -511,20 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         };
         int counter = 0;                                           // steps so far: the scales' ring position
         bool ok = true;
-        auto load_next_q = [&]() {                                 // of the tile that comes next
-            Walk ahead = walk;
-            ManyTile t;
-            int s0, s1;
-            if (next_tile(ahead, t, s0, s1) && half * kHalfRows < t.rows) load_q(t);
-        };
-        load_next_q();
-        for (;;) {
-            ManyTile t;
-            int s0, s1;
-            if (!next_tile(walk, t, s0, s1)) break;
+        const PlannedTile *next = open_tile(0);
+        if (next && half * kHalfRows < next->t.rows) load_q(next->t);
+        for (int idx = 0; next && ok; ++idx) {
+            const ManyTile &t = next->t;                           // in shared memory
+            const int s0 = next->s0, s1 = next->s1;
             const bool runs = half * kHalfRows < t.rows;           // a tile of up to 128 rows is the first half's alone
             const float my_fac = fac;
-            const Walk here = {t.pair, t.head};
             const int sink_blocks = t.sink, block0 = t.block0 - t.sink;
             const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
             const int x = t.row0 + half * kHalfRows + r;
@@ -610,21 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     for (int g = 0; g < 2; ++g) {
                         const float4 f4 = sc[from / 16 + g];
                         const float f = my_fac * f4.x, add = f4.y - ref;
-                        float w0 = 0.0f, w1 = 0.0f;
+                        const uint64_t ff = pair_of(f, f), aa = pair_of(add, add);
+                        uint64_t ww = 0;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const int k = g * 16 + i;
                             float a, b;
-                            fma2(a, b, __uint_as_float(x[k]), __uint_as_float(x[k + 1]), f, add);
+                            unpair(fma2(pair_of(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff, aa), a, b);
                             if (EDGE) {
                                 if (!(bits >> k & 1)) a = -INFINITY;
                                 if (!(bits >> (k + 1) & 1)) b = -INFINITY;
                             }
                             a = ex2(a), b = ex2(b);
-                            add2(w0, w1, a, b);
+                            ww = add2(ww, pair_of(a, b));
                             pk[k / 2] = pack_half2(a, b);
                         }
                         // a block that the row does not see adds nothing, whatever its scale
+                        float w0, w1;
+                        unpair(ww, w0, w1);
                         if (w0 + w1 != 0.0f) part = fmaf(w0 + w1, f4.z, part);
                     }
                     tmem_st16(t_s + from / 2, pk);                 // over scores that have been read
@@ -648,12 +655,15 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             }
             if (!ok) break;
             // the next tile's rows while the last product runs
-            load_next_q();
-            if (!runs) continue;
+            next = open_tile(idx + 1);
+            if (next && half * kHalfRows < next->t.rows) load_q(next->t);
+            if (!runs) {
+                close_tile(idx);
+                continue;
+            }
             if (!mbar_wait_bounded(o_full(half), o_phase, p.status, abort_flag)) break;
             o_phase ^= 1;
             tc_fence_after();
-            t = tile_at(here.pair, here.head);                     // afresh: kept out of the steps' registers
             long long at = 0;
             const bool has = place(t, at);
             if (whole) {
@@ -736,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 }
             }
             tc_fence_before();
+            close_tile(idx);
         }
     } else if (warp < kSoftWarps + kConvWarps) {
         // ------------------------------------------------------------ codes to operands
@@ -801,8 +812,15 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             }
         };
         ManyTile t;
-        int st = 0, s1 = 0;
-        bool more = next_tile(walk, t, st, s1);
+        int st = 0, s1 = 0, idx = 0;
+        bool more = false;
+        auto open = [&]() {
+            const PlannedTile *next = open_tile(idx);
+            more = next != nullptr;
+            if (more) t = next->t, st = next->s0, s1 = next->s1;
+            close_tile(idx++);
+        };
+        open();
         if (more) {
             pages_of(t, st);
             check();
@@ -813,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         for (int counter = 0; more; ++counter) {
             const int stg = counter & 1, ph = (counter >> 1) & 1;
             // the next step's page ids, then its codes as soon as the registers are free
-            if (++st == s1) more = next_tile(walk, t, st, s1);
+            if (++st == s1) open();
             if (more) pages_of(t, st);
             if (!mbar_wait_bounded(k_empty(stg), ph ^ 1, p.status, abort_flag)) break;
             convert(kraw, smem + L::kK + stg * L::kOperand);
@@ -854,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                        idesc_o, fresh ? 0u : 1u);
         };
         auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
-        auto run_tile = [&](const ManyTile &t, int s0, int s1) {
-            const int halves = t.rows > kHalfRows ? 2 : 1;
+        auto run_tile = [&](int rows, int s0, int s1) {
+            const int halves = rows > kHalfRows ? 2 : 1;
             for (int st = s0; st < s1; ++st, ++counter) {
                 const int stg = counter & 1, ph = (counter >> 1) & 1;
                 if (st == s0) {
@@ -888,18 +906,57 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             }
             return true;
         };
-        ManyTile t;
-        int s0, s1;
-        while (next_tile(walk, t, s0, s1)) {
+        for (int idx = 0;; ++idx) {
+            const PlannedTile *next = open_tile(idx);
+            if (!next) break;
             // the same in every lane, and known to be
-            t.rows = __reduce_max_sync(0xffffffffu, t.rows);
-            s0 = __reduce_max_sync(0xffffffffu, s0), s1 = __reduce_max_sync(0xffffffffu, s1);
-            if (!run_tile(t, s0, s1)) {
+            const int rows = __reduce_max_sync(0xffffffffu, next->t.rows);
+            const int s0 = __reduce_max_sync(0xffffffffu, next->s0), s1 = __reduce_max_sync(0xffffffffu, next->s1);
+            close_tile(idx);
+            if (!run_tile(rows, s0, s1)) {
                 // leave with no product in flight
                 commit_elected(drain);
                 for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
                 break;
             }
+        }
+    } else if (warp == kSoftWarps + kConvWarps + 1) {
+        // ------------------------------------------------------------ planner
+        int pr = pair, hd = head, idx = 0;
+        for (bool more = true; more;) {
+            PlannedTile next = {};
+            more = false;
+            while (pr < pairs) {
+                next.t = tile_at(pr, hd);
+                if (next.t.begin >= c1) break;
+                if (++hd == Hk) hd = 0, ++pr;
+                // this CTA's steps of the tile
+                next.s0 = (int)min(max(c0 - next.t.begin - kCost, 0LL), (long long)next.t.steps);
+                next.s1 = (int)min(max(c1 - next.t.begin - kCost, 0LL), (long long)next.t.steps);
+                if (next.s0 < next.s1) {
+                    more = true;
+                    break;
+                }
+            }
+            if (!more) next.s1 = 0;
+            if (idx >= kRing &&
+                !mbar_wait_bounded(plan_empty(idx % kRing), (idx / kRing - 1) & 1, p.status, abort_flag))
+                break;
+            if (lane == 0) {
+                plan[idx % kRing] = next;
+                mbar_arrive(plan_full(idx % kRing));
+            }
+            __syncwarp();
+            // its rows of q towards L2
+            if (more)
+                for (int row = lane; row < next.t.rows; row += 32) {
+                    const int x = next.t.row0 + row, tok = x / group;
+                    const uint16_t *src = static_cast<const uint16_t *>(p.a.q) +
+                                          (long long)(next.t.q0 + tok) * p.a.q_stride + (next.t.head * group + x - tok * group) * D;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+                    if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+                }
+            ++idx;
         }
     }
     __syncwarp();
