@@ -9,6 +9,18 @@ NULL, OK = None, 0x1000                # addresses are never dereferenced: valid
 ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE, ERR_ARG = -1, -2, -4, -5, -9
 
 
+class Cache(ctypes.Structure):         # w4a16_kv_cache_t
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong), ("kv_dtype", ctypes.c_int)]
+
+
+class Batch(ctypes.Structure):         # w4a16_kv_batch_t
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("max_blocks", ctypes.c_int), ("n_tokens", ctypes.c_int)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     from w4a16_group_quantised_gb300 import build
@@ -18,18 +30,16 @@ def lib():
 
 
 def cache(**kw):
-    from w4a16_group_quantised_gb300.kv import _Cache
     f = dict(k=OK, v=OK, k_scale=OK, v_scale=OK, n_pages=8, page_size=16, n_kv_heads=2, head_dim=128,
              page_stride=4096, head_stride=2048, token_stride=128, kv_dtype=0)
     f.update(kw)
-    return ctypes.byref(_Cache(**f))
+    return ctypes.byref(Cache(**f))
 
 
 def batch(**kw):
-    from w4a16_group_quantised_gb300.kv import _Batch
     f = dict(block_table=OK, kv_lens=OK, q_starts=OK, n_seqs=2, max_blocks=4, n_tokens=3)
     f.update(kw)
-    return ctypes.byref(_Batch(**f))
+    return ctypes.byref(Batch(**f))
 
 
 def append(lib, c=None, b=None, k=OK, ks=256, v=OK, vs=256, dt=0):
@@ -157,3 +167,12 @@ def test_binding_refuses_before_the_call():
         w.w4a16_kv_append(c, q, q, ints, ints, ints)
     with pytest.raises(TypeError):
         w.w4a16_kv_free([0], ints, ints, ints)
+
+
+def test_binding_packs_the_structs_as_c_lays_them_out():
+    from w4a16_group_quantised_gb300 import kv
+    assert kv._CACHE.size == ctypes.sizeof(Cache) and kv._BATCH.size == ctypes.sizeof(Batch)
+    raw = Cache.from_buffer_copy(kv._CACHE.pack(1, 2, 3, 4, 5, 6, 7, 8, 1 << 40, 10, 11, 1))
+    assert [getattr(raw, f[0]) for f in Cache._fields_] == [1, 2, 3, 4, 5, 6, 7, 8, 1 << 40, 10, 11, 1]
+    raw = Batch.from_buffer_copy(kv._BATCH.pack(1, 2, 3, 4, 5, 6))
+    assert [getattr(raw, f[0]) for f in Batch._fields_] == [1, 2, 3, 4, 5, 6]

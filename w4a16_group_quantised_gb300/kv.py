@@ -14,9 +14,11 @@ n_kv_heads].
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple
 
-from .binding import _check, _dtype_code, _p, _stream_ptr, load_library
+from .binding import W4A16_BF16, W4A16_F16, _check, _dtype_code, load_library
 
 KV_INT8, KV_E4M3 = 0, 1
 
@@ -29,19 +31,13 @@ class KVCache(NamedTuple):
     v_scale: "torch.Tensor"   # noqa: F821
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
-                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("page_stride", ctypes.c_longlong),
-                ("head_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong), ("kv_dtype", ctypes.c_int)]
+# w4a16_kv_cache_t and w4a16_kv_batch_t, in native layout
+_CACHE = struct.Struct("@PPPPiiiiqqqi4x")
+_BATCH = struct.Struct("@PPPiii4x")
 
 
-class _Batch(ctypes.Structure):
-    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
-                ("n_seqs", ctypes.c_int), ("max_blocks", ctypes.c_int), ("n_tokens", ctypes.c_int)]
-
-
-def _tensor(name, t, dtype=None, dim=None, contiguous=True):
+def _refuse(name, t, dtype, dim, device):
+    """Why `t` is not a contiguous tensor of this dtype and dimension on this CUDA device (None: any)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
@@ -51,126 +47,150 @@ def _tensor(name, t, dtype=None, dim=None, contiguous=True):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if dim is not None and t.dim() != dim:
         raise ValueError(f"{name} must be {dim}-D, got {list(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"operands are on different devices: {name} on {t.device}, others on cuda:{device}")
 
 
-def _one_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"operands are on different devices: {sorted(map(str, devs))}")
+def _ints(name, t, dim, device):
+    """An int32 tensor's address, checked; `device` is a CUDA device's index."""
+    import torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == dim and t.get_device() == device >= 0
+            and t.is_contiguous()):
+        _refuse(name, t, torch.int32, dim, device)
+    return t.data_ptr()
+
+
+def _device_of(name, t):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        _refuse(name, t, None, None, None)
+    return t.get_device()
 
 
 def _cache(c):
-    """The cache as the C struct; TypeError / ValueError for what it cannot be."""
+    """(the cache as the C struct's bytes, device index, pages, heads, page size, head dim)"""
     import torch
     if not isinstance(c, KVCache):
         raise TypeError(f"cache must be a KVCache, got {type(c).__name__}")
-    k, v = _tensor("cache.k", c.k, dim=4, contiguous=False), _tensor("cache.v", c.v, dim=4, contiguous=False)
-    if k.dtype == torch.int8:
-        kind = KV_INT8
-    elif k.dtype == torch.float8_e4m3fn:
-        kind = KV_E4M3
-    else:
+    k, v, ks, vs = c
+    device = _device_of("cache.k", k)
+    kind = KV_INT8 if k.dtype is torch.int8 else KV_E4M3
+    if kind == KV_E4M3 and k.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"cache.k must be int8 or float8_e4m3fn, got {k.dtype}")
-    if v.dtype != k.dtype or v.shape != k.shape or v.stride() != k.stride():
+    if k.dim() != 4:
+        raise ValueError(f"cache.k must be 4-D, got {list(k.shape)}")
+    if _device_of("cache.v", v) != device:
+        raise ValueError(f"operands are on different devices: {k.device}, {v.device}")
+    shape, stride = k.shape, k.stride()
+    if v.dtype is not k.dtype or v.shape != shape or v.stride() != stride:
         raise ValueError("cache.k and cache.v must have the same dtype, shape and strides")
-    n_pages, heads, page_size, head_dim = k.shape
-    sp, sh, st, sd = k.stride()
+    n_pages, heads, page_size, head_dim = shape
+    sp, sh, st, sd = stride
     if sd != 1:
         raise ValueError("the codes' last dimension must be contiguous")
-    for name, t in (("cache.k_scale", c.k_scale), ("cache.v_scale", c.v_scale)):
-        _tensor(name, t, torch.float32, 2)
-        if t.shape[0] != n_pages or t.shape[1] != heads:
+    for name, t in (("cache.k_scale", ks), ("cache.v_scale", vs)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == device
+                and t.dim() == 2 and t.is_contiguous()):
+            _refuse(name, t, torch.float32, 2, device)
+        if t.shape != (n_pages, heads):
             raise ValueError(f"{name} must be [{n_pages}, {heads}], got {list(t.shape)}")
-    _one_device(k, v, c.k_scale, c.v_scale)
-    return _Cache(k.data_ptr(), v.data_ptr(), c.k_scale.data_ptr(), c.v_scale.data_ptr(), n_pages, page_size, heads,
-                  head_dim, sp, sh, st, kind)
+    return (_CACHE.pack(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n_pages, page_size, heads, head_dim,
+                        sp, sh, st, kind), device, n_pages, heads, page_size, head_dim)
 
 
-def _table(block_table, kv_lens):
-    import torch
-    _tensor("block_table", block_table, torch.int32, 2)
-    _tensor("kv_lens", kv_lens, torch.int32, 1)
-    if block_table.shape[0] != kv_lens.shape[0]:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows, kv_lens {kv_lens.shape[0]}")
-    _one_device(block_table, kv_lens)
+def _table(block_table, kv_lens, device):
+    """(table's address, lengths' address, rows, width)"""
+    table, lens = _ints("block_table", block_table, 2, device), _ints("kv_lens", kv_lens, 1, device)
+    rows, width = block_table.shape
+    if kv_lens.shape[0] != rows:
+        raise ValueError(f"block_table has {rows} rows, kv_lens {kv_lens.shape[0]}")
+    return table, lens, rows, width
 
 
 def _batch(block_table, kv_lens, q_starts, n_tokens, device):
-    import torch
-    _table(block_table, kv_lens)
-    _tensor("q_starts", q_starts, torch.int32, 1)
-    n = kv_lens.shape[0]
+    """(the batch as the C struct's bytes, sequences)"""
+    table, lens, n, width = _table(block_table, kv_lens, device)
+    starts = _ints("q_starts", q_starts, 1, device)
     if q_starts.shape[0] != n + 1:
         raise ValueError(f"q_starts must be [n_seqs + 1] = [{n + 1}], got {list(q_starts.shape)}")
-    if block_table.device != device or q_starts.device != device:
-        raise ValueError("block_table, kv_lens and q_starts must be on the cache's device")
-    return _Batch(block_table.data_ptr(), kv_lens.data_ptr(), q_starts.data_ptr(), n, block_table.shape[1], n_tokens)
+    return _BATCH.pack(table, lens, starts, n, width, n_tokens), n
 
 
 def _rows(name, t, heads, head_dim, device):
     """Row stride of a [tokens, heads, head_dim] tensor whose rows are dense."""
-    _tensor(name, t, dim=3, contiguous=False)
-    if t.shape[1] != heads or t.shape[2] != head_dim:
+    import torch
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dim() != 3:
+        if _device_of(name, t) != device:
+            raise ValueError(f"{name} must be on the cache's device")
+        raise ValueError(f"{name} must be 3-D, got {list(t.shape)}")
+    n, h, d = t.shape
+    if h != heads or d != head_dim:
         raise ValueError(f"{name} must be [n_tokens, {heads}, {head_dim}], got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on the cache's device")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != head_dim):
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * head_dim)
+    return row if n > 1 else max(row, heads * head_dim)
+
+
+def _act(t):
+    import torch
+    return W4A16_BF16 if t.dtype is torch.bfloat16 else W4A16_F16 if t.dtype is torch.float16 else _dtype_code(t)
+
+
+def _output(name, t, shape, dtype, device):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and t.dim() == len(shape)):
+        _refuse(name, t, dtype, len(shape), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
 
 
 def _scratch(workspace, need, device, stream):
+    """(workspace tensor, its address, its bytes): the caller's, or one from torch's allocator."""
     import torch
     if workspace is None:
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
             workspace.record_stream(stream)
-    else:
-        _tensor("workspace", workspace)
-        if workspace.device != device:
-            raise ValueError("workspace must be on the cache's device")
-    return workspace, workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), need
+    if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == device and workspace.is_contiguous()):
+        _refuse("workspace", workspace, None, None, device)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream(stream, device):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def w4a16_kv_append(cache, k_new, v_new, block_table, kv_lens, q_starts, stream=None):
     """Quantise k_new, v_new [n_tokens, n_kv_heads, head_dim] (fp16/bf16, rows
     may be strided views) into the cache as each sequence's newest tokens:
     positions kv_lens[b] - (q_starts[b+1] - q_starts[b]) .. kv_lens[b] - 1."""
-    c = _cache(cache)
-    dev = cache.k.device
-    sk = _rows("k_new", k_new, c.n_kv_heads, c.head_dim, dev)
-    sv = _rows("v_new", v_new, c.n_kv_heads, c.head_dim, dev)
-    if v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
+    c, dev, _, heads, _, dim = _cache(cache)
+    sk, sv = _rows("k_new", k_new, heads, dim, dev), _rows("v_new", v_new, heads, dim, dev)
+    if v_new.dtype is not k_new.dtype or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must have the same dtype and shape")
-    dt = _dtype_code(k_new)
-    b = _batch(block_table, kv_lens, q_starts, k_new.shape[0], dev)
+    b, _ = _batch(block_table, kv_lens, q_starts, k_new.shape[0], dev)
     _check("w4a16_kv_append", load_library().w4a16_kv_append(
-        ctypes.byref(c), _p(k_new), sk, _p(v_new), sv, ctypes.byref(b), dt, _stream_ptr(stream)))
+        c, k_new.data_ptr(), sk, v_new.data_ptr(), sv, b, _act(k_new), _stream(stream, dev)))
 
 
 def w4a16_kv_read(cache, block_table, kv_lens, q_starts, n_tokens: int, dtype, k_out=None, v_out=None, stream=None):
     """The newest q_starts[b+1] - q_starts[b] cached tokens of each sequence as
     values of `dtype`: (k, v), each [n_tokens, n_kv_heads, head_dim]."""
-    import torch
-    c = _cache(cache)
-    dev = cache.k.device
-    shape = (n_tokens, c.n_kv_heads, c.head_dim)
-    outs = []
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _tensor(name, t, dtype, 3)
-            if tuple(t.shape) != shape or t.device != dev:
-                raise ValueError(f"{name} must be {list(shape)} on the cache's device")
-        outs.append(t)
-    b = _batch(block_table, kv_lens, q_starts, n_tokens, dev)
+    c, dev, _, heads, _, dim = _cache(cache)
+    k_out = _output("k_out", k_out, (n_tokens, heads, dim), dtype, dev)
+    v_out = _output("v_out", v_out, (n_tokens, heads, dim), dtype, dev)
+    b, _ = _batch(block_table, kv_lens, q_starts, n_tokens, dev)
     _check("w4a16_kv_read", load_library().w4a16_kv_read(
-        ctypes.byref(c), ctypes.byref(b), _p(outs[0]), _p(outs[1]), _dtype_code(outs[0]), _stream_ptr(stream)))
-    return outs[0], outs[1]
+        c, b, k_out.data_ptr(), v_out.data_ptr(), _act(k_out), _stream(stream, dev)))
+    return k_out, v_out
 
 
 def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int, scale=None, window: int = 0,
@@ -180,32 +200,26 @@ def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int,
     n_heads, head_dim].  scale defaults to head_dim ** -0.5; lse, if given, is
     float32 [n_tokens, n_heads] and receives the log-sum-exp of each row."""
     import torch
-    c = _cache(cache)
-    dev = cache.k.device
-    _tensor("q", q, dim=3, contiguous=False)
-    T, H = q.shape[0], q.shape[1]
-    sq = _rows("q", q, H, c.head_dim, dev)
-    dt = _dtype_code(q)
-    if out is None:
-        out = torch.empty((T, H, c.head_dim), dtype=q.dtype, device=dev)
-    else:
-        _tensor("out", out, q.dtype, 3)
-        if out.shape != q.shape or out.device != dev:
-            raise ValueError(f"out must be {list(q.shape)} on the cache's device")
+    c, dev, _, kv_heads, _, dim = _cache(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _refuse("q", q, None, 3, dev)
+    T, H, _ = q.shape
+    sq, dt = _rows("q", q, H, dim, dev), _act(q)
+    out = _output("out", out, (T, H, dim), q.dtype, dev)
     if lse is not None:
-        _tensor("lse", lse, torch.float32, 2)
-        if lse.shape[0] != T or lse.shape[1] != H or lse.device != dev:
-            raise ValueError(f"lse must be [{T}, {H}] on the cache's device")
-    b = _batch(block_table, kv_lens, q_starts, T, dev)
-    lib = load_library()
-    need = ctypes.c_longlong(0)
-    _check("w4a16_kv_attention_workspace", lib.w4a16_kv_attention_workspace(
-        H, c.n_kv_heads, c.head_dim, b.n_seqs, T, ctypes.byref(need)))
-    ws, size = _scratch(workspace, need.value, dev, stream)
-    _check("w4a16_kv_attention", lib.w4a16_kv_attention(
-        _p(q), sq, H, ctypes.byref(c), ctypes.byref(b), max_q_len, c.head_dim ** -0.5 if scale is None else scale,
-        window, sinks, _p(out), _p(lse), dt, _p(ws), size, _stream_ptr(stream)))
+        _output("lse", lse, (T, H), torch.float32, dev)
+    b, n = _batch(block_table, kv_lens, q_starts, T, dev)
+    ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, stream)
+    _check("w4a16_kv_attention", load_library().w4a16_kv_attention(
+        q.data_ptr(), sq, H, c, b, max_q_len, dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), dt, at, size, _stream(stream, dev)))
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_workspace(device, n_heads, n_kv_heads, head_dim, n_seqs, n_tokens):
+    # a function of the device's size and these numbers alone
+    return max(16, w4a16_kv_attention_workspace(n_heads, n_kv_heads, head_dim, n_seqs, n_tokens))
 
 
 def w4a16_kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, n_seqs: int, n_tokens: int) -> int:
@@ -216,33 +230,23 @@ def w4a16_kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, n
     return need.value
 
 
-def _ids(name, t, device):
-    import torch
-    _tensor(name, t, torch.int32, 1)
-    if t.device != device:
-        raise ValueError(f"{name} must be on the cache's device")
-    return t.shape[0]
-
-
-def _refcount(refcount, device, n_pages=None):
-    import torch
-    _tensor("refcount", refcount, torch.int32, 1)
-    if refcount.device != device:
-        raise ValueError("refcount must be on the cache's device")
+def _counts(refcount, device, n_pages=None):
+    at = _ints("refcount", refcount, 1, device)
     if n_pages is not None and refcount.shape[0] != n_pages:
         raise ValueError(f"refcount must be [n_pages] = [{n_pages}], got {list(refcount.shape)}")
+    return at
 
 
 def w4a16_kv_copy_pages(cache, src, dst, stream=None):
     """Pages src[i] (codes and scales) copied to pages dst[i]; pairs with a negative id are skipped."""
-    c = _cache(cache)
-    n = _ids("src", src, cache.k.device)
-    if _ids("dst", dst, cache.k.device) != n:
+    c, dev = _cache(cache)[:2]
+    a, b = _ints("src", src, 1, dev), _ints("dst", dst, 1, dev)
+    if src.shape[0] != dst.shape[0]:
         raise ValueError("src and dst must have the same length")
-    _check("w4a16_kv_copy_pages", load_library().w4a16_kv_copy_pages(
-        ctypes.byref(c), _p(src), _p(dst), n, _stream_ptr(stream)))
+    _check("w4a16_kv_copy_pages", load_library().w4a16_kv_copy_pages(c, a, b, src.shape[0], _stream(stream, dev)))
 
 
+@functools.lru_cache(maxsize=64)
 def w4a16_kv_pool_workspace(n_pages: int) -> int:
     """Bytes of workspace that w4a16_kv_fork and w4a16_kv_compact need."""
     need = ctypes.c_longlong(0)
@@ -253,53 +257,45 @@ def w4a16_kv_pool_workspace(n_pages: int) -> int:
 def w4a16_kv_fork(cache, block_table, kv_lens, refcount, parents, children, workspace=None, stream=None):
     """Rows children[i] of the table continue rows parents[i]: full pages are
     shared, a partly filled last page is copied into the lowest free page."""
-    c = _cache(cache)
-    dev = cache.k.device
-    _table(block_table, kv_lens)
-    _one_device(cache.k, block_table)
-    _refcount(refcount, dev, c.n_pages)
-    n = _ids("parents", parents, dev)
-    if _ids("children", children, dev) != n:
+    c, dev, pages = _cache(cache)[:3]
+    table, lens, rows, width = _table(block_table, kv_lens, dev)
+    counts = _counts(refcount, dev, pages)
+    a, b = _ints("parents", parents, 1, dev), _ints("children", children, 1, dev)
+    if parents.shape[0] != children.shape[0]:
         raise ValueError("parents and children must have the same length")
-    ws, size = _scratch(workspace, w4a16_kv_pool_workspace(c.n_pages), dev, stream)
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream)
     _check("w4a16_kv_fork", load_library().w4a16_kv_fork(
-        ctypes.byref(c), _p(block_table), _p(kv_lens), block_table.shape[0], block_table.shape[1], _p(refcount),
-        _p(parents), _p(children), n, _p(ws), size, _stream_ptr(stream)))
+        c, table, lens, rows, width, counts, a, b, parents.shape[0], at, size, _stream(stream, dev)))
 
 
 def w4a16_kv_free(block_table, kv_lens, refcount, seqs, stream=None):
     """Rows seqs[i] give up their pages: counts go down, entries become -1, lengths 0."""
-    _table(block_table, kv_lens)
-    _refcount(refcount, block_table.device)
-    n = _ids("seqs", seqs, block_table.device)
+    dev = _device_of("block_table", block_table)
+    table, lens, rows, width = _table(block_table, kv_lens, dev)
+    counts, ids = _counts(refcount, dev), _ints("seqs", seqs, 1, dev)
     _check("w4a16_kv_free", load_library().w4a16_kv_free(
-        _p(block_table), _p(kv_lens), block_table.shape[0], block_table.shape[1], _p(refcount), refcount.shape[0],
-        _p(seqs), n, _stream_ptr(stream)))
+        table, lens, rows, width, counts, refcount.shape[0], ids, seqs.shape[0], _stream(stream, dev)))
 
 
 def w4a16_kv_trim(block_table, kv_lens, refcount, page_size: int, window: int, sinks: int = 0, stream=None):
     """Every row gives up the pages that no later token sees with this window and these sinks."""
-    _table(block_table, kv_lens)
-    _refcount(refcount, block_table.device)
+    dev = _device_of("block_table", block_table)
+    table, lens, rows, width = _table(block_table, kv_lens, dev)
+    counts = _counts(refcount, dev)
     _check("w4a16_kv_trim", load_library().w4a16_kv_trim(
-        _p(block_table), _p(kv_lens), block_table.shape[0], block_table.shape[1], _p(refcount), refcount.shape[0],
-        page_size, window, sinks, _stream_ptr(stream)))
+        table, lens, rows, width, counts, refcount.shape[0], page_size, window, sinks, _stream(stream, dev)))
 
 
 def w4a16_kv_compact(cache, block_table, refcount, n_live=None, workspace=None, stream=None):
     """The m pages in use move to pages 0..m-1; table entries and counts
     follow.  n_live, if given, is an int32 [1] tensor that receives m."""
-    import torch
-    c = _cache(cache)
-    dev = cache.k.device
-    _tensor("block_table", block_table, torch.int32, 2)
-    _one_device(cache.k, block_table)
-    _refcount(refcount, dev, c.n_pages)
-    if n_live is not None:
-        _tensor("n_live", n_live, torch.int32, 1)
-        if n_live.shape[0] != 1 or n_live.device != dev:
-            raise ValueError("n_live must be [1] on the cache's device")
-    ws, size = _scratch(workspace, w4a16_kv_pool_workspace(c.n_pages), dev, stream)
+    c, dev, pages = _cache(cache)[:3]
+    table = _ints("block_table", block_table, 2, dev)
+    rows, width = block_table.shape
+    counts = _counts(refcount, dev, pages)
+    live = None if n_live is None else _ints("n_live", n_live, 1, dev)
+    if n_live is not None and n_live.shape[0] != 1:
+        raise ValueError(f"n_live must be [1], got {list(n_live.shape)}")
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream)
     _check("w4a16_kv_compact", load_library().w4a16_kv_compact(
-        ctypes.byref(c), _p(block_table), block_table.shape[0], block_table.shape[1], _p(refcount), _p(n_live),
-        _p(ws), size, _stream_ptr(stream)))
+        c, table, rows, width, counts, live, at, size, _stream(stream, dev)))
