@@ -878,8 +878,12 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     if (e == cudaSuccess && !merged) e = encode_codes(dev, c, c.v, 0, keys, token_first, &v);
     if (e != cudaSuccess) return e;
     if (merged) v = k;
-    // sequences with more rows than a tile of this kernel holds go to the tensor-core kernel
+    // Sequences with more rows than a tile of this kernel holds go to the tensor-core kernel.  When every
+    // sequence brings max_q_len tokens all of them do, and this kernel, which would find nothing to do (about
+    // 4 us), is left out; should max_q_len not be the longest, that kernel has them all the same.
     const bool many = (long long)a.max_q_len * group > kMostRows;
+    if (many && (long long)a.max_q_len * batch.n_seqs == batch.n_tokens)
+        return launch_kv_attention_many(a, c, batch, 0, dev, s, pdl);
     static std::atomic<unsigned long long> launches{0x5ca1ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;

@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kMaxPairs = 1536;           // (sequence, row tile) pairs of a launch
+constexpr int kMaxPairs = 1408;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
 constexpr int kCost = 3;                  // steps that a tile's start and end count for in the shares
 constexpr int kSoftWarps = 8, kConvWarps = 4;
@@ -84,9 +84,10 @@ struct ManySmem {
     static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
     static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
     static constexpr int kScale = kPairSeq + kMaxPairs * 2;       // [4][8] float4 {ks, log2 vs, 1 / vs, -}
-    static constexpr int kPlan = kScale + 4 * 8 * 16;
+    static constexpr int kExchange = kScale + 4 * 8 * 16;         // (M, l) of the second half's rows
+    static constexpr int kPlan = kExchange + kHalfRows * 8;
     static constexpr int kBars = kPlan + kRing * (int)sizeof(PlannedTile);
-    static constexpr int kMisc = kBars + (18 + 2 * kRing) * 8;
+    static constexpr int kMisc = kBars + (22 + 2 * kRing) * 8;
     static constexpr int kEnd = kMisc + 256 + 1024;               // 1024: slack to align the base
 };
 
@@ -287,6 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     const uint32_t drain = bars + 8u * 16;
     auto plan_full = [&](int i) { return bars + 8u * (18 + i); };
     auto plan_empty = [&](int i) { return bars + 8u * (18 + kRing + i); };
+    const uint32_t part_told = bars + 8u * (18 + 2 * kRing), part_read = part_told + 8u;
+    auto meet_bar = [&](int i) { return part_told + 8u * (2 + i); };
     PlannedTile *plan = reinterpret_cast<PlannedTile *>(smem + L::kPlan);
 
     if (tid == 0) {
@@ -301,6 +304,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             mbar_init(v_empty(i), 1);
         }
         mbar_init(drain, 1);
+        mbar_init(part_told, kHalfRows);
+        mbar_init(part_read, kHalfRows);
+        mbar_init(meet_bar(0), kHalfRows);
+        mbar_init(meet_bar(1), kTileRows);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(plan_full(i), 1);
             mbar_init(plan_empty(i), kSoftWarps + kConvWarps + 1);
@@ -444,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         __syncwarp();
         if (lane == 0) mbar_arrive(plan_empty(idx % kRing));
     };
+    // A tile of up to 128 rows has both halves work on the same rows, each on every other step.
+    auto same_rows = [](const ManyTile &t) { return t.rows <= kHalfRows; };
+    auto half_runs = [&](const PlannedTile &t, int half) { return same_rows(t.t) ? t.s1 - t.s0 > half : true; };
     auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
 
     if (warp < kSoftWarps) {
@@ -451,9 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         const int half = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
-        int s_phase = 0, o_phase = 0;
-        auto place = [&](const ManyTile &t, long long &at) {
-            const int row = half * kHalfRows + r;
+        int s_phase = 0, o_phase = 0, other_phase = 0, join_phase = 0, meet_phase[2] = {0, 0};
+        float2 *exchange = reinterpret_cast<float2 *>(smem + L::kExchange);
+        auto place = [&](const ManyTile &t, int base_row, long long &at) {
+            const int row = base_row + r;
             if (row >= t.rows) return false;
             const int x = t.row0 + row, tok = x / group;
             at = (long long)(t.q0 + tok) * p.a.n_heads + t.head * group + x - tok * group;
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         // whole rows; a row's D / 8 lanes find its largest value.
         auto load_q = [&](const ManyTile &t) {
             constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
-            const int row = half * kHalfRows + r, x = t.row0 + row, tok = x / group;
+            const int row = (same_rows(t) ? 0 : half * kHalfRows) + r, x = t.row0 + row, tok = x / group;
             const long long mine = row < t.rows ? (long long)(t.q0 + tok) * p.a.q_stride +
                                                       (long long)(t.head * group + x - tok * group) * D
                                                 : -1;
@@ -523,24 +534,25 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         int counter = 0;                                           // steps so far: the scales' ring position
         bool ok = true;
         const PlannedTile *next = open_tile(0);
-        if (next && half * kHalfRows < next->t.rows) load_q(next->t);
+        if (next && half_runs(*next, half)) load_q(next->t);
         for (int idx = 0; next && ok; ++idx) {
             const ManyTile &t = next->t;                           // in shared memory
             const int s0 = next->s0, s1 = next->s1;
-            const bool runs = half * kHalfRows < t.rows;           // a tile of up to 128 rows is the first half's alone
+            const bool runs = half_runs(*next, half), twice = same_rows(t);
+            const int base_row = twice ? 0 : half * kHalfRows;
             const float my_fac = fac;
             const int sink_blocks = t.sink, block0 = t.block0 - t.sink;
             const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
-            const int x = t.row0 + half * kHalfRows + r;
-            const bool exists = half * kHalfRows + r < t.rows;
+            const int x = t.row0 + base_row + r;
+            const bool exists = base_row + r < t.rows;
             const int pos = exists ? t.first + x / group : -1;
-            const int min_pos = t.first + (t.row0 + half * kHalfRows) / group;
-            const int max_pos = t.first + (min(t.row0 + half * kHalfRows + kHalfRows, t.row0 + t.rows) - 1) / group;
+            const int min_pos = t.first + (t.row0 + base_row) / group;
+            const int max_pos = t.first + (t.row0 + min(base_row + kHalfRows, t.rows) - 1) / group;
             float ref = kRefStart, sum = 0.0f;
-            for (int st = s0; st < s1 && ok; ++st, ++counter) {
-                if (!runs) continue;
+            const int first_st = twice ? s0 + half : s0;
+            for (int st = first_st; st < s1 && runs; st += twice ? 2 : 1) {
                 const int pos0 = (st < sink_blocks ? st : block0 + st) * kKeys;
-                const float4 *sc = scales + (counter & 3) * 8;
+                const float4 *sc = scales + (counter + st - s0 & 3) * 8;
                 if (!mbar_wait_bounded(s_full(half), s_phase, p.status, abort_flag)) {
                     ok = false;
                     break;
@@ -595,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     const float f = ex2(ref - to);
                     ref = to;
                     sum *= f;
-                    if (st > s0) {
+                    if (st > first_st) {
                         // out of the steps before is complete: this step's S was issued after it
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
@@ -654,28 +666,68 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 mbar_arrive(p_ready(half));
             }
             if (!ok) break;
+            counter += s1 - s0;
             // the next tile's rows while the last product runs
             next = open_tile(idx + 1);
-            if (next && half * kHalfRows < next->t.rows) load_q(next->t);
+            if (next && half_runs(*next, half)) load_q(next->t);
             if (!runs) {
+                close_tile(idx);
+                continue;
+            }
+            const bool joins = twice && s1 - s0 > 1;               // both halves have a part of these rows
+            if (joins && half == 1) {
+                // a row's two parts are in the same TMEM lane: the first half reads them both
+                exchange[r] = make_float2(ref, sum);
+                mbar_arrive(part_told);
+                if (!mbar_wait_bounded(part_read, join_phase, p.status, abort_flag)) break;
+                join_phase ^= 1;
+                o_phase ^= 1;
                 close_tile(idx);
                 continue;
             }
             if (!mbar_wait_bounded(o_full(half), o_phase, p.status, abort_flag)) break;
             o_phase ^= 1;
+            float f_here = 1.0f, f_there = 0.0f;
+            if (half == 0) {
+                // the other half's phases, so that its part can be waited for
+                if (joins) {
+                    if (!mbar_wait_bounded(o_full(1), other_phase, p.status, abort_flag)) break;
+                    if (!mbar_wait_bounded(part_told, join_phase, p.status, abort_flag)) break;
+                    join_phase ^= 1;
+                    const float2 z = exchange[r];
+                    const float m = fmaxf(ref, z.x);
+                    f_here = ex2(ref - m), f_there = ex2(z.x - m);
+                    sum = sum * f_here + z.y * f_there;
+                    ref = m;
+                }
+                if (joins || (!twice && t.rows > kHalfRows)) other_phase ^= 1;
+            }
             tc_fence_after();
+            // 32 of the row's dims, of both parts
+            auto read_out = [&](int c, float (&f)[32]) {
+                uint32_t v[32];
+                tmem_ld32(t_o + c, v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(v[k]);
+                if (joins) {
+                    tmem_ld32(t_o + D + c, v);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(v[k]), f_there, f[k] * f_here);
+                }
+            };
             long long at = 0;
-            const bool has = place(t, at);
+            const bool has = place(t, base_row, at);
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(t_o + c, v);
                     float f[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(v[k]);
+                    read_out(c, f);
                     if (has) store(at, c, f, inv);
+                }
+                if (joins) {
+                    tc_fence_before();
+                    mbar_arrive(part_read);
                 }
                 if (has && p.a.lse)
                     p.a.lse[at] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
@@ -684,24 +736,34 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 // the others; the last of them to come adds them up
                 constexpr int kPartVecs = (D / 4 + 1) * kTileRows;
                 auto slot = [&](int c, bool first) { return reinterpret_cast<float4 *>(p.parts) + ((long long)c * 2 + first) * kPartVecs; };
-                const int row = half * kHalfRows + r;
+                const int row = base_row + r;
                 float4 *dst = slot(blockIdx.x, opens);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(t_o + c, v);
+                    float f[32];
+                    read_out(c, f);
                     if (has)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            __stcg(dst + (c + k) / 4 * kTileRows + row,
-                                   make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]),
-                                               __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])));
+                            __stcg(dst + (c + k) / 4 * kTileRows + row, make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]));
+                }
+                if (joins) {
+                    tc_fence_before();
+                    mbar_arrive(part_read);
                 }
                 if (has) __stcg(dst + D / 4 * kTileRows + row, make_float4(ref, sum, 0.0f, 0.0f));
-                const int threads = t.rows > kHalfRows ? 2 * kHalfRows : kHalfRows;
                 const int from = (int)(((t.begin + kCost + 1) * ctas + total - 1) / total - 1);
                 const int to = (int)(((t.begin + kCost + t.steps) * ctas + total - 1) / total - 1);
-                named_barrier_sync(threads == 256 ? 1 : 2, threads);
+                // the tile's threads: of the first half, or of both
+                auto meet = [&]() {
+                    const uint32_t bar = meet_bar(twice ? 0 : 1);
+                    int &phase = meet_phase[twice ? 0 : 1];
+                    mbar_arrive(bar);
+                    const bool met = mbar_wait_bounded(bar, phase, p.status, abort_flag);
+                    phase ^= 1;
+                    return met;
+                };
+                if (!meet()) break;
                 if (tid == 0) {
                     __threadfence();
                     unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
@@ -714,9 +776,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     __threadfence();
                     misc[2] = put == 0;
                 }
-                named_barrier_sync(threads == 256 ? 1 : 2, threads);
+                if (!meet()) break;
                 const bool last = *reinterpret_cast<volatile int *>(misc + 2);
-                named_barrier_sync(threads == 256 ? 1 : 2, threads);      // misc[2] is read before it is written again
+                if (!meet()) break;                                // misc[2] is read before it is written again
                 if (last && has) {
                     float m = kRefStart, l = 0.0f;
                     for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(slot(c, c == from) + D / 4 * kTileRows + row).x);
@@ -776,14 +838,29 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     page[g] = -2;
                 }
         };
-        auto load = [&](const uint8_t *base, const ManyTile &t, int st, uint4 (&raw)[LOADS]) {
+        // where the warp's two groups begin in K, and the lane's 16 bytes within a group
+        const long long to_v = p.c.v - p.c.k;
+        const uint8_t *group_at[2];
+        const long long row_step = ROWS * p.c.token_stride;
+        const long long lane_at = row_in * p.c.token_stride + piece * 16;
+        int rows_there[2];                                         // keys of each group that the cache holds
+        auto locate = [&](const ManyTile &t, int st) {
             const int pos0 = block_of(t, st) * kKeys + w * 32;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int row = row_in + ROWS * i, pos = pos0 + row, g = row >> 4;
-                const uint8_t *src = base + (long long)page[g] * p.c.page_stride + t.head * p.c.head_stride +
-                                     (pos & ((1 << p.c.page_shift) - 1)) * p.c.token_stride + piece * 16;
-                raw[i] = page[g] >= 0 && pos < t.len ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
+            for (int g = 0; g < 2; ++g) {
+                const int at = pos0 + 16 * g;
+                rows_there[g] = page[g] >= 0 ? t.len - at : 0;
+                group_at[g] = p.c.k + (long long)page[g] * p.c.page_stride + t.head * p.c.head_stride +
+                              (at & ((1 << p.c.page_shift) - 1)) * p.c.token_stride + lane_at;
+            }
+        };
+        auto load = [&](long long to, uint4 (&raw)[LOADS]) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const uint8_t *src = group_at[g] + to;
+#pragma unroll
+                for (int i = 0; i < LOADS / 2; ++i, src += row_step)
+                    raw[g * (LOADS / 2) + i] = row_in + ROWS * i < rows_there[g] ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
             }
         };
         auto convert = [&](const uint4 (&raw)[LOADS], uint8_t *tile) {
@@ -824,9 +901,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         if (more) {
             pages_of(t, st);
             check();
-            load(p.c.k, t, st, kraw);
+            locate(t, st);
+            load(0, kraw);
             load_scales(t);
-            load(p.c.v, t, st, vraw);
+            load(to_v, vraw);
         }
         for (int counter = 0; more; ++counter) {
             const int stg = counter & 1, ph = (counter >> 1) & 1;
@@ -843,7 +921,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             if (lane == 0) mbar_arrive(k_full(stg));
             if (more) {
                 check();
-                load(p.c.k, t, st, kraw);
+                locate(t, st);
+                load(0, kraw);
                 load_scales(t);
             }
             if (!mbar_wait_bounded(v_empty(stg), ph ^ 1, p.status, abort_flag)) break;
@@ -851,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full(stg));
-            if (more) load(p.c.v, t, st, vraw);
+            if (more) load(to_v, vraw);
         }
     }
     if (warp == kSoftWarps + kConvWarps) {
@@ -872,13 +951,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                        idesc_o, fresh ? 0u : 1u);
         };
         auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
-        auto run_tile = [&](int rows, int s0, int s1) {
-            const int halves = rows > kHalfRows ? 2 : 1;
-            for (int st = s0; st < s1; ++st, ++counter) {
+        // MMAs run in the order they are issued: P is read before the next S of its half replaces it.
+        auto run_tile = [&](int steps) {                           // two halves of rows, a step together
+            for (int st = 0; st < steps; ++st, ++counter) {
                 const int stg = counter & 1, ph = (counter >> 1) & 1;
-                if (st == s0) {
+                if (st == 0) {
                     if (!wait(k_full(stg), ph)) return false;
-                    for (int h = 0; h < halves; ++h) {
+                    for (int h = 0; h < 2; ++h) {
                         if (!wait(q_full(h), q_phase[h])) return false;
                         q_phase[h] ^= 1;
                         tc_fence_after();
@@ -887,23 +966,50 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     commit_elected(k_empty(stg));
                 }
                 const int nstg = (counter + 1) & 1, nph = ((counter + 1) >> 1) & 1;
-                for (int h = 0; h < halves; ++h) {
+                for (int h = 0; h < 2; ++h) {
                     if (!wait(p_ready(h), p_phase[h])) return false;
                     p_phase[h] ^= 1;
                     if (h == 0 && !wait(v_full(stg), ph)) return false;
                     tc_fence_after();
-                    output(h, stg, st == s0);
-                    if (st + 1 == s1) commit_elected(o_full(h));
-                    if (h + 1 == halves) commit_elected(v_empty(stg));
-                    if (st + 1 < s1) {
-                        // MMAs run in the order they are issued: P is read before the next S replaces it
+                    output(h, stg, st == 0);
+                    if (st + 1 == steps) commit_elected(o_full(h));
+                    if (h == 1) commit_elected(v_empty(stg));
+                    if (st + 1 < steps) {
                         if (h == 0 && !wait(k_full(nstg), nph)) return false;
                         tc_fence_after();
                         scores(h, nstg);
-                        if (h + 1 == halves) commit_elected(k_empty(nstg));
+                        if (h == 1) commit_elected(k_empty(nstg));
                     }
                 }
             }
+            return true;
+        };
+        auto run_same_rows = [&](int steps) {                      // the same rows twice, a half every other step
+            for (int st = -2; st < steps; ++st) {
+                const int h = st & 1;
+                if (st >= 0) {
+                    const int c = counter + st, stg = c & 1, ph = (c >> 1) & 1;
+                    if (!wait(p_ready(h), p_phase[h])) return false;
+                    p_phase[h] ^= 1;
+                    if (!wait(v_full(stg), ph)) return false;
+                    tc_fence_after();
+                    output(h, stg, st < 2);
+                    if (st + 2 >= steps) commit_elected(o_full(h));
+                    commit_elected(v_empty(stg));
+                }
+                if (st + 2 < steps) {
+                    const int c = counter + st + 2, stg = c & 1, ph = (c >> 1) & 1;
+                    if (st < 0) {
+                        if (!wait(q_full(h), q_phase[h])) return false;
+                        q_phase[h] ^= 1;
+                    }
+                    if (!wait(k_full(stg), ph)) return false;
+                    tc_fence_after();
+                    scores(h, stg);
+                    commit_elected(k_empty(stg));
+                }
+            }
+            counter += steps;
             return true;
         };
         for (int idx = 0;; ++idx) {
@@ -911,9 +1017,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             if (!next) break;
             // the same in every lane, and known to be
             const int rows = __reduce_max_sync(0xffffffffu, next->t.rows);
-            const int s0 = __reduce_max_sync(0xffffffffu, next->s0), s1 = __reduce_max_sync(0xffffffffu, next->s1);
+            const int steps = __reduce_max_sync(0xffffffffu, next->s1 - next->s0);
             close_tile(idx);
-            if (!run_tile(rows, s0, s1)) {
+            if (!(rows > kHalfRows ? run_tile(steps) : run_same_rows(steps))) {
                 // leave with no product in flight
                 commit_elected(drain);
                 for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
