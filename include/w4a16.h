@@ -479,7 +479,9 @@ int w4a16_kv_read(const w4a16_kv_cache_t *cache, const w4a16_kv_batch_t *batch, 
  * token at position i sees key j when
  *     j <= i  and  (window == 0  or  i - j < window  or  j < sinks)
  * and out[t, a] = sum_j softmax_j(scale * q . k_j) v_j, [n_tokens, n_heads,
- * head_dim] contiguous, rounded once into dtype from fp32.  lse (optional):
+ * head_dim] contiguous, rounded once into dtype from fp32 (each weight meets
+ * its value as fp16: good to 2^-11, and 0 below 2^-39 of the row's largest,
+ * value scale included).  lse (optional):
  * [n_tokens, n_heads] fp32, log sum_j exp(scale * q . k_j).  A token that
  * sees no key gets zeros and -inf.  Pages that no token of a sequence sees
  * are never read, so their table entries may be -1 (w4a16_kv_trim).

@@ -27,6 +27,8 @@
 // The work is cut as in kv_attention.cu: a line of all tiles' steps, each
 // causal tile with just the steps that its rows see, in equal shares; CTAs
 // that share a tile add their parts up through the workspace, in order.
+#include <cuda.h>
+
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -38,11 +40,11 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kMaxPairs = 1408;           // (sequence, row tile) pairs of a launch
+constexpr int kMaxPairs = 1280;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
 constexpr int kCost = 3;                  // steps that a tile's start and end count for in the shares
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 2);
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 2);   // and the MMA issuer, the planner
 constexpr int kRing = 4;                  // tiles that the planner is ahead of the slowest role
 constexpr float kRefStart = -3.402823466e38f, kTop = 15.9f, kHead = 14.0f;
 
@@ -51,8 +53,9 @@ struct ManyParams {
     KvCache c;
     KvBatch b;
     int row_limit;                        // sequences with up to so many rows a kv head are another kernel's
+    int half_rows;                        // rows of a half in use: whole tokens, at most 128
     int pair_first;                       // this launch's pairs: [pair_first, pair_first + kMaxPairs)
-    float *parts;                         // [grid][2][D / 4 + 1][256] float4: out by dims, then (M, l)
+    float *parts;                         // [grid][2] parts of a tile
     unsigned long long *tickets;          // [grid]
     unsigned long long tag;
     int *status;
@@ -77,17 +80,18 @@ struct ManySmem {
     static constexpr int kBlockBytes = kKeys * 128;               // 128 rows of 64 fp16
     static constexpr int kBlocks = D / 64;
     static constexpr int kOperand = kBlocks * kBlockBytes;
+    static constexpr int kStages = 2;                             // of K and V
     static constexpr int kQ = 0;                                  // two halves
-    static constexpr int kK = kQ + 2 * kOperand;                  // two stages
-    static constexpr int kV = kK + 2 * kOperand;
-    static constexpr int kPre = kV + 2 * kOperand;                // line position of each pair, of one kv head
+    static constexpr int kK = kQ + 2 * kOperand;
+    static constexpr int kV = kK + kStages * kOperand;
+    static constexpr int kPre = kV + kStages * kOperand;                // line position of each pair, of one kv head
     static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
     static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
     static constexpr int kScale = kPairSeq + kMaxPairs * 2;       // [4][8] float4 {ks, log2 vs, 1 / vs, -}
-    static constexpr int kExchange = kScale + 4 * 8 * 16;         // (M, l) of the second half's rows
+    static constexpr int kExchange = kScale + 4 * 8 * 16;                // (M, l) of the second half's rows
     static constexpr int kPlan = kExchange + kHalfRows * 8;
     static constexpr int kBars = kPlan + kRing * (int)sizeof(PlannedTile);
-    static constexpr int kMisc = kBars + (22 + 2 * kRing) * 8;
+    static constexpr int kMisc = kBars + (24 + 2 * kRing) * 8;
     static constexpr int kEnd = kMisc + 256 + 1024;               // 1024: slack to align the base
 };
 
@@ -241,10 +245,19 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block
     return d;
 }
 
-// Codes of a word as fp16 pairs (0, 1) and (2, 3), exactly (see kv_attention.cu).
-template <int KT>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if (KT == kKvInt8) {
+// Codes of a word as pairs (0, 1) and (2, 3) of fp16 (see kv_attention.cu) or
+// bf16, exactly.  int8 as bf16: 0x4300 with the low seven bits is 128 + those,
+// 0x4300 with the sign bit is 128 or 256; their difference is the code.
+template <int KT, bool BF16>
+__device__ __forceinline__ void codes_to_act(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (KT == kKvInt8 && BF16) {
+        const uint32_t low = w & 0x7f7f7f7fu, sign = w & 0x80808080u;
+        const uint32_t a = __byte_perm(low, 0x43434343u, 0x4140), b = __byte_perm(low, 0x43434343u, 0x4342);
+        const uint32_t c = __byte_perm(sign, 0x43434343u, 0x4140), d = __byte_perm(sign, 0x43434343u, 0x4342);
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&c));
+        const __nv_bfloat162 s = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b), *reinterpret_cast<const __nv_bfloat162 *>(&d));
+        lo = *reinterpret_cast<const uint32_t *>(&r), hi = *reinterpret_cast<const uint32_t *>(&s);
+    } else if constexpr (KT == kKvInt8) {
         w ^= 0x80808080u;
         const uint32_t bias = 0x64806480u;
         const uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
@@ -257,16 +270,41 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &lo, uint32_t
             "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
             : "=r"(lo), "=r"(hi)
             : "r"(w));
+        if constexpr (BF16) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+            lo = pack_bf162(a.x, a.y), hi = pack_bf162(b.x, b.y);
+        }
+    }
+}
+
+// A lane's codes, 16-byte piece `piece` of rows row, row + ROWS, .., into an
+// operand tile: 128-byte rows of 64 elements, 16-byte chunks at c ^ (row % 8).
+template <int KT, int D, bool BF16>
+__device__ __forceinline__ void convert_codes(const uint4 (&raw)[D == 128 ? 8 : 4], uint8_t *tile, int row, int piece) {
+    constexpr int ROWS = D == 128 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < (D == 128 ? 8 : 4); ++i, row += ROWS) {
+        uint32_t h[8];
+        codes_to_act<KT, BF16>(raw[i].x, h[0], h[1]);
+        codes_to_act<KT, BF16>(raw[i].y, h[2], h[3]);
+        codes_to_act<KT, BF16>(raw[i].z, h[4], h[5]);
+        codes_to_act<KT, BF16>(raw[i].w, h[6], h[7]);
+        uint8_t *dst = tile + (piece >> 2) * (kKeys * 128) + row * 128;
+        const int c = 2 * piece & 7;
+        *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
 }
 
 template <int KT, int D>
-__global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams p) {
+__global__ void __launch_bounds__(kThreads, 1) 
+    many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const ManyParams p) {
     using L = ManySmem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int Hk = p.c.n_kv_heads, group = p.a.n_heads / Hk, B = p.b.n_seqs;
+    const int Hk = p.c.n_kv_heads, group = p.a.n_heads / Hk, B = p.b.n_seqs, half_rows = p.half_rows;
     long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
     int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
     uint16_t *pair_seq = reinterpret_cast<uint16_t *>(smem + L::kPairSeq);
@@ -281,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     auto p_ready = [&](int i) { return bars + 8u * (2 + i); };
     auto o_full = [&](int i) { return bars + 8u * (4 + i); };
     auto q_full = [&](int i) { return bars + 8u * (6 + i); };
+    auto q_empty = [&](int i) { return bars + 8u * (22 + 2 * kRing + i); };
     auto k_full = [&](int i) { return bars + 8u * (8 + i); };
     auto k_empty = [&](int i) { return bars + 8u * (10 + i); };
     auto v_full = [&](int i) { return bars + 8u * (12 + i); };
@@ -293,11 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     PlannedTile *plan = reinterpret_cast<PlannedTile *>(smem + L::kPlan);
 
     if (tid == 0) {
+        tma_prefetch_desc(&tm_q);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full(i), 1);
             mbar_init(p_ready(i), kHalfRows);
             mbar_init(o_full(i), 1);
-            mbar_init(q_full(i), kHalfRows);
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1);
             mbar_init(k_full(i), kConvWarps);
             mbar_init(k_empty(i), 1);
             mbar_init(v_full(i), kConvWarps);
@@ -321,8 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         ManyTile t;
         t.seq = b;
         t.q0 = s.x, t.n = s.y, t.len = s.z, t.first = s.z - s.y;
-        t.row0 = r * kTileRows;
-        t.rows = min(kTileRows, s.y * group - t.row0);
+        t.row0 = r * 2 * half_rows;
+        t.rows = min(2 * half_rows, s.y * group - t.row0);
         const int lo_pos = t.first + t.row0 / group, hi_pos = t.first + (t.row0 + t.rows - 1) / group;
         const int lo = p.a.window > 0 ? max(0, lo_pos + 1 - p.a.window) : 0;
         t.lo = lo, t.hi = hi_pos;
@@ -363,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         if (i < B) {
             const KvSeq q = kv_sequence(p.b, p.c.page_shift, i, p.status);
             const int rows = q.n * group;
-            mine = rows <= p.row_limit ? 0 : (rows + kTileRows - 1) / kTileRows;
+            mine = rows <= p.row_limit ? 0 : (rows + 2 * half_rows - 1) / (2 * half_rows);
             s = make_int4(q.q0, q.n, q.len, 0);
         }
         long long all;
@@ -451,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         __syncwarp();
         if (lane == 0) mbar_arrive(plan_empty(idx % kRing));
     };
-    // A tile of up to 128 rows has both halves work on the same rows, each on every other step.
-    auto same_rows = [](const ManyTile &t) { return t.rows <= kHalfRows; };
+    // A tile of up to a half's rows has both halves work on the same rows, each on every other step.
+    auto same_rows = [&](const ManyTile &t) { return t.rows <= half_rows; };
     auto half_runs = [&](const PlannedTile &t, int half) { return same_rows(t.t) ? t.s1 - t.s0 > half : true; };
     auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
 
@@ -463,63 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * D;
         int s_phase = 0, o_phase = 0, other_phase = 0, join_phase = 0, meet_phase[2] = {0, 0};
         float2 *exchange = reinterpret_cast<float2 *>(smem + L::kExchange);
-        auto place = [&](const ManyTile &t, int base_row, long long &at) {
-            const int row = base_row + r;
-            if (row >= t.rows) return false;
-            const int x = t.row0 + row, tok = x / group;
-            at = (long long)(t.q0 + tok) * p.a.n_heads + t.head * group + x - tok * group;
-            return true;
-        };
-        float fac = 0.0f;
-        // A warp loads its 32 rows together, two (head dim 128) or four rows a load, so that each load covers
-        // whole rows; a row's D / 8 lanes find its largest value.
-        auto load_q = [&](const ManyTile &t) {
-            constexpr int LANES = D / 8, AT_ONCE = 32 / LANES;
-            const int row = (same_rows(t) ? 0 : half * kHalfRows) + r, x = t.row0 + row, tok = x / group;
-            const long long mine = row < t.rows ? (long long)(t.q0 + tok) * p.a.q_stride +
-                                                      (long long)(t.head * group + x - tok * group) * D
-                                                : -1;
-            const uint16_t *q = static_cast<const uint16_t *>(p.a.q);
-            const int sub = lane / LANES, piece = lane % LANES;
-            uint8_t *dst = smem + L::kQ + half * L::kOperand + (piece >> 3) * L::kBlockBytes;
-            constexpr int BATCH = 8;                               // loads on their way together
-            constexpr int ROUNDS = 32 / AT_ONCE;
-#pragma unroll 1
-            for (int i0 = 0; i0 < ROUNDS; i0 += BATCH) {
-                uint4 v[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const long long at = __shfl_sync(0xffffffffu, mine, (i0 + i) * AT_ONCE + sub);
-                    v[i] = at >= 0 ? ldg_nc_v4(q + at + piece * 8) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    float f[8], top = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint16_t h = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-                        f[j] = p.a.dtype == 0 ? kv_act<0>(h) : kv_act<1>(h);
-                        top = fmaxf(top, fabsf(f[j]));
-                    }
-#pragma unroll
-                    for (int d = 1; d < LANES; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    // a power of two puts the row's largest value in [2^14, 2^15); a negative scale's sign goes along
-                    const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-                    const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23 | (p.a.scale < 0.0f ? 0x80000000u : 0u));
-                    const int rr = (warp & 3) * 32 + (i0 + i) * AT_ONCE + sub;
-                    *reinterpret_cast<uint4 *>(dst + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4)) =
-                        make_uint4(pack_half2(f[0] * up, f[1] * up), pack_half2(f[2] * up, f[3] * up),
-                                   pack_half2(f[4] * up, f[5] * up), pack_half2(f[6] * up, f[7] * up));
-                    // to the lane whose row it is
-                    const int back = __shfl_sync(0xffffffffu, ex, (lane % AT_ONCE) * LANES);
-                    if (lane / AT_ONCE == i0 + i)
-                        fac = __uint_as_float((uint32_t)(back - 14 + 127) << 23) * fabsf(p.a.scale) * 1.4426950408889634f;
-                }
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(q_full(half));
-        };
+        const int r_tok = r / group, r_head = r - r_tok * group;   // the row within its half: token and head
+        const float my_fac = fabsf(p.a.scale) * 1.4426950408889634f;
         auto store = [&](long long at, int d0, const float (&v)[32], float inv) {
             uint16_t *dst = static_cast<uint16_t *>(p.a.out) + at * D + d0;
             uint32_t w[16];
@@ -533,21 +519,19 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         };
         int counter = 0;                                           // steps so far: the scales' ring position
         bool ok = true;
-        const PlannedTile *next = open_tile(0);
-        if (next && half_runs(*next, half)) load_q(next->t);
-        for (int idx = 0; next && ok; ++idx) {
+        for (int idx = 0; ok; ++idx) {
+            const PlannedTile *next = open_tile(idx);
+            if (!next) break;
             const ManyTile &t = next->t;                           // in shared memory
             const int s0 = next->s0, s1 = next->s1;
             const bool runs = half_runs(*next, half), twice = same_rows(t);
-            const int base_row = twice ? 0 : half * kHalfRows;
-            const float my_fac = fac;
+            const int base_row = twice ? 0 : half * half_rows;
             const int sink_blocks = t.sink, block0 = t.block0 - t.sink;
             const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
-            const int x = t.row0 + base_row + r;
-            const bool exists = base_row + r < t.rows;
-            const int pos = exists ? t.first + x / group : -1;
-            const int min_pos = t.first + (t.row0 + base_row) / group;
-            const int max_pos = t.first + (t.row0 + min(base_row + kHalfRows, t.rows) - 1) / group;
+            const bool exists = r < half_rows && base_row + r < t.rows;
+            const int tok0 = (t.row0 + base_row) / group;          // the half's first token
+            const int min_pos = t.first + tok0, pos = exists ? min_pos + r_tok : -1;
+            const int max_pos = t.first + (t.row0 + min(base_row + half_rows, t.rows) - 1) / group;
             float ref = kRefStart, sum = 0.0f;
             const int first_st = twice ? s0 + half : s0;
             for (int st = first_st; st < s1 && runs; st += twice ? 2 : 1) {
@@ -667,9 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             }
             if (!ok) break;
             counter += s1 - s0;
-            // the next tile's rows while the last product runs
-            next = open_tile(idx + 1);
-            if (next && half_runs(*next, half)) load_q(next->t);
             if (!runs) {
                 close_tile(idx);
                 continue;
@@ -700,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     sum = sum * f_here + z.y * f_there;
                     ref = m;
                 }
-                if (joins || (!twice && t.rows > kHalfRows)) other_phase ^= 1;
+                if (joins || !twice) other_phase ^= 1;
             }
             tc_fence_after();
             // 32 of the row's dims, of both parts
@@ -715,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     for (int k = 0; k < 32; ++k) f[k] = fmaf(__uint_as_float(v[k]), f_there, f[k] * f_here);
                 }
             };
-            long long at = 0;
-            const bool has = place(t, base_row, at);
+            const bool has = exists;
+            const long long at = (long long)(t.q0 + tok0 + r_tok) * p.a.n_heads + t.head * group + r_head;
             if (whole) {
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll 1
@@ -734,10 +715,11 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             } else {
                 // a tile that CTAs from..to share: each leaves its part, in slot 1 the first of them, in slot 0
                 // the others; the last of them to come adds them up
-                constexpr int kPartVecs = (D / 4 + 1) * kTileRows;
-                auto slot = [&](int c, bool first) { return reinterpret_cast<float4 *>(p.parts) + ((long long)c * 2 + first) * kPartVecs; };
+                // a part: D / 4 planes of a float4 a row, so that a warp's rows are one run, then (M, l) of the rows
+                constexpr int kPart = kTileRows * (D + 2);
+                auto slot = [&](int c, bool first) { return p.parts + ((long long)c * 2 + first) * kPart; };
                 const int row = base_row + r;
-                float4 *dst = slot(blockIdx.x, opens);
+                float *mine = slot(blockIdx.x, opens);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float f[32];
@@ -745,13 +727,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     if (has)
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            __stcg(dst + (c + k) / 4 * kTileRows + row, make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]));
+                            __stcg(reinterpret_cast<float4 *>(mine) + (c + k) / 4 * kTileRows + row,
+                                   make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]));
                 }
                 if (joins) {
                     tc_fence_before();
                     mbar_arrive(part_read);
                 }
-                if (has) __stcg(dst + D / 4 * kTileRows + row, make_float4(ref, sum, 0.0f, 0.0f));
+                if (has) __stcg(reinterpret_cast<float2 *>(mine + kTileRows * D) + row, make_float2(ref, sum));
                 const int from = (int)(((t.begin + kCost + 1) * ctas + total - 1) / total - 1);
                 const int to = (int)(((t.begin + kCost + t.steps) * ctas + total - 1) / total - 1);
                 // the tile's threads: of the first half, or of both
@@ -780,11 +763,16 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 const bool last = *reinterpret_cast<volatile int *>(misc + 2);
                 if (!meet()) break;                                // misc[2] is read before it is written again
                 if (last && has) {
+                    auto ml_of = [&](int c) {
+                        return __ldcg(reinterpret_cast<const float2 *>(slot(c, c == from) + kTileRows * D) + row);
+                    };
                     float m = kRefStart, l = 0.0f;
-                    for (int c = from; c <= to; ++c) m = fmaxf(m, __ldcg(slot(c, c == from) + D / 4 * kTileRows + row).x);
+#pragma unroll 4
                     for (int c = from; c <= to; ++c) {
-                        const float4 z = __ldcg(slot(c, c == from) + D / 4 * kTileRows + row);
-                        l = fmaf(z.y, ex2(z.x - m), l);
+                        const float2 z = ml_of(c);
+                        const float top = fmaxf(m, z.x);
+                        l = fmaf(z.y, ex2(z.x - top), l * ex2(m - top));
+                        m = top;
                     }
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
@@ -792,14 +780,24 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                         float f[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) f[k] = 0.0f;
-                        for (int c = from; c <= to; ++c) {
-                            const float4 *src = slot(c, c == from) + row;
-                            const float w = ex2(__ldcg(src + D / 4 * kTileRows).x - m);
+#pragma unroll 1
+                        for (int c = from; c <= to; c += 2) {      // two parts on their way together
+                            const bool two = c < to;
+                            const float4 *a = reinterpret_cast<const float4 *>(slot(c, c == from)) + d / 4 * kTileRows + row;
+                            const float4 *b = reinterpret_cast<const float4 *>(slot(c + two, false)) + d / 4 * kTileRows + row;
+                            const float wa = ex2(ml_of(c).x - m), wb = two ? ex2(ml_of(c + 1).x - m) : 0.0f;
+                            float4 x[8], y[8];
 #pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                const float4 z = __ldcg(src + (d + k) / 4 * kTileRows);
-                                f[k] = fmaf(z.x, w, f[k]), f[k + 1] = fmaf(z.y, w, f[k + 1]);
-                                f[k + 2] = fmaf(z.z, w, f[k + 2]), f[k + 3] = fmaf(z.w, w, f[k + 3]);
+                            for (int k = 0; k < 8; ++k) {
+                                x[k] = __ldcg(a + k * kTileRows);
+                                y[k] = two ? __ldcg(b + k * kTileRows) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                f[4 * k] = fmaf(y[k].x, wb, fmaf(x[k].x, wa, f[4 * k]));
+                                f[4 * k + 1] = fmaf(y[k].y, wb, fmaf(x[k].y, wa, f[4 * k + 1]));
+                                f[4 * k + 2] = fmaf(y[k].z, wb, fmaf(x[k].z, wa, f[4 * k + 2]));
+                                f[4 * k + 3] = fmaf(y[k].w, wb, fmaf(x[k].w, wa, f[4 * k + 3]));
                             }
                         }
                         store(at, d, f, inv);
@@ -838,44 +836,33 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     page[g] = -2;
                 }
         };
-        // where the warp's two groups begin in K, and the lane's 16 bytes within a group
+        // where the warp's two groups of 16 keys begin in K, for this lane, and how many keys they hold
+        struct Groups {
+            const uint8_t *at[2];
+            int rows[2];
+        };
         const long long to_v = p.c.v - p.c.k;
-        const uint8_t *group_at[2];
         const long long row_step = ROWS * p.c.token_stride;
         const long long lane_at = row_in * p.c.token_stride + piece * 16;
-        int rows_there[2];                                         // keys of each group that the cache holds
         auto locate = [&](const ManyTile &t, int st) {
+            Groups gr;
             const int pos0 = block_of(t, st) * kKeys + w * 32;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const int at = pos0 + 16 * g;
-                rows_there[g] = page[g] >= 0 ? t.len - at : 0;
-                group_at[g] = p.c.k + (long long)page[g] * p.c.page_stride + t.head * p.c.head_stride +
-                              (at & ((1 << p.c.page_shift) - 1)) * p.c.token_stride + lane_at;
+                gr.rows[g] = page[g] >= 0 ? t.len - at : 0;
+                gr.at[g] = p.c.k + (long long)page[g] * p.c.page_stride + t.head * p.c.head_stride +
+                           (at & ((1 << p.c.page_shift) - 1)) * p.c.token_stride + lane_at;
             }
+            return gr;
         };
-        auto load = [&](long long to, uint4 (&raw)[LOADS]) {
+        auto load = [&](const Groups &gr, long long to, uint4 (&raw)[LOADS]) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const uint8_t *src = group_at[g] + to;
+                const uint8_t *src = gr.at[g] + to;
 #pragma unroll
                 for (int i = 0; i < LOADS / 2; ++i, src += row_step)
-                    raw[g * (LOADS / 2) + i] = row_in + ROWS * i < rows_there[g] ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto convert = [&](const uint4 (&raw)[LOADS], uint8_t *tile) {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int row = w * 32 + row_in + ROWS * i;
-                uint32_t h[8];
-                codes_to_half<KT>(raw[i].x, h[0], h[1]);
-                codes_to_half<KT>(raw[i].y, h[2], h[3]);
-                codes_to_half<KT>(raw[i].z, h[4], h[5]);
-                codes_to_half<KT>(raw[i].w, h[6], h[7]);
-                uint8_t *dst = tile + (piece >> 2) * L::kBlockBytes + row * 128;
-                const int c = 2 * piece & 7;
-                *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(dst + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    raw[g * (LOADS / 2) + i] = row_in + ROWS * i < gr.rows[g] ? ldg_stream_v4(src) : make_uint4(0, 0, 0, 0);
             }
         };
         float ks = 0.0f, vs = 0.0f;
@@ -897,45 +884,79 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             if (more) t = next->t, st = next->s0, s1 = next->s1;
             close_tile(idx++);
         };
-        open();
-        if (more) {
-            pages_of(t, st);
-            check();
-            locate(t, st);
-            load(0, kraw);
-            load_scales(t);
-            load(to_v, vraw);
-        }
-        for (int counter = 0; more; ++counter) {
-            const int stg = counter & 1, ph = (counter >> 1) & 1;
-            // the next step's page ids, then its codes as soon as the registers are free
-            if (++st == s1) open();
-            if (more) pages_of(t, st);
-            if (!mbar_wait_bounded(k_empty(stg), ph ^ 1, p.status, abort_flag)) break;
-            convert(kraw, smem + L::kK + stg * L::kOperand);
+        // K a step ahead of V: S of the next step is wanted before this step's out.  Raw codes are loaded as
+        // soon as their registers are free, a step ahead of their conversion.
+        auto emit_k = [&](int c) {
+            const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
+            if (!mbar_wait_bounded(k_empty(stg), ph ^ 1, p.status, abort_flag)) return false;
+            uint8_t *dst = smem + L::kK + stg * L::kOperand;
+            if (p.a.dtype == 0) convert_codes<KT, D, false>(kraw, dst, w * 32 + row_in, piece);
+            else convert_codes<KT, D, true>(kraw, dst, w * 32 + row_in, piece);
             if (lane < 2)                                          // no page: weight 0 whatever the scores
-                scales[(counter & 3) * 8 + w * 2 + lane] =
+                scales[(c & 3) * 8 + w * 2 + lane] =
                     there ? make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f) : make_float4(0.0f, -INFINITY, 0.0f, 0.0f);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(k_full(stg));
-            if (more) {
-                check();
-                locate(t, st);
-                load(0, kraw);
-                load_scales(t);
-            }
+            return true;
+        };
+        Groups gk = {};
+        bool more_twice = false;                                   // the mode of the step that K's registers hold
+        // the registers of K: the step after the one last loaded, if any
+        auto advance = [&]() {
+            if (++st == s1) open();
+            if (more) pages_of(t, st);
+        };
+        auto load_k = [&]() {
+            check();
+            gk = locate(t, st);
+            more_twice = same_rows(t);
+            load(gk, 0, kraw);
+            load_scales(t);
+        };
+        open();
+        bool have_v = more;                                        // step c of the loop below exists
+        if (more) {
+            pages_of(t, st);
+            load_k();
+            load(gk, to_v, vraw);
+        }
+        bool twice = more_twice;
+        if (more) {
+            advance();
+            if (!emit_k(0)) have_v = false;
+            if (more) load_k();
+        }
+        for (int c = 0; have_v; ++c) {
+            const bool have_k = more;                              // K of step c + 1 is in the registers
+            const bool next_twice = more_twice;
+            auto do_k = [&]() {
+                if (!have_k) return true;
+                advance();
+                if (!emit_k(c + 1)) return false;
+                if (more) load_k();
+                return true;
+            };
+            const Groups after = gk;
+            // The same rows twice: the other half waits for K.  Two halves of rows: K's place is free only once
+            // the second half's S is done, V's before.
+            if (twice && !do_k()) break;
+            const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
             if (!mbar_wait_bounded(v_empty(stg), ph ^ 1, p.status, abort_flag)) break;
-            convert(vraw, smem + L::kV + stg * L::kOperand);
+            convert_codes<KT, D, false>(vraw, smem + L::kV + stg * L::kOperand, w * 32 + row_in, piece);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full(stg));
-            if (more) load(to_v, vraw);
+            have_v = have_k;
+            if (have_v) load(after, to_v, vraw);
+            if (!twice && !do_k()) break;
+            twice = next_twice;
         }
     }
     if (warp == kSoftWarps + kConvWarps) {
         // ------------------------------------------------------------ MMA issuer
-        const uint32_t idesc_s = make_idesc_f16(0, kHalfRows, kKeys);
+        // S in the activations' type, its sign that of the scale (bit 13 negates Q): exponents then rise with scores
+        const uint32_t idesc_s = make_idesc_f16(p.a.dtype, kHalfRows, kKeys) | (p.a.scale < 0.0f ? 1u << 13 : 0u);
         const uint32_t idesc_o = make_idesc_f16(0, kHalfRows, D) | 1u << 16;      // V is MN-major
         const uint32_t sm = smem_u32(smem);
         const uint32_t k_desc = (uint32_t)smem_desc_sw128(0u), v_desc = (uint32_t)desc_mn_sw128(0u, L::kBlockBytes);
@@ -950,22 +971,28 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             mma_output(tmem + 256 + half * D, tmem + half * 128, v_desc + ((sm + L::kV + stg * L::kOperand) >> 4), hi,
                        idesc_o, fresh ? 0u : 1u);
         };
+        auto q_wait = [&](int half) {
+            const int phase = q_phase[half];
+            q_phase[half] ^= 1;
+            return mbar_wait_bounded(q_full(half), phase, p.status, abort_flag);
+        };
+        auto q_done = [&](int half) { commit_elected(q_empty(half)); };
         auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
         // MMAs run in the order they are issued: P is read before the next S of its half replaces it.
         auto run_tile = [&](int steps) {                           // two halves of rows, a step together
             for (int st = 0; st < steps; ++st, ++counter) {
-                const int stg = counter & 1, ph = (counter >> 1) & 1;
+                const int stg = counter % L::kStages, ph = (counter / L::kStages) & 1;
                 if (st == 0) {
                     if (!wait(k_full(stg), ph)) return false;
                     for (int h = 0; h < 2; ++h) {
-                        if (!wait(q_full(h), q_phase[h])) return false;
-                        q_phase[h] ^= 1;
+                        if (!q_wait(h)) return false;
                         tc_fence_after();
                         scores(h, stg);
+                        if (steps == 1) q_done(h);
                     }
                     commit_elected(k_empty(stg));
                 }
-                const int nstg = (counter + 1) & 1, nph = ((counter + 1) >> 1) & 1;
+                const int nstg = (counter + 1) % L::kStages, nph = ((counter + 1) / L::kStages) & 1;
                 for (int h = 0; h < 2; ++h) {
                     if (!wait(p_ready(h), p_phase[h])) return false;
                     p_phase[h] ^= 1;
@@ -979,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                         tc_fence_after();
                         scores(h, nstg);
                         if (h == 1) commit_elected(k_empty(nstg));
+                        if (st + 2 == steps) q_done(h);
                     }
                 }
             }
@@ -988,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             for (int st = -2; st < steps; ++st) {
                 const int h = st & 1;
                 if (st >= 0) {
-                    const int c = counter + st, stg = c & 1, ph = (c >> 1) & 1;
+                    const int c = counter + st, stg = c % L::kStages, ph = (c / L::kStages) & 1;
                     if (!wait(p_ready(h), p_phase[h])) return false;
                     p_phase[h] ^= 1;
                     if (!wait(v_full(stg), ph)) return false;
@@ -998,15 +1026,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                     commit_elected(v_empty(stg));
                 }
                 if (st + 2 < steps) {
-                    const int c = counter + st + 2, stg = c & 1, ph = (c >> 1) & 1;
-                    if (st < 0) {
-                        if (!wait(q_full(h), q_phase[h])) return false;
-                        q_phase[h] ^= 1;
-                    }
+                    const int c = counter + st + 2, stg = c % L::kStages, ph = (c / L::kStages) & 1;
+                    if (st < 0 && !q_wait(h)) return false;
                     if (!wait(k_full(stg), ph)) return false;
                     tc_fence_after();
                     scores(h, stg);
                     commit_elected(k_empty(stg));
+                    if (st + 4 >= steps) q_done(h);
                 }
             }
             counter += steps;
@@ -1019,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
             const int rows = __reduce_max_sync(0xffffffffu, next->t.rows);
             const int steps = __reduce_max_sync(0xffffffffu, next->s1 - next->s0);
             close_tile(idx);
-            if (!(rows > kHalfRows ? run_tile(steps) : run_same_rows(steps))) {
+            if (!(rows > half_rows ? run_tile(steps) : run_same_rows(steps))) {
                 // leave with no product in flight
                 commit_elected(drain);
                 for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
@@ -1028,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
         }
     } else if (warp == kSoftWarps + kConvWarps + 1) {
         // ------------------------------------------------------------ planner
-        int pr = pair, hd = head, idx = 0;
+        int pr = pair, hd = head, idx = 0, q_phase[2] = {0, 0};
         for (bool more = true; more;) {
             PlannedTile next = {};
             more = false;
@@ -1053,15 +1079,24 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
                 mbar_arrive(plan_full(idx % kRing));
             }
             __syncwarp();
-            // its rows of q towards L2
-            if (more)
-                for (int row = lane; row < next.t.rows; row += 32) {
-                    const int x = next.t.row0 + row, tok = x / group;
-                    const uint16_t *src = static_cast<const uint16_t *>(p.a.q) +
-                                          (long long)(next.t.q0 + tok) * p.a.q_stride + (next.t.head * group + x - tok * group) * D;
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-                    if (D == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 64));
+            // its rows of Q: a half's tokens times the group's heads, 64 dims a box, rows in that order
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!more || !half_runs(next, h)) continue;
+                if (!mbar_wait_bounded(q_empty(h), q_phase[h] ^ 1, p.status, abort_flag)) {
+                    more = false;
+                    break;
                 }
+                q_phase[h] ^= 1;
+                if (lane == 0) {
+                    const int tok = next.t.q0 + (next.t.row0 + (same_rows(next.t) ? 0 : h * half_rows)) / group;
+                    mbar_arrive_expect_tx(q_full(h), (uint32_t)(half_rows * D * 2));
+                    for (int b = 0; b < L::kBlocks; ++b)
+                        tma_load_3d(smem_u32(smem) + L::kQ + h * L::kOperand + b * L::kBlockBytes, &tm_q, q_full(h), b * 64,
+                                    next.t.head * group, tok);
+                }
+                __syncwarp();
+            }
             ++idx;
         }
     }
@@ -1071,20 +1106,41 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const ManyParams
     if (warp == kSoftWarps + kConvWarps) tmem_dealloc(tmem, 512u);
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// q as (dim, head, token); a box is 64 dims of a kv head's group over a half's tokens.
+cudaError_t encode_q(const DeviceInfo &dev, const KvAttentionArgs &a, int n_tokens, int head_dim, int group,
+                     CUtensorMap *out) {
+    if (dev.encode_tiled == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)a.n_heads, (cuuint64_t)n_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(kHalfRows / group)}, one[3] = {1, 1, 1};
+    const CUresult r = reinterpret_cast<EncodeTiledFn>(dev.encode_tiled)(
+        out, a.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q),
+        dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int KT, int D>
-cudaError_t launch(const ManyParams &p, int grid, cudaStream_t s, bool pdl) {
+cudaError_t launch(const CUtensorMap &q, const ManyParams &p, int grid, cudaStream_t s, bool pdl) {
     using L = ManySmem<D>;
     auto kern = many_rows_kernel<KT, D>;
     const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(kern), L::kEnd);
     if (e != cudaSuccess) return e;
-    return kv_launch(kern, dim3(grid), dim3(kThreads), L::kEnd, s, pdl, p);
+    return kv_launch(kern, dim3(grid), dim3(kThreads), L::kEnd, s, pdl, q, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
                                      const DeviceInfo &dev, cudaStream_t s, bool pdl) {
-    const int group = a.n_heads / c.n_kv_heads;
+    const int group = a.n_heads / c.n_kv_heads, half_rows = kHalfRows / group * group;
+    CUtensorMap q;
+    cudaError_t e = encode_q(dev, a, batch.n_tokens, c.head_dim, group, &q);
+    if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> launches{0x7e57ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;
@@ -1093,17 +1149,18 @@ cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c,
         b.q_starts += b0;
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
         // as many pairs as these sequences can have at most
-        const long long pairs = (long long)b.n_tokens * group / kTileRows + b.n_seqs;
+        const long long pairs = (long long)b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
-            ManyParams p{a, c, b, row_limit, (int)first, nullptr, nullptr, 0, dev.status};
+            ManyParams p{a, c, b, row_limit, half_rows, (int)first, nullptr, nullptr, 0, dev.status};
             p.tickets = static_cast<unsigned long long *>(a.workspace);
             p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
             p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
             if (p.tag == 0) p.tag = 1;
-            const cudaError_t e =
-                c.kv_dtype == kKvInt8
-                    ? (c.head_dim == 128 ? launch<kKvInt8, 128>(p, dev.sm_count, s, pdl) : launch<kKvInt8, 64>(p, dev.sm_count, s, pdl))
-                    : (c.head_dim == 128 ? launch<kKvE4m3, 128>(p, dev.sm_count, s, pdl) : launch<kKvE4m3, 64>(p, dev.sm_count, s, pdl));
+            const int grid = dev.sm_count;
+            if (c.kv_dtype == kKvInt8)
+                e = c.head_dim == 128 ? launch<kKvInt8, 128>(q, p, grid, s, pdl) : launch<kKvInt8, 64>(q, p, grid, s, pdl);
+            else
+                e = c.head_dim == 128 ? launch<kKvE4m3, 128>(q, p, grid, s, pdl) : launch<kKvE4m3, 64>(q, p, grid, s, pdl);
             if (e != cudaSuccess) return e;
         }
     }
@@ -1111,7 +1168,7 @@ cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c,
 }
 
 long long kv_attention_many_workspace(int head_dim, const DeviceInfo &dev) {
-    return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * (head_dim / 4 + 1) * kTileRows * 16;
+    return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4;
 }
 
 }  // namespace w4a16
