@@ -193,36 +193,80 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // descriptors and addresses stay in uniform registers: issued from a
 // diverged lane, each MMA cost three times its 32 cycles of arithmetic.
 // Descriptors are a low word (address, leading offset) and a constant high
-// word; 16 of the contraction's elements further is a constant step.
+// word; 16 of the contraction's elements further is a constant step.  One
+// statement a step: the election and the predicates are made once.  Predicate
+// p starts the sum or goes on with it, q (an instruction descriptor is never 0)
+// goes on.
 //
 // S = Q K^T: 64 dims are four steps of 32 bytes in a 128-byte row; `far` is
 // the step to the next 64 dims.
 template <int BLOCKS>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi, uint32_t idesc) {
     static_assert(BLOCKS == 1 || BLOCKS == 2, "64 or 128 dims");
-#pragma unroll
-    for (int k = 0; k < 4 * BLOCKS; ++k) {
-        const uint32_t off = (k >> 2) * (kKeys * 128 / 16) + (k & 3) * 2;
+    static_assert(kKeys * 128 / 16 == 1024, "the step to the next 64 dims, below");
+    if (BLOCKS == 2) {
         asm volatile(
-            "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"
-            "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
-            "r"(alo + off), "r"(blo + off), "r"(hi), "r"(idesc), "r"(k > 0 ? 1u : 0u)
+            "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+            "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+            "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 1024;\n\tadd.u32 y, %2, 1024;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 1026;\n\tadd.u32 y, %2, 1026;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 1028;\n\tadd.u32 y, %2, 1028;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 1030;\n\tadd.u32 y, %2, 1030;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "}" ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(0)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+            "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+            "add.u32 x, %1, 2;\n\tadd.u32 y, %2, 2;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 4;\n\tadd.u32 y, %2, 4;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "add.u32 x, %1, 6;\n\tadd.u32 y, %2, 6;\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n\t"
+            "}" ::"r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(0)
             : "memory");
     }
 }
 // out (+)= P V: P in TMEM, 8 columns a step; 16 keys of V are 2048 bytes.
 __device__ __forceinline__ void mma_output(uint32_t d, uint32_t a, uint32_t blo, uint32_t hi, uint32_t idesc,
                                            uint32_t accumulate) {
-#pragma unroll
-    for (int k = 0; k < kKeys / 16; ++k) {
-        asm volatile(
-            "{\n\t.reg .pred e, p;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
-            "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-            "r"(a + 8 * k), "r"(blo + 128 * k), "r"(hi), "r"(idesc), "r"(k > 0 ? 1u : accumulate)
-            : "memory");
-    }
+    static_assert(kKeys == 128, "eight steps");
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "add.u32 x, %1, 0;\n\tadd.u32 y, %2, 0;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 32;\n\tadd.u32 y, %2, 512;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 40;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 48;\n\tadd.u32 y, %2, 768;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "add.u32 x, %1, 56;\n\tadd.u32 y, %2, 896;\n\tmov.b64 b, {y, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, q;\n\t"
+        "}" ::"r"(d), "r"(a), "r"(blo), "r"(hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 __device__ __forceinline__ void commit_elected(uint32_t bar) {
     asm volatile(
