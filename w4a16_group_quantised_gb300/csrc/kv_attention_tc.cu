@@ -40,9 +40,11 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kMaxPairs = 1280;           // (sequence, row tile) pairs of a launch
+constexpr int kMaxPairs = 1216;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
 constexpr int kCost = 3;                  // steps that a tile's start and end count for in the shares
+constexpr int kSorted = 256;              // up to so many pairs may be dealt out whole, the longest first
+constexpr int kSplitCost = 4;             // steps that parts of shared tiles cost a CTA
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 2);   // and the MMA issuer, the planner
 constexpr int kRing = 4;                  // tiles that the planner is ahead of the slowest role
@@ -87,7 +89,8 @@ struct ManySmem {
     static constexpr int kPre = kV + kStages * kOperand;                // line position of each pair, of one kv head
     static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
     static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
-    static constexpr int kScale = kPairSeq + kMaxPairs * 2;       // [4][8] float4 {ks, log2 vs, 1 / vs, -}
+    static constexpr int kOrder = kPairSeq + kMaxPairs * 2;       // pairs by falling steps
+    static constexpr int kScale = kOrder + kSorted * 2;        // [4][8] float4 {ks, log2 vs, 1 / vs, -}
     static constexpr int kExchange = kScale + 4 * 8 * 16;                // (M, l) of the second half's rows
     static constexpr int kPlan = kExchange + kHalfRows * 8;
     static constexpr int kBars = kPlan + kRing * (int)sizeof(PlannedTile);
@@ -482,6 +485,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     total *= Hk;
     __syncthreads();
 
+    // Whole tiles or equal shares?  With few tiles the longest first, dealt out to and fro, can come close to
+    // equal shares without the parts that shared tiles leave; each thread adds up one CTA's hand.
+    uint16_t *order = reinterpret_cast<uint16_t *>(smem + L::kOrder);
+    const int grid = gridDim.x;
+    auto dealt = [&](int cta, int round) { return round * grid + (round & 1 ? grid - 1 - cta : cta); };
+    bool deal = false;
+    if (pairs <= kSorted) {
+        for (int i = tid; i < pairs; i += kThreads) {
+            const long long mine = pre[i + 1] - pre[i];
+            int rank = 0;
+            for (int j = 0; j < pairs; ++j) {
+                const long long x = pre[j + 1] - pre[j];
+                rank += x > mine || (x == mine && j < i);
+            }
+            order[rank] = (uint16_t)i;
+        }
+        __syncthreads();
+        long long most = 0;
+        for (int cta = tid; cta < grid; cta += kThreads) {
+            long long hand = 0;
+            for (int round = 0; round * grid < pairs * Hk; ++round) {
+                const int i = dealt(cta, round);
+                if (i < pairs * Hk) hand += pre[order[i / Hk] + 1] - pre[order[i / Hk]];
+            }
+            most = max(most, hand);
+        }
+        for (int d = 16; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+        if (lane == 0) s_scan[warp] = most;
+        __syncthreads();
+        for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_scan[w]);
+        deal = most <= total / grid + kSplitCost;
+    }
+
     auto tile_at = [&](int pair, int head) {
         const int b = pair_seq[pair];
         const int4 s = seqs[b];
@@ -499,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return lo;
     };
-    const long long ctas = min((long long)gridDim.x, (total + kCost) / (1 + kCost));
-    if (blockIdx.x >= ctas) return;
+    const long long ctas = min((long long)grid, (total + kCost) / (1 + kCost));
+    if (deal ? (int)blockIdx.x >= pairs * Hk : blockIdx.x >= ctas) return;
     if (tid < 2) {
         long long at = ((long long)blockIdx.x + tid) * total / ctas;
         if (at > 0 && at < total) {
@@ -521,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = static_cast<uint32_t>(misc[1]);
     // the tile at c0, and the walk from there
     int pair = 0, head = 0;
-    if (c0 < c1) {
+    if (!deal && c0 < c1) {
         pair = find_pair(c0);
         head = (int)((c0 - pre[pair] * Hk) / (pre[pair + 1] - pre[pair]));
     }
@@ -1102,7 +1138,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (bool more = true; more;) {
             PlannedTile next = {};
             more = false;
-            while (pr < pairs) {
+            if (deal) {
+                const int i = dealt(blockIdx.x, idx);
+                if (i < pairs * Hk) {
+                    next.t = tile_at(order[i / Hk], i % Hk);
+                    next.s1 = next.t.steps;
+                    more = true;
+                }
+            }
+            while (!deal && pr < pairs) {
                 next.t = tile_at(pr, hd);
                 if (next.t.begin >= c1) break;
                 if (++hd == Hk) hd = 0, ++pr;
