@@ -80,7 +80,11 @@ class Problem:
                 big[:, :, :-1, :-16] = t
                 t = big[:, :, :-1, :-16]
             return t.view(STORE[self.store])
-        cache = w.KVCache(put(self.k), put(self.v), self.ks.cuda(), self.vs.cuda())
+        if self.layout == "pairs":                # K and V of a page next to each other in one tensor
+            both = torch.stack([self.k.view(torch.int8), self.v.view(torch.int8)], 1).cuda()
+            cache = w.KVCache(both[:, 0].view(STORE[self.store]), both[:, 1].view(STORE[self.store]), self.ks.cuda(), self.vs.cuda())
+        else:
+            cache = w.KVCache(put(self.k), put(self.v), self.ks.cuda(), self.vs.cuda())
         return (cache, self.table.cuda(), torch.tensor(self.lens, dtype=torch.int32).cuda(), self.starts.cuda(),
                 self.rows.cuda())
 

@@ -42,9 +42,10 @@ def test_single_tokens(cuda_lib, store, act, dim, heads, kv_heads):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
-@pytest.mark.parametrize("layout", ["heads", "tokens", "padded"])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "padded", "pairs"])
 def test_pages_and_layouts(cuda_lib, page, layout):
     check(cuda_lib, Problem([5, 130, 300, 129], [1, 2, 1, 5], page=page, layout=layout, store="int8", seed=page))
+    check(cuda_lib, Problem([50, 130, 300], [50, 2, 130], page=page, layout=layout, store="e4m3", seed=page))
     check(cuda_lib, Problem([5, 130, 300, 129], [1, 2, 1, 5], page=page, layout=layout, store="e4m3", dim=64, act="f16",
                             seed=page + 1))
 
@@ -319,3 +320,33 @@ def test_values_before_a_bad_block_stay_finite(cuda_lib, new):
     sees = torch.arange(48, 48 + new) >= last * 16
     bad = torch.isnan(out.float()).any(-1).any(-1).cpu()
     assert torch.equal(bad, sees)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("order", ["values first", "the same tensor"])
+def test_where_k_and_v_lie(cuda_lib, new, order):
+    """V below K in memory, and one tensor as both."""
+    w = cuda_lib
+    p = Problem([200 + new, new], [new, new], seed=13)
+    if order == "the same tensor":
+        p.v, p.vs = p.k, p.ks
+    cache, table, lens, starts, rows = p.to_cuda(w)
+    if order == "the same tensor":
+        cache = w.KVCache(cache.k, cache.k, cache.k_scale, cache.k_scale)
+    else:
+        both = torch.stack([cache.v, cache.k])
+        cache = w.KVCache(both[1], both[0], cache.k_scale, cache.v_scale)
+    q = rows[:, :p.heads * p.dim].unflatten(1, (p.heads, p.dim))
+    out = w.w4a16_kv_attention(q, cache, table, lens, starts, new)
+    want, _, spread = attention(p)
+    assert bool(((out.cpu().double() - want).abs() <= attention_tolerance(p, want, spread)).all())
+    assert w.w4a16_last_device_error() == 0
+
+
+def test_many_sequences(cuda_lib):
+    """More sequences, and more row tiles, than one launch takes."""
+    new = [(i * 7) % 4 if i % 3 else 80 for i in range(600)]
+    lens = [n + (i * 13) % 50 for i, n in enumerate(new)]
+    check(cuda_lib, Problem(lens, new, heads=16, kv_heads=1, dim=64, act="f16", seed=14))
+    new = [1 + i % 2 for i in range(1100)]
+    check(cuda_lib, Problem([n + i % 70 for i, n in enumerate(new)], new, heads=2, kv_heads=1, dim=64, seed=15))

@@ -114,7 +114,7 @@ def test_workspaces(lib):
 
 def test_copy_pages(lib):
     f = lib.w4a16_kv_copy_pages
-    assert f(cache(), OK, OK, -1, None) == ERR_SHAPE
+    assert f(cache(), OK, OK, -1, None) == ERR_SHAPE and f(cache(), OK, OK, 1 << 30, None) == ERR_SHAPE
     assert f(cache(), NULL, OK, 1, None) == ERR_NULL and f(cache(), OK, NULL, 1, None) == ERR_NULL
     assert f(cache(), OK + 1, OK, 1, None) == ERR_ALIGN
     assert f(cache(page_size=24), OK, OK, 1, None) == ERR_SHAPE

@@ -166,7 +166,7 @@ int w4a16_kv_copy_pages(const w4a16_kv_cache_t *cache, const int32_t *src, const
                         w4a16_stream_t stream) {
     KvCache c;
     W4A16_TRY(check_cache(cache, &c));
-    if (n < 0 || n > (1 << 24)) return W4A16_ERR_SHAPE;
+    if (n < 0 || (long long)n * c.n_kv_heads >= (1LL << 31)) return W4A16_ERR_SHAPE;
     if (n == 0) return W4A16_OK;
     if (src == nullptr || dst == nullptr) return W4A16_ERR_NULL;
     if (!aligned(src, 4) || !aligned(dst, 4)) return W4A16_ERR_ALIGN;

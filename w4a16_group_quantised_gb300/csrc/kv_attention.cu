@@ -872,7 +872,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     const int keys = c.page_shift >= 5 ? 32 : 16;
     // one map over both tensors, from the lower one up, where their distance fits a stride
     const long long apart = c.v - c.k, distance = apart < 0 ? -apart : apart;
-    const bool merged = distance < 1LL << 40;
+    const bool merged = distance > 0 && distance < 1LL << 40;
     CUtensorMap k, v;
     cudaError_t e = encode_codes(dev, c, merged && apart < 0 ? c.v : c.k, merged ? distance : 0, keys, token_first, &k);
     if (e == cudaSuccess && !merged) e = encode_codes(dev, c, c.v, 0, keys, token_first, &v);
