@@ -38,16 +38,21 @@ from .binding import (  # noqa: F401
     w4a16_pack_zeros,
     w4a16_select_path,
 )
-from .kv import (  # noqa: F401
-    KVCache,
-    w4a16_kv_append,
-    w4a16_kv_attention,
-    w4a16_kv_attention_workspace,
-    w4a16_kv_compact,
-    w4a16_kv_copy_pages,
-    w4a16_kv_fork,
-    w4a16_kv_free,
-    w4a16_kv_pool_workspace,
-    w4a16_kv_read,
-    w4a16_kv_trim,
-)
+
+_KV = ("KVCache", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_workspace", "w4a16_kv_compact",
+       "w4a16_kv_copy_pages", "w4a16_kv_fork", "w4a16_kv_free", "w4a16_kv_pool_workspace", "w4a16_kv_read",
+       "w4a16_kv_trim")
+
+
+def __getattr__(name):
+    # kv.py imports torch: on first use, so that building the library does not
+    if name in _KV:
+        from . import kv
+        for n in _KV:
+            globals()[n] = getattr(kv, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(list(globals()) + list(_KV))

@@ -18,6 +18,8 @@ import functools
 import struct
 from typing import NamedTuple
 
+import torch
+
 from .binding import W4A16_BF16, W4A16_F16, _check, _dtype_code, load_library
 
 KV_INT8, KV_E4M3 = 0, 1
@@ -25,10 +27,10 @@ KV_INT8, KV_E4M3 = 0, 1
 
 class KVCache(NamedTuple):
     """Codes and scales of a paged cache (see the module's docstring)."""
-    k: "torch.Tensor"         # noqa: F821
-    v: "torch.Tensor"         # noqa: F821
-    k_scale: "torch.Tensor"   # noqa: F821
-    v_scale: "torch.Tensor"   # noqa: F821
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
 
 
 # w4a16_kv_cache_t and w4a16_kv_batch_t, in native layout
@@ -38,7 +40,6 @@ _BATCH = struct.Struct("@PPPiii4x")
 
 def _refuse(name, t, dtype, dim, device):
     """Why `t` is not a contiguous tensor of this dtype and dimension on this CUDA device (None: any)."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.device.type != "cuda":
@@ -54,7 +55,6 @@ def _refuse(name, t, dtype, dim, device):
 
 def _ints(name, t, dim, device):
     """An int32 tensor's address, checked; `device` is a CUDA device's index."""
-    import torch
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.dim() == dim and t.get_device() == device >= 0
             and t.is_contiguous()):
         _refuse(name, t, torch.int32, dim, device)
@@ -62,7 +62,6 @@ def _ints(name, t, dim, device):
 
 
 def _device_of(name, t):
-    import torch
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         _refuse(name, t, None, None, None)
     return t.get_device()
@@ -70,7 +69,6 @@ def _device_of(name, t):
 
 def _cache(c):
     """(the cache as the C struct's bytes, device index, pages, heads, page size, head dim)"""
-    import torch
     if not isinstance(c, KVCache):
         raise TypeError(f"cache must be a KVCache, got {type(c).__name__}")
     k, v, ks, vs = c
@@ -119,7 +117,6 @@ def _batch(block_table, kv_lens, q_starts, n_tokens, device):
 
 def _rows(name, t, heads, head_dim, device):
     """Row stride of a [tokens, heads, head_dim] tensor whose rows are dense."""
-    import torch
     if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dim() != 3:
         if _device_of(name, t) != device:
             raise ValueError(f"{name} must be on the cache's device")
@@ -134,12 +131,10 @@ def _rows(name, t, heads, head_dim, device):
 
 
 def _act(t):
-    import torch
     return W4A16_BF16 if t.dtype is torch.bfloat16 else W4A16_F16 if t.dtype is torch.float16 else _dtype_code(t)
 
 
 def _output(name, t, shape, dtype, device):
-    import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
@@ -152,7 +147,6 @@ def _output(name, t, shape, dtype, device):
 
 def _scratch(workspace, need, device, stream):
     """(workspace tensor, its address, its bytes): the caller's, or one from torch's allocator."""
-    import torch
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
         if stream is not None:
@@ -164,7 +158,6 @@ def _scratch(workspace, need, device, stream):
 
 
 def _stream(stream, device):
-    import torch
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
@@ -199,7 +192,6 @@ def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int,
     an optional sliding window (0: none) and sink tokens; out [n_tokens,
     n_heads, head_dim].  scale defaults to head_dim ** -0.5; lse, if given, is
     float32 [n_tokens, n_heads] and receives the log-sum-exp of each row."""
-    import torch
     c, dev, _, kv_heads, _, dim = _cache(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         _refuse("q", q, None, 3, dev)
