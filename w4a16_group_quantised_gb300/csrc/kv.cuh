@@ -69,11 +69,20 @@ __device__ __forceinline__ void kv_decode4(uint32_t w, float (&v)[4]) {
     }
 }
 
-// RN to the nearest code, ties to even, saturated.
+// Four values as a word of codes: to the nearest, ties to even.  int8: adding
+// 1.5 * 2^23 rounds to an integer whose low byte is the code; |v| <= 127 (a
+// block's scale is its largest value's), so nothing needs saturating.  A value
+// that is not finite gives any code: its block's scale says so.
 template <int KT>
-__device__ __forceinline__ uint32_t kv_encode(float v) {
-    if (KT == kKvInt8) return (uint32_t)(uint8_t)(int8_t)min(max(__float2int_rn(v), -127), 127);
-    return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t kv_encode4(float a, float b, float c, float d) {
+    if (KT == kKvInt8) {
+        const float big = 12582912.0f;
+        const uint32_t x = __byte_perm(__float_as_uint(__fadd_rn(a, big)), __float_as_uint(__fadd_rn(b, big)), 0x0040);
+        const uint32_t y = __byte_perm(__float_as_uint(__fadd_rn(c, big)), __float_as_uint(__fadd_rn(d, big)), 0x0040);
+        return __byte_perm(x, y, 0x5410);
+    }
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
+           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
 __host__ __device__ inline int kv_log2(int v) {

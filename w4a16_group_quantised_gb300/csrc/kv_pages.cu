@@ -159,14 +159,15 @@ __device__ int select_bit(const uint32_t *bits, const int *counts, int n_chunks,
     return s_at;
 }
 
-// One CTA per child.
+// `parts` CTAs per child: each finds the child's page, the first of them also
+// writes the tables and counts, and each copies its part of the page.
 __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
-                            const int *parents, const int *children, int n, const uint32_t *free_bits,
-                            const int *free_counts, int *status) {
+                            const int *parents, const int *children, int n, int parts,
+                            const uint32_t *free_bits, const int *free_counts, int *status) {
     kv_begin();
     __shared__ int scratch[32];
     const int shift = c.page_shift, part_mask = (1 << shift) - 1;
-    const int me = blockIdx.x;
+    const int me = blockIdx.x / parts, part = blockIdx.x % parts;
     const int par = parents[me], chi = children[me];
     if (par < 0 || par >= n_seqs || chi < 0 || chi >= n_seqs) {
         if (threadIdx.x == 0) kv_report(status);
@@ -190,7 +191,7 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
     const int full = len >> shift;
     const int *from = table + (long long)par * max_blocks;
     int *to = table + (long long)chi * max_blocks;
-    for (int k = threadIdx.x; k < max_blocks; k += blockDim.x) {
+    for (int k = threadIdx.x; part == 0 && k < max_blocks; k += blockDim.x) {
         int p = -1;
         if (ok && k < full) {
             p = from[k];
@@ -204,22 +205,20 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
         }
         to[k] = p;
     }
-    if (threadIdx.x == 0) {
+    if (part == 0 && threadIdx.x == 0) {
         lens[chi] = ok ? len : 0;
         if (!ok) kv_report(status);
         else if (tail) refcount[fresh] = 1;
     }
     if (ok && tail) {
         const int src = from[full];
-        if (src >= 0 && src < c.n_pages) copy_page(c, src, fresh, 0, 1);
+        if (src >= 0 && src < c.n_pages) copy_page(c, src, fresh, part, parts);
         else if (threadIdx.x == 0) kv_report(status);
     }
 }
 
-// Give up table entry *e: whoever takes the page id out of it lowers the count.
-__device__ __forceinline__ void drop_entry(int *e, int *refcount, int n_pages, int *status) {
-    if (*e < 0) return;
-    const int p = atomicExch(e, -1);
+// A table entry that named page p is gone: its count goes down.
+__device__ __forceinline__ void drop_page(int p, int *refcount, int n_pages, int *status) {
     if (p < 0) return;
     if (p >= n_pages) {
         kv_report(status);
@@ -237,8 +236,9 @@ __global__ void free_kernel(int *table, int *lens, int n_seqs, int max_blocks, i
         if (threadIdx.x == 0) kv_report(status);
         return;
     }
+    // a sequence listed twice: whoever takes the page id out of an entry lowers the count
     for (int k = threadIdx.x; k < max_blocks; k += blockDim.x)
-        drop_entry(table + (long long)i * max_blocks + k, refcount, n_pages, status);
+        drop_page(atomicExch(table + (long long)i * max_blocks + k, -1), refcount, n_pages, status);
     if (threadIdx.x == 0) lens[i] = 0;
 }
 
@@ -250,8 +250,12 @@ __global__ void trim_kernel(int *table, const int *lens, int max_blocks, int *re
     // blocks [lo, hi) lie whole in positions [sinks, len - window + 1)
     const int lo = (int)(((long long)sinks + ps - 1) >> shift);
     const int hi = max(len - window + 1, 0) >> shift;
-    for (int k = lo + threadIdx.x; k < hi; k += blockDim.x)
-        drop_entry(table + (long long)i * max_blocks + k, refcount, n_pages, status);
+    for (int k = lo + threadIdx.x; k < hi; k += blockDim.x) {
+        int *e = table + (long long)i * max_blocks + k;
+        const int p = *e;
+        if (p >= 0) *e = -1;
+        drop_page(p, refcount, n_pages, status);
+    }
 }
 
 struct CompactScratch {
@@ -377,19 +381,20 @@ cudaError_t launch_kv_fork(const KvCache &c, int *table, int *lens, int n_seqs, 
     const cudaError_t e = kv_launch(bitmap_kernel, dim3((c.n_pages + kChunk - 1) / kChunk), dim3(kChunk), 0, s, pdl,
                                     refcount, c.n_pages, 1, w.bits, w.counts);
     if (e != cudaSuccess) return e;
-    return kv_launch(fork_kernel, dim3(n), dim3(kCopyThreads), 0, s, pdl, c, table, lens, n_seqs, max_blocks, refcount,
-                     parents, children, n, w.bits, w.counts, dev.status);
+    const int parts = std::min(copy_parts(c), 4);
+    return kv_launch(fork_kernel, dim3((unsigned)n * parts), dim3(kCopyThreads), 0, s, pdl, c, table, lens, n_seqs,
+                     max_blocks, refcount, parents, children, n, parts, w.bits, w.counts, dev.status);
 }
 
 cudaError_t launch_kv_free(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                            const int *seqs, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
-    return kv_launch(free_kernel, dim3(n), dim3(256), 0, s, pdl, table, lens, n_seqs, max_blocks, refcount, n_pages,
+    return kv_launch(free_kernel, dim3(n), dim3(512), 0, s, pdl, table, lens, n_seqs, max_blocks, refcount, n_pages,
                      seqs, dev.status);
 }
 
 cudaError_t launch_kv_trim(int *table, const int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                            int page_size, int window, int sinks, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
-    return kv_launch(trim_kernel, dim3(n_seqs), dim3(256), 0, s, pdl, table, lens, max_blocks, refcount, n_pages,
+    return kv_launch(trim_kernel, dim3(n_seqs), dim3(512), 0, s, pdl, table, lens, max_blocks, refcount, n_pages,
                      kv_log2(page_size), window, sinks, dev.status);
 }
 
