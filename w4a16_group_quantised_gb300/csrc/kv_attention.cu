@@ -860,13 +860,27 @@ cudaError_t launch_few(const FewParams &p, const CUtensorMap &k, const CUtensorM
     return kv_launch(kern, dim3(grid), dim3(32 * NW), L::kEnd, s, pdl, k, v, p);
 }
 
-constexpr int kMostRows = 16;
+constexpr int kTileRows = 16;             // the most rows of a tile here
+
+// Rows a kv head up to which a sequence is this kernel's.  A second tile reads
+// the keys again, out of L2; with 32 keys a block or 64 dims that still costs
+// less than a mostly empty 128-row tile, with 16 keys of 128 dims it need not.
+// Measured, this kernel / the other, in us, at 32 rows of 24 sequences of 128
+// to 4001 tokens: pages of 64 75 / 83, 64 dims 50 / 59, pages of 16 98 / 86; at
+// 40 rows (three tiles) 99 / 84, 66 / 60 and 131 / 86; at 16 rows 66 / 85.
+int most_rows(const KvCache &c) { return c.page_shift >= 5 || c.head_dim == 64 ? 2 * kTileRows : kTileRows; }
 
 }  // namespace
 
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, const DeviceInfo &dev,
                                 cudaStream_t s, bool pdl) {
-    const int group = a.n_heads / c.n_kv_heads;
+    const int group = a.n_heads / c.n_kv_heads, most = most_rows(c);
+    // Sequences with more rows go to the tensor-core kernel.  When every sequence brings max_q_len tokens all of
+    // them do, and this kernel, which would find nothing to do (about 4 us), is left out; should max_q_len not be
+    // the longest, that kernel has them all the same.
+    const bool many = (long long)a.max_q_len * group > most;
+    if (many && (long long)a.max_q_len * batch.n_seqs == batch.n_tokens)
+        return launch_kv_attention_many(a, c, batch, 0, dev, s, pdl);
     const bool token_first = c.n_kv_heads > 1 && c.head_stride < c.token_stride;
     // blocks of 32 keys where a page holds them: half the boxes and look-ups
     const int keys = c.page_shift >= 5 ? 32 : 16;
@@ -878,12 +892,6 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     if (e == cudaSuccess && !merged) e = encode_codes(dev, c, c.v, 0, keys, token_first, &v);
     if (e != cudaSuccess) return e;
     if (merged) v = k;
-    // Sequences with more rows than a tile of this kernel holds go to the tensor-core kernel.  When every
-    // sequence brings max_q_len tokens all of them do, and this kernel, which would find nothing to do (about
-    // 4 us), is left out; should max_q_len not be the longest, that kernel has them all the same.
-    const bool many = (long long)a.max_q_len * group > kMostRows;
-    if (many && (long long)a.max_q_len * batch.n_seqs == batch.n_tokens)
-        return launch_kv_attention_many(a, c, batch, 0, dev, s, pdl);
     static std::atomic<unsigned long long> launches{0x5ca1ab1e0000ull};
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;
@@ -899,7 +907,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         if (p.tag == 0) p.tag = 1;
         const int grid = dev.sm_count;
         const bool few = (long long)a.max_q_len * group <= 8;
-        if (many) p.row_limit = kMostRows;
+        if (many) p.row_limit = most;
         // <codes, dims, 8-row tiles, keys a block, blocks a step, warps, ring stages>
 #define W4A16_FEW(KT)                                                                                              \
     if (keys == 32)                                                                                                \
@@ -920,12 +928,12 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
 #undef W4A16_FEW
         if (e != cudaSuccess) return e;
     }
-    return many ? launch_kv_attention_many(a, c, batch, kMostRows, dev, s, pdl) : cudaSuccess;
+    return many ? launch_kv_attention_many(a, c, batch, most, dev, s, pdl) : cudaSuccess;
 }
 
 long long kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int, int n_tokens, const DeviceInfo &dev) {
-    if ((long long)n_tokens * (n_heads / n_kv_heads) > kMostRows) return kv_attention_many_workspace(head_dim, dev);
-    return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * kMostRows * (head_dim + 2) * 4;
+    if ((long long)n_tokens * (n_heads / n_kv_heads) > kTileRows) return kv_attention_many_workspace(head_dim, dev);
+    return (long long)((dev.sm_count + 1) & ~1) * 8 + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4;
 }
 
 }  // namespace w4a16
