@@ -46,9 +46,10 @@
  * w4a16_debug_set_config(3, {0}, 1)).
  *
  * Kernel-selection log: with the environment variable W4A16_LOG=1 (read on
- * the first call on a device) each GEMM entry point prints the kernel it
- * launched -- path, kernel, its configuration, grid, early start, epilogue
- * -- to stderr, each distinct line once; W4A16_LOG=2 prints every call.
+ * the first call on a device) each GEMM entry point, and w4a16_kv_attention,
+ * prints the kernel it launched -- path, kernel, its configuration, grid,
+ * early start, epilogue -- to stderr, each distinct line once; W4A16_LOG=2
+ * prints every call.
  *
  * Errors: arguments are validated on the host before anything is launched;
  * an invalid call returns a negative w4a16_status_t and launches nothing.

@@ -57,6 +57,16 @@ def test_window_and_sinks(cuda_lib, window, sinks, new):
     check(cuda_lib, Problem(lens, [new] * len(lens), seed=window + sinks + new), window, sinks)
 
 
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [[4, 4], [5, 5], [8, 8], [9, 9], [1, 4, 5, 8, 9, 0, 40]])
+def test_rows_around_the_kernels_limits(cuda_lib, new, dim, page):
+    """16, 20, 32 and 36 rows a kv head: one tile or two of the few-rows kernel, or the other kernel's."""
+    lens = [n + past for n, past in zip(new, [300, 0, 77, 1000, 15, 60, 129])]
+    check(cuda_lib, Problem(lens, new, 8, 2, dim, page, "int8", "heads", "bf16", seed=sum(new) + dim))
+    check(cuda_lib, Problem(lens, new, 8, 2, dim, page, "e4m3", "tokens", "f16", seed=sum(new) + page), 50, 3)
+
+
 @pytest.mark.parametrize("new", [[2], [3, 0, 1], [16, 17], [0, 33, 0], [64, 1, 65], [1, 200, 7]])
 @pytest.mark.parametrize("heads, kv_heads, dim", [(8, 2, 128), (2, 2, 64), (14, 2, 128), (16, 1, 64)])
 def test_several_tokens(cuda_lib, new, heads, kv_heads, dim):

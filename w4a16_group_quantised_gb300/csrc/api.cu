@@ -481,6 +481,10 @@ bool pdl_enabled() {
 
 int device_info(const DeviceInfo **out) { return get_device(out); }
 
+bool kernel_log_on() {
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    return g_log > 0;
+}
 void log_kernel_selection(const char *line) { log_selection(line); }
 
 bool pdl_for_stream(cudaStream_t s) {

@@ -134,10 +134,11 @@ cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_
                               void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
 long long kv_pool_workspace(int n_pages);
 
-// ---- api.cu helpers used by kv_api.cu: the current device's state (W4A16_OK
+// ---- api.cu helpers used by kv_api.cu and kv_attention.cu: the current device's state (W4A16_OK
 // or an error), the early-launch switch, the kernel-selection log
 int device_info(const DeviceInfo **out);
 bool pdl_enabled();
+bool kernel_log_on();
 void log_kernel_selection(const char *line);
 
 // ---- api.cu helpers used by noalloc.cu

