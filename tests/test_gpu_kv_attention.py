@@ -57,6 +57,15 @@ def test_window_and_sinks(cuda_lib, window, sinks, new):
     check(cuda_lib, Problem(lens, [new] * len(lens), seed=window + sinks + new), window, sinks)
 
 
+@pytest.mark.parametrize("lens", [[30000], [20011, 9999], [17000, 0, 17777, 16000], [40000, 12]])
+@pytest.mark.parametrize("heads, kv_heads, new", [(8, 2, 1), (4, 1, 1), (8, 8, 1), (16, 2, 2)])
+def test_few_long_sequences_token_first(cuda_lib, lens, heads, kv_heads, new):
+    """Tiles of one sequence cut into the same number of pieces, or not where that would be uneven."""
+    news = [min(new, n) for n in lens]
+    check(cuda_lib, Problem(lens, news, heads, kv_heads, 128, 64, "e4m3", "tokens", "f16", seed=len(lens)))
+    check(cuda_lib, Problem(lens, news, heads, kv_heads, 64, 16, "int8", "tokens", "bf16", seed=kv_heads))
+
+
 @pytest.mark.parametrize("page", [16, 32])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("new", [[4, 4], [5, 5], [8, 8], [9, 9], [1, 4, 5, 8, 9, 0, 40]])

@@ -37,8 +37,8 @@
 //    Tickets carry the launch's number, so scratch needs no initialisation.
 //
 // Measured (32 query heads on 8 kv heads, 128 dims): 4 sequences of 98302 to
-// 131071 keys, e4m3, pages of 64: 156 us for 1.0 GB, 6.4 TB/s, 0.95 of a copy's
-// bandwidth.  64 sequences of 4 to 4096 keys, int8, pages of 16: 59 us for 273
+// 131071 keys, e4m3, pages of 64: 154 us for 1.0 GB, 6.5 TB/s, 0.96 of a copy's
+// bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys, int8, pages of 16: 59 us for 273
 // MB, 4.6 TB/s; the arithmetic pipes are 39 % busy and 1.7 instructions a cycle
 // go out, about 390 for 16 keys, most of them conversions; about 5 us go by
 // before the first key and 8 after the last.  One sequence of 77 keys: 8.5 us,
@@ -58,6 +58,7 @@ namespace {
 constexpr int kMaxSeqs = 512;             // sequences of a launch
 constexpr int kShort = 256;               // tiles of up to so many keys stay in one CTA
 constexpr int kLeast = 2;                 // fewest steps worth a CTA
+constexpr int kFewSeqs = 16;              // so many sequences may have their tiles cut alike
 constexpr int kTileCost = 32;             // keys that the start and end of a tile count for in the shares
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     long long *s_scan = reinterpret_cast<long long *>(smem + L::kMisc), *s_cut = s_scan + NW;
     int &s_abort = *reinterpret_cast<int *>(s_cut + NW + 1);
     int *s_out = &s_abort + 1, *s_from = s_out + 2, *s_to = s_from + 2;      // tiles shared with other CTAs
+    int &s_alike = s_to[2];
     int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
     long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
     int *tiles_before = reinterpret_cast<int *>(smem + L::kTiles);
@@ -277,7 +279,42 @@ __global__ void __launch_bounds__(32 * NW, 1)
         // past the last tile of a sequence that has any, the next one's first step
         return pre[b] + (long long)idx * steps + min(max(st - COST, 0), steps);
     };
-    if (warp == 0) {
+    // Where a page's tokens hold all heads side by side, warps that go through the same keys of different heads
+    // should do so at the same time, or every stretch of 1 KB or so is fetched in pieces (4 sequences of 98302 to
+    // 131071 keys of 8 heads: 175 us).  So with few long tiles those of one sequence get the same whole number of
+    // warps' pieces, as near to equal shares as that allows (160 us; head by head, where a head's tokens are
+    // contiguous, equal shares take 154).
+    const int pieces = (int)ctas * NW;
+    auto pieces_of = [&](int b, int done, long long each) {        // a tile's, of sequence b, `done` pieces before it
+        const int tiles = max(seqs[b].w * Hk, 1);
+        const long long end = pre[b] + (long long)tiles_before[b] * COST + seqs[b].w * Hk * each;
+        return (int)min((end * pieces / total - done + tiles / 2) / tiles, (long long)(pieces - done) / tiles);
+    };
+    const bool alike = p.token_first && B <= kFewSeqs && tiles_all * 16 <= pieces;
+    if (alike && warp == 0) {
+        const int i = blockIdx.x * NW + min(lane, NW);
+        long long at = total - (long long)tiles_all * COST;        // the line's end
+        bool fits = true;
+        int done = 0;
+        for (int b = 0; b < B; ++b) {
+            const int tiles = seqs[b].w * Hk, steps = span(seqs[b].y, seqs[b].z).steps, each = steps + COST;
+            if (tiles == 0) continue;
+            const int n = pieces_of(b, done, each);
+            // pieces of some length, and hardly longer than an equal share
+            fits = fits && n >= 8 && each >= n * (4 + COST) && (long long)each * pieces * 25 <= n * total * 26;
+            if (!fits) break;
+            if (i >= done && i < done + tiles * n) {
+                const int tile = (i - done) / n, k = (i - done) % n;
+                at = pre[b] + (long long)tile * steps + max((int)((long long)each * k / n) - COST, 0);
+            }
+            done += tiles * n;
+        }
+        if (lane <= NW) s_cut[lane] = at;
+        if (lane == 0) s_alike = fits;
+    }
+    if (alike) __syncthreads();
+    const bool by_tile = alike && s_alike;
+    if (!by_tile && warp == 0) {
         long long v = ((long long)blockIdx.x + min(lane, 1)) * total / ctas, moved;
         const long long end = step_of(v, true, moved);
         const long long v0 = __shfl_sync(0xffffffffu, moved, 0), v1 = __shfl_sync(0xffffffffu, moved, 1);
@@ -754,8 +791,18 @@ __global__ void __launch_bounds__(32 * NW, 1)
             const long long begin = c0 + sh.begin + (long long)(tiles_before[b] + idx) * COST;
             const long long end = begin + sh.end - sh.begin + COST;
             // the last CTA whose share begins by the tile's first step, and by its last
-            const int from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
-            const int to = (int)((end * ctas + total - 1) / total - 1);
+            int from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
+            int to = (int)((end * ctas + total - 1) / total - 1);
+            if (by_tile) {
+                int done = 0, n = 0;
+                for (int i = 0; i <= b; ++i) {
+                    if (seqs[i].w == 0) continue;
+                    n = pieces_of(i, done, span(seqs[i].y, seqs[i].z).steps + COST);
+                    if (i < b) done += n * seqs[i].w * Hk;
+                }
+                from = (done + idx * n) / NW;
+                to = (done + idx * n + n - 1) / NW;
+            }
             __threadfence();                                       // after the barrier: for the whole CTA's parts
             unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
             do {
