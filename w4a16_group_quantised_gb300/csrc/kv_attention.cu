@@ -38,10 +38,11 @@
 //
 // Measured (32 query heads on 8 kv heads, 128 dims): 4 sequences of 98302 to
 // 131071 keys, e4m3, pages of 64: 154 us for 1.0 GB, 6.5 TB/s, 0.96 of a copy's
-// bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys, int8, pages of 16: 59 us for 273
-// MB, 4.6 TB/s; the arithmetic pipes are 39 % busy and 1.7 instructions a cycle
-// go out, about 390 for 16 keys, most of them conversions; about 5 us go by
-// before the first key and 8 after the last.  One sequence of 77 keys: 8.5 us,
+// bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys, int8, pages of 16: 58 us for 273
+// MB, 4.7 TB/s (5.6 between the first key and the last); the arithmetic pipes
+// are 39 % busy and 1.7 instructions a cycle go out, about 390 for 16 keys, most
+// of them conversions; about 4 us go by before the first key and 8 after the
+// last.  One sequence of 77 keys: 8.5 us,
 // a chain of dependent loads.
 #include <cuda.h>
 
@@ -116,7 +117,7 @@ struct FewSmem {
     static constexpr int kBars = kTiles + kMaxSeqs * 4;
     static constexpr int kShared = kBars + NW * NS * 8;            // tiles that warps share: the CTA's first, then by warp
     static constexpr int kMisc = kShared + (NW + 1) * 32;
-    static constexpr int kEnd = kMisc + (2 * NW + 1) * 8 + 32 + 1024;       // 1024: slack to align the base
+    static constexpr int kEnd = kMisc + (2 * NW + 1) * 8 + 32 + (NW + 2) * 4 + 1024;       // 1024: slack to align the base
     static_assert(NS * kStage >= kPart * 4, "the last piece is parked in the ring");
 };
 
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     long long *s_scan = reinterpret_cast<long long *>(smem + L::kMisc), *s_cut = s_scan + NW;
     int &s_abort = *reinterpret_cast<int *>(s_cut + NW + 1);
     int *s_out = &s_abort + 1, *s_from = s_out + 2, *s_to = s_from + 2;      // tiles shared with other CTAs
-    int &s_alike = s_to[2];
+    int &s_alike = s_to[2], *s_seq = s_to + 3;
     int4 *seqs = reinterpret_cast<int4 *>(smem + L::kSeq);
     long long *pre = reinterpret_cast<long long *>(smem + L::kPre);
     int *tiles_before = reinterpret_cast<int *>(smem + L::kTiles);
@@ -249,9 +250,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
     __syncthreads();
     if (total == 0) return;
 
-    // the sequence of a position of the line: of steps alone (cost = 0), or with the tiles' cost
-    auto find = [&](long long at, int cost = 0) {
-        int lo = 0, hi = B - 1;
+    // the sequence, one of lo..hi, of a position of the line: of steps alone (cost = 0), or with the tiles' cost
+    auto find = [&](long long at, int cost, int lo, int hi) {
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (pre[mid] + (long long)tiles_before[mid] * cost <= at) lo = mid;
@@ -263,9 +263,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
     if (blockIdx.x >= ctas) return;
     // The step where an equal share of the work begins: `at` steps and tiles' costs into the line.  In a
     // short tile, when `snap`, the tile's first; *moved is where that is with the costs.
-    auto step_of = [&](long long at, bool snap, long long &moved) {
+    auto step_of = [&](long long at, bool snap, long long &moved, int lo, int hi, int &b) {
         moved = at;
-        const int b = find(at, COST);
+        b = find(at, COST, lo, hi);
         const int4 s = seqs[b];
         const Span sp = span(s.y, s.z);
         const int steps = sp.steps;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         const int i = blockIdx.x * NW + min(lane, NW);
         long long at = total - (long long)tiles_all * COST;        // the line's end
         bool fits = true;
-        int done = 0;
+        int done = 0, of = B - 1;
         for (int b = 0; b < B; ++b) {
             const int tiles = seqs[b].w * Hk, steps = span(seqs[b].y, seqs[b].z).steps, each = steps + COST;
             if (tiles == 0) continue;
@@ -306,22 +306,26 @@ __global__ void __launch_bounds__(32 * NW, 1)
             if (i >= done && i < done + tiles * n) {
                 const int tile = (i - done) / n, k = (i - done) % n;
                 at = pre[b] + (long long)tile * steps + max((int)((long long)each * k / n) - COST, 0);
+                of = b;
             }
             done += tiles * n;
         }
-        if (lane <= NW) s_cut[lane] = at;
+        if (lane <= NW) s_cut[lane] = at, s_seq[lane] = of;
         if (lane == 0) s_alike = fits;
     }
     if (alike) __syncthreads();
     const bool by_tile = alike && s_alike;
     if (!by_tile && warp == 0) {
         long long v = ((long long)blockIdx.x + min(lane, 1)) * total / ctas, moved;
-        const long long end = step_of(v, true, moved);
+        int of;
+        const long long end = step_of(v, true, moved, 0, B - 1, of);
+        const int of0 = __shfl_sync(0xffffffffu, of, 0), of1 = __shfl_sync(0xffffffffu, of, 1);
         const long long v0 = __shfl_sync(0xffffffffu, moved, 0), v1 = __shfl_sync(0xffffffffu, moved, 1);
         const long long c0 = __shfl_sync(0xffffffffu, end, 0), c1 = __shfl_sync(0xffffffffu, end, 1);
         if (lane <= NW) {
-            const long long mid = step_of(v0 + (v1 - v0) * lane / NW, false, moved);
+            const long long mid = step_of(v0 + (v1 - v0) * lane / NW, false, moved, of0, of1, of);
             s_cut[lane] = lane == 0 ? c0 : lane == NW ? c1 : min(max(mid, c0), c1);
+            s_seq[lane] = of;                                      // what is in a warp's piece is of s_seq[warp]..s_seq[warp + 1]
         }
     }
     __syncthreads();
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     const int mine = (int)(s_cut[NW] - c0);
     if (mine <= 0) return;
     auto warp_start = [&](int w) { return (int)(s_cut[w] - c0); };
-    const int w0 = warp_start(warp), w1 = warp_start(warp + 1);
+    const int w0 = warp_start(warp), w1 = warp_start(warp + 1), seq_lo = s_seq[warp], seq_hi = s_seq[warp + 1];
 
     // ---- blocks looked up a lane each, those of LOOK steps: first the page id, then, once it is here, the scales
     auto look_up = [&](int at) {
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         at += lane / BPS;
         if (at < w1) {
             const long long line = c0 + at;
-            const int b = find(line);
+            const int b = find(line, 0, seq_lo, seq_hi);
             const int4 s = seqs[b];
             const Span sp = span(s.y, s.z);
             const long long rem = line - pre[b];
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     auto load_rows = [&](int at) {
         Tile tl;
         const long long line = c0 + at;
-        const int b = find(line);
+        const int b = find(line, 0, seq_lo, seq_hi);
         const int4 s = seqs[b];
         const int steps = span(s.y, s.z).steps;
         const long long rem = line - pre[b];
@@ -786,7 +790,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         if (tid < 2 && out[tid]) {
             const Shared sh = shared[s_out[tid]];
             // with the costs, the tile begins and ends at
-            const int b = find(c0 + sh.begin);
+            const int b = find(c0 + sh.begin, 0, s_seq[0], s_seq[NW]);
             const int idx = line_div(c0 + sh.begin - pre[b], sh.end - sh.begin);
             const long long begin = c0 + sh.begin + (long long)(tiles_before[b] + idx) * COST;
             const long long end = begin + sh.end - sh.begin + COST;
