@@ -38,12 +38,12 @@
 //
 // Measured (32 query heads on 8 kv heads, 128 dims): 4 sequences of 98302 to
 // 131071 keys, e4m3, pages of 64: 154 us for 1.0 GB, 6.5 TB/s, 0.96 of a copy's
-// bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys, int8, pages of 16: 58 us for 273
-// MB, 4.7 TB/s (5.6 between the first key and the last); the arithmetic pipes
-// are 39 % busy and 1.7 instructions a cycle go out, about 390 for 16 keys, most
-// of them conversions; about 4 us go by before the first key and 8 after the
-// last.  One sequence of 77 keys: 8.5 us,
-// a chain of dependent loads.
+// bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys,
+// int8, pages of 16: 58 us for 273 MB, 4.7 TB/s (5.6 between the first key and
+// the last); the arithmetic pipes are 39 % busy and 1.7 instructions a cycle go
+// out, about 390 for 16 keys, most of them conversions; about 4 us go by before
+// the first key and 8 after the last.  One sequence of 77 keys: 8.5 us, a chain
+// of dependent loads.
 #include <cuda.h>
 
 #include <algorithm>
@@ -785,18 +785,21 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
     }
     if (out[0] || out[1]) {
-        __syncthreads();
-        // tickets: which CTAs share the tile follows from where it begins and ends
-        if (tid < 2 && out[tid]) {
-            const Shared sh = shared[s_out[tid]];
+        // tickets: which CTAs share the tile follows from where it begins and ends (a warp that has hardly had
+        // anything to sum: eight rows are 256 pieces at most)
+        const int nth = tid - 32 * (NW - 1);
+        const bool asks = nth >= 0 && nth < 2 && out[nth & 1];
+        int from = 0, to = 0;
+        if (asks) {
+            const Shared sh = shared[s_out[nth]];
             // with the costs, the tile begins and ends at
             const int b = find(c0 + sh.begin, 0, s_seq[0], s_seq[NW]);
             const int idx = line_div(c0 + sh.begin - pre[b], sh.end - sh.begin);
             const long long begin = c0 + sh.begin + (long long)(tiles_before[b] + idx) * COST;
             const long long end = begin + sh.end - sh.begin + COST;
             // the last CTA whose share begins by the tile's first step, and by its last
-            int from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
-            int to = (int)((end * ctas + total - 1) / total - 1);
+            from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
+            to = (int)((end * ctas + total - 1) / total - 1);
             if (by_tile) {
                 int done = 0, n = 0;
                 for (int i = 0; i <= b; ++i) {
@@ -807,17 +810,22 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 from = (done + idx * n) / NW;
                 to = (done + idx * n + n - 1) / NW;
             }
+        }
+        __syncthreads();
+        if (asks) {
             __threadfence();                                       // after the barrier: for the whole CTA's parts
-            unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
-            do {
+            // the guess that all others have come: right for the last, for whom it counts
+            unsigned long long *tk = p.tickets + from, seen = p.tag << 16 | (unsigned long long)(to - from), put = 0;
+            for (;;) {
+                const unsigned long long old = atomicCAS(tk, seen, put);
+                if (old == seen) break;
                 seen = old;
                 const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
                 put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
-                old = atomicCAS(tk, seen, put);
-            } while (old != seen);
+            }
             __threadfence();
-            s_from[tid] = put == 0 ? from : -1;
-            s_to[tid] = to;
+            s_from[nth] = put == 0 ? from : -1;
+            s_to[nth] = to;
         }
     }
     // those within the CTA: each by the warp that holds the first part
