@@ -134,9 +134,15 @@ def _act(t):
     return W4A16_BF16 if t.dtype is torch.bfloat16 else W4A16_F16 if t.dtype is torch.float16 else _dtype_code(t)
 
 
+@functools.lru_cache(maxsize=None)
+def _device(index):
+    # an index in a call's place costs torch more than the object: 1.8 us an allocation
+    return torch.device("cuda", index)
+
+
 def _output(name, t, shape, dtype, device):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=_device(device))
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
             and t.dim() == len(shape)):
         _refuse(name, t, dtype, len(shape), device)
@@ -145,10 +151,26 @@ def _output(name, t, shape, dtype, device):
     return t
 
 
-def _scratch(workspace, need, device, stream):
-    """(workspace tensor, its address, its bytes): the caller's, or one from torch's allocator."""
+class _Block:
+    """Scratch of a stream from torch's allocator, given back with the object (2 us less than a tensor)."""
+    __slots__ = ("at",)
+
+    def __init__(self, size, stream):
+        self.at = 0
+        self.at = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, stream)
+
+    def __del__(self):
+        if self.at:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(self.at)
+
+
+def _scratch(workspace, need, device, stream, handle):
+    """(what holds the scratch, its address, its bytes): the caller's tensor, or from torch's allocator."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if torch._C._cuda_getDevice() == device:
+            block = _Block(need, handle)
+            return block, block.at, need
+        workspace = torch.empty(need, dtype=torch.uint8, device=_device(device))
         if stream is not None:
             workspace.record_stream(stream)
         return workspace, workspace.data_ptr(), need
@@ -201,10 +223,11 @@ def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int,
     if lse is not None:
         _output("lse", lse, (T, H), torch.float32, dev)
     b, n = _batch(block_table, kv_lens, q_starts, T, dev)
-    ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, stream)
+    handle = _stream(stream, dev)
+    ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, stream, handle)
     _check("w4a16_kv_attention", load_library().w4a16_kv_attention(
         q.data_ptr(), sq, H, c, b, max_q_len, dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), dt, at, size, _stream(stream, dev)))
+        None if lse is None else lse.data_ptr(), dt, at, size, handle))
     return out
 
 
@@ -255,9 +278,10 @@ def w4a16_kv_fork(cache, block_table, kv_lens, refcount, parents, children, work
     a, b = _ints("parents", parents, 1, dev), _ints("children", children, 1, dev)
     if parents.shape[0] != children.shape[0]:
         raise ValueError("parents and children must have the same length")
-    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream)
+    handle = _stream(stream, dev)
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream, handle)
     _check("w4a16_kv_fork", load_library().w4a16_kv_fork(
-        c, table, lens, rows, width, counts, a, b, parents.shape[0], at, size, _stream(stream, dev)))
+        c, table, lens, rows, width, counts, a, b, parents.shape[0], at, size, handle))
 
 
 def w4a16_kv_free(block_table, kv_lens, refcount, seqs, stream=None):
@@ -288,6 +312,7 @@ def w4a16_kv_compact(cache, block_table, refcount, n_live=None, workspace=None, 
     live = None if n_live is None else _ints("n_live", n_live, 1, dev)
     if n_live is not None and n_live.shape[0] != 1:
         raise ValueError(f"n_live must be [1], got {list(n_live.shape)}")
-    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream)
+    handle = _stream(stream, dev)
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream, handle)
     _check("w4a16_kv_compact", load_library().w4a16_kv_compact(
-        c, table, rows, width, counts, live, at, size, _stream(stream, dev)))
+        c, table, rows, width, counts, live, at, size, handle))
