@@ -39,10 +39,10 @@
 // Measured (32 query heads on 8 kv heads, 128 dims): 4 sequences of 98302 to
 // 131071 keys, e4m3, pages of 64: 154 us for 1.0 GB, 6.5 TB/s, 0.96 of a copy's
 // bandwidth (tokens before heads: 159 us).  64 sequences of 4 to 4096 keys,
-// int8, pages of 16: 58 us for 273 MB, 4.7 TB/s (5.6 between the first key and
+// int8, pages of 16: 57 us for 273 MB, 4.8 TB/s (5.6 between the first key and
 // the last); the arithmetic pipes are 39 % busy and 1.7 instructions a cycle go
 // out, about 390 for 16 keys, most of them conversions; about 4 us go by before
-// the first key and 8 after the last.  One sequence of 77 keys: 8.5 us, a chain
+// the first key and 6 after the last.  One sequence of 77 keys: 8.5 us, a chain
 // of dependent loads.
 #include <cuda.h>
 
