@@ -142,3 +142,24 @@ def test_bad_device_arguments_touch_nothing(cuda_lib):
     k, v = w.w4a16_kv_read(cache, bad, lens, starts, 4, torch.float16)
     assert reported()
     assert bool((k[0] == 0).all()) or bool((k[1] == 0).all())
+
+
+def test_more_units_than_a_grid_has_rows(cuda_lib):
+    """70000 sequences of one token: the kernel's pages go on in a second plane of its grid."""
+    w, n = cuda_lib, 70000
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((n, 2, 64), generator=g).half()
+    k = torch.zeros((n, 1, 16, 64), dtype=torch.int8, device="cuda")
+    v, ks, vs = torch.zeros_like(k), torch.zeros((n, 1), device="cuda"), torch.zeros((n, 1), device="cuda")
+    cache = w.KVCache(k, v, ks, vs)
+    table = torch.arange(n, dtype=torch.int32, device="cuda").flip(0).unsqueeze(1).contiguous()
+    lens = torch.ones(n, dtype=torch.int32, device="cuda")
+    starts = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    rows = x.cuda()
+    w.w4a16_kv_append(cache, rows[:, :1], rows[:, 1:], table, lens, starts)
+    got = w.w4a16_kv_read(cache, table, lens, starts, n, torch.float16)
+    for have, want in zip(got, (x[:, :1].double(), x[:, 1:].double())):
+        step = want.abs().amax(dim=-1, keepdim=True) / 127
+        # half a step, a little more for the two roundings before the code's, and the output's own
+        assert bool(((have.cpu().double() - want).abs() <= step * (0.5 + 2.0 ** -14) + want.abs() * 2.0 ** -10).all())
+    assert w.w4a16_last_device_error() == 0

@@ -7,6 +7,8 @@
 // and when s > s_old the older codes are rounded again against s.  The
 // products and the division are fp32: RN(1 / s) is one rounding away from
 // 1 / s, far below half a code step, so one reciprocal serves a whole block.
+#include <algorithm>
+
 #include "kv.cuh"
 
 namespace w4a16 {
@@ -54,15 +56,16 @@ __device__ __forceinline__ int warp_find(int n, int at, Key key) {
 // loads (starts, then values and page id together, then the scales), and how
 // much is on its way during one: K and V apart, 32 bytes a thread, took 28 us
 // where both together take 23 us for 15,200 tokens of 8 heads.
-// That call with its read-back takes 38 us against 28 us for its bytes at a
-// copy's bandwidth; 64 sequences' single tokens take 6.8 us.
+// That call with its read-back takes 37 us against 28 us for its bytes at a
+// copy's bandwidth; 64 sequences' single tokens take 6.5 us.
+constexpr int kRows = 65535;               // of a grid: units go on in the next plane
 template <int DT, int KT>
 __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long long k_stride, const uint16_t *v_new,
                               long long v_stride, int *status) {
     kv_begin();
     __shared__ uint32_t warp_max[2][32];
     const int shift = c.page_shift;
-    const int unit = blockIdx.x, head = blockIdx.y;
+    const int unit = blockIdx.z * kRows + blockIdx.y, head = blockIdx.x;
     const int i = warp_find(b.n_seqs, unit, [&](int j) { return append_base(b, shift, j); });
     const KvSeq s = kv_sequence(b, shift, i, status);
     const int first = s.len - s.n;                       // position of the first new token
@@ -107,7 +110,8 @@ __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long 
     const long long at = page * c.page_stride + head * c.head_stride + slot * c.token_stride + d0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        for (int w = 0; w < (int)blockDim.x / 32; ++w) top[t] = max(top[t], warp_max[t][w]);
+        const int lane = threadIdx.x & 31;
+        top[t] = __reduce_max_sync(0xffffffffu, lane < (int)blockDim.x / 32 ? warp_max[t][lane] : 0u);
         const float need = __fdiv_rn(kv_act<DT>((uint16_t)top[t]), kv_qmax<KT>());
         float s_new = need <= s_old[t] ? s_old[t] : need;    // a NaN on either side stays
         if (s_old[t] != s_old[t]) s_new = s_old[t];
@@ -195,7 +199,10 @@ cudaError_t launch_kv_append(const KvCache &c, const KvBatch &b, const void *k_n
                              const void *v_new, long long v_stride, int dtype, const DeviceInfo &dev, cudaStream_t s,
                              bool pdl) {
     const int ps = 1 << c.page_shift;
-    const dim3 grid((b.n_tokens >> c.page_shift) + 2 * b.n_seqs, c.n_kv_heads);
+    // heads next to one another: they read neighbouring bytes of the same rows (38 us for the call above where
+    // units come first)
+    const int units = (b.n_tokens >> c.page_shift) + 2 * b.n_seqs;
+    const dim3 grid(c.n_kv_heads, std::min(units, kRows), (units + kRows - 1) / kRows);
     const dim3 block(ps * c.head_dim / 16);
     auto kern = dtype == 0 ? (c.kv_dtype == kKvInt8 ? append_kernel<0, kKvInt8> : append_kernel<0, kKvE4m3>)
                            : (c.kv_dtype == kKvInt8 ? append_kernel<1, kKvInt8> : append_kernel<1, kKvE4m3>);
