@@ -307,11 +307,12 @@ __global__ void plan_kernel(CompactScratch w, int n_pages, int *n_live) {
     }
     before = block_sum(before, scratch);
     const int m = block_sum(all, scratch);
-    // in-use pages below m: whole chunks, then the words of the chunk that holds m
+    // in-use pages below m: whole chunks, then the words of the chunk that holds m (none when m is all chunks' end; a
+    // full pool's m is in its last chunk unless that is full too)
     int below = 0;
     for (int i = threadIdx.x; i < min(m / kChunk, n_chunks); i += blockDim.x) below += w.counts[i];
     const int w0 = m / kChunk * (kChunk / 32), wm = m >> 5;
-    if (m < n_pages) {
+    if (m < n_chunks * kChunk) {
         for (int i = w0 + threadIdx.x; i < wm; i += blockDim.x) below += __popc(w.bits[i]);
         if (threadIdx.x == 0) below += __popc(w.bits[wm] & ((1u << (m & 31)) - 1));
     }
