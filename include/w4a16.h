@@ -429,8 +429,10 @@ typedef enum {
 } w4a16_kv_dtype_t;
 
 /* Smallest scale the append stores (that of a block of zeros): 2^-60.  Every
- * scale of a page in use must be positive; a block whose values are not
- * finite gets a scale that is not, and attention that sees it gives NaN. */
+ * scale of a page in use must be positive, and every code finite (no e4m3
+ * NaN).  A block with a value that is not finite gets a scale that is not and
+ * codes of 0: attention of tokens that see it gives NaN, that of others is
+ * not touched by it. */
 #define W4A16_KV_SCALE_MIN 8.673617379884035e-19f
 
 typedef struct {

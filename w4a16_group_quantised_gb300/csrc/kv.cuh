@@ -71,8 +71,8 @@ __device__ __forceinline__ void kv_decode4(uint32_t w, float (&v)[4]) {
 
 // Four values as a word of codes: to the nearest, ties to even.  int8: adding
 // 1.5 * 2^23 rounds to an integer whose low byte is the code; |v| <= 127 (a
-// block's scale is its largest value's), so nothing needs saturating.  A value
-// that is not finite gives any code: its block's scale says so.
+// block's scale is its largest value's), so nothing needs saturating.  What a
+// value that is not finite gives is the caller's to replace.
 template <int KT>
 __device__ __forceinline__ uint32_t kv_encode4(float a, float b, float c, float d) {
     if (KT == kKvInt8) {

@@ -7,6 +7,9 @@
 // and when s > s_old the older codes are rounded again against s.  The
 // products and the division are fp32: RN(1 / s) is one rounding away from
 // 1 / s, far below half a code step, so one reciprocal serves a whole block.
+// A block with a value that is not finite gets a scale that is not, and codes
+// of 0: the scale tells whoever sees the block (0 * inf is NaN), while a NaN
+// code would also reach rows that do not, through a weight of 0.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -117,6 +120,7 @@ __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long 
         if (s_old[t] != s_old[t]) s_new = s_old[t];
         if (s_new < kKvScaleMin) s_new = kKvScaleMin;
         const float r = __frcp_rn(s_new);
+        const bool finite = s_new < INFINITY;
         uint8_t *dst = (t ? c.v : c.k) + at;
         uint4 o;
         uint32_t *ow = &o.x;
@@ -127,7 +131,7 @@ __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long 
                 ow[j] = kv_encode4<KT>(__fmul_rn(kv_act<DT>((uint16_t)lo), r), __fmul_rn(kv_act<DT>((uint16_t)(lo >> 16)), r),
                                        __fmul_rn(kv_act<DT>((uint16_t)hi), r), __fmul_rn(kv_act<DT>((uint16_t)(hi >> 16)), r));
             }
-            *reinterpret_cast<uint4 *>(dst) = o;
+            *reinterpret_cast<uint4 *>(dst) = finite ? o : make_uint4(0, 0, 0, 0);
         } else if (slot < old && s_new != s_old[t]) {
             const uint4 q = *reinterpret_cast<const uint4 *>(dst);
             const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
@@ -138,7 +142,7 @@ __global__ void append_kernel(KvCache c, KvBatch b, const uint16_t *k_new, long 
                 ow[j] = kv_encode4<KT>(__fmul_rn(__fmul_rn(v[0], s_old[t]), r), __fmul_rn(__fmul_rn(v[1], s_old[t]), r),
                                        __fmul_rn(__fmul_rn(v[2], s_old[t]), r), __fmul_rn(__fmul_rn(v[3], s_old[t]), r));
             }
-            *reinterpret_cast<uint4 *>(dst) = o;
+            *reinterpret_cast<uint4 *>(dst) = finite ? o : make_uint4(0, 0, 0, 0);
         }
         if (threadIdx.x == 0) (t ? c.v_scale : c.k_scale)[at_scale] = s_new;
     }
