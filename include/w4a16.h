@@ -447,13 +447,16 @@ typedef struct {
 /* The sequences of a call.  Sequence b brings q_starts[b+1] - q_starts[b]
  * tokens (0 is fine), rows q_starts[b].. of the call's token tensors: its
  * newest, at positions kv_lens[b] - that many .. kv_lens[b] - 1.  All on the
- * device. */
+ * device.  Rows before q_starts[0] and from q_starts[n_seqs] on are no
+ * sequence's (a captured call replayed with fewer tokens): nothing of them is
+ * appended, and w4a16_kv_read and w4a16_kv_attention give zeros for them, a
+ * log-sum-exp of -inf. */
 typedef struct {
     const int32_t *block_table; /* [n_seqs, max_blocks]; entries no token needs may hold anything */
     const int32_t *kv_lens;     /* [n_seqs], the call's own tokens included                       */
-    const int32_t *q_starts;    /* [n_seqs + 1], from 0, non-decreasing                           */
+    const int32_t *q_starts;    /* [n_seqs + 1], non-decreasing, within [0, n_tokens]             */
     int n_seqs, max_blocks;
-    int n_tokens;               /* rows of the token tensors, q_starts[n_seqs]                    */
+    int n_tokens;               /* rows of the token tensors                                      */
 } w4a16_kv_batch_t;
 
 /* Quantise the batch's new keys and values into their pages.  k_new, v_new:

@@ -44,6 +44,18 @@ __device__ __forceinline__ int kv_page(const KvCache &c, const KvBatch &b, int i
     return -1;
 }
 
+// Rows of the output that no sequence owns, before `lo` and from `hi` on: zeros,
+// and a log-sum-exp of -inf.  A row a CTA, all CTAs and threads of the launch.
+__device__ __forceinline__ void kv_empty_rows(const KvAttentionArgs &a, const KvBatch &b, int head_dim, int lo, int hi) {
+    const int vecs = a.n_heads * head_dim / 8;
+    for (long long r = blockIdx.x; r < (long long)lo + b.n_tokens - hi; r += gridDim.x) {
+        const long long row = r < lo ? r : r - lo + hi;
+        for (int i = threadIdx.x; i < vecs; i += blockDim.x)
+            static_cast<uint4 *>(a.out)[row * vecs + i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; a.lse && i < a.n_heads; i += blockDim.x) a.lse[row * a.n_heads + i] = -INFINITY;
+    }
+}
+
 // ---- activations
 template <int DT>
 __device__ __forceinline__ float kv_act(uint16_t v) {

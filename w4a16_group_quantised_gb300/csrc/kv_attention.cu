@@ -72,6 +72,7 @@ struct FewParams {
     int row_limit;                        // sequences with more rows a kv head than this are another kernel's (0: none)
     int token_first;                      // tensor map dims are (dim, head, token, page, K or V), not (dim, token, head, ...)
     int merged;                           // one box brings K and V; else the second map brings V
+    int before, after;                    // rows before the first sequence's, after the last one's are this launch's
     int k_at, v_at;                       // where a stage holds K and V, in tiles
     float *parts;                         // [grid][2][ROWS][D + 2]
     unsigned long long *tickets;          // [grid]
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
     }
     __syncthreads();
+    kv_empty_rows(p.a, p.b, D, p.before ? seqs[0].x : 0, p.after ? seqs[B - 1].x + seqs[B - 1].y : p.b.n_tokens);
     if (total == 0) return;
 
     // the sequence, one of lo..hi, of a position of the line: of steps alone (cost = 0), or with the tiles' cost
@@ -979,7 +981,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         b.kv_lens += b0;
         b.q_starts += b0;
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
-        FewParams p{a, c, b, 0, token_first ? 1 : 0, merged ? 1 : 0, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,
+        FewParams p{a, c, b, 0, token_first ? 1 : 0, merged ? 1 : 0, b0 == 0, b0 + b.n_seqs == batch.n_seqs, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,
                     nullptr, nullptr, 0, dev.status};
         p.tickets = static_cast<unsigned long long *>(a.workspace);
         p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));

@@ -68,6 +68,7 @@ struct ManyParams {
     KvBatch b;
     int row_limit;                        // sequences with up to so many rows a kv head are another kernel's
     int half_rows;                        // rows of a half in use: whole tokens, at most 128
+    int before, after;                    // rows before the first sequence's, after the last one's are this launch's
     int pair_first;                       // this launch's pairs: [pair_first, pair_first + kMaxPairs)
     float *parts;                         // [grid][2] parts of a tile
     unsigned long long *tickets;          // [grid]
@@ -472,8 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         pairs += (int)all;
     }
     pairs = min(pairs - p.pair_first, kMaxPairs);
-    if (pairs <= 0) return;
     __syncthreads();
+    if (p.before | p.after)
+        kv_empty_rows(p.a, p.b, D, p.before ? seqs[0].x : 0, p.after ? seqs[B - 1].x + seqs[B - 1].y : p.b.n_tokens);
+    if (pairs <= 0) return;
     long long total = 0;
     for (int base = 0; base < pairs; base += kThreads) {
         const int i = base + tid;
@@ -1254,7 +1257,9 @@ cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c,
         // as many pairs as these sequences can have at most
         const long long pairs = (long long)b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
-            ManyParams p{a, c, b, row_limit, half_rows, (int)first, nullptr, nullptr, 0, dev.status};
+            // with a row limit the other kernel has seen to the rows that no sequence owns
+            const bool mine = row_limit == 0 && first == 0;
+            ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first, nullptr, nullptr, 0, dev.status};
             p.tickets = static_cast<unsigned long long *>(a.workspace);
             p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
             p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
