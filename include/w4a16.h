@@ -520,8 +520,9 @@ int w4a16_kv_copy_pages(const w4a16_kv_cache_t *cache, const int32_t *src, const
  * that is not full is copied into a free one: the children that need one
  * take the free pages in ascending order, child by child.  Without enough of
  * them the children that get none are left empty (row -1, length 0) and the
- * status word reads W4A16_ERR_ARG.  What a child's row named before is not
- * freed.  No row may be a child twice, or both a parent and a child.
+ * status word reads W4A16_ERR_ARG.  Where a parent's own last page is not
+ * there (an id out of range, reported) the child gets none for it.  What a
+ * child's row named before is not freed.  No row may be a child twice, or both a parent and a child.
  * workspace: w4a16_kv_pool_workspace bytes. */
 int w4a16_kv_fork(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *kv_lens, int n_seqs,
                   int max_blocks, int32_t *refcount, const int32_t *parents, const int32_t *children, int n,

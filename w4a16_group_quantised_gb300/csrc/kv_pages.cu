@@ -181,21 +181,27 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
     }
     const int cap = max_blocks << shift;
     const int len = min(max(lens[par], 0), cap);
+    const int full = len >> shift;
+    const int *from = table + (long long)par * max_blocks;
+    // a partly filled last page is copied; where the parent's is not there, the child has none either
     const bool tail = (len & part_mask) != 0;
+    const int src = tail ? from[full] : -1;
+    const bool takes = src >= 0 && src < c.n_pages;
     int fresh = -1;
-    if (tail) {
+    if (takes) {
         int before = 0;                                  // children ahead of this one that take a page
         for (int j = threadIdx.x; j < me; j += blockDim.x) {
             const int p = parents[j], ch = children[j];
-            if (p >= 0 && p < n_seqs && ch >= 0 && ch < n_seqs)
-                before += (min(max(lens[p], 0), cap) & part_mask) != 0;
+            if (p < 0 || p >= n_seqs || ch < 0 || ch >= n_seqs) continue;
+            const int l = min(max(lens[p], 0), cap);
+            if ((l & part_mask) == 0) continue;
+            const int last = table[(long long)p * max_blocks + (l >> shift)];
+            before += last >= 0 && last < c.n_pages;
         }
         before = block_sum(before, scratch);
         fresh = select_bit(free_bits, free_counts, (c.n_pages + kChunk - 1) / kChunk, before, scratch);
     }
-    const bool ok = !tail || fresh >= 0;
-    const int full = len >> shift;
-    const int *from = table + (long long)par * max_blocks;
+    const bool ok = !takes || fresh >= 0;
     int *to = table + (long long)chi * max_blocks;
     for (int k = threadIdx.x; part == 0 && k < max_blocks; k += blockDim.x) {
         int p = -1;
@@ -206,21 +212,17 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
                 p = -1;
             }
             if (p >= 0) atomicAdd(refcount + p, 1);      // a trimmed entry (-1) stays one
-        } else if (ok && tail && k == full) {
+        } else if (k == full) {
             p = fresh;
         }
         to[k] = p;
     }
     if (part == 0 && threadIdx.x == 0) {
         lens[chi] = ok ? len : 0;
-        if (!ok) kv_report(status);
-        else if (tail) refcount[fresh] = 1;
+        if (!ok || (tail && !takes)) kv_report(status);
+        if (fresh >= 0) refcount[fresh] = 1;
     }
-    if (ok && tail) {
-        const int src = from[full];
-        if (src >= 0 && src < c.n_pages) copy_page(c, src, fresh, part, parts);
-        else if (threadIdx.x == 0) kv_report(status);
-    }
+    if (fresh >= 0) copy_page(c, src, fresh, part, parts);
 }
 
 // A table entry that named page p is gone: its count goes down.
