@@ -123,3 +123,22 @@ def test_fork_of_a_last_page_that_is_not_there(cuda_lib):
         if q >= 0:
             named[q] += 1
     assert ref.tolist() == named
+
+
+def test_lengths_past_the_table(cuda_lib):
+    """Fork and trim take what the table holds, and report."""
+    w = cuda_lib
+    p = Problem([48, 40], [0, 0], seed=5)
+    cache, table, lens, _, _ = p.to_cuda(w)
+    ref = torch.zeros(p.n_pages, dtype=torch.int32, device="cuda")
+    ref[table[table >= 0].long()] = 1
+    lens[0] = 1000                                        # the table has three blocks
+    t = table.clone()
+    w.w4a16_kv_trim(table, lens, ref, 16, 17, 0)
+    assert reported(w)
+    assert table[0].tolist() == [-1, -1, int(t[0, 2])] and table[1].tolist() == [-1] + t[1, 1:].tolist()
+    rows = torch.cat([t, torch.full_like(t[:1], -1)])
+    lens = torch.tensor([1000, 40, 0], dtype=torch.int32, device="cuda")
+    w.w4a16_kv_fork(cache, rows, lens, ref, torch.tensor([0], dtype=torch.int32).cuda(), torch.tensor([2], dtype=torch.int32).cuda())
+    assert reported(w)
+    assert rows[2].tolist() == t[0].tolist() and lens.tolist() == [1000, 40, 48]

@@ -180,7 +180,7 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
         return;
     }
     const int cap = max_blocks << shift;
-    const int len = min(max(lens[par], 0), cap);
+    const int said = lens[par], len = min(max(said, 0), cap);
     const int full = len >> shift;
     const int *from = table + (long long)par * max_blocks;
     // a partly filled last page is copied; where the parent's is not there, the child has none either
@@ -219,7 +219,7 @@ __global__ void fork_kernel(KvCache c, int *table, int *lens, int n_seqs, int ma
     }
     if (part == 0 && threadIdx.x == 0) {
         lens[chi] = ok ? len : 0;
-        if (!ok || (tail && !takes)) kv_report(status);
+        if (!ok || (tail && !takes) || len != said) kv_report(status);
         if (fresh >= 0) refcount[fresh] = 1;
     }
     if (fresh >= 0) copy_page(c, src, fresh, part, parts);
@@ -254,7 +254,8 @@ __global__ void trim_kernel(int *table, const int *lens, int max_blocks, int *re
                             int window, int sinks, int *status) {
     kv_begin();
     const int i = blockIdx.x, ps = 1 << shift;
-    const int len = min(max(lens[i], 0), max_blocks << shift);
+    const int said = lens[i], len = min(max(said, 0), max_blocks << shift);
+    if (len != said && threadIdx.x == 0) kv_report(status);
     // blocks [lo, hi) lie whole in positions [sinks, len - window + 1)
     const int lo = (int)(((long long)sinks + ps - 1) >> shift);
     const int hi = max(len - window + 1, 0) >> shift;
