@@ -455,7 +455,7 @@ typedef struct {
     const int32_t *block_table; /* [n_seqs, max_blocks]; entries no token needs may hold anything */
     const int32_t *kv_lens;     /* [n_seqs], the call's own tokens included                       */
     const int32_t *q_starts;    /* [n_seqs + 1], non-decreasing, within [0, n_tokens]             */
-    int n_seqs, max_blocks;
+    int n_seqs, max_blocks;     /* max_blocks * page_size at most 2^31 - 2^25                     */
     int n_tokens;               /* rows of the token tensors                                      */
 } w4a16_kv_batch_t;
 

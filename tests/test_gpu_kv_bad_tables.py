@@ -61,6 +61,25 @@ def test_all_pages_wrong_is_an_empty_row(cuda_lib, new):
     assert bool(((out[new:].cpu().double() - want[new:]).abs() <= attention_tolerance(p, want, spread)[new:]).all())
 
 
+@pytest.mark.parametrize("new", [3, 200])
+@pytest.mark.parametrize("window", [0, 5, 2 ** 31 - 1])
+def test_more_new_tokens_than_the_sequence_is_long(cuda_lib, new, window):
+    """Tokens at negative positions are empty rows; those at positions from 0 on get their answer."""
+    w = cuda_lib
+    p = Problem([new], [new], seed=new)
+    cache, table, lens, starts, rows = p.to_cuda(w)
+    gone = new // 2
+    lens -= gone
+    q = rows[:, :p.heads * p.dim].unflatten(1, (p.heads, p.dim))
+    out = w.w4a16_kv_attention(q, cache, table, lens, starts, new, window=window)
+    assert reported(w)
+    p.lens = [new - gone]
+    p.new, p.rows, p.T = [new - gone], p.rows[gone:], new - gone
+    want, _, spread = attention(p, None, window)
+    assert bool((out[:gone] == 0).all())
+    assert bool(((out[gone:].cpu().double() - want).abs() <= attention_tolerance(p, want, spread)).all())
+
+
 def test_read_gives_zeros_for_the_rows_of_a_wrong_page(cuda_lib):
     w = cuda_lib
     p = Problem([40, 20], [20, 10], act="f16", seed=1)

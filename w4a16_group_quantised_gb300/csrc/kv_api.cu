@@ -42,8 +42,12 @@ int check_cache(const w4a16_kv_cache_t *c, KvCache *out) {
     return W4A16_OK;
 }
 
+// Positions of a sequence: a step's keys more than the last, or a window and a call's tokens less than the first, are
+// still 32-bit numbers.
+constexpr long long kMaxPositions = (1LL << 31) - (1LL << 25);
+
 int check_table(const void *table, const void *lens, int n_seqs, int max_blocks, int page_size) {
-    if (n_seqs < 0 || n_seqs > (1 << 20) || max_blocks <= 0 || (long long)max_blocks * page_size >= (1LL << 31))
+    if (n_seqs < 0 || n_seqs > (1 << 20) || max_blocks <= 0 || (long long)max_blocks * page_size > kMaxPositions)
         return W4A16_ERR_SHAPE;
     if (n_seqs > 0 && (table == nullptr || lens == nullptr)) return W4A16_ERR_NULL;
     if (!aligned(table, 4) || !aligned(lens, 4)) return W4A16_ERR_ALIGN;
@@ -144,6 +148,8 @@ int w4a16_kv_attention(const void *q, long long q_stride, int n_heads, const w4a
     if (need > 0 && workspace == nullptr) return W4A16_ERR_NULL;
     if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
     if (workspace_bytes < need) return W4A16_ERR_ARG;
+    // no sequence is as long as the table is wide and a window: every token sees all keys before it
+    if (window >= b.max_blocks * cache->page_size) window = 0;
     KvAttentionArgs a{q, q_stride, n_heads, max_q_len, window, sinks, scale, out, lse_or_null, (int)dtype, workspace};
     return done(launch_kv_attention(a, c, b, *dev, str(stream), pdl_enabled()));
 }
