@@ -3,7 +3,7 @@
 Every function has the name of the C entry point it calls and the semantics
 include/w4a16.h states; tensors' data pointers and the current CUDA stream are
 handed over unchanged.  Scratch is allocated per call on that stream unless
-the caller passes a workspace.
+the caller passes a workspace.  The tensors have to be on the current device.
 
 A cache is a KVCache of four tensors.  Its codes are [n_pages, n_kv_heads,
 page_size, head_dim] in that order of dimensions, int8 or float8_e4m3fn, with
@@ -67,12 +67,20 @@ def _device_of(name, t):
     return t.get_device()
 
 
+def _current(device):
+    """`device`, which has to be the current one: the library launches there."""
+    if torch._C._cuda_getDevice() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{torch._C._cuda_getDevice()}: "
+                         f"call under torch.cuda.device({device})")
+    return device
+
+
 def _cache(c):
     """(the cache as the C struct's bytes, device index, pages, heads, page size, head dim)"""
     if not isinstance(c, KVCache):
         raise TypeError(f"cache must be a KVCache, got {type(c).__name__}")
     k, v, ks, vs = c
-    device = _device_of("cache.k", k)
+    device = _current(_device_of("cache.k", k))
     kind = KV_INT8 if k.dtype is torch.int8 else KV_E4M3
     if kind == KV_E4M3 and k.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"cache.k must be int8 or float8_e4m3fn, got {k.dtype}")
@@ -164,16 +172,11 @@ class _Block:
             torch._C._cuda_cudaCachingAllocator_raw_delete(self.at)
 
 
-def _scratch(workspace, need, device, stream, handle):
+def _scratch(workspace, need, device, handle):
     """(what holds the scratch, its address, its bytes): the caller's tensor, or from torch's allocator."""
     if workspace is None:
-        if torch._C._cuda_getDevice() == device:
-            block = _Block(need, handle)
-            return block, block.at, need
-        workspace = torch.empty(need, dtype=torch.uint8, device=_device(device))
-        if stream is not None:
-            workspace.record_stream(stream)
-        return workspace, workspace.data_ptr(), need
+        block = _Block(need, handle)
+        return block, block.at, need
     if not (isinstance(workspace, torch.Tensor) and workspace.get_device() == device and workspace.is_contiguous()):
         _refuse("workspace", workspace, None, None, device)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -224,7 +227,7 @@ def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int,
         _output("lse", lse, (T, H), torch.float32, dev)
     b, n = _batch(block_table, kv_lens, q_starts, T, dev)
     handle = _stream(stream, dev)
-    ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, stream, handle)
+    ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, handle)
     _check("w4a16_kv_attention", load_library().w4a16_kv_attention(
         q.data_ptr(), sq, H, c, b, max_q_len, dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
         None if lse is None else lse.data_ptr(), dt, at, size, handle))
@@ -279,14 +282,14 @@ def w4a16_kv_fork(cache, block_table, kv_lens, refcount, parents, children, work
     if parents.shape[0] != children.shape[0]:
         raise ValueError("parents and children must have the same length")
     handle = _stream(stream, dev)
-    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream, handle)
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, handle)
     _check("w4a16_kv_fork", load_library().w4a16_kv_fork(
         c, table, lens, rows, width, counts, a, b, parents.shape[0], at, size, handle))
 
 
 def w4a16_kv_free(block_table, kv_lens, refcount, seqs, stream=None):
     """Rows seqs[i] give up their pages: counts go down, entries become -1, lengths 0."""
-    dev = _device_of("block_table", block_table)
+    dev = _current(_device_of("block_table", block_table))
     table, lens, rows, width = _table(block_table, kv_lens, dev)
     counts, ids = _counts(refcount, dev), _ints("seqs", seqs, 1, dev)
     _check("w4a16_kv_free", load_library().w4a16_kv_free(
@@ -295,7 +298,7 @@ def w4a16_kv_free(block_table, kv_lens, refcount, seqs, stream=None):
 
 def w4a16_kv_trim(block_table, kv_lens, refcount, page_size: int, window: int, sinks: int = 0, stream=None):
     """Every row gives up the pages that no later token sees with this window and these sinks."""
-    dev = _device_of("block_table", block_table)
+    dev = _current(_device_of("block_table", block_table))
     table, lens, rows, width = _table(block_table, kv_lens, dev)
     counts = _counts(refcount, dev)
     _check("w4a16_kv_trim", load_library().w4a16_kv_trim(
@@ -313,6 +316,6 @@ def w4a16_kv_compact(cache, block_table, refcount, n_live=None, workspace=None, 
     if n_live is not None and n_live.shape[0] != 1:
         raise ValueError(f"n_live must be [1], got {list(n_live.shape)}")
     handle = _stream(stream, dev)
-    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, stream, handle)
+    ws, at, size = _scratch(workspace, w4a16_kv_pool_workspace(pages), dev, handle)
     _check("w4a16_kv_compact", load_library().w4a16_kv_compact(
         c, table, rows, width, counts, live, at, size, handle))
