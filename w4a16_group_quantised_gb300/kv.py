@@ -4,6 +4,9 @@ Every function has the name of the C entry point it calls and the semantics
 include/w4a16.h states; tensors' data pointers and the current CUDA stream are
 handed over unchanged.  Scratch is allocated per call on that stream unless
 the caller passes a workspace.  The tensors have to be on the current device.
+With `stream`, the work runs there, and a result that is allocated here is
+that stream's memory, safe to use on the current stream once that has waited
+for it; the tensors passed in are the caller's to keep.
 
 A cache is a KVCache of four tensors.  Its codes are [n_pages, n_kv_heads,
 page_size, head_dim] in that order of dimensions, int8 or float8_e4m3fn, with
@@ -148,8 +151,23 @@ def _device(index):
     return torch.device("cuda", index)
 
 
-def _output(name, t, shape, dtype, device):
+def _on(stream, shape, dtype, device):
+    """A result that work on `stream` writes: that stream's memory, so that what used it before is done, and held back
+    after its end for the current stream, where the caller goes on."""
+    here = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, _device(device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=_device(device))
+    if stream != here:
+        t.record_stream(here)
+    return t
+
+
+def _output(name, t, shape, dtype, device, stream):
     if t is None:
+        if stream is not None:
+            return _on(stream, shape, dtype, device)
         return torch.empty(shape, dtype=dtype, device=_device(device))
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.is_contiguous()
             and t.dim() == len(shape)):
@@ -203,8 +221,8 @@ def w4a16_kv_read(cache, block_table, kv_lens, q_starts, n_tokens: int, dtype, k
     """The newest q_starts[b+1] - q_starts[b] cached tokens of each sequence as
     values of `dtype`: (k, v), each [n_tokens, n_kv_heads, head_dim]."""
     c, dev, _, heads, _, dim = _cache(cache)
-    k_out = _output("k_out", k_out, (n_tokens, heads, dim), dtype, dev)
-    v_out = _output("v_out", v_out, (n_tokens, heads, dim), dtype, dev)
+    k_out = _output("k_out", k_out, (n_tokens, heads, dim), dtype, dev, stream)
+    v_out = _output("v_out", v_out, (n_tokens, heads, dim), dtype, dev, stream)
     b, _ = _batch(block_table, kv_lens, q_starts, n_tokens, dev)
     _check("w4a16_kv_read", load_library().w4a16_kv_read(
         c, b, k_out.data_ptr(), v_out.data_ptr(), _act(k_out), _stream(stream, dev)))
@@ -222,9 +240,9 @@ def w4a16_kv_attention(q, cache, block_table, kv_lens, q_starts, max_q_len: int,
         _refuse("q", q, None, 3, dev)
     T, H, _ = q.shape
     sq, dt = _rows("q", q, H, dim, dev), _act(q)
-    out = _output("out", out, (T, H, dim), q.dtype, dev)
+    out = _output("out", out, (T, H, dim), q.dtype, dev, stream)
     if lse is not None:
-        _output("lse", lse, (T, H), torch.float32, dev)
+        _output("lse", lse, (T, H), torch.float32, dev, stream)
     b, n = _batch(block_table, kv_lens, q_starts, T, dev)
     handle = _stream(stream, dev)
     ws, at, size = _scratch(workspace, _attention_workspace(dev, H, kv_heads, dim, n, T), dev, handle)
