@@ -91,10 +91,12 @@ def _cache(c):
         raise ValueError(f"cache.k must be 4-D, got {list(k.shape)}")
     if _device_of("cache.v", v) != device:
         raise ValueError(f"operands are on different devices: {k.device}, {v.device}")
-    shape, stride = k.shape, k.stride()
-    if v.dtype is not k.dtype or v.shape != shape or v.stride() != stride:
-        raise ValueError("cache.k and cache.v must have the same dtype, shape and strides")
+    shape, stride, v_stride = k.shape, k.stride(), v.stride()
     n_pages, heads, page_size, head_dim = shape
+    if n_pages == 1 or heads == 1:             # strides of one element say nothing
+        stride, v_stride = (tuple(x if n > 1 else 0 for n, x in zip(shape, y)) for y in (stride, v_stride))
+    if v.dtype is not k.dtype or v.shape != shape or v_stride != stride:
+        raise ValueError("cache.k and cache.v must have the same dtype, shape and strides")
     sp, sh, st, sd = stride
     if sd != 1:
         raise ValueError("the codes' last dimension must be contiguous")
@@ -138,7 +140,7 @@ def _rows(name, t, heads, head_dim, device):
     row, head, one = t.stride()
     if one != 1 or (heads > 1 and head != head_dim):
         raise ValueError(f"each row of {name} must be contiguous")
-    return row if n > 1 else max(row, heads * head_dim)
+    return row if n > 1 else heads * head_dim
 
 
 def _act(t):
