@@ -440,7 +440,8 @@ typedef struct {
     float *k_scale, *v_scale;   /* [n_pages, n_kv_heads], contiguous                       */
     int n_pages, page_size;     /* page_size 16, 32, 64 or 128                             */
     int n_kv_heads, head_dim;   /* head_dim 64 or 128                                      */
-    long long page_stride, head_stride, token_stride;   /* bytes, multiples of 16; k and v alike */
+    long long page_stride, head_stride, token_stride;   /* bytes, multiples of 16; k and v alike; no
+                                   two rows of head_dim bytes overlap                      */
     int kv_dtype;               /* w4a16_kv_dtype_t                                        */
 } w4a16_kv_cache_t;
 

@@ -2,6 +2,9 @@
 // and dispatch to kv_append.cu, kv_attention.cu and kv_pages.cu.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cstdlib>
+
 #include "kernels.h"
 #include "w4a16.h"
 
@@ -18,6 +21,32 @@ int shift_of(int page_size) {
 
 int check_dtype(int dtype) { return dtype == W4A16_F16 || dtype == W4A16_BF16 ? W4A16_OK : W4A16_ERR_DTYPE; }
 
+// Whether no two rows of head_dim bytes, of all pages, heads and tokens, overlap.
+bool rows_apart(const w4a16_kv_cache_t *c) {
+    struct { long long n, stride; } dims[3] = {
+        {c->page_size, c->token_stride}, {c->n_kv_heads, c->head_stride}, {c->n_pages, c->page_stride}};
+    std::sort(dims, dims + 3, [](const auto &a, const auto &b) { return a.stride < b.stride; });
+    // one dimension within the next: every ordinary layout
+    long long extent = c->head_dim;
+    bool nested = true;
+    for (const auto &d : dims) {
+        if (d.n == 1) continue;
+        nested = nested && d.stride >= extent;
+        extent += (d.n - 1) * d.stride;
+    }
+    if (nested) return true;
+    // else every distance in tokens and heads against the nearest one in pages
+    const long long pages = c->n_pages - 1, sp = c->page_stride;
+    for (int t = 0; t < c->page_size; ++t)
+        for (int h = 1 - c->n_kv_heads; h < c->n_kv_heads; ++h) {
+            const long long at = t * c->token_stride + h * c->head_stride;
+            const long long near = sp > 0 ? -at / sp : 0;
+            for (long long p = std::max(near - 1, -pages); p <= std::min(near + 1, pages); ++p)
+                if ((t != 0 || h != 0 || p != 0) && std::llabs(at + p * sp) < c->head_dim) return false;
+        }
+    return true;
+}
+
 int check_cache(const w4a16_kv_cache_t *c, KvCache *out) {
     if (c == nullptr) return W4A16_ERR_NULL;
     if (c->kv_dtype != W4A16_KV_INT8 && c->kv_dtype != W4A16_KV_E4M3) return W4A16_ERR_DTYPE;
@@ -30,10 +59,10 @@ int check_cache(const w4a16_kv_cache_t *c, KvCache *out) {
         if (s < 0 || s >= (1LL << 40)) return W4A16_ERR_SHAPE;
         if (s % 16 != 0) return W4A16_ERR_ALIGN;
     }
-    // rows of one head, and the heads and tokens of a page, do not overlap
     if (c->token_stride < c->head_dim || (c->n_kv_heads > 1 && c->head_stride < c->head_dim) ||
         (c->n_pages > 1 && c->page_stride < c->head_dim))
         return W4A16_ERR_SHAPE;
+    if (!rows_apart(c)) return W4A16_ERR_SHAPE;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
         return W4A16_ERR_ALIGN;
     *out = KvCache{static_cast<uint8_t *>(c->k), static_cast<uint8_t *>(c->v), c->k_scale, c->v_scale,
