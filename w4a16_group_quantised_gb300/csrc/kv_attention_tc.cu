@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_mbar_init();
         misc[0] = 0;
     }
-    kv_begin();
+    grid_dependency_wait();
 
     auto tile_of = [&](const int4 s, int b, int r) {
         ManyTile t;
@@ -571,6 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The next kernel may start only now: one that takes TMEM before it waits for this grid must not have it first.
+    grid_dependents_launch();
     const long long c0 = s_cut[0], c1 = s_cut[1];
     const uint32_t tmem = static_cast<uint32_t>(misc[1]);
     // the tile at c0, and the walk from there
