@@ -397,7 +397,9 @@ int w4a16_version(void);
  * while on, the decode kernel issues no weight copies, so every CTA's bounded
  * wait for them runs out (about 2 s), the kernel leaves without touching
  * memory beyond its own output and records W4A16_ERR_TIMEOUT in the status
- * word (its output is then meaningless); n = 0 turns it off;
+ * word (its output is then meaningless); so does the attention over the
+ * 8-bit cache, in all its CTAs (1) or in every vals[0]-th (2 and more); n = 0
+ * turns it off;
  * n = 0 restores the built-in choice for which = 1, 2, 4 or 8.  An invalid
  * configuration is rejected here or, for the decode shape limits, by the
  * next w4a16_gemm call with W4A16_ERR_ARG. */

@@ -479,6 +479,11 @@ bool pdl_enabled() {
     return g_pdl != 0;
 }
 
+int hold_copies() {
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    return g_hold_copies;
+}
+
 int device_info(const DeviceInfo **out) { return get_device(out); }
 
 bool kernel_log_on() {
@@ -827,7 +832,7 @@ int w4a16_debug_set_config(int which, const int *vals, int n) {
     if (which == 7) {
         if (n == 0) { g_hold_copies = 0; return W4A16_OK; }
         if (n != 1 || vals == nullptr) return W4A16_ERR_ARG;
-        g_hold_copies = vals[0] != 0;
+        g_hold_copies = vals[0];
         return W4A16_OK;
     }
     if (which == 4) {

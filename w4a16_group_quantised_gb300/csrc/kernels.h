@@ -135,9 +135,10 @@ cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_
 long long kv_pool_workspace(int n_pages);
 
 // ---- api.cu helpers used by kv_api.cu and kv_attention.cu: the current device's state (W4A16_OK
-// or an error), the early-launch switch, the kernel-selection log
+// or an error), the early-launch switch, the timeout hook, the kernel-selection log
 int device_info(const DeviceInfo **out);
 bool pdl_enabled();
+int hold_copies();                        // test hook: see w4a16_debug_set_config(7)
 bool kernel_log_on();
 void log_kernel_selection(const char *line);
 

@@ -56,6 +56,9 @@ __device__ __forceinline__ void kv_empty_rows(const KvAttentionArgs &a, const Kv
     }
 }
 
+// Test hook: whether this CTA of an attention kernel issues no copies, so that its waits run out.
+__device__ __forceinline__ bool kv_holds(int hold) { return hold != 0 && (hold < 2 || blockIdx.x % hold == 0); }
+
 // ---- activations
 template <int DT>
 __device__ __forceinline__ float kv_act(uint16_t v) {

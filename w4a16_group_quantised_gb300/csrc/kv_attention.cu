@@ -77,6 +77,7 @@ struct FewParams {
     float *parts;                         // [grid][2][ROWS][D + 2]
     unsigned long long *tickets;          // [grid]
     unsigned long long tag;
+    int hold;                             // test hook (kv_holds)
     int *status;
 };
 
@@ -371,8 +372,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
         m.ks = __ldg(p.c.k_scale + i);
         m.vs = __ldg(p.c.v_scale + i);
     };
+    const bool holds = kv_holds(p.hold);
     auto issue = [&](int stage, int page, int where) {
-        if (lane == 0) {
+        if (lane == 0 && !holds) {
             const uint32_t bar = bars + stage * 8, dst = ring + stage * L::kStage;
             mbar_arrive_expect_tx(bar, L::kStage);
             const int tok = where & 255, head = where >> 8;
@@ -578,7 +580,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
             if (!mbar_wait_bounded(bars + stage * 8, phase, p.status, &s_abort)) failed = true;
             if (++stage == NS) stage = 0, phase ^= 1;
         }
-        if (failed) break;
+        if (__any_sync(0xffffffffu, failed)) {                     // the whole warp: what follows is the warp's
+            failed = true;
+            break;
+        }
 #pragma unroll
         for (int b = 0; b < BPS; ++b)
 #pragma unroll
@@ -982,7 +987,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         b.q_starts += b0;
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
         FewParams p{a, c, b, 0, token_first ? 1 : 0, merged ? 1 : 0, b0 == 0, b0 + b.n_seqs == batch.n_seqs, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,
-                    nullptr, nullptr, 0, dev.status};
+                    nullptr, nullptr, 0, hold_copies(), dev.status};
         p.tickets = static_cast<unsigned long long *>(a.workspace);
         p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
         p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;

@@ -59,6 +59,7 @@ constexpr int kCost = 3;                  // steps that a tile's start and end c
 constexpr int kSorted = 256;              // up to so many pairs may be dealt out whole, the longest first
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 2);   // and the MMA issuer, the planner
+constexpr int kDrainTries = 1 << 16;      // looks at a barrier, up to 20 us each, before leaving all the same
 constexpr int kRing = 4;                  // tiles that the planner is ahead of the slowest role
 constexpr float kRefStart = -3.402823466e38f, kTop = 15.9f, kHead = 14.0f;
 
@@ -73,6 +74,7 @@ struct ManyParams {
     float *parts;                         // [grid][2] parts of a tile
     unsigned long long *tickets;          // [grid]
     unsigned long long tag;
+    int hold;                             // test hook (kv_holds)
     int *status;
 };
 
@@ -581,10 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         pair = find_pair(c0);
         head = (int)((c0 - pre[pair] * Hk) / (pre[pair + 1] - pre[pair]));
     }
+    // Every wait is a whole warp's, and so is its giving up: what follows is full of warp-wide instructions.
+    auto wait = [&](uint32_t bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase, p.status, abort_flag));
+    };
     // The list of this CTA's tiles, written by the planner ahead of the other roles.  open_tile waits for
     // the idx-th (null: the end, or a wait that ran out), close_tile gives its place back.
     auto open_tile = [&](int idx) -> const PlannedTile * {
-        if (!mbar_wait_bounded(plan_full(idx % kRing), (idx / kRing) & 1, p.status, abort_flag)) return nullptr;
+        if (!wait(plan_full(idx % kRing), (idx / kRing) & 1)) return nullptr;
         const PlannedTile *t = plan + idx % kRing;
         return t->s1 > 0 ? t : nullptr;
     };
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int st = first_st; st < s1 && runs; st += twice ? 2 : 1) {
                 const int pos0 = (st < sink_blocks ? st : block0 + st) * kKeys;
                 const float4 *sc = scales + (counter + st - s0 & 3) * 8;
-                if (!mbar_wait_bounded(s_full(half), s_phase, p.status, abort_flag)) {
+                if (!wait(s_full(half), s_phase)) {
                     ok = false;
                     break;
                 }
@@ -760,20 +766,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a row's two parts are in the same TMEM lane: the first half reads them both
                 exchange[r] = make_float2(ref, sum);
                 mbar_arrive(part_told);
-                if (!mbar_wait_bounded(part_read, join_phase, p.status, abort_flag)) break;
+                if (!wait(part_read, join_phase)) break;
                 join_phase ^= 1;
                 o_phase ^= 1;
                 close_tile(idx);
                 continue;
             }
-            if (!mbar_wait_bounded(o_full(half), o_phase, p.status, abort_flag)) break;
+            if (!wait(o_full(half), o_phase)) break;
             o_phase ^= 1;
             float f_here = 1.0f, f_there = 0.0f;
             if (half == 0) {
                 // the other half's phases, so that its part can be waited for
                 if (joins) {
-                    if (!mbar_wait_bounded(o_full(1), other_phase, p.status, abort_flag)) break;
-                    if (!mbar_wait_bounded(part_told, join_phase, p.status, abort_flag)) break;
+                    if (!wait(o_full(1), other_phase)) break;
+                    if (!wait(part_told, join_phase)) break;
                     join_phase ^= 1;
                     const float2 z = exchange[r];
                     const float m = fmaxf(ref, z.x);
@@ -842,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bar = meet_bar(twice ? 0 : 1);
                     int &phase = meet_phase[twice ? 0 : 1];
                     mbar_arrive(bar);
-                    const bool met = mbar_wait_bounded(bar, phase, p.status, abort_flag);
+                    const bool met = wait(bar, phase);
                     phase ^= 1;
                     return met;
                 };
@@ -988,7 +994,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // soon as their registers are free, a step ahead of their conversion.
         auto emit_k = [&](int c) {
             const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
-            if (!mbar_wait_bounded(k_empty(stg), ph ^ 1, p.status, abort_flag)) return false;
+            if (!wait(k_empty(stg), ph ^ 1)) return false;
             uint8_t *dst = smem + L::kK + stg * L::kOperand;
             if (p.a.dtype == 0) convert_codes<KT, D, false>(kraw, dst, w * 32 + row_in, piece);
             else convert_codes<KT, D, true>(kraw, dst, w * 32 + row_in, piece);
@@ -1042,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the second half's S is done, V's before.
             if (twice && !do_k()) break;
             const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
-            if (!mbar_wait_bounded(v_empty(stg), ph ^ 1, p.status, abort_flag)) break;
+            if (!wait(v_empty(stg), ph ^ 1)) break;
             convert_codes<KT, D, false>(vraw, smem + L::kV + stg * L::kOperand, w * 32 + row_in, piece);
             fence_proxy_async_smem();
             __syncwarp();
@@ -1074,10 +1080,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto q_wait = [&](int half) {
             const int phase = q_phase[half];
             q_phase[half] ^= 1;
-            return mbar_wait_bounded(q_full(half), phase, p.status, abort_flag);
+            return wait(q_full(half), phase);
         };
         auto q_done = [&](int half) { commit_elected(q_empty(half)); };
-        auto wait = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
         // MMAs run in the order they are issued: P is read before the next S of its half replaces it.
         auto run_tile = [&](int steps) {                           // two halves of rows, a step together
             for (int st = 0; st < steps; ++st, ++counter) {
@@ -1145,12 +1150,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = __reduce_max_sync(0xffffffffu, next->t.rows);
             const int steps = __reduce_max_sync(0xffffffffu, next->s1 - next->s0);
             close_tile(idx);
-            if (!(rows > half_rows ? run_tile(steps) : run_same_rows(steps))) {
-                // leave with no product in flight
-                commit_elected(drain);
-                for (int i = 0; i < 1 << 16 && !mbar_try_wait(drain, 0); ++i) {}
-                break;
-            }
+            if (!(rows > half_rows ? run_tile(steps) : run_same_rows(steps))) break;
+        }
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+            // leave with no product in flight
+            commit_elected(drain);
+            for (int i = 0; i < kDrainTries && !mbar_try_wait(drain, 0); ++i) {}
+            __syncwarp();
         }
     } else if (warp == kSoftWarps + kConvWarps + 1) {
         // ------------------------------------------------------------ planner
@@ -1180,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!more) next.s1 = 0;
             if (idx >= kRing &&
-                !mbar_wait_bounded(plan_empty(idx % kRing), (idx / kRing - 1) & 1, p.status, abort_flag))
+                !wait(plan_empty(idx % kRing), (idx / kRing - 1) & 1))
                 break;
             if (lane == 0) {
                 plan[idx % kRing] = next;
@@ -1191,12 +1197,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (!more || !half_runs(next, h)) continue;
-                if (!mbar_wait_bounded(q_empty(h), q_phase[h] ^ 1, p.status, abort_flag)) {
+                if (!wait(q_empty(h), q_phase[h] ^ 1)) {
                     more = false;
                     break;
                 }
                 q_phase[h] ^= 1;
-                if (lane == 0) {
+                if (lane == 0 && !kv_holds(p.hold)) {
                     const int tok = next.t.q0 + (next.t.row0 + (same_rows(next.t) ? 0 : h * half_rows)) / group;
                     mbar_arrive_expect_tx(q_full(h), (uint32_t)(half_rows * D * 2));
                     for (int b = 0; b < L::kBlocks; ++b)
@@ -1206,6 +1212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             ++idx;
+        }
+        if (__any_sync(0xffffffffu, *abort_flag != 0) && !kv_holds(p.hold)) {
+            // leave with no copy in flight: q_phase counts a half's copies
+            for (int h = 0; h < 2; ++h)
+                for (int i = 0; i < kDrainTries && !mbar_try_wait(q_full(h), q_phase[h] ^ 1); ++i) {}
+            __syncwarp();
         }
     }
     __syncwarp();
@@ -1261,7 +1273,7 @@ cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c,
         for (long long first = 0; first < pairs; first += kMaxPairs) {
             // with a row limit the other kernel has seen to the rows that no sequence owns
             const bool mine = row_limit == 0 && first == 0;
-            ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first, nullptr, nullptr, 0, dev.status};
+            ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first, nullptr, nullptr, 0, hold_copies(), dev.status};
             p.tickets = static_cast<unsigned long long *>(a.workspace);
             p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
             p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
