@@ -497,7 +497,8 @@ int w4a16_kv_read(const w4a16_kv_cache_t *cache, const w4a16_kv_batch_t *batch, 
  * max_q_len: the most tokens that one sequence brings.  It picks kernels
  * only: the result holds whatever it is.
  * workspace: w4a16_kv_attention_workspace bytes, 16-byte aligned, not shared
- * with a call that may run at the same time. */
+ * with a call that may run at the same time.  Nothing in it needs clearing,
+ * not after W4A16_ERR_TIMEOUT either. */
 int w4a16_kv_attention(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
                        const w4a16_kv_batch_t *batch, int max_q_len, float scale, int window, int sinks,
                        void *out, float *lse_or_null, w4a16_dtype_t dtype, void *workspace,

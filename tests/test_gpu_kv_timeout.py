@@ -39,3 +39,31 @@ def test_waits_run_out_and_the_next_call_is_right(cuda_lib, new, lens, dim, page
     want, _, spread = attention(p)
     assert bool(((out.cpu().double() - want).abs() <= attention_tolerance(p, want, spread)).all())
     assert w.w4a16_last_device_error() == 0
+
+
+@pytest.mark.parametrize("new, lens", CASES)
+@pytest.mark.parametrize("dim, page, layout", [(128, 16, "heads"), (64, 64, "tokens")])
+@pytest.mark.parametrize("hold", [1, 2, 3])
+def test_tickets_are_back_at_zero(cuda_lib, new, lens, dim, page, layout, hold):
+    """A replay of the same launch counts on from what it finds: every ticket taken has to be given back."""
+    w = cuda_lib
+    p = Problem(lens, new, heads=8, kv_heads=2, dim=dim, page=page, layout=layout, seed=len(new))
+    cache, table, n, starts, rows = p.to_cuda(w)
+    q = rows[:, :8 * dim].unflatten(1, (8, dim))
+    ws = torch.zeros(w.w4a16_kv_attention_workspace(8, 2, dim, len(new), p.T), dtype=torch.uint8, device="cuda")
+    tickets = ws.view(torch.int64)[:torch.cuda.get_device_properties(0).multi_processor_count]
+
+    def call():
+        return w.w4a16_kv_attention(q, cache, table, n, starts, max(new), workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    assert not bool(tickets.any())
+    held(w, hold, call)
+    assert not bool(tickets.any())
+    out = call()
+    torch.cuda.synchronize()
+    want, _, spread = attention(p)
+    assert bool(((out.cpu().double() - want).abs() <= attention_tolerance(p, want, spread)).all())
+    assert not bool(tickets.any())
+    assert w.w4a16_last_device_error() == 0

@@ -750,7 +750,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
         if (tile.end > mine) s_out[1] = 1 + warp;
     }
     __syncthreads();
-    if (s_abort) return;
+    // A CTA that gave a wait up has no results, but its tickets are counted: they are back at 0 after every launch,
+    // also for a replay, whose tag is the same.
+    const bool gave_up = s_abort != 0;
 
     // ---- tiles that more than one warp holds a part of, summed in warp order
     // Parts of a shared tile: the first warp's (its last piece when the tile begins there), then the first
@@ -779,7 +781,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         out[i] = s_out[i] >= 0;
-        if (!out[i]) continue;
+        if (!out[i] || gave_up) continue;
         const Shared sh = shared[s_out[i]];
         const int rows = min(ROWS, sh.n * group - sh.row);
         float *dst = p.parts + ((long long)blockIdx.x * 2 + i) * L::kPart;
@@ -791,19 +793,22 @@ __global__ void __launch_bounds__(32 * NW, 1)
             if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + ROWS * D + 2 * row), make_float2(m, l));
         }
     }
-    if (out[0] || out[1]) {
+    if (out[0] || out[1] || gave_up) {
         // tickets: which CTAs share the tile follows from where it begins and ends (a warp that has hardly had
         // anything to sum: eight rows are 256 pieces at most)
         const int nth = tid - 32 * (NW - 1);
-        const bool asks = nth >= 0 && nth < 2 && out[nth & 1];
+        bool asks = nth >= 0 && nth < 2 && (out[nth & 1] || gave_up);
         int from = 0, to = 0;
         if (asks) {
-            const Shared sh = shared[s_out[nth]];
+            // the tile of the CTA's first step or of its last
+            const long long line = c0 + (nth ? mine - 1 : 0);
+            const int b = find(line, 0, s_seq[0], s_seq[NW]), steps = span(seqs[b].y, seqs[b].z).steps;
+            const int idx = line_div(line - pre[b], steps);
+            const long long first = pre[b] + (long long)idx * steps;
+            if (gave_up) asks = nth ? first >= c0 && first + steps > c0 + mine : first < c0;
             // with the costs, the tile begins and ends at
-            const int b = find(c0 + sh.begin, 0, s_seq[0], s_seq[NW]);
-            const int idx = line_div(c0 + sh.begin - pre[b], sh.end - sh.begin);
-            const long long begin = c0 + sh.begin + (long long)(tiles_before[b] + idx) * COST;
-            const long long end = begin + sh.end - sh.begin + COST;
+            const long long begin = first + (long long)(tiles_before[b] + idx) * COST;
+            const long long end = begin + steps + COST;
             // the last CTA whose share begins by the tile's first step, and by its last
             from = (int)(((begin + COST + 1) * ctas + total - 1) / total - 1);
             to = (int)((end * ctas + total - 1) / total - 1);
@@ -835,6 +840,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             s_to[nth] = to;
         }
     }
+    if (gave_up) return;
     // those within the CTA: each by the warp that holds the first part
     {
         const Shared sh = shared[1 + warp];

@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(plan_empty(i), kSoftWarps + kConvWarps + 1);
         }
         fence_mbar_init();
-        misc[0] = 0;
+        misc[0] = misc[3] = 0;                                     // misc[3]: tickets taken, 1 the first tile's, 2 the last's
     }
     grid_dependency_wait();
 
@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const long long ctas = min((long long)grid, (total + kCost) / (1 + kCost));
     if (deal ? (int)blockIdx.x >= pairs * Hk : blockIdx.x >= ctas) return;
+    if (tid == 0) misc[4] = deal, misc[5] = pairs;
     if (tid < 2) {
         long long at = ((long long)blockIdx.x + tid) * total / ctas;
         if (at > 0 && at < total) {
@@ -602,6 +603,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto same_rows = [&](const ManyTile &t) { return t.rows <= half_rows; };
     auto half_runs = [&](const PlannedTile &t, int half) { return same_rows(t.t) ? t.s1 - t.s0 > half : true; };
     auto block_of = [](const ManyTile &t, int st) { return st < t.sink ? st : t.block0 + st - t.sink; };
+
+    // The CTAs that share a tile: the last whose share begins by its first step, and by its last.
+    auto first_cta = [](const ManyTile &t, long long ctas, long long total) {
+        return (int)(((t.begin + kCost + 1) * ctas + total - 1) / total - 1);
+    };
+    auto last_cta = [](const ManyTile &t, long long ctas, long long total) {
+        return (int)(((t.begin + kCost + t.steps) * ctas + total - 1) / total - 1);
+    };
+    // This CTA's ticket of a shared tile, from one thread; true for the last to come.
+    auto ticket = [&](int from, int to) {
+        unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
+        do {
+            seen = old;
+            const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
+            put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
+            old = atomicCAS(tk, seen, put);
+        } while (old != seen);
+        return put == 0;
+    };
 
     if (warp < kSoftWarps) {
         // ------------------------------------------------------------ softmax, Q, output
@@ -841,8 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(part_read);
                 }
                 if (has) __stcg(reinterpret_cast<float2 *>(mine + kTileRows * D) + row, make_float2(ref, sum));
-                const int from = (int)(((t.begin + kCost + 1) * ctas + total - 1) / total - 1);
-                const int to = (int)(((t.begin + kCost + t.steps) * ctas + total - 1) / total - 1);
+                const int from = first_cta(t, ctas, total), to = last_cta(t, ctas, total);
                 // the tile's threads: of the first half, or of both
                 auto meet = [&]() {
                     const uint32_t bar = meet_bar(twice ? 0 : 1);
@@ -855,15 +874,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!meet()) break;
                 if (tid == 0) {
                     __threadfence();
-                    unsigned long long *tk = p.tickets + from, old = __ldcg(tk), seen, put;
-                    do {
-                        seen = old;
-                        const unsigned long long n = (seen >> 16) == p.tag ? (seen & 0xffff) + 1 : 1;
-                        put = n == (unsigned long long)(to - from + 1) ? 0 : p.tag << 16 | n;
-                        old = atomicCAS(tk, seen, put);
-                    } while (old != seen);
+                    const bool done = ticket(from, to);
+                    misc[3] |= opens ? 2 : 1;
                     __threadfence();
-                    misc[2] = put == 0;
+                    misc[2] = done;
                 }
                 if (!meet()) break;
                 const bool last = *reinterpret_cast<volatile int *>(misc + 2);
@@ -1223,6 +1237,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && tid == 0 && !misc[4]) {
+        // A CTA that gave a wait up has no results, but its tickets are counted: they are back at 0 after every
+        // launch, also for a replay, whose tag is the same.  All out of shared memory: the loops have no register to
+        // spare for what is needed here.
+        const int n = misc[5];
+        const long long all = pre[n] * Hk, shares = min((long long)gridDim.x, (all + kCost) / (1 + kCost));
+        const long long from = s_cut[0], to = s_cut[1];
+        for (int i = 0; i < 2 && from < to; ++i) {
+            const long long at = i ? to - 1 : from;
+            int pr = 0;
+            while (pr + 1 < n && pre[pr + 1] * Hk <= at) ++pr;
+            const ManyTile t = tile_at(pr, (int)((at - pre[pr] * Hk) / (pre[pr + 1] - pre[pr])));
+            const long long s0 = max(from - t.begin - kCost, 0LL), s1 = min(to - t.begin - kCost, (long long)t.steps);
+            const bool others = s0 < s1 && (i ? s0 == 0 && s1 < t.steps : s0 > 0);
+            if (others && !(misc[3] >> i & 1)) ticket(first_cta(t, shares, all), last_cta(t, shares, all));
+        }
+    }
     if (warp == kSoftWarps + kConvWarps) tmem_dealloc(tmem, 512u);
 }
 
