@@ -59,7 +59,8 @@ namespace {
 constexpr int kMaxSeqs = 512;             // sequences of a launch
 constexpr int kShort = 256;               // tiles of up to so many keys stay in one CTA
 constexpr int kLeast = 2;                 // fewest steps worth a CTA
-constexpr int kFewSeqs = 16;              // so many sequences may have their tiles cut alike
+constexpr int kFewSeqs = 16;              // so many sequences may have their tiles cut alike ...
+constexpr int kManyHeads = 8;             // ... of so many kv heads
 constexpr int kTileCost = 32;             // keys that the start and end of a tile count for in the shares
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
@@ -283,17 +284,19 @@ __global__ void __launch_bounds__(32 * NW, 1)
         return pre[b] + (long long)idx * steps + min(max(st - COST, 0), steps);
     };
     // Where a page's tokens hold all heads side by side, warps that go through the same keys of different heads
-    // should do so at the same time, or every stretch of 1 KB or so is fetched in pieces (4 sequences of 98302 to
-    // 131071 keys of 8 heads: 175 us).  So with few long tiles those of one sequence get the same whole number of
-    // warps' pieces, as near to equal shares as that allows (160 us; head by head, where a head's tokens are
-    // contiguous, equal shares take 154).
+    // should do so at the same time, or every stretch of some heads' rows is fetched in pieces.  So with few long
+    // tiles of many heads those of one sequence get the same whole number of warps' pieces, as near to equal shares as
+    // that allows.  4 sequences of 98302 to 131071 keys, this / equal shares, us on two GPUs of this kind: 8 heads of
+    // 128 dims 155 / 159 and 159 / 177, 8 of 64 86 / 137 and 86 / 141, 16 of 64 160 / 304 and 164 / 334.  With fewer
+    // heads the whole pieces cost more than they save: 4 heads of 128 86 / 84, 2 heads 57 / 54, 9 sequences of 2 heads
+    // 57 / 51 on any GPU.
     const int pieces = (int)ctas * NW;
     auto pieces_of = [&](int b, int done, long long each) {        // a tile's, of sequence b, `done` pieces before it
         const int tiles = max(seqs[b].w * Hk, 1);
         const long long end = pre[b] + (long long)tiles_before[b] * COST + seqs[b].w * Hk * each;
         return (int)min((end * pieces / total - done + tiles / 2) / tiles, (long long)(pieces - done) / tiles);
     };
-    const bool alike = p.token_first && B <= kFewSeqs && tiles_all * 16 <= pieces;
+    const bool alike = p.token_first && Hk >= kManyHeads && B <= kFewSeqs && tiles_all * 16 <= pieces;
     if (alike && warp == 0) {
         const int i = blockIdx.x * NW + min(lane, NW);
         long long at = total - (long long)tiles_all * COST;        // the line's end
