@@ -31,12 +31,16 @@
 // that share a tile add their parts up through the workspace, in order.  Where
 // whole tiles come close to that, the longest first, they are dealt out whole.
 //
-// Bound by the chain of a step: S, softmax (1.05 us), out, 1.9 us in all with
-// the waits between, beside 2.1 us of conversion; the tensor cores need 1.1 us
-// of it (S takes its operands from shared memory, 64 cycles for 16 dims).
-// Measured: a prompt of 8192 tokens (32 heads on 8, 128 dims, int8) 541 us, 1020
-// TFLOP/s, 0.53 of the measured matrix rate, tensor pipe 42 % active; 1920
-// tokens 48 us.  Tried and slower: S in two 64-key pieces (more operand reads),
+// Bound by the chain of a step, 2.4 to 2.5 us for two halves of rows: a softmax
+// takes 1.05 to 1.2 us, and its wait for the next S 1.2 us, in which the other
+// half's products and softmax go on; the tensor cores need 1.07 us of it
+// (S takes its operands from shared memory, 64 cycles for 16 dims).  Where one
+// half's worth of rows is all there is a step takes 2.15 us, set by the
+// conversion warps.
+// Measured: a prompt of 8192 tokens (32 heads on 8, 128 dims, int8), 33,280
+// steps, 219 an SM: 549 us, 1000 TFLOP/s, 0.52 of the measured matrix rate,
+// tensor pipe 42 % active; 1920 tokens 50 us.  P is fp16 and the sums are fp32,
+// for the reasons that kv_attention.cu gives.  Tried and slower: S in two 64-key pieces (more operand reads),
 // conversion by 8 warps (the softmax then spills), 16-key units over 6 warps,
 // raw codes by TMA through the 24 KB of shared memory that are left (too few
 // bytes in flight), one stage of K and V with Q doubled.
@@ -585,8 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         head = (int)((c0 - pre[pair] * Hk) / (pre[pair + 1] - pre[pair]));
     }
     // Every wait is a whole warp's, and so is its giving up: what follows is full of warp-wide instructions.
-    // In the MMA and conversion warps the vote is left until a step's end, off its chain (chunks 392 us without that,
-    // 387 with): a step worked through on what is not there touches nothing but this CTA's operands and tensor memory.
+    // In the MMA warp the vote is left until a step's end, off its chain: a step issued on what is not there touches
+    // nothing but this CTA's operands and tensor memory.  A prompt of 8192 tokens takes 549 us so, 560 with a vote at each
+    // of its waits; at a step's end in the conversion warps, with loads on their way, it costs more, 570.
     auto look = [&](uint32_t bar, int phase) { return mbar_wait_bounded(bar, phase, p.status, abort_flag); };
     auto all = [](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
     auto wait = [&](uint32_t bar, int phase) { return all(look(bar, phase)); };
@@ -1010,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // soon as their registers are free, a step ahead of their conversion.
         auto emit_k = [&](int c) {
             const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
-            const bool ok = look(k_empty(stg), ph ^ 1);
+            if (!wait(k_empty(stg), ph ^ 1)) return false;
             uint8_t *dst = smem + L::kK + stg * L::kOperand;
             if (p.a.dtype == 0) convert_codes<KT, D, false>(kraw, dst, w * 32 + row_in, piece);
             else convert_codes<KT, D, true>(kraw, dst, w * 32 + row_in, piece);
@@ -1020,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(k_full(stg));
-            return all(ok);
+            return true;
         };
         Groups gk = {};
         bool more_twice = false;                                   // the mode of the step that K's registers hold
@@ -1064,12 +1069,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the second half's S is done, V's before.
             if (twice && !do_k()) break;
             const int stg = c % L::kStages, ph = (c / L::kStages) & 1;
-            const bool ok = look(v_empty(stg), ph ^ 1);
+            if (!wait(v_empty(stg), ph ^ 1)) break;
             convert_codes<KT, D, false>(vraw, smem + L::kV + stg * L::kOperand, w * 32 + row_in, piece);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(v_full(stg));
-            if (!all(ok)) break;
             have_v = have_k;
             if (have_v) load(after, to_v, vraw);
             if (!twice && !do_k()) break;
