@@ -470,8 +470,11 @@ typedef struct {
  *     s = max(s_old, amax / 127 (int8) or / 448 (e4m3), W4A16_KV_SCALE_MIN)
  *     code = RN(x * RN(1 / s)), ties to even, saturated
  * all in fp32.  When s > s_old the older codes of the block are rounded
- * again, code = RN((code * s_old) * RN(1 / s)); otherwise they stay.  No
- * other slot changes.  Appending the same tokens again changes nothing.  No
+ * again, code = RN((code * s_old) * RN(1 / s)); otherwise they stay.  Each
+ * such rounding adds up to half the codes' spacing to an older token's error
+ * (int8: s / 2; e4m3: 2^-4 of the value), and s only grows: with int8 a token
+ * whose page's scale grew g times after it is within (g + 1) / 2 of the page's
+ * s, page_size / 2 at most.  No other slot changes.  Appending the same tokens again changes nothing.  No
  * two sequences of the batch may append to the same page. */
 int w4a16_kv_append(const w4a16_kv_cache_t *cache, const void *k_new, long long k_stride, const void *v_new,
                     long long v_stride, const w4a16_kv_batch_t *batch, w4a16_dtype_t dtype,
@@ -489,8 +492,8 @@ int w4a16_kv_read(const w4a16_kv_cache_t *cache, const w4a16_kv_batch_t *batch, 
  *     j <= i  and  (window == 0  or  i - j < window  or  j < sinks)
  * and out[t, a] = sum_j softmax_j(scale * q . k_j) v_j, [n_tokens, n_heads,
  * head_dim] contiguous, rounded once into dtype from fp32 (each weight meets
- * its value as fp16: good to 2^-11, and 0 below 2^-39 of the row's largest,
- * value scale included).  lse (optional):
+ * its value as fp16: good to 2^-11 down to 2^-28 of the row's largest, value
+ * scales included, to fewer bits from there on, and 0 below 2^-39).  lse (optional):
  * [n_tokens, n_heads] fp32, log sum_j exp(scale * q . k_j).  A token that
  * sees no key gets zeros and -inf.  Pages that no token of a sequence sees
  * are never read, so their table entries may be -1 (w4a16_kv_trim).
