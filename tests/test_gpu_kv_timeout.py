@@ -43,7 +43,7 @@ def test_waits_run_out_and_the_next_call_is_right(cuda_lib, new, lens, dim, page
 
 @pytest.mark.parametrize("new, lens", CASES)
 @pytest.mark.parametrize("dim, page, layout", [(128, 16, "heads"), (64, 64, "tokens")])
-@pytest.mark.parametrize("hold", [1, 2, 3])
+@pytest.mark.parametrize("hold", [2, 3])
 def test_tickets_are_back_at_zero(cuda_lib, new, lens, dim, page, layout, hold):
     """A replay of the same launch counts on from what it finds: every ticket taken has to be given back."""
     w = cuda_lib

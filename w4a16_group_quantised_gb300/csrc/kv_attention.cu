@@ -8,8 +8,19 @@
 // weights 2^e_j multiply the codes as they are, and the denominator gets
 // 2^e_j / vs.  M is a running reference of each row, moved only when some e_j
 // passes 15.9, and then so that the largest is at 2^14: the weights fit fp16,
-// good to 2^-11 down to 2^-28 of the row's largest and zero below 2^-39; the
-// sums (out, the denominator) are fp32.
+// good to 2^-11 down to 2^-28 of the row's largest, to ever fewer bits below
+// that, and zero below 2^-39; the sums (out, the denominator) are fp32.
+//
+// Fewer bits than 32, and why.  The weights are fp16 because the matrix
+// instructions take 16-bit operands, and fp16 has three bits more than bf16;
+// two halves of each weight would double the products and the registers.  It
+// costs fp16 outputs 2.6e-4 to 2.8e-4 of relative error, where 32-bit weights
+// rounded once give 2.1e-4; bf16 outputs have 1.7e-3 either way.  Queries in
+// bf16 become fp16 after a power of two has put a row's largest value at 2^14,
+// so that one conversion of the codes, to fp16, serves both types: exact down
+// to 2^-28 of that value, and what is below is that much smaller than the
+// scores' fp32 sums resolve.  ex2.approx and the reciprocals are good to 2^-22,
+// far below a weight's 2^-11.
 //
 // Bound by the cache read (256 bytes a key and kv head at 128 dims) when pages
 // are large, by the conversion of the codes when they hold 16 keys.  So the
@@ -57,7 +68,10 @@ namespace w4a16 {
 namespace {
 
 constexpr int kMaxSeqs = 512;             // sequences of a launch
-constexpr int kShort = 256;               // tiles of up to so many keys stay in one CTA
+// Tiles of up to so many keys stay in one CTA.  256 / never / 1024, us, contexts of 100 to 300 keys: 256 sequences 32.7 /
+// 33.4 / 31.4, 64 16.1 / 16.1 / 15.2, 8 12.2 / 11.7 / 11.6; 64 of 500 to 1000 28.5 / 28.4 / 30.5, one of 1000 14.4 / 14.4 /
+// 16.0: 1024 takes too long where there are few tiles, never costs some where there are many.
+constexpr int kShort = 256;
 constexpr int kLeast = 2;                 // fewest steps worth a CTA
 constexpr int kFewSeqs = 16;              // so many sequences may have their tiles cut alike ...
 constexpr int kManyHeads = 8;             // ... of so many kv heads
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // a power of two puts the row's largest value in [2^14, 2^15): exact for fp16, and for
-            // bf16 down to 2^-28 of that value
+            // bf16 down to 2^-28 of that value (why fp16: the file's header)
             const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
             const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
 #pragma unroll
@@ -952,8 +966,8 @@ constexpr int kTileRows = 16;             // the most rows of a tile here
 // the keys again, out of L2; with 32 keys a block or 64 dims that still costs
 // less than a mostly empty 128-row tile, with 16 keys of 128 dims it need not.
 // Measured, this kernel / the other, in us, at 32 rows of 24 sequences of 128
-// to 4001 tokens: pages of 64 75 / 83, 64 dims 50 / 59, pages of 16 98 / 86; at
-// 40 rows (three tiles) 99 / 84, 66 / 60 and 131 / 86; at 16 rows 66 / 85.
+// to 4001 tokens: pages of 64 75 / 80, 64 dims 49 / 59, pages of 16 100 / 84; at
+// 40 rows (three tiles) 99 / 81, 66 / 59 and 131 / 84; at 16 rows 65 / 85.
 int most_rows(const KvCache &c) { return c.page_shift >= 5 || c.head_dim == 64 ? 2 * kTileRows : kTileRows; }
 
 }  // namespace
@@ -1005,6 +1019,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
         const bool few = (long long)a.max_q_len * group <= 8;
         if (many) p.row_limit = most;
         // <codes, dims, 8-row tiles, keys a block, blocks a step, warps, ring stages>
+        // Two blocks a step where the registers allow it: one costs 68 us instead of 57 (64 ragged contexts, pages of
+        // 16), 55 instead of 44 (the same at 64 dims), 41 instead of 34 (64 dims, pages of 64), 61 instead of 52 (24 x 5
+        // tokens, 64 dims, pages of 16).  Rings of 128 to 160 KB, what fits beside the parts: a stage or two more or
+        // less changes up to 2 %, but for 16-row tiles of 128 dims and 16 keys, where three stages take 60.5 us for 24 x
+        // 4 tokens and these four 65.4.
 #define W4A16_FEW(KT)                                                                                              \
     if (keys == 32)                                                                                                \
         e = c.head_dim == 128 ? (few ? launch_few<KT, 128, 1, 32, 1, 8, 2>(p, k, v, grid, s, pdl)                  \

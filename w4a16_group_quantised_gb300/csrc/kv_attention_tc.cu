@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         for (int w = 0; w < kThreads / 32; ++w) most = max(most, s_scan[w]);
         // Parts cost a CTA about 8 steps, and an eighth of its time: prompts of 300 / 1920 / 8192 tokens dealt whole
-        // take 18 / 48 / 540 us, in shares 21 / 65 / 566; five tokens each over 24 contexts, where a whole tile is
-        // most of a CTA's share, take 97 us dealt and 51 in shares.
+        // take 18 / 50 / 549 us, in shares 23 / 68 / 578; five tokens each over 24 contexts, where a whole tile is
+        // most of a CTA's share, take 76 us dealt and 51 in shares.
         deal = most <= total / grid + 8 + total / grid / 8;
     }
 

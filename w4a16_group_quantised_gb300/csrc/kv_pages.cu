@@ -7,7 +7,7 @@
 // change by integer atomics, whose order does not show.
 //
 // Measured (8 kv heads, 128 dims): 3001 pages of 16 copied in 32 us, 0.90 of a
-// copy's bandwidth.  16 prompts forked to 8 sequences each: 10 us, three short
+// copy's bandwidth.  16 prompts forked to 8 sequences each: 6.5 us, two short
 // launches.  Freeing 40 of 96 sequences, trimming the rest to a window and
 // compacting: 68 us, of them 49 the moves (44 at a copy's bandwidth), the rest
 // four short launches.
