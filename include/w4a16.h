@@ -70,7 +70,11 @@ extern "C" {
 /* Same type as cudaStream_t; NULL is the legacy default stream. */
 typedef struct CUstream_st *w4a16_stream_t;
 
-typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype_t;
+typedef enum {
+    W4A16_F16 = 0,
+    W4A16_BF16 = 1,
+    W4A16_F32 = 2            /* logits of w4a16_beam_select only              */
+} w4a16_dtype_t;
 
 typedef enum {
     W4A16_PATH_AUTO = 0,     /* the dispatcher decides from M and the shape   */
@@ -535,6 +539,43 @@ int w4a16_kv_fork(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *
                   int max_blocks, int32_t *refcount, const int32_t *parents, const int32_t *children, int n,
                   void *workspace, long long workspace_bytes, w4a16_stream_t stream);
 
+/* Grow: room for new_lens[b] more tokens of every row b of the tables, from
+ * how many it holds now.  Rows are served in ascending order, each taking the
+ * lowest free pages (count 0 becomes 1) for
+ *   - a copy of its partly filled last page, when the page's count is above 1
+ *     at the row's turn (fork and reorder leave such pages shared, or a
+ *     caller does); the old page's count goes down by one.  So of the rows
+ *     that share a last page the last one keeps it, if all of them grow;
+ *   - the blocks its new tokens begin; what their entries held before is
+ *     overwritten and not freed.
+ * kv_lens[b] grows by new_lens[b].  With the lengths come the rows of the
+ * step's token tensors, as every other entry point of the cache takes them:
+ * q_starts [n_seqs + 1] (the running sum of the tokens, from 0), and of each
+ * token its position [n_tokens] and its slot [n_tokens], page * page_size +
+ * position % page_size.  Rows of no sequence, from q_starts[n_seqs] on, get
+ * position and slot -1.  From the first row on for which the free pages, or
+ * the n_tokens rows, do not suffice, none grows (their tokens are none), and
+ * the status word reads W4A16_ERR_ARG; so it does when a row asks for what
+ * cannot be (a negative count, a length past the table's width, a partly
+ * filled last page that is not there), which then does not grow itself.
+ * n_seqs at most 8192, n_tokens 2^24.
+ * workspace: w4a16_kv_grow_workspace bytes, 16-byte aligned. */
+int w4a16_kv_grow(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks,
+                  int32_t *refcount, const int32_t *new_lens, int n_tokens, int32_t *q_starts, int32_t *positions,
+                  long long *slots, void *workspace, long long workspace_bytes, w4a16_stream_t stream);
+int w4a16_kv_grow_workspace(int n_pages, int n_seqs, long long *bytes);
+
+/* Reorder: for i < n, row dst[i] of the tables (row i where dst is NULL) becomes
+ * what row src[i] was before the call, entries and length; a negative src[i]
+ * leaves it empty (entries -1, length 0).  The pages that rows come to name
+ * gain counts, those that they named before lose them; nothing is copied, so
+ * that a partly filled last page may then be in several rows: w4a16_kv_grow
+ * gives all but one a copy before anything is appended to it.  An id out of
+ * range is reported in the status word and its row left as it is.  No row may
+ * be a dst twice.  n at most 16384. */
+int w4a16_kv_reorder(int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount, int n_pages,
+                     const int32_t *dst_or_null, const int32_t *src, int n, w4a16_stream_t stream);
+
 /* Free sequences: every page that rows seqs[0..n) name loses one count, the
  * rows become -1 and their lengths 0. */
 int w4a16_kv_free(int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount,
@@ -557,6 +598,38 @@ int w4a16_kv_compact(const w4a16_kv_cache_t *cache, int32_t *block_table, int n_
 
 /* Scratch bytes of w4a16_kv_fork and w4a16_kv_compact for a pool of n_pages. */
 int w4a16_kv_pool_workspace(int n_pages, long long *bytes);
+
+/* ------------------------------------------------------------------------
+ * Beam search's selection.  Beams [g * width, (g + 1) * width) are request g's.
+ * logits: [n_groups * width, vocab] of dtype (fp16, bf16 or fp32), rows
+ * row_stride elements apart, any alignment; scores: fp32 [n_groups * width],
+ * the beams' cumulative log-probabilities.  Beam b goes on by token t with
+ *     c(b, t) = scores[b] + logits[b, t] - log sum_t' exp(logits[b, t'])
+ * and out_scores, out_rows, out_tokens [n_groups, n_out] receive each
+ * request's n_out best: c, the beam's row in [0, n_groups * width) and the
+ * token, in falling order: tokens of one beam as their logits are, equal ones in
+ * the order of (row, token).  Beams are compared in 64 bits; what is off in c
+ * is its beam's logarithm, by 2^-18 at most and some 2^-26 in earnest (sums of
+ * exponentials in 32 bits).  c is rounded once.
+ *   - A token of logit -inf, a beam whose score is not finite, and one whose
+ *     logits are all -inf give nothing.  Where too few are left the rest of the
+ *     n_out places are empty: -inf, row -1, token -1.
+ *   - A beam with finished[b] != 0 (optional, [n_groups * width]) goes on as it
+ *     is, with end_token and its score; its logits are not read.  out_finished
+ *     (optional, [n_groups, n_out]): 1 where the beam had finished or the token
+ *     is end_token (negative: none ends a beam; in the vocabulary with finished).
+ *   - A beam with a logit that is NaN or +inf gives nothing, and the status
+ *     word reads W4A16_ERR_ARG.
+ * out_rows is what w4a16_kv_reorder takes as src where n_out == width.
+ * width and n_out 1..64, vocab up to 2^24, at most 2^20 beams.  The outputs
+ * may not overlap the inputs.
+ * workspace: w4a16_beam_select_workspace bytes, 16-byte aligned, not shared
+ * with a call that may run at the same time. */
+int w4a16_beam_select(const void *logits, long long row_stride, w4a16_dtype_t dtype, const float *scores,
+                      const uint8_t *finished_or_null, int n_groups, int width, int vocab, int end_token, int n_out,
+                      float *out_scores, int32_t *out_rows, int32_t *out_tokens, uint8_t *out_finished_or_null,
+                      void *workspace, long long workspace_bytes, w4a16_stream_t stream);
+int w4a16_beam_select_workspace(int n_groups, int width, int vocab, int n_out, long long *bytes);
 
 #ifdef __cplusplus
 }

@@ -6,7 +6,8 @@ K as [N, K/8], per-group scales [N, K/G] (G in {32, 64, 128}), symmetric
 [N/8, K/G]), fp32 accumulation.
 
 Beside it, for whole decoder layers: a paged key/value cache in 8 bits (kv.py:
-append, attention with an optional window and sinks, page operators).
+append, attention with an optional window and sinks or over a common prefix,
+page operators), and beam search's selection (beam.py).
 
 The compute path is the C-ABI shared library ``libw4a16.so`` built from
 ``csrc/`` (hand-written CUDA for sm_103a); ``binding`` marshals torch tensors
@@ -40,19 +41,26 @@ from .binding import (  # noqa: F401
 )
 
 _KV = ("KVCache", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_workspace", "w4a16_kv_compact",
-       "w4a16_kv_copy_pages", "w4a16_kv_fork", "w4a16_kv_free", "w4a16_kv_pool_workspace", "w4a16_kv_read",
-       "w4a16_kv_trim")
+       "w4a16_kv_copy_pages", "w4a16_kv_fork", "w4a16_kv_free", "w4a16_kv_grow", "w4a16_kv_grow_workspace",
+       "w4a16_kv_pool_workspace", "w4a16_kv_read", "w4a16_kv_reorder", "w4a16_kv_trim")
+
+_BEAM = ("w4a16_beam_select", "w4a16_beam_select_workspace")
 
 
 def __getattr__(name):
-    # kv.py imports torch: on first use, so that building the library does not
+    # kv.py and beam.py import torch: on first use, so that building the library does not
     if name in _KV:
         from . import kv
         for n in _KV:
             globals()[n] = getattr(kv, n)
         return globals()[name]
+    if name in _BEAM:
+        from . import beam
+        for n in _BEAM:
+            globals()[n] = getattr(beam, n)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted(list(globals()) + list(_KV))
+    return sorted(list(globals()) + list(_KV) + list(_BEAM))

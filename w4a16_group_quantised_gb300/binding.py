@@ -86,10 +86,15 @@ def load_library():
             "w4a16_kv_attention_workspace": [I, I, I, I, I, P],
             "w4a16_kv_copy_pages": [P, P, P, I, P],
             "w4a16_kv_fork": [P, P, P, I, I, P, P, P, I, P, L, P],
+            "w4a16_kv_grow": [P, P, P, I, I, P, P, I, P, P, P, P, L, P],
+            "w4a16_kv_grow_workspace": [I, I, P],
+            "w4a16_kv_reorder": [P, P, I, I, P, I, P, P, I, P],
             "w4a16_kv_free": [P, P, I, I, P, I, P, I, P],
             "w4a16_kv_trim": [P, P, I, I, P, I, I, I, I, P],
             "w4a16_kv_compact": [P, P, I, I, P, P, P, L, P],
             "w4a16_kv_pool_workspace": [I, P],
+            "w4a16_beam_select": [P, L, I, P, P, I, I, I, I, I, P, P, P, P, P, L, P],
+            "w4a16_beam_select_workspace": [I, I, I, I, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)

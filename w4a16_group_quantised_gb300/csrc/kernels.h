@@ -126,6 +126,14 @@ cudaError_t launch_kv_copy_pages(const KvCache &c, const int *src, const int *ds
 cudaError_t launch_kv_fork(const KvCache &c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
                            const int *parents, const int *children, int n, void *workspace, const DeviceInfo &dev,
                            cudaStream_t s, bool pdl);
+constexpr int kGrowSeqs = 8192;           // rows of a call of grow
+constexpr int kReorderRows = 16384;       // of reorder
+cudaError_t launch_kv_grow(const KvCache &c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
+                           const int *new_lens, int n_tokens, int *q_starts, int *positions, long long *slots,
+                           void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
+long long kv_grow_workspace(int n_pages, int n_seqs);
+cudaError_t launch_kv_reorder(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
+                              const int *dst, const int *src, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl);
 cudaError_t launch_kv_free(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                            const int *seqs, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl);
 cudaError_t launch_kv_trim(int *table, const int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
@@ -133,6 +141,22 @@ cudaError_t launch_kv_trim(int *table, const int *lens, int n_seqs, int max_bloc
 cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_blocks, int *refcount, int *n_live,
                               void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
 long long kv_pool_workspace(int n_pages);
+
+// ---- beam.cu
+constexpr int kBeamMost = 64;             // beams of a request, and continuations that come out of it
+struct BeamArgs {
+    const void *logits;
+    long long row_stride;                 // elements
+    int dtype;                            // 0 fp16, 1 bf16, 2 fp32
+    const float *scores;
+    const uint8_t *finished;              // or null
+    int n_groups, width, vocab, end_token, n_out;
+    float *out_scores;
+    int *out_rows, *out_tokens;
+    uint8_t *out_finished;                // or null
+};
+cudaError_t launch_beam_select(const BeamArgs &a, void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
+long long beam_select_workspace(int n_groups, int width, int vocab, int n_out, const DeviceInfo &dev);
 
 // ---- api.cu helpers used by kv_api.cu and kv_attention.cu: the current device's state (W4A16_OK
 // or an error), the early-launch switch, the timeout hook, the kernel-selection log

@@ -1,5 +1,6 @@
-// kv_api.cu -- C ABI of the paged 8-bit key/value cache: host-side validation
-// and dispatch to kv_append.cu, kv_attention.cu and kv_pages.cu.
+// kv_api.cu -- C ABI of the paged 8-bit key/value cache and of beam search's
+// selection: host-side validation and dispatch to kv_append.cu,
+// kv_attention.cu, kv_pages.cu and beam.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -225,6 +226,46 @@ int w4a16_kv_fork(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *
                                *dev, str(stream), pdl_enabled()));
 }
 
+int w4a16_kv_grow(const w4a16_kv_cache_t *cache, int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks,
+                  int32_t *refcount, const int32_t *new_lens, int n_tokens, int32_t *q_starts, int32_t *positions,
+                  long long *slots, void *workspace, long long workspace_bytes, w4a16_stream_t stream) {
+    KvCache c;
+    W4A16_TRY(check_cache(cache, &c));
+    W4A16_TRY(check_table(block_table, kv_lens, n_seqs, max_blocks, cache->page_size));
+    if (n_seqs > kGrowSeqs || n_tokens < 0 || n_tokens > (1 << 24)) return W4A16_ERR_SHAPE;
+    if (q_starts == nullptr || (n_seqs > 0 && new_lens == nullptr)) return W4A16_ERR_NULL;
+    if (n_tokens > 0 && (positions == nullptr || slots == nullptr)) return W4A16_ERR_NULL;
+    if (refcount == nullptr || workspace == nullptr) return W4A16_ERR_NULL;
+    if (!aligned(refcount, 4) || !aligned(new_lens, 4) || !aligned(q_starts, 4) || !aligned(positions, 4) ||
+        !aligned(slots, 8) || !aligned(workspace, 16))
+        return W4A16_ERR_ALIGN;
+    if (workspace_bytes < kv_grow_workspace(c.n_pages, n_seqs)) return W4A16_ERR_ARG;
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    return done(launch_kv_grow(c, block_table, kv_lens, n_seqs, max_blocks, refcount, new_lens, n_tokens, q_starts,
+                               positions, slots, workspace, *dev, str(stream), pdl_enabled()));
+}
+
+int w4a16_kv_grow_workspace(int n_pages, int n_seqs, long long *bytes) {
+    if (bytes == nullptr) return W4A16_ERR_NULL;
+    if (n_pages <= 0 || n_pages > (1 << 28) || n_seqs < 0 || n_seqs > kGrowSeqs) return W4A16_ERR_SHAPE;
+    *bytes = kv_grow_workspace(n_pages, n_seqs);
+    return W4A16_OK;
+}
+
+int w4a16_kv_reorder(int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount, int n_pages,
+                     const int32_t *dst_or_null, const int32_t *src, int n, w4a16_stream_t stream) {
+    W4A16_TRY(check_table(block_table, kv_lens, n_seqs, max_blocks, 1));
+    if (n < 0 || n > n_seqs || n > kReorderRows || n_pages <= 0) return W4A16_ERR_SHAPE;
+    if (n == 0) return W4A16_OK;
+    if (refcount == nullptr || src == nullptr) return W4A16_ERR_NULL;
+    if (!aligned(refcount, 4) || !aligned(src, 4) || !aligned(dst_or_null, 4)) return W4A16_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    return done(launch_kv_reorder(block_table, kv_lens, n_seqs, max_blocks, refcount, n_pages, dst_or_null, src, n, *dev,
+                                  str(stream), pdl_enabled()));
+}
+
 int w4a16_kv_free(int32_t *block_table, int32_t *kv_lens, int n_seqs, int max_blocks, int32_t *refcount, int n_pages,
                   const int32_t *seqs, int n, w4a16_stream_t stream) {
     W4A16_TRY(check_table(block_table, kv_lens, n_seqs, max_blocks, 1));
@@ -264,6 +305,44 @@ int w4a16_kv_compact(const w4a16_kv_cache_t *cache, int32_t *block_table, int n_
     W4A16_TRY(device_info(&dev));
     return done(launch_kv_compact(c, block_table, n_seqs, max_blocks, refcount, n_live_or_null, workspace, *dev,
                                   str(stream), pdl_enabled()));
+}
+
+static int check_beams(int n_groups, int width, int vocab, int n_out) {
+    if (n_groups < 0 || width < 1 || width > kBeamMost || n_out < 1 || n_out > kBeamMost) return W4A16_ERR_SHAPE;
+    if ((long long)n_groups * width > (1 << 20) || vocab < 1 || vocab > (1 << 24)) return W4A16_ERR_SHAPE;
+    return W4A16_OK;
+}
+
+int w4a16_beam_select(const void *logits, long long row_stride, w4a16_dtype_t dtype, const float *scores,
+                      const uint8_t *finished_or_null, int n_groups, int width, int vocab, int end_token, int n_out,
+                      float *out_scores, int32_t *out_rows, int32_t *out_tokens, uint8_t *out_finished_or_null,
+                      void *workspace, long long workspace_bytes, w4a16_stream_t stream) {
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16 && dtype != W4A16_F32) return W4A16_ERR_DTYPE;
+    W4A16_TRY(check_beams(n_groups, width, vocab, n_out));
+    if (row_stride < vocab || row_stride >= (1LL << 32)) return W4A16_ERR_SHAPE;
+    if (finished_or_null != nullptr && (end_token < 0 || end_token >= vocab)) return W4A16_ERR_ARG;
+    if (n_groups == 0) return W4A16_OK;
+    if (logits == nullptr || scores == nullptr || out_scores == nullptr || out_rows == nullptr || out_tokens == nullptr ||
+        workspace == nullptr)
+        return W4A16_ERR_NULL;
+    if (!aligned(logits, dtype == W4A16_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
+        !aligned(out_rows, 4) || !aligned(out_tokens, 4) || !aligned(workspace, 16))
+        return W4A16_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    if (workspace_bytes < beam_select_workspace(n_groups, width, vocab, n_out, *dev)) return W4A16_ERR_ARG;
+    const BeamArgs a{logits, row_stride, (int)dtype, scores, finished_or_null, n_groups, width, vocab, end_token, n_out,
+                     out_scores, out_rows, out_tokens, out_finished_or_null};
+    return done(launch_beam_select(a, workspace, *dev, str(stream), pdl_enabled()));
+}
+
+int w4a16_beam_select_workspace(int n_groups, int width, int vocab, int n_out, long long *bytes) {
+    if (bytes == nullptr) return W4A16_ERR_NULL;
+    W4A16_TRY(check_beams(n_groups, width, vocab, n_out));
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    *bytes = beam_select_workspace(n_groups, width, vocab, n_out, *dev);
+    return W4A16_OK;
 }
 
 int w4a16_kv_pool_workspace(int n_pages, long long *bytes) {

@@ -1,4 +1,4 @@
-// kv_pages.cu -- page pool of the paged cache: copy, fork, free, trim, compact.
+// kv_pages.cu -- page pool of the paged cache: copy, fork, grow, reorder, free, trim, compact.
 //
 // All of it is integer bookkeeping on the device (no count reaches the host),
 // plus page copies, which are bound by memory: 2 bytes of traffic per byte of
@@ -82,9 +82,8 @@ __global__ void copy_kernel(KvCache c, const int *src, const int *dst, int n, in
 
 // Bitmap of the pages whose count is (not) zero, and its population by chunk.
 // One CTA of 1024 threads per chunk.
-__global__ void bitmap_kernel(const int *refcount, int n_pages, int want_free, uint32_t *bits, int *counts) {
-    kv_begin();
-    __shared__ int s_count[32];
+__device__ __forceinline__ void chunk_bits(const int *refcount, int n_pages, int want_free, uint32_t *bits, int *counts,
+                                           int *s_count) {
     const int p = blockIdx.x * kChunk + threadIdx.x;
     const bool set = p < n_pages && ((refcount[p] == 0) == (want_free != 0));
     const uint32_t w = __ballot_sync(0xffffffffu, set);
@@ -99,6 +98,12 @@ __global__ void bitmap_kernel(const int *refcount, int n_pages, int want_free, u
     }
 }
 
+__global__ void bitmap_kernel(const int *refcount, int n_pages, int want_free, uint32_t *bits, int *counts) {
+    kv_begin();
+    __shared__ int s_count[32];
+    chunk_bits(refcount, n_pages, want_free, bits, counts, s_count);
+}
+
 // Sum over the CTA (every thread gets it).
 __device__ __forceinline__ int block_sum(int v, int *scratch) {
     v = __reduce_add_sync(0xffffffffu, v);
@@ -111,20 +116,21 @@ __device__ __forceinline__ int block_sum(int v, int *scratch) {
 }
 
 // Sum of the threads before this one; *total gets the CTA's sum.
-__device__ __forceinline__ int block_before(int v, int *scratch, int *total) {
+template <typename T>
+__device__ __forceinline__ T block_before(T v, T *scratch, T *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
+    T inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        const T o = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += o;
     }
     __syncthreads();
     if (lane == 31) scratch[warp] = inc;
     __syncthreads();
-    int ahead = 0, all = 0;
+    T ahead = 0, all = 0;
     for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-        const int t = scratch[w];
+        const T t = scratch[w];
         all += t;
         ahead += w < warp ? t : 0;
     }
@@ -236,6 +242,195 @@ __device__ __forceinline__ void drop_page(int p, int *refcount, int n_pages, int
     }
 }
 
+// A row of a call of grow.
+struct GrowRow {
+    int tokens, pages;   // of all rows up to this one
+    int n, need;         // of this row; `need` pages, the first of them for the copy of its last one if `copies`
+    int len, last;       // its length, its partly filled last page (-1 without one)
+    int copies, pad;
+};
+
+// What a call of grow works out on the way to its tables.
+struct GrowScratch {
+    int *total;          // [0] free pages
+    int *counts;         // of each chunk
+    uint32_t *bits;      // free pages
+    int *list;           // free pages by rank
+    GrowRow *rows;
+};
+
+// Open addressing over the partly filled last pages that several rows name:
+// how many growing rows name a page, and the last of these rows.
+struct LastPages {
+    int *page, *rows, *last;
+    unsigned mask;
+    __device__ unsigned slot(int p, bool insert) const {
+        for (unsigned i = (unsigned)p * 2654435761u >> 7 & mask;; i = (i + 1) & mask) {   // half of the places stay free
+            const int was = insert ? atomicCAS(page + i, -1, p) : page[i];
+            if (was == -1 || was == p) return i;
+        }
+    }
+};
+
+// What a row asks for.  One that cannot be met (a length or a count out of
+// range, a last page that is not there) asks for nothing.
+__device__ __forceinline__ GrowRow growth_of(const KvCache &c, const int *table, const int *lens, const int *new_lens,
+                                             int max_blocks, int i, int *status) {
+    const int cap = max_blocks << c.page_shift, said = lens[i], asked = new_lens[i];
+    GrowRow g = {0, 0, asked, 0, min(max(said, 0), cap), -1, 0, 0};
+    bool ok = g.len == said && asked >= 0 && asked <= cap - g.len;
+    if (ok && asked > 0 && (g.len & ((1 << c.page_shift) - 1)) != 0) {
+        g.last = table[(long long)i * max_blocks + (g.len >> c.page_shift)];
+        if (g.last < 0 || g.last >= c.n_pages) ok = false;
+    }
+    if (!ok) {
+        kv_report(status);
+        g.n = 0, g.last = -1;
+    }
+    return g;
+}
+
+// CTAs 0 .. gridDim.x - 2: the bitmap of free pages.  The last: what every row
+// needs, summed up over the rows before it.  A row whose partly filled last
+// page others name too takes a copy, but for the last of the rows that grow
+// when these are all that name it.
+__global__ void __launch_bounds__(kChunk)
+    grow_plan_kernel(KvCache c, const int *table, const int *lens, const int *new_lens, int n_seqs, int max_blocks,
+                     const int *refcount, unsigned places, GrowScratch w, int *status) {
+    kv_begin();
+    extern __shared__ __align__(16) int grow_smem[];     // no static shared memory: the launch may ask for all there is
+    if (blockIdx.x + 1 < gridDim.x) {
+        chunk_bits(refcount, c.n_pages, 1, w.bits, w.counts, grow_smem);
+        return;
+    }
+    long long *scratch = reinterpret_cast<long long *>(grow_smem);
+    int *pages_at = grow_smem + 64;
+    const LastPages h = {pages_at, pages_at + places, pages_at + 2 * places, places - 1};
+    for (unsigned i = threadIdx.x; i < places; i += blockDim.x) h.page[i] = -1, h.rows[i] = 0, h.last[i] = -1;
+    __syncthreads();
+    const int ps = 1 << c.page_shift;
+    for (int i = threadIdx.x; i < n_seqs; i += blockDim.x) {
+        GrowRow g = growth_of(c, table, lens, new_lens, max_blocks, i, status);
+        g.need = ((g.len + g.n + ps - 1) >> c.page_shift) - ((g.len + ps - 1) >> c.page_shift);
+        if (g.last >= 0) g.copies = refcount[g.last];     // for now: how many name it
+        if (g.copies > 1) {
+            const unsigned s = h.slot(g.last, true);
+            atomicAdd(h.rows + s, 1);
+            atomicMax(h.last + s, i);
+        }
+        w.rows[i] = g;
+    }
+    __syncthreads();
+    constexpr long long kMost = 0x7fffffff;              // more tokens or pages than any call may have
+    long long tokens = 0, pages = 0;
+    for (int base = 0; base < n_seqs; base += blockDim.x) {
+        const int i = base + threadIdx.x;
+        GrowRow g = {};
+        if (i < n_seqs) {
+            g = w.rows[i];                               // this thread's own
+            if (g.copies > 1) {
+                const unsigned s = h.slot(g.last, false);
+                g.copies = h.rows[s] < g.copies || h.last[s] != i;
+            } else {
+                g.copies = 0;
+            }
+            g.need += g.copies;
+        }
+        long long all_tokens, all_pages;
+        const long long t = tokens + g.n + block_before<long long>(g.n, scratch, &all_tokens);
+        const long long p = pages + g.need + block_before<long long>(g.need, scratch, &all_pages);
+        if (i < n_seqs) {
+            g.tokens = (int)min(t, kMost), g.pages = (int)min(p, kMost);
+            w.rows[i] = g;
+        }
+        tokens += all_tokens, pages += all_pages;
+    }
+}
+
+// The free pages by rank: each CTA those of its chunk.
+__global__ void __launch_bounds__(kChunk) grow_list_kernel(GrowScratch w, int n_pages) {
+    kv_begin();
+    __shared__ int scratch[32];
+    const int n_chunks = (n_pages + kChunk - 1) / kChunk;
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < n_chunks; i += blockDim.x) {
+        const int v = w.counts[i];
+        all += v;
+        before += i < (int)blockIdx.x ? v : 0;
+    }
+    before = block_sum(before, scratch);
+    all = block_sum(all, scratch);
+    const int p = blockIdx.x * kChunk + threadIdx.x;
+    const bool is_free = w.bits[p >> 5] >> (threadIdx.x & 31) & 1;
+    int total;
+    const int at = before + block_before<int>(is_free, scratch, &total);
+    if (is_free) w.list[at] = p;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *w.total = all;
+}
+
+// `parts` CTAs a row: its entries, its tokens' positions and slots, the copy of
+// its last page.  From the first row on for which the free pages, or the rows
+// of the token tensors, do not suffice, none grows.
+__global__ void grow_fill_kernel(KvCache c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
+                                 GrowScratch w, int n_tokens, int *q_starts, int *positions, long long *slots,
+                                 int parts, int *status) {
+    kv_begin();
+    __shared__ int s_total;
+    const int me = blockIdx.x / parts, part = blockIdx.x % parts, shift = c.page_shift;
+    const int free_pages = *w.total;
+    auto fits = [&](const GrowRow &r) { return r.tokens <= n_tokens && r.pages <= free_pages; };
+    int total = 0;                                       // tokens of the rows that grow
+    if (n_seqs > 0) {
+        const GrowRow end = w.rows[n_seqs - 1];
+        total = end.tokens;
+        if (!fits(end)) {
+            if (threadIdx.x == 0) s_total = 0;
+            __syncthreads();
+            for (int i = threadIdx.x; i + 1 < n_seqs; i += blockDim.x) {
+                const GrowRow r = w.rows[i];
+                if (fits(r) && !fits(w.rows[i + 1])) s_total = r.tokens;
+            }
+            __syncthreads();
+            total = s_total;
+            if (blockIdx.x == 0 && threadIdx.x == 0) kv_report(status);
+        }
+    }
+    // rows of the token tensors that are no sequence's
+    for (long long i = (long long)total + (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_tokens;
+         i += (long long)gridDim.x * blockDim.x) {
+        positions[i] = -1;
+        slots[i] = -1;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) q_starts[0] = 0;
+    if (me >= n_seqs) return;
+    const GrowRow g = w.rows[me];
+    const bool ok = fits(g);
+    if (part == 0 && threadIdx.x == 0) q_starts[me + 1] = ok ? g.tokens : total;
+    if (!ok || g.n == 0) return;
+    const int *list = w.list + (g.pages - g.need);
+    // the row's new pages are those of blocks `start` and on
+    const int start = ((g.len + (1 << shift) - 1) >> shift) - g.copies;
+    for (int t = part * blockDim.x + threadIdx.x; t < g.n; t += parts * blockDim.x) {
+        const int pos = g.len + t, blk = pos >> shift;
+        const int p = blk >= start ? list[blk - start] : g.last;
+        positions[g.tokens - g.n + t] = pos;
+        slots[g.tokens - g.n + t] = ((long long)p << shift) + (pos & ((1 << shift) - 1));
+    }
+    if (part == 0) {
+        int *to = table + (long long)me * max_blocks + start;
+        for (int k = threadIdx.x; k < g.need; k += blockDim.x) {
+            const int p = list[k];
+            to[k] = p;
+            refcount[p] = 1;
+        }
+        if (threadIdx.x == 0) {
+            lens[me] = g.len + g.n;
+            if (g.copies) drop_page(g.last, refcount, c.n_pages, status);
+        }
+    }
+    if (g.copies) copy_page(c, g.last, list[0], part, parts);
+}
+
 __global__ void free_kernel(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                             const int *seqs, int *status) {
     kv_begin();
@@ -264,6 +459,53 @@ __global__ void trim_kernel(int *table, const int *lens, int max_blocks, int *re
         const int p = *e;
         if (p >= 0) *e = -1;
         drop_page(p, refcount, n_pages, status);
+    }
+}
+
+// Row dst[i] becomes what row src[i] was: each CTA does so for `cols` columns of
+// all rows, reading all it needs of them before it writes any, and the first
+// for the lengths too.  A row that keeps an entry leaves its page's count alone,
+// so beams that go on from one another cost counts for the pages since they
+// parted only.  Whoever takes a page id out of an entry lowers its count: the
+// counts are right whatever the lists say.
+__global__ void reorder_kernel(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
+                               const int *dst, const int *src, int n, int cols, int *status) {
+    kv_begin();
+    extern __shared__ int dyn[];
+    constexpr int kSkip = -2;                            // the row stays as it is
+    int *entries = dyn, *old_lens = dyn + n * cols;
+    const bool first = blockIdx.x == 0;
+    const int col0 = blockIdx.x * cols, width = min(cols, max_blocks - col0);
+    auto row_to = [&](int i) { return dst ? dst[i] : i; };
+    for (int i = threadIdx.x; first && i < n; i += blockDim.x) {
+        const int s = src[i], d = row_to(i);
+        const bool bad = s >= n_seqs || d < 0 || d >= n_seqs;
+        if (bad) kv_report(status);
+        old_lens[i] = bad ? kSkip : s < 0 ? 0 : lens[s];
+    }
+#pragma unroll 4
+    for (int k = threadIdx.x; k < n * cols; k += blockDim.x) {
+        const int i = k / cols, at = k % cols, s = src[i], d = row_to(i);
+        int v = kSkip;
+        if (at < width && s < n_seqs && d >= 0 && d < n_seqs) {
+            v = s < 0 ? -1 : table[(long long)s * max_blocks + col0 + at];
+            if (v >= n_pages) kv_report(status);
+            if (v < 0 || v >= n_pages) v = -1;
+        }
+        entries[k] = v;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; first && i < n; i += blockDim.x)
+        if (old_lens[i] != kSkip) lens[row_to(i)] = old_lens[i];
+#pragma unroll 4
+    for (int k = threadIdx.x; k < n * cols; k += blockDim.x) {
+        const int v = entries[k];
+        if (v == kSkip) continue;
+        int *e = table + (long long)row_to(k / cols) * max_blocks + col0 + k % cols;
+        if (*e == v) continue;
+        const int was = atomicExch(e, v);
+        if (v >= 0) atomicAdd(refcount + v, 1);
+        drop_page(was, refcount, n_pages, status);
     }
 }
 
@@ -396,6 +638,59 @@ cudaError_t launch_kv_fork(const KvCache &c, int *table, int *lens, int n_seqs, 
                      max_blocks, refcount, parents, children, n, parts, w.bits, w.counts, dev.status);
 }
 
+namespace {
+GrowScratch grow_scratch(void *ws, int n_pages) {
+    const long long chunks = (n_pages + kChunk - 1) / kChunk;
+    char *p = static_cast<char *>(ws);
+    GrowScratch s;
+    auto take = [&](long long bytes) {
+        char *q = p;
+        p += round16(bytes);
+        return q;
+    };
+    s.total = reinterpret_cast<int *>(take(16));
+    s.counts = reinterpret_cast<int *>(take(chunks * 4));
+    s.bits = reinterpret_cast<uint32_t *>(take(chunks * kChunk / 8));
+    s.list = reinterpret_cast<int *>(take((long long)n_pages * 4));
+    s.rows = reinterpret_cast<GrowRow *>(p);
+    return s;
+}
+}  // namespace
+
+cudaError_t launch_kv_grow(const KvCache &c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
+                           const int *new_lens, int n_tokens, int *q_starts, int *positions, long long *slots,
+                           void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
+    const GrowScratch w = grow_scratch(workspace, c.n_pages);
+    const int chunks = (c.n_pages + kChunk - 1) / kChunk;
+    unsigned places = 32;
+    while ((int)places < 2 * n_seqs) places *= 2;
+    const size_t smem = 256 + places * 12;
+    cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(grow_plan_kernel), smem);
+    if (e != cudaSuccess) return e;
+    e = kv_launch(grow_plan_kernel, dim3(chunks + 1), dim3(kChunk), smem, s, pdl, c, table, lens, new_lens, n_seqs,
+                  max_blocks, refcount, places, w, dev.status);
+    if (e != cudaSuccess) return e;
+    e = kv_launch(grow_list_kernel, dim3(chunks), dim3(kChunk), 0, s, pdl, w, c.n_pages);
+    if (e != cudaSuccess) return e;
+    // CTAs a row: for the copy of a page, or for a few of an even share of the tokens
+    const int rows = std::max(n_seqs, 1);
+    const int parts = std::max(std::min(copy_parts(c), 4), std::min(n_tokens / rows / (4 * kCopyThreads) + 1, 16));
+    return kv_launch(grow_fill_kernel, dim3((unsigned)rows * parts), dim3(kCopyThreads), 0, s, pdl, c, table, lens, n_seqs,
+                     max_blocks, refcount, w, n_tokens, q_starts, positions, slots, parts, dev.status);
+}
+
+cudaError_t launch_kv_reorder(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
+                              const int *dst, const int *src, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
+    // a sector's columns a CTA, fewer where the rows would not fit
+    int cols = 8;
+    while (cols > 1 && (long long)n * cols * 4 > 64 << 10) cols /= 2;
+    const size_t smem = (size_t)n * (cols + 1) * 4;
+    const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(reorder_kernel), smem);
+    if (e != cudaSuccess) return e;
+    return kv_launch(reorder_kernel, dim3((max_blocks + cols - 1) / cols), dim3(512), smem, s, pdl, table, lens, n_seqs,
+                     max_blocks, refcount, n_pages, dst, src, n, cols, dev.status);
+}
+
 cudaError_t launch_kv_free(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                            const int *seqs, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
     return kv_launch(free_kernel, dim3(n), dim3(512), 0, s, pdl, table, lens, n_seqs, max_blocks, refcount, n_pages,
@@ -424,6 +719,12 @@ cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_
     const int renamers = (int)std::min<long long>((entries + kCopyThreads - 1) / kCopyThreads, dev.sm_count);
     return kv_launch(move_kernel, dim3(movers + renamers), dim3(kCopyThreads), 0, s, pdl, c, w, table, entries,
                      refcount, movers, parts, dev.status);
+}
+
+long long kv_grow_workspace(int n_pages, int n_seqs) {
+    const long long chunks = (n_pages + kChunk - 1) / kChunk;
+    return 16 + round16(chunks * 4) + round16(chunks * kChunk / 8) + round16((long long)n_pages * 4) +
+           (long long)n_seqs * sizeof(GrowRow);
 }
 
 long long kv_pool_workspace(int n_pages) {

@@ -307,6 +307,50 @@ def w4a16_kv_fork(cache, block_table, kv_lens, refcount, parents, children, work
         c, table, lens, rows, width, counts, a, b, parents.shape[0], at, size, handle))
 
 
+@functools.lru_cache(maxsize=256)
+def w4a16_kv_grow_workspace(n_pages: int, n_seqs: int) -> int:
+    """Bytes of workspace that w4a16_kv_grow needs."""
+    need = ctypes.c_longlong(0)
+    _check("w4a16_kv_grow_workspace", load_library().w4a16_kv_grow_workspace(n_pages, n_seqs, ctypes.byref(need)))
+    return need.value
+
+
+def w4a16_kv_grow(cache, block_table, kv_lens, refcount, new_lens, n_tokens: int, q_starts=None, positions=None, slots=None,
+                  workspace=None, stream=None):
+    """Room for new_lens[b] more tokens of every row: pages from the free ones,
+    a last page that other rows name too copied.  kv_lens grows with them.
+    Returns (q_starts int32 [rows + 1], positions int32 [n_tokens], slots int64
+    [n_tokens]): the rows of the step's token tensors, where each token is in
+    its sequence and in the pool; -1 past the last token."""
+    c, dev, pages = _cache(cache)[:3]
+    table, lens, rows, width = _table(block_table, kv_lens, dev)
+    counts, new = _counts(refcount, dev, pages), _ints("new_lens", new_lens, 1, dev)
+    if new_lens.shape[0] != rows:
+        raise ValueError(f"block_table has {rows} rows, new_lens {new_lens.shape[0]}")
+    q_starts = _output("q_starts", q_starts, (rows + 1,), torch.int32, dev, stream)
+    positions = _output("positions", positions, (n_tokens,), torch.int32, dev, stream)
+    slots = _output("slots", slots, (n_tokens,), torch.int64, dev, stream)
+    handle = _stream(stream, dev)
+    ws, at, size = _scratch(workspace, w4a16_kv_grow_workspace(pages, rows), dev, handle)
+    _check("w4a16_kv_grow", load_library().w4a16_kv_grow(
+        c, table, lens, rows, width, counts, new, n_tokens, q_starts.data_ptr(), positions.data_ptr(), slots.data_ptr(), at,
+        size, handle))
+    return q_starts, positions, slots
+
+
+def w4a16_kv_reorder(block_table, kv_lens, refcount, src, dst=None, stream=None):
+    """Rows dst[i] (or i) become what rows src[i] were, none where src[i] is
+    negative; pages' counts follow, nothing is copied."""
+    dev = _current(_device_of("block_table", block_table))
+    table, lens, rows, width = _table(block_table, kv_lens, dev)
+    counts, a = _counts(refcount, dev), _ints("src", src, 1, dev)
+    b = None if dst is None else _ints("dst", dst, 1, dev)
+    if dst is not None and dst.shape[0] != src.shape[0]:
+        raise ValueError("src and dst must have the same length")
+    _check("w4a16_kv_reorder", load_library().w4a16_kv_reorder(
+        table, lens, rows, width, counts, refcount.shape[0], b, a, src.shape[0], _stream(stream, dev)))
+
+
 def w4a16_kv_free(block_table, kv_lens, refcount, seqs, stream=None):
     """Rows seqs[i] give up their pages: counts go down, entries become -1, lengths 0."""
     dev = _current(_device_of("block_table", block_table))
