@@ -46,7 +46,7 @@
  * w4a16_debug_set_config(3, {0}, 1)).
  *
  * Kernel-selection log: with the environment variable W4A16_LOG=1 (read on
- * the first call on a device) each GEMM entry point, and w4a16_kv_attention,
+ * the first call on a device) each GEMM entry point, and the two of attention,
  * prints the kernel it launched -- path, kernel, its configuration, grid,
  * early start, epilogue -- to stderr, each distinct line once; W4A16_LOG=2
  * prints every call.
@@ -515,6 +515,26 @@ int w4a16_kv_attention(const void *q, long long q_stride, int n_heads, const w4a
  * whatever the lengths. */
 int w4a16_kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
                                  long long *bytes);
+
+/* The same attention, without a window, of a batch whose sequences have their
+ * first pages in common: samples or beams of one prompt (w4a16_kv_fork,
+ * w4a16_kv_reorder), users of one system prompt.  Sequences [group_starts[g],
+ * group_starts[g + 1]) are group g, and their first prefix_lens[g] positions
+ * are in the same pages (group_starts [n_groups + 1], non-decreasing, within
+ * [0, n_seqs]; prefix_lens [n_groups], 0 or more; device, read there like the
+ * lengths; what is wrong in them is reported in the status word).  Sequences of
+ * no group share nothing.  The whole pages among these positions that lie
+ * before every new token of the group are read once for all of its tokens,
+ * and from the row of its first sequence that brings any: with rows that do
+ * name the same pages the result is w4a16_kv_attention's but for rounding
+ * (sums over the shared keys and over the others are joined in fp32).
+ * workspace: w4a16_kv_attention_shared_workspace bytes, as above. */
+int w4a16_kv_attention_shared(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
+                              const w4a16_kv_batch_t *batch, int max_q_len, const int32_t *group_starts,
+                              const int32_t *prefix_lens, int n_groups, float scale, void *out, float *lse_or_null,
+                              w4a16_dtype_t dtype, void *workspace, long long workspace_bytes, w4a16_stream_t stream);
+int w4a16_kv_attention_shared_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups,
+                                        int n_tokens, long long *bytes);
 
 /* Page pool.  refcount[p] counts the block-table entries that name page p; a
  * page with count 0 is free.  The caller sets the count when it hands a page

@@ -1,9 +1,10 @@
-"""What growth, reordering and beam selection refuse on the host, before any
-device is touched, and what the binding refuses before the C call."""
+"""What attention over a common prefix, growth, reordering and beam selection refuse on the
+host, before any device is touched, and what the binding refuses before the C call."""
 import pytest
 import torch
 
-from test_kv_refusals_cpu import ERR_ALIGN, ERR_ARG, ERR_DTYPE, ERR_NULL, ERR_SHAPE, NULL, OK, cache, lib  # noqa: F401
+from test_kv_refusals_cpu import (ERR_ALIGN, ERR_ARG, ERR_DTYPE, ERR_NULL, ERR_SHAPE, NULL, OK, batch, cache,  # noqa: F401
+                                  lib)
 
 
 def grow(lib, c=None, table=OK, lens=OK, seqs=2, blocks=4, ref=OK, new=OK, tokens=3, starts=OK, pos=OK, slots=OK, ws=OK,
@@ -19,6 +20,36 @@ def select(lib, logits=OK, stride=100, dtype=0, scores=OK, finished=NULL, groups
            rows=OK, tokens=OK, fin=OK, ws=OK, size=1 << 40):
     return lib.w4a16_beam_select(logits, stride, dtype, scores, finished, groups, width, vocab, end, n, os, rows, tokens, fin,
                                  ws, size, None)
+
+
+def shared(lib, c=None, b=None, q=OK, qs=1024, heads=8, most=1, starts=OK, prefix=OK, groups=1, scale=0.1, out=OK, lse=None,
+           dt=0, ws=OK, size=1 << 40):
+    return lib.w4a16_kv_attention_shared(q, qs, heads, c or cache(), b or batch(), most, starts, prefix, groups, scale, out, lse,
+                                         dt, ws, size, None)
+
+
+def test_attention_shared(lib):  # noqa: F811
+    assert shared(lib, dt=2) == ERR_DTYPE and shared(lib, c=cache(kv_dtype=2)) == ERR_DTYPE
+    for bad in (dict(heads=0), dict(heads=7), dict(heads=2 * 129), dict(groups=-1), dict(groups=3), dict(qs=1000),
+                dict(c=cache(page_size=8)), dict(b=batch(n_seqs=-1)), dict(b=batch(n_tokens=1 << 24), heads=256, qs=1 << 15)):
+        assert shared(lib, **bad) == ERR_SHAPE, bad
+    for bad in (dict(q=NULL), dict(out=NULL), dict(ws=NULL), dict(starts=NULL), dict(prefix=NULL),
+                dict(b=batch(kv_lens=NULL))):
+        assert shared(lib, **bad) == ERR_NULL, bad
+    for bad in (dict(q=OK + 8), dict(out=OK + 4), dict(lse=OK + 2), dict(ws=OK + 8), dict(starts=OK + 2), dict(prefix=OK + 1),
+                dict(qs=1028)):
+        assert shared(lib, **bad) == ERR_ALIGN, bad
+    assert shared(lib, most=-1) == ERR_ARG and shared(lib, scale=float("nan")) == ERR_ARG
+    assert shared(lib, b=batch(n_tokens=0), q=NULL, out=NULL, ws=NULL, starts=NULL) == 0
+
+
+def test_attention_shared_workspace(lib):  # noqa: F811
+    import ctypes
+    need = ctypes.c_longlong(0)
+    assert lib.w4a16_kv_attention_shared_workspace(8, 2, 128, 4, 1, 4, None) == ERR_NULL
+    for bad in ((0, 2, 128, 4, 1, 4), (8, 3, 128, 4, 1, 4), (8, 2, 96, 4, 1, 4), (8, 2, 128, -1, 0, 4), (8, 2, 128, 4, 5, 4),
+                (8, 2, 128, 4, -1, 4), (8, 2, 128, 4, 1, -1)):
+        assert lib.w4a16_kv_attention_shared_workspace(*bad, ctypes.byref(need)) == ERR_SHAPE, bad
 
 
 def test_grow(lib):  # noqa: F811
@@ -82,6 +113,8 @@ def test_binding():
                    torch.zeros((4, 1)), torch.zeros((4, 1)))
     with pytest.raises(ValueError, match="cache.k"):
         w.w4a16_kv_grow(kv, i.view(2, 2), i[:2], i, i[:2], 3)
+    with pytest.raises(ValueError, match="cache.k"):
+        w.w4a16_kv_attention_shared(torch.zeros((2, 4, 64)), kv, i.view(2, 2), i[:2], i[:3], 1, i[:2], i[:1])
     with pytest.raises(ValueError, match="block_table"):
         w.w4a16_kv_reorder(i.view(2, 2), i[:2], i, i[:2])
     with pytest.raises(ValueError, match="logits"):

@@ -40,7 +40,8 @@ from .binding import (  # noqa: F401
     w4a16_select_path,
 )
 
-_KV = ("KVCache", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_workspace", "w4a16_kv_compact",
+_KV = ("KVCache", "w4a16_kv_append", "w4a16_kv_attention", "w4a16_kv_attention_shared",
+       "w4a16_kv_attention_shared_workspace", "w4a16_kv_attention_workspace", "w4a16_kv_compact",
        "w4a16_kv_copy_pages", "w4a16_kv_fork", "w4a16_kv_free", "w4a16_kv_grow", "w4a16_kv_grow_workspace",
        "w4a16_kv_pool_workspace", "w4a16_kv_read", "w4a16_kv_reorder", "w4a16_kv_trim")
 

@@ -84,6 +84,8 @@ def load_library():
             "w4a16_kv_read": [P, P, P, P, I, P],
             "w4a16_kv_attention": [P, L, I, P, P, I, F, I, I, P, P, I, P, L, P],
             "w4a16_kv_attention_workspace": [I, I, I, I, I, P],
+            "w4a16_kv_attention_shared": [P, L, I, P, P, I, P, P, I, F, P, P, I, P, L, P],
+            "w4a16_kv_attention_shared_workspace": [I, I, I, I, I, I, P],
             "w4a16_kv_copy_pages": [P, P, P, I, P],
             "w4a16_kv_fork": [P, P, P, I, I, P, P, P, I, P, L, P],
             "w4a16_kv_grow": [P, P, P, I, I, P, P, I, P, P, P, P, L, P],

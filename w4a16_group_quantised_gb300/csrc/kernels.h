@@ -108,6 +108,21 @@ struct KvAttentionArgs {
     int dtype;                            // 0 fp16, 1 bf16
     void *workspace;
 };
+// Attention of a batch whose sequences share pages (kv_attention_shared.cu): a
+// pass over the shared keys, an entry for each group, then one over the rest,
+// an entry for each sequence.
+struct KvEntry {
+    int q0, n;                            // rows of the token tensors
+    int len, pad;                         // keys, from position 0 of the first page on
+    long long pages;                      // where its page ids begin in the block table
+    long long pad2;
+};
+struct KvShare {
+    const KvEntry *entries;
+    int step;                             // 0: the shared keys, which every row sees; 1: the others, row t up to len - n + t
+    float *out;                           // [n_tokens, n_heads, head_dim] sums over the shared keys, not yet divided
+    float *ml;                            // [n_tokens, n_heads, 2] their references and denominators
+};
 cudaError_t launch_kv_append(const KvCache &c, const KvBatch &b, const void *k_new, long long k_stride,
                              const void *v_new, long long v_stride, int dtype, const DeviceInfo &dev, cudaStream_t s,
                              bool pdl);
@@ -115,9 +130,19 @@ cudaError_t launch_kv_read(const KvCache &c, const KvBatch &b, void *k_out, void
                            const DeviceInfo &dev, cudaStream_t s, bool pdl);
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, const DeviceInfo &dev,
                                 cudaStream_t s, bool pdl);
-// sequences with more than row_limit rows (tokens * query heads of a kv head), in kv_attention_tc.cu
+// sequences with more than row_limit rows (tokens * query heads of a kv head), in kv_attention_tc.cu; share: or null
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, int row_limit,
-                                     const DeviceInfo &dev, cudaStream_t s, bool pdl);
+                                     const DeviceInfo &dev, cudaStream_t s, bool pdl, const KvShare *share = nullptr);
+int kv_few_rows_most(const KvCache &c);   // rows up to which kv_few_rows.cuh's kernel is the faster one
+// sequences [group_starts[g], group_starts[g + 1]) have their first prefix_lens[g] positions in the same pages
+struct KvGroups {
+    const int *group_starts, *prefix_lens;
+    int n_groups;
+};
+cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, const KvGroups &g,
+                                       const DeviceInfo &dev, cudaStream_t s, bool pdl);
+long long kv_attention_shared_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups,
+                                        int n_tokens, const DeviceInfo &dev);
 long long kv_attention_many_workspace(int head_dim, const DeviceInfo &dev);
 long long kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
                                  const DeviceInfo &dev);

@@ -184,6 +184,49 @@ int w4a16_kv_attention(const void *q, long long q_stride, int n_heads, const w4a
     return done(launch_kv_attention(a, c, b, *dev, str(stream), pdl_enabled()));
 }
 
+int w4a16_kv_attention_shared(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
+                              const w4a16_kv_batch_t *batch, int max_q_len, const int32_t *group_starts,
+                              const int32_t *prefix_lens, int n_groups, float scale, void *out, float *lse_or_null,
+                              w4a16_dtype_t dtype, void *workspace, long long workspace_bytes, w4a16_stream_t stream) {
+    KvCache c;
+    KvBatch b;
+    W4A16_TRY(check_dtype((int)dtype));
+    W4A16_TRY(check_cache(cache, &c));
+    W4A16_TRY(check_batch(batch, cache->page_size, &b));
+    if (n_heads <= 0 || n_heads % c.n_kv_heads != 0 || n_heads / c.n_kv_heads > 128 || n_heads > 4096)
+        return W4A16_ERR_SHAPE;
+    if ((long long)b.n_tokens * n_heads >= (1LL << 31)) return W4A16_ERR_SHAPE;
+    if (n_groups < 0 || n_groups > b.n_seqs) return W4A16_ERR_SHAPE;
+    if (max_q_len < 0 || !(scale == scale)) return W4A16_ERR_ARG;
+    if (b.n_tokens == 0) return W4A16_OK;
+    if (q == nullptr || out == nullptr || workspace == nullptr) return W4A16_ERR_NULL;
+    if (n_groups > 0 && (group_starts == nullptr || prefix_lens == nullptr)) return W4A16_ERR_NULL;
+    W4A16_TRY(check_rows(q, q_stride, (long long)n_heads * c.head_dim));
+    if (!aligned(out, 16) || !aligned(lse_or_null, 4) || !aligned(workspace, 16) || !aligned(group_starts, 4) ||
+        !aligned(prefix_lens, 4))
+        return W4A16_ERR_ALIGN;
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    if (workspace_bytes <
+        kv_attention_shared_workspace(n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, n_groups, b.n_tokens, *dev))
+        return W4A16_ERR_ARG;
+    const KvAttentionArgs a{q, q_stride, n_heads, max_q_len, 0, 0, scale, out, lse_or_null, (int)dtype, workspace};
+    return done(launch_kv_attention_shared(a, c, b, KvGroups{group_starts, prefix_lens, n_groups}, *dev, str(stream),
+                                           pdl_enabled()));
+}
+
+int w4a16_kv_attention_shared_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups,
+                                        int n_tokens, long long *bytes) {
+    if (bytes == nullptr) return W4A16_ERR_NULL;
+    if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 128 || n_heads > 4096 ||
+        (head_dim != 64 && head_dim != 128) || n_seqs < 0 || n_groups < 0 || n_groups > n_seqs || n_tokens < 0)
+        return W4A16_ERR_SHAPE;
+    const DeviceInfo *dev = nullptr;
+    W4A16_TRY(device_info(&dev));
+    *bytes = kv_attention_shared_workspace(n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens, *dev);
+    return W4A16_OK;
+}
+
 int w4a16_kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_tokens,
                                  long long *bytes) {
     if (bytes == nullptr) return W4A16_ERR_NULL;

@@ -1,7 +1,7 @@
 // kv_attention_tc.cu -- attention of many query rows over the paged 8-bit
 // cache, on the 5th-generation tensor cores (tcgen05 + TMEM).
 //
-// The mathematics of kv_attention.cu: weights 2^e_j with e_j = x_j +
+// The mathematics of kv_few_rows.cuh: weights 2^e_j with e_j = x_j +
 // log2(vs_j) - M, M a reference of each row that moves only when some e_j
 // passes 15.9, so that the value scales stay out of the products and the
 // weights fit fp16.  The rows of a tile are the tokens of one sequence times
@@ -26,7 +26,7 @@
 //    work on the other half's out += P V and next S.
 //  * Warp 13: lists the CTA's tiles ahead of the others, and brings Q by TMA.
 //
-// The work is cut as in kv_attention.cu: a line of all tiles' steps, each
+// The work is cut as in kv_few_rows.cuh: a line of all tiles' steps, each
 // causal tile with just the steps that its rows see, in equal shares; CTAs
 // that share a tile add their parts up through the workspace, in order.  Where
 // whole tiles come close to that, the longest first, they are dealt out whole.
@@ -40,7 +40,7 @@
 // Measured: a prompt of 8192 tokens (32 heads on 8, 128 dims, int8), 33,280
 // steps, 219 an SM: 549 us, 1000 TFLOP/s, 0.52 of the measured matrix rate,
 // tensor pipe 42 % active; 1920 tokens 50 us.  P is fp16 and the sums are fp32,
-// for the reasons that kv_attention.cu gives.  Tried and slower: S in two 64-key pieces (more operand reads),
+// for the reasons that kv_few_rows.cuh gives.  Tried and slower: S in two 64-key pieces (more operand reads),
 // conversion by 8 warps (the softmax then spills), 16-key units over 6 warps,
 // raw codes by TMA through the 24 KB of shared memory that are left (too few
 // bytes in flight), one stage of K and V with Q doubled.
@@ -80,6 +80,7 @@ struct ManyParams {
     unsigned long long tag;
     int hold;                             // test hook (kv_holds)
     int *status;
+    KvShare share;                        // of a call with SHARED: what its sequences are (kv_attention_shared.cu)
 };
 
 struct ManyTile {
@@ -88,6 +89,7 @@ struct ManyTile {
     int steps, sink, block0;              // key blocks [0, sink) and from block0 on
     int lo, hi;                           // its rows see positions below `sinks` and lo..hi
     long long begin;                      // on the line
+    long long pages;                      // where its page ids begin in the block table (SHARED)
 };
 
 // A tile with this CTA's steps [s0, s1) of it; s1 == 0 ends the list.
@@ -311,7 +313,7 @@ __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block
     return d;
 }
 
-// Codes of a word as pairs (0, 1) and (2, 3) of fp16 (see kv_attention.cu) or
+// Codes of a word as pairs (0, 1) and (2, 3) of fp16 (see kv_few_rows.cuh) or
 // bf16, exactly.  int8 as bf16: 0x4300 with the low seven bits is 128 + those,
 // 0x4300 with the sign bit is 128 or 256; their difference is the code.
 template <int KT, bool BF16>
@@ -363,7 +365,7 @@ __device__ __forceinline__ void convert_codes(const uint4 (&raw)[D == 128 ? 8 : 
     }
 }
 
-template <int KT, int D>
+template <bool SHARED, int KT, int D>
 __global__ void __launch_bounds__(kThreads, 1) 
     many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const ManyParams p) {
     using L = ManySmem<D>;
@@ -424,20 +426,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     grid_dependency_wait();
 
+    // the position of a tile's tok-th token
+    auto position = [&](int first, int tok) { return SHARED ? first + tok * p.share.step : first + tok; };
     auto tile_of = [&](const int4 s, int b, int r) {
         ManyTile t;
         t.seq = b;
-        t.q0 = s.x, t.n = s.y, t.len = s.z, t.first = s.z - s.y;
+        t.q0 = s.x, t.n = s.y, t.len = s.z, t.first = SHARED && p.share.step == 0 ? s.z - 1 : s.z - s.y;
         t.row0 = r * 2 * half_rows;
         t.rows = min(2 * half_rows, s.y * group - t.row0);
-        const int lo_pos = t.first + t.row0 / group, hi_pos = t.first + (t.row0 + t.rows - 1) / group;
+        const int lo_pos = position(t.first, t.row0 / group), hi_pos = position(t.first, (t.row0 + t.rows - 1) / group);
         const int lo = p.a.window > 0 ? max(0, lo_pos + 1 - p.a.window) : 0;
         t.lo = lo, t.hi = hi_pos;
         t.block0 = lo / kKeys;
         t.sink = min((min(p.a.sinks, lo) + kKeys - 1) / kKeys, t.block0);
         t.steps = max(t.sink + (max(hi_pos + 1, 0) + kKeys - 1) / kKeys - t.block0, 1);
         t.pair = t.head = 0;
-        t.begin = 0;
+        t.begin = t.pages = 0;
         return t;
     };
     // Sum over the threads before this one, and of all; every thread calls.
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int4 s = make_int4(0, 0, 0, 0);
         int mine = 0;
         if (i < B) {
-            const KvSeq q = kv_sequence(p.b, p.c.page_shift, i, p.status);
+            const KvSeq q = SHARED ? kv_entry(p.share, i) : kv_sequence(p.b, p.c.page_shift, i, p.status);
             const int rows = q.n * group;
             mine = rows <= p.row_limit ? 0 : (rows + 2 * half_rows - 1) / (2 * half_rows);
             s = make_int4(q.q0, q.n, q.len, 0);
@@ -548,6 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ManyTile t = tile_of(s, b, pair - s.w);
         t.pair = pair, t.head = head;
         t.begin = pre[pair] * Hk + (long long)head * (t.steps + kCost);
+        if (SHARED) t.pages = p.share.entries[b].pages;
         return t;
     };
     auto find_pair = [&](long long at) {                           // the pair of a position of the line
@@ -663,8 +668,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
             const bool exists = r < half_rows && base_row + r < t.rows;
             const int tok0 = (t.row0 + base_row) / group;          // the half's first token
-            const int min_pos = t.first + tok0, pos = exists ? min_pos + r_tok : -1;
-            const int max_pos = t.first + (t.row0 + min(base_row + half_rows, t.rows) - 1) / group;
+            const int min_pos = position(t.first, tok0), pos = exists ? position(min_pos, r_tok) : -1;
+            const int max_pos = position(t.first, (t.row0 + min(base_row + half_rows, t.rows) - 1) / group);
             float ref = kRefStart, sum = 0.0f;
             const int first_st = twice ? s0 + half : s0;
             for (int st = first_st; st < s1 && runs; st += twice ? 2 : 1) {
@@ -837,13 +842,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < D; c += 32) {
                     float f[32];
                     read_out(c, f);
-                    if (has) store(at, c, f, inv);
+                    if (has) {
+                        if constexpr (SHARED) kv_store_joined<D>(p.a, p.share, at, c, f, 32, sum, ref);
+                        else store(at, c, f, inv);
+                    }
                 }
                 if (joins) {
                     tc_fence_before();
                     mbar_arrive(part_read);
                 }
-                if (has && p.a.lse)
+                if (!SHARED && has && p.a.lse)
                     p.a.lse[at] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.6931471805599453f;
             } else {
                 // a tile that CTAs from..to share: each leaves its part, in slot 1 the first of them, in slot 0
@@ -927,9 +935,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 f[4 * k + 3] = fmaf(y[k].w, wb, fmaf(x[k].w, wa, f[4 * k + 3]));
                             }
                         }
-                        store(at, d, f, inv);
+                        if constexpr (SHARED) kv_store_joined<D>(p.a, p.share, at, d, f, 32, l, m);
+                        else store(at, d, f, inv);
                     }
-                    if (p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+                    if (!SHARED && p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
                 }
             }
             tc_fence_before();
@@ -952,7 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 2; ++g) {
                 const int at = pos0 + 16 * g;
                 const bool needed = at <= t.hi && at < t.len && (at + 15 >= t.lo || at < p.a.sinks);
-                page[g] = needed ? p.b.block_table[(long long)t.seq * p.b.max_blocks + (at >> p.c.page_shift)] : -2;
+                const long long row = SHARED ? t.pages : (long long)t.seq * p.b.max_blocks;
+                page[g] = needed ? p.b.block_table[row + (at >> p.c.page_shift)] : -2;
             }
         };
         auto check = [&]() {
@@ -1286,49 +1296,64 @@ cudaError_t encode_q(const DeviceInfo &dev, const KvAttentionArgs &a, int n_toke
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int KT, int D>
+template <bool SHARED, int KT, int D>
 cudaError_t launch(const CUtensorMap &q, const ManyParams &p, int grid, cudaStream_t s, bool pdl) {
     using L = ManySmem<D>;
-    auto kern = many_rows_kernel<KT, D>;
+    auto kern = many_rows_kernel<SHARED, KT, D>;
     const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(kern), L::kEnd);
     if (e != cudaSuccess) return e;
     return kv_launch(kern, dim3(grid), dim3(kThreads), L::kEnd, s, pdl, q, p);
 }
 
-}  // namespace
-
-cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
-                                     const DeviceInfo &dev, cudaStream_t s, bool pdl) {
+template <bool SHARED>
+cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
+                        const DeviceInfo &dev, cudaStream_t s, bool pdl, KvShare share) {
     const int group = a.n_heads / c.n_kv_heads, half_rows = kHalfRows / group * group;
     CUtensorMap q;
     cudaError_t e = encode_q(dev, a, batch.n_tokens, c.head_dim, group, &q);
     if (e != cudaSuccess) return e;
-    static std::atomic<unsigned long long> launches{0x7e57ab1e0000ull};
+    static std::atomic<unsigned long long> launches{SHARED ? 0x7e57ab1f0000ull : 0x7e57ab1e0000ull};
+    const KvEntry *entries = share.entries;
     for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
         KvBatch b = batch;
-        b.block_table += (long long)b0 * b.max_blocks;
-        b.kv_lens += b0;
-        b.q_starts += b0;
+        if constexpr (SHARED) {
+            share.entries = entries + b0;
+        } else {
+            b.block_table += (long long)b0 * b.max_blocks;
+            b.kv_lens += b0;
+            b.q_starts += b0;
+        }
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
         // as many pairs as these sequences can have at most
         const long long pairs = (long long)b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
             // with a row limit the other kernel has seen to the rows that no sequence owns
-            const bool mine = row_limit == 0 && first == 0;
-            ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first, nullptr, nullptr, 0, hold_copies(), dev.status};
+            const bool mine = row_limit == 0 && first == 0 && (!SHARED || share.step != 0);
+            ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first,
+                         nullptr, nullptr, 0, hold_copies(), dev.status, share};
             p.tickets = static_cast<unsigned long long *>(a.workspace);
             p.parts = reinterpret_cast<float *>(p.tickets + ((dev.sm_count + 1) & ~1));
             p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
             if (p.tag == 0) p.tag = 1;
             const int grid = dev.sm_count;
             if (c.kv_dtype == kKvInt8)
-                e = c.head_dim == 128 ? launch<kKvInt8, 128>(q, p, grid, s, pdl) : launch<kKvInt8, 64>(q, p, grid, s, pdl);
+                e = c.head_dim == 128 ? launch<SHARED, kKvInt8, 128>(q, p, grid, s, pdl)
+                                      : launch<SHARED, kKvInt8, 64>(q, p, grid, s, pdl);
             else
-                e = c.head_dim == 128 ? launch<kKvE4m3, 128>(q, p, grid, s, pdl) : launch<kKvE4m3, 64>(q, p, grid, s, pdl);
+                e = c.head_dim == 128 ? launch<SHARED, kKvE4m3, 128>(q, p, grid, s, pdl)
+                                      : launch<SHARED, kKvE4m3, 64>(q, p, grid, s, pdl);
             if (e != cudaSuccess) return e;
         }
     }
     return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
+                                     const DeviceInfo &dev, cudaStream_t s, bool pdl, const KvShare *share) {
+    return share ? launch_many<true>(a, c, batch, row_limit, dev, s, pdl, *share)
+                 : launch_many<false>(a, c, batch, row_limit, dev, s, pdl, KvShare{});
 }
 
 long long kv_attention_many_workspace(int head_dim, const DeviceInfo &dev) {

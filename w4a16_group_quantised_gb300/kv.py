@@ -268,6 +268,46 @@ def w4a16_kv_attention_workspace(n_heads: int, n_kv_heads: int, head_dim: int, n
     return need.value
 
 
+def w4a16_kv_attention_shared(q, cache, block_table, kv_lens, q_starts, max_q_len: int, group_starts, prefix_lens, scale=None,
+                              out=None, lse=None, workspace=None, stream=None):
+    """w4a16_kv_attention, without a window, of a batch whose sequences
+    [group_starts[g], group_starts[g + 1]) have their first prefix_lens[g]
+    positions in the same pages: these are read once for all of a group."""
+    c, dev, _, kv_heads, _, dim = _cache(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _refuse("q", q, None, 3, dev)
+    T, H, _ = q.shape
+    sq, dt = _rows("q", q, H, dim, dev), _act(q)
+    out = _output("out", out, (T, H, dim), q.dtype, dev, stream)
+    if lse is not None:
+        _output("lse", lse, (T, H), torch.float32, dev, stream)
+    b, n = _batch(block_table, kv_lens, q_starts, T, dev)
+    starts, prefix = _ints("group_starts", group_starts, 1, dev), _ints("prefix_lens", prefix_lens, 1, dev)
+    groups = prefix_lens.shape[0]
+    if group_starts.shape[0] != groups + 1:
+        raise ValueError(f"group_starts must be [n_groups + 1] = [{groups + 1}], got {list(group_starts.shape)}")
+    handle = _stream(stream, dev)
+    ws, at, size = _scratch(workspace, _shared_workspace(dev, H, kv_heads, dim, n, groups, T), dev, handle)
+    _check("w4a16_kv_attention_shared", load_library().w4a16_kv_attention_shared(
+        q.data_ptr(), sq, H, c, b, max_q_len, starts, prefix, groups, dim ** -0.5 if scale is None else scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), dt, at, size, handle))
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _shared_workspace(device, n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens):
+    return max(16, w4a16_kv_attention_shared_workspace(n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens))
+
+
+def w4a16_kv_attention_shared_workspace(n_heads: int, n_kv_heads: int, head_dim: int, n_seqs: int, n_groups: int,
+                                        n_tokens: int) -> int:
+    """Bytes of workspace that w4a16_kv_attention_shared needs for these sizes, whatever the lengths."""
+    need = ctypes.c_longlong(0)
+    _check("w4a16_kv_attention_shared_workspace", load_library().w4a16_kv_attention_shared_workspace(
+        n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens, ctypes.byref(need)))
+    return need.value
+
+
 def _counts(refcount, device, n_pages=None):
     at = _ints("refcount", refcount, 1, device)
     if n_pages is not None and refcount.shape[0] != n_pages:
