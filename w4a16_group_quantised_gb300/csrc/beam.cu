@@ -7,24 +7,27 @@
 // and the n best of a request's beams come out in order, ties to the lower
 // beam, then the lower token.  Bound by reading the logits once.
 //
-//  * A CTA takes a part of one beam's logits, a tile of 32 per thread at a time.
-//    Each thread keeps a sum of its own, so nothing but the candidates is
+//  * The logits of all beams that go on are a line of tiles, cut in equal pieces
+//    over the CTAs; a beam's parts, one for each CTA that has tiles of it, are
+//    joined by a second kernel.  The next tile is on its way while one is worked on.
+//  * Each thread keeps a sum of its own, so nothing but the candidates is
 //    exchanged: 2^(x log2 e - R) with R the integer next to its largest x log2 e,
 //    so that sums with other references differ by a power of two, exactly.
-//    log2 e is two fp32 numbers; a tile is summed in fp32, tiles in 64 bits: the
-//    continuations of different beams, a few 1e-2 apart in earnest, are told
-//    apart down to about 1e-8.
+//    log2 e is two fp32 numbers; a tile is summed in fp32, tiles in two fp32
+//    numbers, threads in 64 bits: the continuations of different beams, a few
+//    1e-2 apart in earnest, are told apart down to about 1e-8.  Which thread
+//    sums what goes by the token alone, so that equal beams have equal sums.
 //  * Within a beam c rises with x: candidates are logits, kept as 64-bit keys
-//    (the value's order, then the lower token).  A tile's threads whose largest
-//    logit is above the n-th best key so far append theirs to a list; only when
-//    it might overflow is the list cut to its n best.  How long it can get is
-//    known: of the n threads with the largest maxima come at most 32 n, which is
-//    also how the first tile, where all are candidates, finds its threshold.
-//  * A second kernel, a CTA per request, joins the parts' sums, scores the
+//    (the value's order, then the lower token).  Threads whose largest logit of
+//    a tile is above the n-th best so far append theirs to a list, which is cut
+//    to its n best when it has grown.  A part's first tile gets its threshold
+//    from the least of the maxima of n groups of threads: n logits at least reach
+//    it, a few times n in earnest.  Where more do than the list holds (many equal
+//    ones), the n threads with the best maxima are found out, of which at most
+//    n times a thread's share can come.
+//  * The second kernel, a CTA per request, joins the parts' sums, scores the
 //    candidates in 64 bits and picks the n best by counting who is better.
 //    Of sorted lists only the n with the best heads can hold any.
-#include <float.h>
-
 #include <algorithm>
 
 #include "kv.cuh"
@@ -32,20 +35,22 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPer = 32;                               // logits of a tile per thread, in vectors of 8
-constexpr int kTile = kThreads * kPer;
-constexpr int kList = (kPer + 1) * kBeamMost;          // candidates that a part may have in hand
-constexpr int kMergeThreads = 512;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBatch = 8;                              // tiles between two cuts of a list
+constexpr int kList = 33 * kBeamMost;                  // its room: n candidates, and n threads' logits of a tile
+constexpr int kMergeThreads = 256;
 constexpr int kMaxLists = 1024;                        // (beam, part) pairs of a request
+constexpr int kMaxRows = 2048;                         // beams among which those that go on are looked up first
 constexpr float kHuge = 536870912.0f;                  // 2^29: from here on logits are 32 and more apart
 
+// Logits of a tile per thread, in vectors of 8: as many as 16 registers hold.
+template <int DT> constexpr int kPer = DT == 2 ? 16 : 32;
 // The sum of a part of a beam's logits: l = sum 2^(x log2 e - reference(m)), m the
 // largest x.  Where |m| >= 2^29 nothing but the logits that equal m counts, and l is their number.
 struct PartSum {
     double l;
     float m;
-    int pad;
+    int parts;                                         // of the beam (in its first part)
 };
 
 __device__ __forceinline__ float ex2(float v) {
@@ -53,17 +58,41 @@ __device__ __forceinline__ float ex2(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.92596299112661746887e-8f;   // their sum is log2 e
 __device__ __forceinline__ float reference(float m) { return rintf(m * kLog2e); }
-// 2^k for whole k, 0 far below the range
-__device__ __forceinline__ double pow2(float k) {
-    return k < -1000.0f ? 0.0 : __longlong_as_double((long long)((int)k + 1023) << 52);
+// 2^k for whole k <= 127, 0 below the normal numbers
+__device__ __forceinline__ float pow2(float k) {
+    return k < -126.0f ? 0.0f : __uint_as_float((uint32_t)((int)k + 127) << 23);
 }
 // What a sum with largest m counts for in one whose largest is `top` (>= m).
-__device__ __forceinline__ double carried(float m, float top) {
-    if (fabsf(top) >= kHuge) return m == top ? 1.0 : 0.0;
-    if (fabsf(m) >= kHuge) return 0.0;
+__device__ __forceinline__ float carried(float m, float top) {
+    if (fabsf(top) >= kHuge) return m == top ? 1.0f : 0.0f;
+    if (fabsf(m) >= kHuge) return 0.0f;
     return pow2(reference(m) - reference(top));
+}
+// (hi, lo) += v, exactly but for the last bits of lo
+__device__ __forceinline__ void add_to(float &hi, float &lo, float v) {
+    const float s = __fadd_rn(hi, v), z = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, z)), __fsub_rn(v, z)));
+    hi = s;
 }
 
 // Order of fp32 values as unsigned numbers (-0 as 0), and back.
@@ -80,263 +109,455 @@ __device__ __forceinline__ unsigned long long key_of(float x, int token) {
 __device__ __forceinline__ float key_value(unsigned long long k) { return from_ordered((uint32_t)(k >> 32)); }
 __device__ __forceinline__ int key_token(unsigned long long k) { return (int)~(uint32_t)k; }
 
-// Logits [at, at + 8) of a row, -inf from `end` on.
+// The same of 64 bits; no number but a NaN's is 0.
+__device__ __forceinline__ unsigned long long ordered64(double x) {
+    const long long u = __double_as_longlong(x + 0.0);
+    return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | 1ull << 63;
+}
+__device__ __forceinline__ double from_ordered64(unsigned long long u) {
+    return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+
+// A vector of 8 logits as it is in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void *row, bool wide, int at, int end, float (&x)[8]) {
-    if (wide && at + 8 <= end) {
-        if (DT == 2) {
-            const uint4 a = ldg_stream_v4(static_cast<const float *>(row) + at);
-            const uint4 b = ldg_stream_v4(static_cast<const float *>(row) + at + 4);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+struct Raw {
+    uint32_t w[DT == 2 ? 8 : 4];
+};
+// Logits [at, at + 8) of a row at most `align` bytes aligned, -inf from `end` on.
+template <int DT>
+__device__ __forceinline__ Raw<DT> load8(const char *row, int align, int at, int end) {
+    Raw<DT> r;
+    constexpr int N = DT == 2 ? 8 : 4, SIZE = DT == 2 ? 4 : 2;
+    const char *p = row + (long long)at * SIZE;
+    if (at + 8 <= end && align >= 4) {
+        if (align >= 16) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+            for (int i = 0; i < N; i += 4) {
+                const uint4 a = ldg_stream_v4(p + 4 * i);
+                r.w[i] = a.x, r.w[i + 1] = a.y, r.w[i + 2] = a.z, r.w[i + 3] = a.w;
+            }
         } else {
-            const uint4 a = ldg_stream_v4(static_cast<const uint16_t *>(row) + at);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = kv_act<DT == 2 ? 1 : DT>((uint16_t)(w[i / 2] >> (16 * (i & 1))));
+            for (int i = 0; i < N; ++i) r.w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
         }
-        return;
+        return r;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = -INFINITY;
-        if (at + i < end)
-            x[i] = DT == 2 ? static_cast<const float *>(row)[at + i]
-                           : kv_act<DT == 2 ? 1 : DT>(static_cast<const uint16_t *>(row)[at + i]);
+    for (int i = 0; i < N; ++i) {
+        if (DT == 2) {
+            r.w[i] = at + i < end ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0xff800000u;
+        } else {
+            const uint32_t none = DT == 0 ? 0xfc00u : 0xff80u;
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(p) + 2 * i;
+            r.w[i] = (at + 2 * i < end ? __ldg(h) : none) | (at + 2 * i + 1 < end ? (uint32_t)__ldg(h + 1) : none) << 16;
+        }
     }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float value_of(const Raw<DT> &r, int i) {
+    if constexpr (DT == 2) return __uint_as_float(r.w[i]);
+    else if constexpr (DT == 1) return __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+    else return kv_act<0>((uint16_t)(r.w[i / 2] >> (16 * (i & 1))));
 }
 
 // Whether a beam is a source of continuations by its logits.
 __device__ __forceinline__ bool goes_on(const BeamArgs &a, int row) {
-    return isfinite(a.scores[row]) && !(a.finished && a.finished[row]);
+    const float s = a.scores[row];
+    const bool ended = a.finished && a.finished[row];
+    return isfinite(s) && !ended;
 }
 
+// How the line of tiles is cut: host and device alike.
+struct Cut {
+    int row_tiles;                                     // tiles of a beam
+    int least;                                         // fewest tiles of a CTA, so that a request has kMaxLists parts at most
+    int slots;                                         // places for a beam's parts
+};
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const BeamArgs a, int parts, int part_tiles, PartSum *sums,
-                                                        unsigned long long *lists) {
-    kv_begin();
+__global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, const Cut cut, PartSum *sums,
+                                                           unsigned long long *lists) {
+    constexpr int PER = kPer<DT>, NV = PER / 8, TILE = kThreads * PER;
     __shared__ unsigned long long list[kList];
-    __shared__ unsigned long long maxima[kThreads];
+    __shared__ unsigned long long s_best[kBeamMost], s_maxima[kThreads];
+    __shared__ float s_group[kThreads];
     __shared__ unsigned long long s_least;
-    __shared__ double s_sum[kThreads / 32];
-    __shared__ float s_max[kThreads / 32];
+    __shared__ float s_hi[kWarps], s_lo[kWarps], s_max[kWarps];
+    __shared__ int s_count[kWarps];
+    __shared__ uint16_t s_rows[kMaxRows];
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.n_out;
-    const int row = blockIdx.x / parts, part = blockIdx.x % parts;
-    if (!goes_on(a, row)) return;
-    const void *x0 = static_cast<const char *>(a.logits) + row * a.row_stride * (DT == 2 ? 4 : 2);
-    const bool wide = (reinterpret_cast<uintptr_t>(x0) & 15) == 0;
-    const int begin = part * part_tiles * kTile, end = min(a.vocab, begin + part_tiles * kTile);
-    float m = -INFINITY, least = -INFINITY;               // of this thread; the n-th best so far
-    double l = 0.0;
-    int at_most = 0;                                       // an upper bound of the list's length
+    const int rows = a.n_groups * a.width;
     if (tid == 0) s_n = 0;
+    grid_dependency_wait();
 
-    // The list cut to its n best, in order.
-    auto cut = [&]() {
-        __syncthreads();
-        const int n = s_n;
-        unsigned long long mine[(kList + kThreads - 1) / kThreads];
-        int place[(kList + kThreads - 1) / kThreads];
+    // ---- the beams that go on, in order (all of them where there are too many to look)
+    int alive = rows;
+    if (rows <= kMaxRows) {
+        alive = 0;
+        for (int base = 0; base < rows; base += kThreads) {
+            const bool on = base + tid < rows && goes_on(a, base + tid);
+            const uint32_t bits = __ballot_sync(0xffffffffu, on);
+            __syncthreads();
+            if (lane == 0) s_count[warp] = __popc(bits);
+            __syncthreads();
+            int at = alive + __popc(bits & ((1u << lane) - 1));
 #pragma unroll
-        for (int i = 0; i < (kList + kThreads - 1) / kThreads; ++i) {
-            const int at = tid + i * kThreads;
-            place[i] = K;
-            if (at < n) {
-                mine[i] = list[at];
-                place[i] = 0;
-                for (int j = 0; j < n; ++j) place[i] += list[j] > mine[i];
+            for (int w = 0; w < kWarps; ++w) {
+                at += w < warp ? s_count[w] : 0;
+                alive += s_count[w];
             }
+            if (on) s_rows[at] = (uint16_t)(base + tid);
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < (kList + kThreads - 1) / kThreads; ++i)
-            if (place[i] < K) list[place[i]] = mine[i];
-        if (tid == 0) s_n = min(n, K);
+    }
+    const long long total = (long long)alive * cut.row_tiles;
+    const long long ctas = max(1LL, min((long long)gridDim.x, total / cut.least));
+    if (blockIdx.x >= ctas) return;
+    const long long t0 = blockIdx.x * total / ctas, t1 = (blockIdx.x + 1) * total / ctas;
+
+    float m = -INFINITY, hi = 0.0f, lo = 0.0f;             // of this thread and part
+    float least = -INFINITY;                               // the n-th best so far
+    int kept = 0;                                          // candidates that the list was last cut to
+    // The list of n candidates cut to the K best, in order.
+    auto shorten = [&](int n) {
+#pragma unroll 1
+        for (int i = tid; i < n; i += kThreads) {
+            const unsigned long long mine = list[i];
+            int better = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) better += list[j] > mine;
+            if (better < K) s_best[better] = mine;
+        }
         __syncthreads();
-        if (n >= K) least = key_value(list[K - 1]);
-        at_most = min(n, K);
+        if (tid < min(n, K)) list[tid] = s_best[tid];
+        if (tid == 0) s_n = min(n, K);
+        if (n >= K) least = key_value(s_best[K - 1]);
+        __syncthreads();
     };
 
-    for (int base = begin; base < end; base += kTile) {
-        float x[kPer / 8][8];
+    auto row_of = [&](long long t) {
+        const int o = (int)(t / cut.row_tiles);
+        return rows <= kMaxRows ? (int)s_rows[o] : o;
+    };
+    const char *logits = static_cast<const char *>(a.logits);
+    auto load = [&](Raw<DT> (&x)[NV], int row, int tile) {
+        const int end = rows <= kMaxRows || goes_on(a, row) ? a.vocab : 0;
+        const char *p = logits + row * a.row_stride * (DT == 2 ? 4 : 2);
+        const int low = (int)(reinterpret_cast<uintptr_t>(p) & 15), align = low == 0 ? 16 : low & 3 ? 2 : 4;
 #pragma unroll
-        for (int j = 0; j < kPer / 8; ++j) load8<DT>(x0, wide, base + (j * kThreads + tid) * 8, end, x[j]);
+        for (int j = 0; j < NV; ++j) x[j] = load8<DT>(p, align, tile * TILE + (j * kThreads + tid) * 8, end);
+    };
+    auto largest_of = [&](const Raw<DT> (&x)[NV]) {
         float top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < kPer / 8; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, x[j][e]);
+            for (int e = 0; e < 8; e += 2)
+                asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(value_of<DT>(x[j], e)), "f"(value_of<DT>(x[j], e + 1)));
+        return top;
+    };
+    // A tile's candidates when there are too many of them: those of the K threads with the best maxima.
+    auto careful = [&](int row, int tile) {
+        Raw<DT> x[NV];
+        load(x, row, tile);
+        const float top = largest_of(x);
+        const int base = tile * TILE;
+        unsigned long long best = 0;
+#pragma unroll
+        for (int j = NV - 1; j >= 0; --j)
+#pragma unroll
+            for (int e = 7; e >= 0; --e) {                 // the lowest token of the largest logit
+                const float v = value_of<DT>(x[j], e);
+                if (v == top && v > least) best = key_of(v, base + (j * kThreads + tid) * 8 + e);
+            }
+        s_maxima[tid] = best;
+        if (tid == 0) s_least = 0;
+        __syncthreads();
+        int better = 0;
+#pragma unroll 4
+        for (int j = 0; j < kThreads; ++j) better += s_maxima[j] > best;
+        if (best != 0 && better == K - 1) s_least = best;
+        __syncthreads();
+        const unsigned long long from = s_least;
+        if (best >= from)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = value_of<DT>(x[j], e);
+                    const unsigned long long k = key_of(v, base + (j * kThreads + tid) * 8 + e);
+                    if (v > least && k >= from) list[atomicAdd(&s_n, 1)] = k;
+                }
+        __syncthreads();
+        const int n = s_n;
+        __syncthreads();
+        shorten(n);
+    };
+
+    Raw<DT> next[NV];
+    int row = 0, tile = 0;
+    if (t0 < t1) {
+        row = row_of(t0), tile = (int)(t0 % cut.row_tiles);
+        load(next, row, tile);
+    }
+    int first = tile;                                      // of the tiles whose candidates are in the list uncut
+    bool fresh = true;                                     // the part's first tile
+    for (long long t = t0; t < t1; ++t) {
+        const int here = row, this_tile = tile, base = tile * TILE;
+        Raw<DT> x[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) x[j] = next[j];
+        const bool ends = ++tile == cut.row_tiles || t + 1 == t1;
+        if (t + 1 < t1) {
+            if (tile == cut.row_tiles) tile = 0, row = row_of(t + 1);
+            load(next, row, tile);
+        }
+        const float top = largest_of(x);
         // ---- the sum
         const float to = fmaxf(m, top);
-        l *= carried(m, to);
-        m = to;
-        float s = 0.0f;
+        if (to != m) {
+            const float f = carried(m, to);
+            hi *= f, lo *= f;
+            m = to;
+        }
+        float s;
         if (fabsf(to) < kHuge) {
-            const float r = reference(to);
+            const float r = -reference(to);
+            const uint64_t rr = pair_of(r, r), ll = pair_of(kLog2e, kLog2e), low = pair_of(kLog2eLow, kLog2eLow);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < kPer / 8; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += ex2(fmaf(x[j][e], kLog2eLow, fmaf(x[j][e], kLog2e, -r)));
+                for (int e = 0; e < 8; e += 2) {
+                    const uint64_t v = pair_of(value_of<DT>(x[j], e), value_of<DT>(x[j], e + 1));
+                    float p, q;
+                    unpair(fma2(v, low, fma2(v, ll, rr)), p, q);
+                    sum[e >> 1 & 1] = add2(sum[e >> 1 & 1], pair_of(ex2(p), ex2(q)));
+                }
+            float p, q;
+            unpair(add2(sum[0], sum[1]), p, q);
+            s = p + q;
         } else {
+            s = 0.0f;
 #pragma unroll
-            for (int j = 0; j < kPer / 8; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)                // a NaN stays one; no logit but -inf so far: none counts
-                    s += x[j][e] != x[j][e] ? x[j][e] : x[j][e] == to && to > -INFINITY ? 1.0f : 0.0f;
+                for (int e = 0; e < 8; ++e) {              // a NaN stays one; no logit but -inf so far: none counts
+                    const float v = value_of<DT>(x[j], e);
+                    s += v != v ? v : v == to && to > -INFINITY ? 1.0f : 0.0f;
+                }
         }
-        l += s;
-        // ---- candidates
-        int passing = __syncthreads_count(top > least);
-        if (passing == 0) continue;
-        unsigned long long from = 0;
-        if (at_most + kPer * passing > kList) {
-            cut();
-            passing = __syncthreads_count(top > least);
-            if (at_most + kPer * passing > kList) {        // more than n threads, then
-                unsigned long long best = 0;
+        add_to(hi, lo, s);
+        // ---- candidates: x > least, and in a part's first tile x >= bound
+        float bound = -INFINITY;
+        if (fresh) {
+            // groups of every so-manieth thread: a last tile of few tokens is in the first threads
+            const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, across = min(groups, 32);
+            float g = top;
+            for (int d = 16; d >= across; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+            s_group[tid] = g;
+            __syncthreads();
+            float even = -INFINITY, odd = -INFINITY;
 #pragma unroll
-                for (int j = kPer / 8 - 1; j >= 0; --j)
-#pragma unroll
-                    for (int e = 7; e >= 0; --e)           // the lowest token of the largest logit
-                        if (x[j][e] == top && top > least) best = key_of(top, base + (j * kThreads + tid) * 8 + e);
-                maxima[tid] = best;
-                __syncthreads();
-                int better = 0;
-                for (int j = 0; j < kThreads; ++j) better += maxima[j] > best;
-                if (best != 0 && better == K - 1) s_least = best;
-                __syncthreads();
-                from = s_least;
-                passing = K;
+            for (int w = 0; w < kWarps; w += 2) {
+                even = fmaxf(even, s_group[w * 32 + lane]);
+                odd = fmaxf(odd, s_group[(w + 1) * 32 + lane]);
             }
+            bound = groups == 64 ? fminf(even, odd) : fmaxf(even, odd);
+            for (int d = across / 2; d > 0; d >>= 1) bound = fminf(bound, __shfl_xor_sync(0xffffffffu, bound, d));
         }
-        at_most += kPer * passing;
-        if (top > least) {
+        if (top > least && top >= bound) {
 #pragma unroll
-            for (int j = 0; j < kPer / 8; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (x[j][e] > least) {
-                        const unsigned long long k = key_of(x[j][e], base + (j * kThreads + tid) * 8 + e);
-                        if (k >= from) list[atomicAdd(&s_n, 1)] = k;
+                for (int e = 0; e < 8; ++e) {
+                    const float v = value_of<DT>(x[j], e);
+                    if (v > least && v >= bound) {
+                        const int at = atomicAdd(&s_n, 1);
+                        if (at < kList) list[at] = key_of(v, base + (j * kThreads + tid) * 8 + e);
                     }
+                }
         }
+        if (!ends && !fresh && this_tile - first < kBatch - 1) continue;
+        __syncthreads();
+        int n = s_n;
+        __syncthreads();
+        if (n > kList) {
+            // again, tile by tile, after what the list had been cut to before
+            if (tid == 0) s_n = kept;
+            for (int i = first; i <= this_tile; ++i) careful(here, i);
+            n = s_n;
+            __syncthreads();
+        }
+        shorten(n);
+        n = kept = min(n, K);
+        first = this_tile + 1;
+        fresh = false;
+        if (!ends) continue;
+        // ---- the part's end: its candidates, and the threads' sums joined
+        const long long o = t / cut.row_tiles, line0 = o * cut.row_tiles, line1 = line0 + cut.row_tiles - 1;
+        // the CTAs that hold the beam's first tile and its last
+        const int c0 = (int)(((line0 + 1) * ctas - 1) / total), c1 = (int)(((line1 + 1) * ctas - 1) / total);
+        const long long slot = (long long)here * cut.slots + (blockIdx.x - c0);
+        if (tid < K) lists[slot * K + tid] = tid < n ? list[tid] : 0;
+        float all = m;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
+        if (lane == 0) s_max[warp] = all;
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all = fmaxf(all, s_max[w]);
+        const float f = carried(m, all);
+        hi *= f, lo *= f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, hi, d), r = __shfl_xor_sync(0xffffffffu, lo, d);
+            add_to(hi, lo, h);
+            lo += r;
+        }
+        if (lane == 0) s_hi[warp] = hi, s_lo[warp] = lo;
+        __syncthreads();
+        if (tid == 0) {
+            hi = s_hi[0], lo = s_lo[0];
+            for (int w = 1; w < kWarps; ++w) {
+                add_to(hi, lo, s_hi[w]);
+                lo += s_lo[w];
+            }
+            sums[slot] = PartSum{(double)hi + (double)lo, all, c1 - c0 + 1};
+        }
+        m = -INFINITY, hi = lo = 0.0f, least = -INFINITY;
+        fresh = true, first = tile, kept = 0;
     }
-    cut();
-    const int n = s_n;
-    unsigned long long *out = lists + (long long)blockIdx.x * K;
-    for (int i = tid; i < K; i += kThreads) out[i] = i < n ? list[i] : 0;
-    // ---- the threads' sums joined
-    float top = m;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) s_max[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, s_max[w]);
-    l *= carried(m, top);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) s_sum[warp] = l;
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kThreads / 32; ++w) l += s_sum[w];
-        sums[blockIdx.x] = PartSum{l, top, 0};
-    }
+}
+
+// The logarithm of a sum of 0.25 and more, to about 2^-32: of its fraction f in
+// [0.7, 1.4] as 2 atanh(q), q = (f - 1) / (f + 1), in two fp32 numbers and a
+// series in q^2.  64-bit arithmetic is slow here: log() takes 1.5 us.
+__device__ __forceinline__ double log_of(double l) {
+    const long long bits = __double_as_longlong(l);
+    int e = (int)(bits >> 52) - 1023;
+    double f = __longlong_as_double((bits & 0xfffffffffffffLL) | 0x3ff0000000000000LL);
+    if (f > 1.41421356) f *= 0.5, ++e;
+    const float fh = (float)f, fl = (float)(f - fh);
+    const float n = fh - 1.0f, d = fh + 1.0f, dl = (fh - (d - 1.0f)) + fl;   // n exactly, d to its rounding, which dl holds
+    const float q = n / d, ql = (fmaf(-q, d, n) + fl - q * dl) / d, z = q * fmaf(2.0f, ql, q);
+    float s = 1.0f / 13.0f;                            // z^6 / 13 < 6e-11
+    s = fmaf(s, z, 1.0f / 11.0f);
+    s = fmaf(s, z, 1.0f / 9.0f);
+    s = fmaf(s, z, 1.0f / 7.0f);
+    s = fmaf(s, z, 1.0f / 5.0f);
+    s = fmaf(s, z, 1.0f / 3.0f);
+    const float rest = 2.0f * fmaf(q * z, s, ql);
+    return fma((double)e, 0.693147180559945309417, (double)(2.0f * q) + (double)rest);
 }
 
 // A CTA per request: its beams' sums, then the best of the candidates.
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, int parts, const PartSum *sums,
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, const Cut cut, const PartSum *sums,
                                                               const unsigned long long *lists, int *status) {
-    kv_begin();
-    const int tid = threadIdx.x, K = a.n_out, W = a.width, n_lists = W * parts;
+    // One is better than another when it is greater.  The order of its score, 0 for none; among equal ones the lower
+    // beam, the greater logit, the lower token.  Integers: comparing 64-bit numbers is slow here.
+    struct Candidate {
+        unsigned long long score, key;                     // key: 63 - beam, the logit's order, 2^24 - 1 - token
+        __device__ bool operator>(const Candidate &o) const { return score > o.score || (score == o.score && key > o.key); }
+    };
     // no static shared memory: raise_smem_cap
     extern __shared__ double dyn[];
-    double *s_top = dyn, *s_log = s_top + kBeamMost;       // of each beam: its largest logit (NaN: none), and with x as
-                                                           // x - s_top, log sum e^x
-    double *s_heads = s_log + kBeamMost, *s_score = s_heads + kMaxLists;
-    int *s_from = reinterpret_cast<int *>(s_score + K * K);   // list * n + place in it
-    double &s_least = *reinterpret_cast<double *>(s_from + (K * K + 1) / 2 * 2);
-    int &s_least_at = *reinterpret_cast<int *>(&s_least + 1), &s_n = *(&s_least_at + 1);
+    const int tid = threadIdx.x, lane = tid & 31, K = a.n_out, W = a.width, slots = cut.slots, n_lists = W * slots;
+    double *s_top = dyn, *s_cum = s_top + kBeamMost;       // of each beam: its largest logit; its score less log sum
+                                                           // e^(x - largest)
+    Candidate *s_least = reinterpret_cast<Candidate *>(s_cum + kBeamMost);
+    Candidate *s_heads = s_least + 1, *s_cand = s_heads + kMaxLists;
+    int *s_parts = reinterpret_cast<int *>(s_cand + K * K);   // of each beam: lists it has, -1 where it has finished
+    int &s_n = s_parts[kBeamMost];
     const int row0 = blockIdx.x * W;
-    if (tid == 0) s_n = 0, s_least = -INFINITY, s_least_at = 0x7fffffff;
-    for (int b = tid; b < W; b += kMergeThreads) {
-        double largest = NAN, log_sum = 0.0;
-        if (goes_on(a, row0 + b)) {
-            const PartSum *p = sums + (long long)(row0 + b) * parts;
-            float top = -INFINITY;
-            for (int i = 0; i < parts; ++i) top = fmaxf(top, p[i].m);
-            double l = 0.0;
-            for (int i = 0; i < parts; ++i) l += p[i].l * carried(p[i].m, top);
+    if (tid == 0) s_n = 0, *s_least = Candidate{0, 0};
+    kv_begin();
+    const unsigned long long *mine = lists + (long long)row0 * slots * K;
+    // all loads at once: what a beam has no part for is not looked at
+    unsigned long long head = 0;
+    if (tid < n_lists) head = mine[(long long)tid * K];
+    for (int b = tid >> 5; b < W; b += kMergeThreads / 32) {
+        const PartSum *p = sums + (long long)(row0 + b) * slots;
+        const float score = a.scores[row0 + b];
+        const bool ended = a.finished && a.finished[row0 + b];
+        PartSum part = {0.0, 0.0f, 0};
+        if (lane < slots) part = p[lane];
+        double largest = 0.0, log_sum = 0.0;
+        int parts = __shfl_sync(0xffffffffu, part.parts, 0);
+        if (ended || !isfinite(score)) {
+            parts = isfinite(score) ? -1 : 0;
+        } else {
+            float top = lane < parts ? part.m : -INFINITY;
+            for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, p[i].m);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            double l = lane < parts ? part.l * carried(part.m, top) : 0.0;
+            for (int i = lane + 32; i < parts; i += 32) l += p[i].l * carried(p[i].m, top);
+            for (int d = parts > 8 ? 16 : parts > 2 ? 4 : 1; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
             // the row of a NaN or +inf has no probabilities, one without any token but -inf has no continuations
             if (top == INFINITY || l != l) {
-                kv_report(status);
-            } else if (top > -INFINITY) {
+                if (lane == 0) kv_report(status);
+                parts = 0;
+            } else if (top == -INFINITY) {
+                parts = 0;
+            } else {
                 largest = top;
                 // relative to the largest, which may be far larger than the sum's logarithm
-                log_sum = fabsf(top) >= kHuge ? log(l) : log(l) + ((double)reference(top) * 0.693147180559945309417 - largest);
+                log_sum = log_of(l);
+                if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
             }
         }
-        s_top[b] = largest, s_log[b] = log_sum;
+        if (lane == 0) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
     }
     __syncthreads();
-    const unsigned long long *mine = lists + (long long)row0 * parts * K;
-    // the score of a list's i-th candidate, NaN where there is none
-    auto score_of = [&](int list, int i) -> double {
-        const int b = list / parts, row = row0 + b;
-        const double s = a.scores[row];
-        if (!isfinite(s)) return NAN;
-        if (a.finished && a.finished[row]) return list % parts == 0 && i == 0 ? s : (double)NAN;
-        if (s_top[b] != s_top[b]) return NAN;
-        const unsigned long long k = mine[(long long)list * K + i];
-        return k == 0 ? (double)NAN : s + (((double)key_value(k) - s_top[b]) - s_log[b]);
-    };
-    // the at-th candidate of all, of score s, before the than-th of score t: equal ones by their beams, and within a beam as
-    // the logits say, which may differ by less than the scores resolve
-    auto better = [&](double s, int at, double t, int than) {
-        if (s != t) return s > t;
-        const int b = at / (parts * K), c = than / (parts * K);
-        return b != c ? b < c : at != than && mine[at] > mine[than];
+    // a list's i-th candidate
+    auto candidate = [&](int list, int i, unsigned long long key) {
+        const int b = list / slots, part = list - b * slots, parts = s_parts[b];
+        const unsigned long long beam = (unsigned long long)(63 - b) << 56;
+        if (parts < 0)                                     // goes on as it is
+            return Candidate{part == 0 && i == 0 ? ordered64(s_cum[b]) : 0ull, beam | (0xffffffu - a.end_token)};
+        if (part >= parts || key == 0) return Candidate{0, 0};
+        return Candidate{ordered64(s_cum[b] + ((double)key_value(key) - s_top[b])),
+                         beam | key >> 32 << 24 | (0xffffffu - key_token(key))};
     };
     // of so many sorted lists only the n with the best heads matter
     if (n_lists >= K) {
-        for (int i = tid; i < n_lists; i += kMergeThreads) s_heads[i] = score_of(i, 0);
+        for (int i = tid; i < n_lists; i += kMergeThreads) s_heads[i] = candidate(i, 0, i == tid ? head : mine[(long long)i * K]);
         __syncthreads();
         for (int i = tid; i < n_lists; i += kMergeThreads) {
-            const double s = s_heads[i];
+            const Candidate c = s_heads[i];
+            if (c.score == 0) continue;
             int place = 0;
-            for (int j = 0; j < n_lists; ++j) place += better(s_heads[j], j * K, s, i * K);
-            if (s == s && place == K - 1) s_least = s, s_least_at = i * K;
+#pragma unroll 4
+            for (int j = 0; j < n_lists; ++j) place += s_heads[j] > c;
+            if (place == K - 1) *s_least = c;
         }
         __syncthreads();
     }
-    const double least = s_least;
-    const int least_at = s_least_at;
+    const Candidate least = *s_least;
     for (int i = tid; i < n_lists * K; i += kMergeThreads) {
-        const double s = score_of(i / K, i % K);
-        if (s > least || (s == least && !better(least, least_at, s, i))) {
-            const int at = atomicAdd(&s_n, 1);
-            s_score[at] = s;
-            s_from[at] = i;
-        }
+        const int list = i / K, at = i - list * K;
+        if (n_lists >= K && least > s_heads[list]) continue;
+        const Candidate c = candidate(list, at, mine[i]);
+        if (c.score != 0 && !(least > c)) s_cand[atomicAdd(&s_n, 1)] = c;
     }
     __syncthreads();
     const int n = s_n;
     for (int i = tid; i < n; i += kMergeThreads) {
-        const double s = s_score[i];
-        const int from = s_from[i];
+        const Candidate c = s_cand[i];
         int place = 0;
-        for (int j = 0; j < n; ++j) place += better(s_score[j], s_from[j], s, from);
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += s_cand[j] > c;
         if (place >= K) continue;
-        const int list = from / K, row = row0 + list / parts;
-        const bool was = a.finished && a.finished[row];
-        const int token = was ? a.end_token : key_token(mine[from]);
+        const int b = 63 - (int)(c.key >> 56), token = 0xffffff - (int)(c.key & 0xffffffu);
         const long long at = (long long)blockIdx.x * K + place;
-        a.out_scores[at] = (float)s;
-        a.out_rows[at] = row;
+        a.out_scores[at] = (float)from_ordered64(c.score);
+        a.out_rows[at] = row0 + b;
         a.out_tokens[at] = token;
-        if (a.out_finished) a.out_finished[at] = was || token == a.end_token;
+        if (a.out_finished) a.out_finished[at] = s_parts[b] < 0 || token == a.end_token;
     }
     for (int i = n + tid; i < K; i += kMergeThreads) {
         const long long at = (long long)blockIdx.x * K + i;
@@ -346,38 +567,40 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
     }
 }
 
-// Parts of a row and tiles of each: enough CTAs for every SM to have three.
-void split_rows(int rows, int width, int vocab, int sm_count, int *parts, int *part_tiles) {
-    const int tiles = std::max((vocab + kTile - 1) / kTile, 1);
-    const int want = std::max(1, std::min(3 * sm_count / std::max(rows, 1), kMaxLists / width));
-    *part_tiles = (tiles + want - 1) / want;
-    *parts = (tiles + *part_tiles - 1) / *part_tiles;
+// Pieces of the line are as small as that a request's beams have kMaxLists parts at most.
+Cut cut_of(int width, int vocab, int dtype) {
+    const int tile = kThreads * (dtype == 2 ? kPer<2> : kPer<0>);
+    Cut c;
+    c.row_tiles = (vocab + tile - 1) / tile;
+    const int most = kMaxLists / width;
+    c.least = most > c.row_tiles ? 1 : (c.row_tiles + most - 2) / (most - 1);
+    c.slots = std::min(c.row_tiles, (c.row_tiles + c.least - 1) / c.least + 1);
+    return c;
 }
 
 }  // namespace
 
 cudaError_t launch_beam_select(const BeamArgs &a, void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
     const int rows = a.n_groups * a.width;
-    int parts, part_tiles;
-    split_rows(rows, a.width, a.vocab, dev.sm_count, &parts, &part_tiles);
+    const Cut cut = cut_of(a.width, a.vocab, a.dtype);
     PartSum *sums = static_cast<PartSum *>(workspace);
-    unsigned long long *lists = reinterpret_cast<unsigned long long *>(sums + (long long)rows * parts);
-    const dim3 grid((unsigned)rows * parts), block(kThreads);
-    const cudaError_t e =
-        a.dtype == 0   ? kv_launch(scan_kernel<0>, grid, block, 0, s, pdl, a, parts, part_tiles, sums, lists)
-        : a.dtype == 1 ? kv_launch(scan_kernel<1>, grid, block, 0, s, pdl, a, parts, part_tiles, sums, lists)
-                       : kv_launch(scan_kernel<2>, grid, block, 0, s, pdl, a, parts, part_tiles, sums, lists);
+    unsigned long long *lists = reinterpret_cast<unsigned long long *>(sums + (long long)rows * cut.slots);
+    const dim3 grid((unsigned)std::min<long long>(std::max<long long>((long long)rows * cut.row_tiles / cut.least, 1), 3 * dev.sm_count));
+    const dim3 block(kThreads);
+    cudaError_t e = a.dtype == 0   ? kv_launch(scan_kernel<0>, grid, block, 0, s, pdl, a, cut, sums, lists)
+                    : a.dtype == 1 ? kv_launch(scan_kernel<1>, grid, block, 0, s, pdl, a, cut, sums, lists)
+                                   : kv_launch(scan_kernel<2>, grid, block, 0, s, pdl, a, cut, sums, lists);
     if (e != cudaSuccess) return e;
-    const size_t smem = (2 * kBeamMost + kMaxLists) * 8 + (size_t)a.n_out * a.n_out * 12 + 4 + 16;
-    const cudaError_t f = raise_smem_cap(reinterpret_cast<const void *>(merge_kernel), smem);
-    if (f != cudaSuccess) return f;
-    return kv_launch(merge_kernel, dim3(a.n_groups), dim3(kMergeThreads), smem, s, pdl, a, parts, sums, lists, dev.status);
+    const size_t smem = 2 * kBeamMost * 8 + (1 + kMaxLists + (size_t)a.n_out * a.n_out) * 16 + (kBeamMost + 1) * 4;
+    e = raise_smem_cap(reinterpret_cast<const void *>(merge_kernel), smem);
+    if (e != cudaSuccess) return e;
+    return kv_launch(merge_kernel, dim3(a.n_groups), dim3(kMergeThreads), smem, s, pdl, a, cut, sums, lists, dev.status);
 }
 
-long long beam_select_workspace(int n_groups, int width, int vocab, int n_out, const DeviceInfo &dev) {
-    int parts, part_tiles;
-    split_rows(n_groups * width, width, vocab, dev.sm_count, &parts, &part_tiles);
-    return (long long)n_groups * width * parts * (sizeof(PartSum) + 8LL * n_out);
+long long beam_select_workspace(int n_groups, int width, int vocab, int n_out) {
+    // of the type with the smallest tiles
+    const Cut cut = cut_of(width, vocab, 2);
+    return (long long)n_groups * width * cut.slots * (sizeof(PartSum) + 8LL * n_out);
 }
 
 }  // namespace w4a16

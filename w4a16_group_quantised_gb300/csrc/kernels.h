@@ -181,7 +181,7 @@ struct BeamArgs {
     uint8_t *out_finished;                // or null
 };
 cudaError_t launch_beam_select(const BeamArgs &a, void *workspace, const DeviceInfo &dev, cudaStream_t s, bool pdl);
-long long beam_select_workspace(int n_groups, int width, int vocab, int n_out, const DeviceInfo &dev);
+long long beam_select_workspace(int n_groups, int width, int vocab, int n_out);
 
 // ---- api.cu helpers used by kv_api.cu and kv_attention.cu: the current device's state (W4A16_OK
 // or an error), the early-launch switch, the timeout hook, the kernel-selection log

@@ -371,9 +371,9 @@ int w4a16_beam_select(const void *logits, long long row_stride, w4a16_dtype_t dt
     if (!aligned(logits, dtype == W4A16_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(out_scores, 4) ||
         !aligned(out_rows, 4) || !aligned(out_tokens, 4) || !aligned(workspace, 16))
         return W4A16_ERR_ALIGN;
+    if (workspace_bytes < beam_select_workspace(n_groups, width, vocab, n_out)) return W4A16_ERR_ARG;
     const DeviceInfo *dev = nullptr;
     W4A16_TRY(device_info(&dev));
-    if (workspace_bytes < beam_select_workspace(n_groups, width, vocab, n_out, *dev)) return W4A16_ERR_ARG;
     const BeamArgs a{logits, row_stride, (int)dtype, scores, finished_or_null, n_groups, width, vocab, end_token, n_out,
                      out_scores, out_rows, out_tokens, out_finished_or_null};
     return done(launch_beam_select(a, workspace, *dev, str(stream), pdl_enabled()));
@@ -382,9 +382,7 @@ int w4a16_beam_select(const void *logits, long long row_stride, w4a16_dtype_t dt
 int w4a16_beam_select_workspace(int n_groups, int width, int vocab, int n_out, long long *bytes) {
     if (bytes == nullptr) return W4A16_ERR_NULL;
     W4A16_TRY(check_beams(n_groups, width, vocab, n_out));
-    const DeviceInfo *dev = nullptr;
-    W4A16_TRY(device_info(&dev));
-    *bytes = beam_select_workspace(n_groups, width, vocab, n_out, *dev);
+    *bytes = beam_select_workspace(n_groups, width, vocab, n_out);
     return W4A16_OK;
 }
 
