@@ -7,9 +7,9 @@
 // and the n best of a request's beams come out in order, ties to the lower
 // beam, then the lower token.  Bound by reading the logits once.
 //
-//  * The logits of all beams that go on are a line of tiles, cut in equal pieces
-//    over the CTAs; a beam's parts, one for each CTA that has tiles of it, are
-//    joined by a second kernel.  The next tile is on its way while one is worked on.
+//  * The logits of each beam that goes on are tiles, cut into as many pieces as
+//    fill the GPU; a second kernel joins a beam's pieces.  The next tile is on its
+//    way while one is worked on.
 //  * Each thread keeps a sum of its own, so nothing but the candidates is
 //    exchanged: 2^(x log2 e - R) with R the integer next to its largest x log2 e,
 //    so that sums with other references differ by a power of two, exactly.
@@ -20,12 +20,12 @@
 //  * Within a beam c rises with x: candidates are logits, kept as 64-bit keys
 //    (the value's order, then the lower token).  Threads whose largest logit of
 //    a tile is above the n-th best so far append theirs to a list, which is cut
-//    to its n best when it has grown.  A part's first tile gets its threshold
+//    to its n best when it has grown.  A piece's first tile gets its threshold
 //    from the least of the maxima of n groups of threads: n logits at least reach
 //    it, a few times n in earnest.  Where more do than the list holds (many equal
 //    ones), the n threads with the best maxima are found out, of which at most
 //    n times a thread's share can come.
-//  * The second kernel, a CTA per request, joins the parts' sums, scores the
+//  * The second kernel, a CTA per request, joins the pieces' sums, scores the
 //    candidates in 64 bits and picks the n best by counting who is better.
 //    Of sorted lists only the n with the best heads can hold any.
 #include <algorithm>
@@ -36,8 +36,10 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kPieceCost = 3;                          // tiles that a piece's start and end count for
 constexpr int kBatch = 8;                              // tiles between two cuts of a list
 constexpr int kList = 33 * kBeamMost;                  // its room: n candidates, and n threads' logits of a tile
+constexpr int kVectors = 1024;                         // vectors with candidates between two cuts
 constexpr int kMergeThreads = 256;
 constexpr int kMaxLists = 1024;                        // (beam, part) pairs of a request
 constexpr int kMaxRows = 2048;                         // beams among which those that go on are looked up first
@@ -45,12 +47,12 @@ constexpr float kHuge = 536870912.0f;                  // 2^29: from here on log
 
 // Logits of a tile per thread, in vectors of 8: as many as 16 registers hold.
 template <int DT> constexpr int kPer = DT == 2 ? 16 : 32;
-// The sum of a part of a beam's logits: l = sum 2^(x log2 e - reference(m)), m the
+// The sum of a piece of a beam's logits: l = sum 2^(x log2 e - reference(m)), m the
 // largest x.  Where |m| >= 2^29 nothing but the logits that equal m counts, and l is their number.
 struct PartSum {
     double l;
     float m;
-    int parts;                                         // of the beam (in its first part)
+    int parts;                                         // pieces of the beam
 };
 
 __device__ __forceinline__ float ex2(float v) {
@@ -123,36 +125,39 @@ template <int DT>
 struct Raw {
     uint32_t w[DT == 2 ? 8 : 4];
 };
-// Logits [at, at + 8) of a row at most `align` bytes aligned, -inf from `end` on.
-template <int DT>
-__device__ __forceinline__ Raw<DT> load8(const char *row, int align, int at, int end) {
-    Raw<DT> r;
+// A thread's vectors of a tile, at `at` and every kThreads vectors, of a row
+// aligned to `align` bytes; -inf from `end` on.
+template <int DT, int NV>
+__device__ __forceinline__ void load_tile(Raw<DT> (&x)[NV], const char *row, int align, int at, int end) {
     constexpr int N = DT == 2 ? 8 : 4, SIZE = DT == 2 ? 4 : 2;
     const char *p = row + (long long)at * SIZE;
-    if (at + 8 <= end && align >= 4) {
-        if (align >= 16) {
+    constexpr int STEP = kThreads * 8;
+    if (align == 16 && at + (NV - 1) * STEP + 8 <= end) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
-                const uint4 a = ldg_stream_v4(p + 4 * i);
-                r.w[i] = a.x, r.w[i + 1] = a.y, r.w[i + 2] = a.z, r.w[i + 3] = a.w;
+                const uint4 v = ldg_stream_v4(p + j * STEP * SIZE + 4 * i);
+                x[j].w[i] = v.x, x[j].w[i + 1] = v.y, x[j].w[i + 2] = v.z, x[j].w[i + 3] = v.w;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) r.w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
-        }
-        return r;
+        return;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (DT == 2) {
-            r.w[i] = at + i < end ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0xff800000u;
-        } else {
-            const uint32_t none = DT == 0 ? 0xfc00u : 0xff80u;
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(p) + 2 * i;
-            r.w[i] = (at + 2 * i < end ? __ldg(h) : none) | (at + 2 * i + 1 < end ? (uint32_t)__ldg(h + 1) : none) << 16;
+    for (int j = 0; j < NV; ++j, p += STEP * SIZE, at += STEP) {
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(p);
+        const uint16_t *halves = reinterpret_cast<const uint16_t *>(p);
+        const uint32_t none = DT == 0 ? 0xfc00u : 0xff80u;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (DT == 2)
+                x[j].w[i] = at + i < end ? __ldg(words + i) : 0xff800000u;
+            else if (align >= 4 && at + 2 * i + 1 < end)
+                x[j].w[i] = __ldg(words + i);
+            else
+                x[j].w[i] = (at + 2 * i < end ? __ldg(halves + 2 * i) : none) |
+                            (at + 2 * i + 1 < end ? (uint32_t)__ldg(halves + 2 * i + 1) : none) << 16;
         }
     }
-    return r;
 }
 template <int DT>
 __device__ __forceinline__ float value_of(const Raw<DT> &r, int i) {
@@ -168,11 +173,9 @@ __device__ __forceinline__ bool goes_on(const BeamArgs &a, int row) {
     return isfinite(s) && !ended;
 }
 
-// How the line of tiles is cut: host and device alike.
+// A beam's logits as tiles, and the pieces that they are cut into at most.
 struct Cut {
-    int row_tiles;                                     // tiles of a beam
-    int least;                                         // fewest tiles of a CTA, so that a request has kMaxLists parts at most
-    int slots;                                         // places for a beam's parts
+    int row_tiles, slots;
 };
 
 template <int DT>
@@ -186,10 +189,12 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
     __shared__ float s_hi[kWarps], s_lo[kWarps], s_max[kWarps];
     __shared__ int s_count[kWarps];
     __shared__ uint16_t s_rows[kMaxRows];
-    __shared__ int s_n;
+    __shared__ int vectors[kVectors];                      // the first tokens of vectors with candidates
+    __shared__ int s_n, s_vectors;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.n_out;
     const int rows = a.n_groups * a.width;
-    if (tid == 0) s_n = 0;
+    if (tid == 0) s_n = s_vectors = 0;
+    // The next kernel is not let start early: with its CTAs waiting for room, a call of more CTAs than SMs took 24 us more.
     grid_dependency_wait();
 
     // ---- the beams that go on, in order (all of them where there are too many to look)
@@ -212,15 +217,29 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
         }
         __syncthreads();
     }
-    const long long total = (long long)alive * cut.row_tiles;
-    const long long ctas = max(1LL, min((long long)gridDim.x, total / cut.least));
-    if (blockIdx.x >= ctas) return;
-    const long long t0 = blockIdx.x * total / ctas, t1 = (blockIdx.x + 1) * total / ctas;
+    if (alive == 0) return;
+    // Pieces of a beam: as many as fill the grid once, twice and so on, whichever takes least with the cost of a piece's
+    // start and end.  Lane i tries i + 1 rounds.
+    const int T = cut.row_tiles, grid = gridDim.x;
+    int q;
+    {
+        const long long fits = (long long)(lane + 1) * grid / alive;
+        q = (int)max(1LL, min(fits, (long long)cut.slots));
+        const long long rounds = ((long long)alive * q + grid - 1) / grid;
+        long long cost = rounds * ((T + q - 1) / q + kPieceCost) << 5 | lane;
+        long long least_cost = cost;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) least_cost = min(least_cost, __shfl_xor_sync(0xffffffffu, least_cost, d));
+        q = __shfl_sync(0xffffffffu, q, (int)(least_cost & 31));
+    }
+    const long long units = (long long)alive * q;
+    const long long u0 = blockIdx.x * units / grid, u1 = (blockIdx.x + 1) * units / grid;
+    if (u0 == u1) return;
 
-    float m = -INFINITY, hi = 0.0f, lo = 0.0f;             // of this thread and part
+    float m = -INFINITY, hi = 0.0f, lo = 0.0f;             // of this thread and piece
     float least = -INFINITY;                               // the n-th best so far
     int kept = 0;                                          // candidates that the list was last cut to
-    // The list of n candidates cut to the K best, in order.
+    // The K best of the list's n candidates, in order; and the list cut to them.
     auto shorten = [&](int n) {
 #pragma unroll 1
         for (int i = tid; i < n; i += kThreads) {
@@ -231,47 +250,33 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
             if (better < K) s_best[better] = mine;
         }
         __syncthreads();
+    };
+    auto keep_best = [&](int n) {
         if (tid < min(n, K)) list[tid] = s_best[tid];
         if (tid == 0) s_n = min(n, K);
         if (n >= K) least = key_value(s_best[K - 1]);
         __syncthreads();
     };
 
-    auto row_of = [&](long long t) {
-        const int o = (int)(t / cut.row_tiles);
-        return rows <= kMaxRows ? (int)s_rows[o] : o;
+    auto start_of = [&](int row) {
+        return static_cast<const char *>(a.logits) + row * a.row_stride * (DT == 2 ? 4 : 2);
     };
-    const char *logits = static_cast<const char *>(a.logits);
-    auto load = [&](Raw<DT> (&x)[NV], int row, int tile) {
-        const int end = rows <= kMaxRows || goes_on(a, row) ? a.vocab : 0;
-        const char *p = logits + row * a.row_stride * (DT == 2 ? 4 : 2);
-        const int low = (int)(reinterpret_cast<uintptr_t>(p) & 15), align = low == 0 ? 16 : low & 3 ? 2 : 4;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) x[j] = load8<DT>(p, align, tile * TILE + (j * kThreads + tid) * 8, end);
-    };
-    auto largest_of = [&](const Raw<DT> (&x)[NV]) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(value_of<DT>(x[j], e)), "f"(value_of<DT>(x[j], e + 1)));
-        return top;
+    auto logit = [&](int row, int token) {
+        const char *p = start_of(row);
+        if constexpr (DT == 2) return __ldg(reinterpret_cast<const float *>(p) + token);
+        else return kv_act<DT>(__ldg(reinterpret_cast<const uint16_t *>(p) + token));
     };
     // A tile's candidates when there are too many of them: those of the K threads with the best maxima.
     auto careful = [&](int row, int tile) {
-        Raw<DT> x[NV];
-        load(x, row, tile);
-        const float top = largest_of(x);
         const int base = tile * TILE;
+        auto token_of = [&](int k) { return base + ((k >> 3) * kThreads + tid) * 8 + (k & 7); };
         unsigned long long best = 0;
-#pragma unroll
-        for (int j = NV - 1; j >= 0; --j)
-#pragma unroll
-            for (int e = 7; e >= 0; --e) {                 // the lowest token of the largest logit
-                const float v = value_of<DT>(x[j], e);
-                if (v == top && v > least) best = key_of(v, base + (j * kThreads + tid) * 8 + e);
-            }
+#pragma unroll 4
+        for (int k = 0; k < PER; ++k) {
+            const int token = token_of(k);
+            const float v = token < a.vocab ? logit(row, token) : -INFINITY;
+            if (v > least) best = max(best, key_of(v, token));
+        }
         s_maxima[tid] = best;
         if (tid == 0) s_least = 0;
         __syncthreads();
@@ -280,41 +285,59 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
         for (int j = 0; j < kThreads; ++j) better += s_maxima[j] > best;
         if (best != 0 && better == K - 1) s_least = best;
         __syncthreads();
-        const unsigned long long from = s_least;
-        if (best >= from)
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = value_of<DT>(x[j], e);
-                    const unsigned long long k = key_of(v, base + (j * kThreads + tid) * 8 + e);
-                    if (v > least && k >= from) list[atomicAdd(&s_n, 1)] = k;
-                }
+        if (best >= max(s_least, 1ull))
+#pragma unroll 1
+            for (int k = 0; k < PER; ++k) {
+                const int token = token_of(k);
+                const float v = token < a.vocab ? logit(row, token) : -INFINITY;
+                if (v > least && key_of(v, token) >= s_least) list[atomicAdd(&s_n, 1)] = key_of(v, token);
+            }
         __syncthreads();
         const int n = s_n;
-        __syncthreads();
         shorten(n);
+        keep_best(n);
     };
 
     Raw<DT> next[NV];
-    int row = 0, tile = 0;
-    if (t0 < t1) {
-        row = row_of(t0), tile = (int)(t0 % cut.row_tiles);
-        load(next, row, tile);
-    }
-    int first = tile;                                      // of the tiles whose candidates are in the list uncut
-    bool fresh = true;                                     // the part's first tile
-    for (long long t = t0; t < t1; ++t) {
-        const int here = row, this_tile = tile, base = tile * TILE;
+    int row = 0, piece = 0, tile = 0, last = 0;            // what is being loaded: a beam's piece, up to tile `last`
+    auto open = [&](long long u) {
+        const int o = (int)(u / q);
+        piece = (int)(u - (long long)o * q);
+        row = rows <= kMaxRows ? (int)s_rows[o] : o;
+        tile = (int)((long long)piece * T / q), last = (int)((long long)(piece + 1) * T / q) - 1;
+    };
+    int first = 0;                                         // of the tiles whose candidates are not in the list
+    long long u = u0 - 1;
+    for (bool started = false, fresh = true;;) {
+        const int here = row, here_piece = piece, this_tile = tile, base = tile * TILE;
+        const bool ends = !started || tile == last;
         Raw<DT> x[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) x[j] = next[j];
-        const bool ends = ++tile == cut.row_tiles || t + 1 == t1;
-        if (t + 1 < t1) {
-            if (tile == cut.row_tiles) tile = 0, row = row_of(t + 1);
-            load(next, row, tile);
+        if (!ends || u + 1 < u1) {
+            if (ends) open(++u);
+            else ++tile;
+            const int end = rows <= kMaxRows || goes_on(a, row) ? a.vocab : 0;
+            const char *p = start_of(row);
+            const int low = (int)(reinterpret_cast<uintptr_t>(p) & 15), align = low == 0 ? 16 : low & 3 ? 2 : 4;
+            load_tile<DT>(next, p, align, tile * TILE + tid * 8, end);
+        } else {
+            ++u;
         }
-        const float top = largest_of(x);
+        if (!started) {
+            started = true;
+            first = tile;
+            continue;
+        }
+        float tops[NV], top = -INFINITY;                   // of each vector
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            tops[j] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+                asm("max.f32 %0, %0, %1, %2;" : "+f"(tops[j]) : "f"(value_of<DT>(x[j], e)), "f"(value_of<DT>(x[j], e + 1)));
+            top = fmaxf(top, tops[j]);
+        }
         // ---- the sum
         const float to = fmaxf(m, top);
         if (to != m) {
@@ -340,21 +363,22 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
             unpair(add2(sum[0], sum[1]), p, q);
             s = p + q;
         } else {
+            // a NaN stays one; no logit but -inf so far: none counts
             s = 0.0f;
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {              // a NaN stays one; no logit but -inf so far: none counts
+                for (int e = 0; e < 8; ++e) {
                     const float v = value_of<DT>(x[j], e);
                     s += v != v ? v : v == to && to > -INFINITY ? 1.0f : 0.0f;
                 }
         }
         add_to(hi, lo, s);
-        // ---- candidates: x > least, and in a part's first tile x >= bound
+        // ---- candidates are in vectors with an x > least, in a piece's first tile an x >= bound
         float bound = -INFINITY;
         if (fresh) {
             // groups of every so-manieth thread: a last tile of few tokens is in the first threads
-            const int groups = K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, across = min(groups, 32);
+            const int groups = K <= 4 ? 4 : K <= 8 ? 8 : K <= 16 ? 16 : K <= 32 ? 32 : 64, across = min(groups, 32);
             float g = top;
             for (int d = 16; d >= across; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
             s_group[tid] = g;
@@ -371,37 +395,46 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
         if (top > least && top >= bound) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = value_of<DT>(x[j], e);
-                    if (v > least && v >= bound) {
-                        const int at = atomicAdd(&s_n, 1);
-                        if (at < kList) list[at] = key_of(v, base + (j * kThreads + tid) * 8 + e);
-                    }
+                if (tops[j] > least && tops[j] >= bound) {
+                    const int at = atomicAdd(&s_vectors, 1);
+                    if (at < kVectors) vectors[at] = base + (j * kThreads + tid) * 8;
                 }
         }
         if (!ends && !fresh && this_tile - first < kBatch - 1) continue;
+        // ---- the candidates of the tiles since the last time
+        __syncthreads();
+        const int found = s_vectors;
+        if (found <= kVectors)
+            for (int i = tid; i < 8 * found; i += kThreads) {
+                const int token = vectors[i >> 3] + (i & 7);
+                const float v = token < a.vocab ? logit(here, token) : -INFINITY;
+                if (v > least && v >= bound) {
+                    const int at = atomicAdd(&s_n, 1);
+                    if (at < kList) list[at] = key_of(v, token);
+                }
+            }
         __syncthreads();
         int n = s_n;
-        __syncthreads();
-        if (n > kList) {
-            // again, tile by tile, after what the list had been cut to before
+        if (found > kVectors || n > kList) {
+            // too many: again, tile by tile, after what the list had been cut to before
+            __syncthreads();
             if (tid == 0) s_n = kept;
+#pragma unroll 1
             for (int i = first; i <= this_tile; ++i) careful(here, i);
             n = s_n;
-            __syncthreads();
         }
+        if (tid == 0) s_vectors = 0;
         shorten(n);
-        n = kept = min(n, K);
-        first = this_tile + 1;
-        fresh = false;
-        if (!ends) continue;
-        // ---- the part's end: its candidates, and the threads' sums joined
-        const long long o = t / cut.row_tiles, line0 = o * cut.row_tiles, line1 = line0 + cut.row_tiles - 1;
-        // the CTAs that hold the beam's first tile and its last
-        const int c0 = (int)(((line0 + 1) * ctas - 1) / total), c1 = (int)(((line1 + 1) * ctas - 1) / total);
-        const long long slot = (long long)here * cut.slots + (blockIdx.x - c0);
-        if (tid < K) lists[slot * K + tid] = tid < n ? list[tid] : 0;
+        fresh = ends;
+        if (!ends) {
+            keep_best(n);
+            kept = min(n, K);
+            first = this_tile + 1;
+            continue;
+        }
+        // ---- the piece's end: its candidates, and the threads' sums joined
+        const long long slot = (long long)here * cut.slots + here_piece;
+        if (tid < K) lists[slot * K + tid] = tid < n ? s_best[tid] : 0;
         float all = m;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
@@ -426,14 +459,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
                 add_to(hi, lo, s_hi[w]);
                 lo += s_lo[w];
             }
-            sums[slot] = PartSum{(double)hi + (double)lo, all, c1 - c0 + 1};
+            sums[slot] = PartSum{(double)hi + (double)lo, all, q};
         }
+        if (u == u1) return;
         m = -INFINITY, hi = lo = 0.0f, least = -INFINITY;
-        fresh = true, first = tile, kept = 0;
+        first = tile, kept = 0;
     }
 }
 
-// The logarithm of a sum of 0.25 and more, to about 2^-32: of its fraction f in
+// The logarithm of a sum of 0.25 and more, to 2^-29: of its fraction f in
 // [0.7, 1.4] as 2 atanh(q), q = (f - 1) / (f + 1), in two fp32 numbers and a
 // series in q^2.  64-bit arithmetic is slow here: log() takes 1.5 us.
 __device__ __forceinline__ double log_of(double l) {
@@ -567,15 +601,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
     }
 }
 
-// Pieces of the line are as small as that a request's beams have kMaxLists parts at most.
+// A request's beams have kMaxLists pieces at most.
 Cut cut_of(int width, int vocab, int dtype) {
-    const int tile = kThreads * (dtype == 2 ? kPer<2> : kPer<0>);
-    Cut c;
-    c.row_tiles = (vocab + tile - 1) / tile;
-    const int most = kMaxLists / width;
-    c.least = most > c.row_tiles ? 1 : (c.row_tiles + most - 2) / (most - 1);
-    c.slots = std::min(c.row_tiles, (c.row_tiles + c.least - 1) / c.least + 1);
-    return c;
+    const int tile = kThreads * (dtype == 2 ? kPer<2> : kPer<0>), tiles = (vocab + tile - 1) / tile;
+    return Cut{tiles, std::min(tiles, kMaxLists / width)};
 }
 
 }  // namespace
@@ -585,7 +614,7 @@ cudaError_t launch_beam_select(const BeamArgs &a, void *workspace, const DeviceI
     const Cut cut = cut_of(a.width, a.vocab, a.dtype);
     PartSum *sums = static_cast<PartSum *>(workspace);
     unsigned long long *lists = reinterpret_cast<unsigned long long *>(sums + (long long)rows * cut.slots);
-    const dim3 grid((unsigned)std::min<long long>(std::max<long long>((long long)rows * cut.row_tiles / cut.least, 1), 3 * dev.sm_count));
+    const dim3 grid((unsigned)std::min<long long>((long long)rows * cut.slots, 3 * dev.sm_count));
     const dim3 block(kThreads);
     cudaError_t e = a.dtype == 0   ? kv_launch(scan_kernel<0>, grid, block, 0, s, pdl, a, cut, sums, lists)
                     : a.dtype == 1 ? kv_launch(scan_kernel<1>, grid, block, 0, s, pdl, a, cut, sums, lists)
