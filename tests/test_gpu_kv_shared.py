@@ -257,7 +257,7 @@ def test_captured(cuda_lib, members):
 def test_other_stream_and_workspace(cuda_lib):
     """A workspace of its own, used by one call after the other, with other sizes and with the plain attention."""
     w = cuda_lib
-    ws = torch.full((64 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = torch.full((160 << 20,), 0xff, dtype=torch.uint8, device="cuda")
     for i, members in enumerate((3, 40, 5, 70)):
         p, starts, prefix = grouped([(300, [(9, 1 + i)] * members)], seed=16 + i)
         check(w, p, starts, prefix, workspace=ws)

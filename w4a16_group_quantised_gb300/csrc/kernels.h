@@ -109,8 +109,10 @@ struct KvAttentionArgs {
     void *workspace;
 };
 // Attention of a batch whose sequences share pages (kv_attention_shared.cu): a
-// pass over the shared keys, an entry for each group, then one over the rest,
-// an entry for each sequence.
+// pass over the shared keys, an entry for each group, and one over the rest,
+// an entry for each sequence.  What a pass finds for a row (a token and query
+// head) is sums that are not yet divided, relative to 2^m with denominator l:
+// in its arrays, or as the parts of a tile that several CTAs share.
 struct KvEntry {
     int q0, n;                            // rows of the token tensors
     int len, pad;                         // keys, from position 0 of the first page on
@@ -120,9 +122,17 @@ struct KvEntry {
 struct KvShare {
     const KvEntry *entries;
     int step;                             // 0: the shared keys, which every row sees; 1: the others, row t up to len - n + t
-    float *out;                           // [n_tokens, n_heads, head_dim] sums over the shared keys, not yet divided
-    float *ml;                            // [n_tokens, n_heads, 2] their references and denominators
+    int defer;                            // parts are left where they are; else the last CTA to come sums them
+    float *out;                           // [n_tokens, n_heads, head_dim] sums
+    float *ml;                            // [n_tokens, n_heads, 2] m and l
+    unsigned long long *where;            // [n_tokens, n_heads]: kv_where, 0 where the pass has nothing
 };
+enum { kKvNone = 0, kKvInArrays = 1, kKvFewParts = 2, kKvManyParts = 3 };
+// Parts of row `row` of a tile, in slot 1 of CTA `from` and slot 0 of the CTAs after it up to `to`.
+__host__ __device__ inline unsigned long long kv_where(int kind, int row, int from, int to) {
+    return (unsigned long long)kind | (unsigned long long)row << 2 | (unsigned long long)from << 16 |
+           (unsigned long long)to << 32;
+}
 cudaError_t launch_kv_append(const KvCache &c, const KvBatch &b, const void *k_new, long long k_stride,
                              const void *v_new, long long v_stride, int dtype, const DeviceInfo &dev, cudaStream_t s,
                              bool pdl);
@@ -133,6 +143,8 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
 // sequences with more than row_limit rows (tokens * query heads of a kv head), in kv_attention_tc.cu; share: or null
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, int row_limit,
                                      const DeviceInfo &dev, cudaStream_t s, bool pdl, const KvShare *share = nullptr);
+int kv_attention_many_launches(const KvBatch &b, int group);   // kernels that a call of it runs
+constexpr int kManyTileRows = 256;        // of a tile of kv_attention_tc.cu, and of its parts
 int kv_few_rows_most(const KvCache &c);   // rows up to which kv_few_rows.cuh's kernel is the faster one
 // sequences [group_starts[g], group_starts[g + 1]) have their first prefix_lens[g] positions in the same pages
 struct KvGroups {

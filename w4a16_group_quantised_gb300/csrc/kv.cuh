@@ -75,48 +75,17 @@ __device__ __forceinline__ uint16_t kv_to_act(float v) {
     return DT == 0 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// ---- sums over two sets of keys, each relative to 2^m with denominator l, joined
-struct KvJoin {
-    float here, there, l, m;
-};
-__device__ __forceinline__ KvJoin kv_join(float m, float l, float m2, float l2) {
-    KvJoin j;
-    j.m = fmaxf(m, m2);
-    j.here = exp2f(m - j.m), j.there = l2 == 0.0f ? 0.0f : exp2f(m2 - j.m);
-    j.l = l * j.here + l2 * j.there;
-    return j;
-}
-
-// `count` dims from d0 on of a row's sums v: over shared keys (step 0), to be
-// joined; or over the others, joined with those and written to the output.
+// `count` dims from d0 on of a row's sums, to the pass's arrays.
 template <int D>
-__device__ __forceinline__ void kv_store_joined(const KvAttentionArgs &a, const KvShare &sh, long long at, int d0,
-                                                const float *v, int count, float l, float m) {
-    float4 *part = reinterpret_cast<float4 *>(sh.out + at * D + d0);
-    float2 *ml = reinterpret_cast<float2 *>(sh.ml) + at;
-    if (sh.step == 0) {
+__device__ __forceinline__ void kv_store_sums(const KvShare &sh, long long at, int d0, const float *v, int count, float l,
+                                              float m) {
+    float4 *dst = reinterpret_cast<float4 *>(sh.out + at * D + d0);
 #pragma unroll
-        for (int i = 0; i < count; i += 4) part[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        if (d0 == 0) *ml = make_float2(m, l);
-        return;
+    for (int i = 0; i < count; i += 4) dst[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    if (d0 == 0) {
+        reinterpret_cast<float2 *>(sh.ml)[at] = make_float2(m, l);
+        sh.where[at] = kv_where(kKvInArrays, 0, 0, 0);
     }
-    const float2 z = *ml;
-    const KvJoin j = kv_join(m, l, z.x, z.y);
-    const float r = j.l == 0.0f ? 0.0f : 1.0f / j.l, x = j.here * r, y = j.there * r;
-    uint16_t *dst = static_cast<uint16_t *>(a.out) + at * D + d0;
-#pragma unroll
-    for (int i = 0; i < count; i += 4) {
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (z.y != 0.0f) o = part[i / 4];                  // else nothing has been written there
-        const float w[4] = {v[i] * x + o.x * y, v[i + 1] * x + o.y * y, v[i + 2] * x + o.z * y, v[i + 3] * x + o.w * y};
-        uint2 u;
-        u.x = a.dtype == 0 ? kv_to_act<0>(w[0]) | (uint32_t)kv_to_act<0>(w[1]) << 16
-                           : kv_to_act<1>(w[0]) | (uint32_t)kv_to_act<1>(w[1]) << 16;
-        u.y = a.dtype == 0 ? kv_to_act<0>(w[2]) | (uint32_t)kv_to_act<0>(w[3]) << 16
-                           : kv_to_act<1>(w[2]) | (uint32_t)kv_to_act<1>(w[3]) << 16;
-        *reinterpret_cast<uint2 *>(dst + i) = u;
-    }
-    if (a.lse && d0 == 0) a.lse[at] = j.l == 0.0f ? -INFINITY : (j.m + __log2f(j.l)) * 0.6931471805599453f;
 }
 
 // ---- codes

@@ -6,16 +6,19 @@
 // and l_i = sum_j 2^(x_j - m_i) over each, and m the larger of m_1 and m_2,
 //     out = (2^(m_1 - m) o_1 + 2^(m_2 - m) o_2) / (2^(m_1 - m) l_1 + 2^(m_2 - m) l_2).
 // So the keys that a group's sequences have in common are read once, for the
-// tokens of all of them as the rows of one problem, and every row's sum over
-// its own keys is joined with that where the row is written.  Three kernels:
+// tokens of all of them as the rows of one problem, and joined with every row's
+// sum over its own keys at the end.  Four kernels:
 //  * the plan: what a group shares (whole pages that lie before all of its new
 //    tokens), as an entry of rows, keys and a place in the block table for
 //    each group and for the rest of each sequence;
-//  * the shared keys, all rows of a group seeing all of them: sums in fp32 with
-//    reference and denominator to scratch;
-//  * the others, joined on the way out.
-// The last two are the kernels of kv_few_rows.cuh and kv_attention_tc.cu with
-// entries in place of sequences; which of them follows from the rows.
+//  * the shared keys, all rows of a group seeing all of them;
+//  * the others;
+//  * the join, a warp or half of one a row.
+// The middle two are the kernels of kv_few_rows.cuh and kv_attention_tc.cu with
+// entries in place of sequences; which of them follows from the rows.  A group's
+// tile is long, and there are few of them, so that each is cut over many CTAs:
+// the parts that these leave are read by the join, by all SMs, where in
+// kv_attention the last CTA to come sums them alone.
 #include <algorithm>
 #include <cstdio>
 
@@ -29,19 +32,21 @@ constexpr int kPlanThreads = 1024;
 struct PlanParams {
     KvBatch b;
     KvGroups g;
-    int page_shift, rows;                 // rows: n_tokens * n_heads
+    int page_shift;
     KvEntry *groups, *seqs;
     int *shared;                          // positions that each group shares
-    float *ml;
+    uint4 *where;                         // of both passes, to be cleared
+    long long where_vecs;
     int *status;
 };
 
-// The first CTA: groups, a warp each, then sequences.  The others: no row has a sum over shared keys yet.
+// The first CTA: groups, a warp each, then sequences.  The others: no row has a sum yet.
 __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanParams p) {
     kv_begin();
     if (blockIdx.x > 0) {
-        for (int i = (blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < p.rows; i += (gridDim.x - 1) * kPlanThreads)
-            reinterpret_cast<float2 *>(p.ml)[i] = make_float2(kRefStart, 0.0f);
+        for (long long i = (long long)(blockIdx.x - 1) * kPlanThreads + threadIdx.x; i < p.where_vecs;
+             i += (long long)(gridDim.x - 1) * kPlanThreads)
+            p.where[i] = make_uint4(0, 0, 0, 0);
         return;
     }
     const int lane = threadIdx.x & 31, n_seqs = p.b.n_seqs, n_groups = p.g.n_groups;
@@ -87,13 +92,87 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
     }
 }
 
+// What the join reads of a pass.
+struct PassSums {
+    const unsigned long long *where;
+    const float *out, *ml;
+    const float *few, *many;              // parts
+    int few_rows;                         // of a tile of kv_few_rows.cuh
+};
+struct JoinParams {
+    KvAttentionArgs a;
+    PassSums pass[2];
+    int rows;
+};
+
+// A row's sums of both passes, D / 4 lanes a row, four dims each.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+    kv_begin();
+    constexpr int LANES = D / 4;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+    const int d = threadIdx.x % LANES * 4;
+    if (row >= p.rows) return;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m = kRefStart, l = 0.0f;
+    auto add = [&](float2 ml, float4 x) {
+        const float top = fmaxf(m, ml.x), f = ex2(m - top), w = ex2(ml.x - top);
+        m = top;
+        l = fmaf(ml.y, w, l * f);
+        o = make_float4(fmaf(x.x, w, o.x * f), fmaf(x.y, w, o.y * f), fmaf(x.z, w, o.z * f), fmaf(x.w, w, o.w * f));
+    };
+    unsigned long long where[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) where[i] = p.pass[i].where[row];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const PassSums &s = p.pass[i];
+        const int kind = (int)(where[i] & 3), r = (int)(where[i] >> 2 & 511);
+        const int from = (int)(where[i] >> 16 & 0xffff), to = (int)(where[i] >> 32 & 0xffff);
+        if (kind == kKvNone) continue;
+        if (kind == kKvInArrays) {
+            add(reinterpret_cast<const float2 *>(s.ml)[row], *reinterpret_cast<const float4 *>(s.out + row * D + d));
+            continue;
+        }
+        const bool few = kind == kKvFewParts;
+        const int tile = few ? s.few_rows : kManyTileRows, part = tile * (D + 2);
+        // where a part has the row's four dims, and its (m, l)
+        const float *base = few ? s.few : s.many;
+        const int at = few ? r * D + d : d * tile + 4 * r, ml_at = tile * D + 2 * r;
+        constexpr int N = 8;                               // parts whose loads are on their way together
+        for (int c = from; c <= to; c += N) {
+            float2 ml[N];
+            float4 x[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int cta = min(c + k, to);
+                const float *src = base + (2LL * cta + (cta == from)) * part;
+                ml[k] = *reinterpret_cast<const float2 *>(src + ml_at);
+                x[k] = *reinterpret_cast<const float4 *>(src + at);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (c + k <= to) add(ml[k], x[k]);
+        }
+    }
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    uint2 w;
+    if (p.a.dtype == 0) w.x = pack_half2(o.x * r, o.y * r), w.y = pack_half2(o.z * r, o.w * r);
+    else w.x = pack_bf162(o.x * r, o.y * r), w.y = pack_bf162(o.z * r, o.w * r);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.a.out) + row * D + d) = w;
+    if (p.a.lse && d == 0) p.a.lse[row] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 struct Scratch {
-    void *attention;                      // of the two passes, one after the other
+    void *few[2], *many[2];               // of the passes' kernels: tickets, parts
     KvEntry *groups, *seqs;
     int *shared;
-    float *ml, *out;
+    unsigned long long *where[2];
+    float *ml[2], *out[2];
     long long bytes;
 };
+
+long long tickets_bytes(const DeviceInfo &dev) { return (long long)((dev.sm_count + 1) & ~1) * 8; }
 
 Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups, int n_tokens,
                    const DeviceInfo &dev) {
@@ -104,13 +183,19 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
         return q;
     };
     Scratch s;
-    s.attention = take(kv_attention_workspace(n_heads, n_kv_heads, head_dim, n_seqs, n_tokens, dev));
+    const long long rows = (long long)n_tokens * n_heads;
+    const bool many = (long long)n_tokens * (n_heads / n_kv_heads) > kTileRows;
     s.groups = reinterpret_cast<KvEntry *>(take((long long)n_groups * sizeof(KvEntry)));
     s.seqs = reinterpret_cast<KvEntry *>(take((long long)n_seqs * sizeof(KvEntry)));
     s.shared = reinterpret_cast<int *>(take((long long)n_groups * 4));
-    const long long rows = (long long)n_tokens * n_heads;
-    s.ml = reinterpret_cast<float *>(take(rows * 8));
-    s.out = reinterpret_cast<float *>(take(rows * head_dim * 4));
+    s.where[0] = reinterpret_cast<unsigned long long *>(take(2 * ((rows * 8 + 15) & ~15LL)));
+    s.where[1] = s.where[0] + ((rows + 1) & ~1LL);
+    for (int i = 0; i < 2; ++i) {
+        s.few[i] = take(tickets_bytes(dev) + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4);
+        s.many[i] = many ? take(kv_attention_many_workspace(head_dim, dev)) : nullptr;
+        s.ml[i] = reinterpret_cast<float *>(take(rows * 8));
+        s.out[i] = reinterpret_cast<float *>(take(rows * head_dim * 4));
+    }
     s.bytes = p - static_cast<char *>(ws);
     return s;
 }
@@ -121,8 +206,10 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
                                        const DeviceInfo &dev, cudaStream_t s, bool pdl) {
     const Scratch w = scratch_of(a.workspace, a.n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, g.n_groups, b.n_tokens, dev);
     const int group = a.n_heads / c.n_kv_heads, most = kv_few_rows_most(c), rows = b.n_tokens * a.n_heads;
-    const PlanParams plan{b, g, c.page_shift, rows, w.groups, w.seqs, w.shared, w.ml, dev.status};
-    const int fill = std::min((rows + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
+    const long long vecs = ((long long)rows + 1) / 2 * 2;
+    const PlanParams plan{b, g, c.page_shift, w.groups, w.seqs, w.shared, reinterpret_cast<uint4 *>(w.where[0]), vecs,
+                          dev.status};
+    const int fill = (int)std::min<long long>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
     cudaError_t e = kv_launch(plan_shared_kernel, dim3(1 + fill), dim3(kPlanThreads), 0, s, pdl, plan);
     if (e != cudaSuccess) return e;
     // Shared keys: by the tokens that a group has in the mean when that decides, else each kernel those it is for.
@@ -142,24 +229,33 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
                       all_many ? "many_rows" : many ? "few_rows+many_rows" : "few_rows", most, dev.sm_count, pdl ? 1 : 0);
         log_kernel_selection(line);
     }
-    KvAttentionArgs args = a;
-    args.workspace = w.attention;
-    KvBatch batch = b;
-    if (g.n_groups > 0) {
-        const KvShare share{w.groups, 0, w.out, w.ml};
-        batch.n_seqs = g.n_groups;
-        args.max_q_len = b.n_tokens;                       // picks tiles of 8 or 16 rows
-        if (!all_many_shared) e = launch_few_rows<true>(args, c, batch, many_shared ? most : 0, share, dev, s, pdl);
-        if (e == cudaSuccess && many_shared)
-            e = launch_kv_attention_many(args, c, batch, all_many_shared ? 0 : most, dev, s, pdl, &share);
-        if (e != cudaSuccess) return e;
+    JoinParams join{a, {}, rows};
+    for (int i = 0; i < 2; ++i) {
+        KvBatch batch = b;
+        batch.n_seqs = i ? b.n_seqs : g.n_groups;
+        KvAttentionArgs args = a;
+        if (i == 0) args.max_q_len = b.n_tokens;           // picks tiles of 8 or 16 rows
+        const bool some_many = i ? many : many_shared, only_many = i ? all_many : all_many_shared;
+        KvShare share{i ? w.seqs : w.groups, i, 0, w.out[i], w.ml[i], w.where[i]};
+        if (!only_many) {
+            args.workspace = w.few[i];
+            share.defer = batch.n_seqs <= kMaxSeqs;        // one launch: its parts stay until the join
+            e = launch_few_rows<true>(args, c, batch, some_many ? most : 0, share, dev, s, pdl);
+            if (e != cudaSuccess) return e;
+        }
+        if (some_many) {
+            args.workspace = w.many[i];
+            share.defer = kv_attention_many_launches(batch, group) == 1;
+            e = launch_kv_attention_many(args, c, batch, only_many ? 0 : most, dev, s, pdl, &share);
+            if (e != cudaSuccess) return e;
+        }
+        auto parts = [&](void *ws) { return reinterpret_cast<const float *>(static_cast<char *>(ws) + tickets_bytes(dev)); };
+        join.pass[i] = PassSums{w.where[i], w.out[i], w.ml[i], parts(w.few[i]), w.many[i] ? parts(w.many[i]) : nullptr,
+                                few_tile_rows(args.max_q_len, group)};
     }
-    const KvShare share{w.seqs, 1, w.out, w.ml};
-    batch.n_seqs = b.n_seqs;
-    args.max_q_len = a.max_q_len;
-    if (!all_many) e = launch_few_rows<true>(args, c, batch, many ? most : 0, share, dev, s, pdl);
-    if (e == cudaSuccess && many) e = launch_kv_attention_many(args, c, batch, all_many ? 0 : most, dev, s, pdl, &share);
-    return e;
+    const dim3 grid((unsigned)(((long long)rows * (c.head_dim / 4) + 255) / 256));
+    return c.head_dim == 128 ? kv_launch(join_kernel<128>, grid, dim3(256), 0, s, pdl, join)
+                             : kv_launch(join_kernel<64>, grid, dim3(256), 0, s, pdl, join);
 }
 
 long long kv_attention_shared_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups,

@@ -55,7 +55,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kHalfRows = 128, kTileRows = 256, kKeys = 128;
+constexpr int kHalfRows = 128, kTileRows = kManyTileRows, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
 constexpr int kMaxPairs = 1216;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float f[32];
                     read_out(c, f);
                     if (has) {
-                        if constexpr (SHARED) kv_store_joined<D>(p.a, p.share, at, c, f, 32, sum, ref);
+                        if constexpr (SHARED) kv_store_sums<D>(p.share, at, c, f, 32, sum, ref);
                         else store(at, c, f, inv);
                     }
                 }
@@ -877,6 +877,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (has) __stcg(reinterpret_cast<float2 *>(mine + kTileRows * D) + row, make_float2(ref, sum));
                 const int from = first_cta(t, ctas, total), to = last_cta(t, ctas, total);
+                if (SHARED && p.share.defer) {                     // whoever reads the rows sums the parts
+                    if (has && opens) p.share.where[at] = kv_where(kKvManyParts, row, from, to);
+                    tc_fence_before();
+                    close_tile(idx);
+                    continue;
+                }
                 // the tile's threads: of the first half, or of both
                 auto meet = [&]() {
                     const uint32_t bar = meet_bar(twice ? 0 : 1);
@@ -935,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 f[4 * k + 3] = fmaf(y[k].w, wb, fmaf(x[k].w, wa, f[4 * k + 3]));
                             }
                         }
-                        if constexpr (SHARED) kv_store_joined<D>(p.a, p.share, at, d, f, 32, l, m);
+                        if constexpr (SHARED) kv_store_sums<D>(p.share, at, d, f, 32, l, m);
                         else store(at, d, f, inv);
                     }
                     if (!SHARED && p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
@@ -1258,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && tid == 0 && !misc[4]) {
+    if (*abort_flag && tid == 0 && !misc[4] && !(SHARED && p.share.defer)) {
         // A CTA that gave a wait up has no results, but its tickets are counted: they are back at 0 after every
         // launch, also for a replay, whose tag is the same.  All out of shared memory: the loops have no register to
         // spare for what is needed here.
@@ -1328,7 +1334,7 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
         const long long pairs = (long long)b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
             // with a row limit the other kernel has seen to the rows that no sequence owns
-            const bool mine = row_limit == 0 && first == 0 && (!SHARED || share.step != 0);
+            const bool mine = !SHARED && row_limit == 0 && first == 0;
             ManyParams p{a, c, b, row_limit, half_rows, mine && b0 == 0, mine && b0 + b.n_seqs == batch.n_seqs, (int)first,
                          nullptr, nullptr, 0, hold_copies(), dev.status, share};
             p.tickets = static_cast<unsigned long long *>(a.workspace);
@@ -1349,6 +1355,16 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
 }
 
 }  // namespace
+
+int kv_attention_many_launches(const KvBatch &batch, int group) {
+    const int half_rows = kHalfRows / group * group;
+    int n = 0;
+    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
+        const long long pairs = (long long)batch.n_tokens * group / (2 * half_rows) + std::min(kMaxSeqs, batch.n_seqs - b0);
+        n += (int)((pairs + kMaxPairs - 1) / kMaxPairs);
+    }
+    return n;
+}
 
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
                                      const DeviceInfo &dev, cudaStream_t s, bool pdl, const KvShare *share) {

@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
     };
     auto store_row = [&](long long at, int d0, const float *v, int count, float l, float m) {
         if constexpr (SHARED) {
-            kv_store_joined<D>(p.a, p.share, at, d0, v, count, l, m);
+            kv_store_sums<D>(p.share, at, d0, v, count, l, m);
             return;
         }
         const float r = l == 0.0f ? 0.0f : 1.0f / l;
@@ -818,7 +818,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
             if (d == 0) __stcg(reinterpret_cast<float2 *>(dst + ROWS * D + 2 * row), make_float2(m, l));
         }
     }
-    if (out[0] || out[1] || gave_up) {
+    const bool defer = SHARED && p.share.defer;                    // whoever reads the rows sums the parts
+    if (!defer && (out[0] || out[1] || gave_up)) {
         // tickets: which CTAs share the tile follows from where it begins and ends (a warp that has hardly had
         // anything to sum: eight rows are 256 pieces at most)
         const int nth = tid - 32 * (NW - 1);
@@ -866,6 +867,29 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
     }
     if (gave_up) return;
+    if (defer && out[1] && warp == NW - 1) {
+        // the tile that begins here: the last CTA whose share begins by its last step
+        const Shared sh = shared[s_out[1]];
+        const long long line = c0 + mine - 1;
+        const int b = find(line, 0, s_seq[0], s_seq[NW]), steps = span(seqs[b].y, seqs[b].z).steps;
+        const int idx = line_div(line - pre[b], steps);
+        const long long end = pre[b] + (long long)idx * steps + (long long)(tiles_before[b] + idx) * COST + steps + COST;
+        int to = (int)((end * ctas + total - 1) / total - 1);
+        if (by_tile) {
+            int done = 0, n = 0;
+            for (int i = 0; i <= b; ++i) {
+                if (seqs[i].w == 0) continue;
+                n = pieces_of(i, done, span(seqs[i].y, seqs[i].z).steps + COST);
+                if (i < b) done += n * seqs[i].w * Hk;
+            }
+            to = (done + idx * n + n - 1) / NW;
+        }
+        const Tile tl = {sh.begin, sh.end, sh.q0, sh.n, sh.row, sh.head, 0};
+        for (int row = lane; row < ROWS; row += 32) {
+            long long at;
+            if (place(tl, row, at)) p.share.where[at] = kv_where(kKvFewParts, row, blockIdx.x, to);
+        }
+    }
     // those within the CTA: each by the warp that holds the first part
     {
         const Shared sh = shared[1 + warp];
@@ -880,7 +904,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             }
         }
     }
-    if (!out[0] && !out[1]) return;
+    if (defer || (!out[0] && !out[1])) return;
     __syncthreads();
     // ---- a tile that CTAs from..to share: the last of them to come sums it
 #pragma unroll
@@ -970,6 +994,9 @@ cudaError_t launch_few(const FewParams &p, const CUtensorMap &k, const CUtensorM
 
 constexpr int kTileRows = 16;             // the most rows of a tile here
 
+// Rows of a tile for a batch whose sequences have up to so many tokens.
+inline int few_tile_rows(int max_q_len, int group) { return (long long)max_q_len * group <= 8 ? 8 : kTileRows; }
+
 // All sequences of the batch, or those of up to row_limit rows a kv head (0: all).
 template <bool SHARED>
 cudaError_t launch_few_rows(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,
@@ -998,7 +1025,7 @@ cudaError_t launch_few_rows(const KvAttentionArgs &a, const KvCache &c, const Kv
             b.q_starts += b0;
         }
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
-        const bool owns = !SHARED || share.step != 0;          // rows that are no sequence's
+        const bool owns = !SHARED;                              // rows that are no sequence's
         FewParams p{a, c, b, row_limit, token_first ? 1 : 0, merged ? 1 : 0, owns && b0 == 0,
                     owns && b0 + b.n_seqs == batch.n_seqs, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,
                     nullptr, nullptr, 0, hold_copies(), dev.status, share};
@@ -1007,7 +1034,7 @@ cudaError_t launch_few_rows(const KvAttentionArgs &a, const KvCache &c, const Kv
         p.tag = (launches.fetch_add(1) * 0x9e3779b97f4a7c15ull) >> 16;
         if (p.tag == 0) p.tag = 1;
         const int grid = dev.sm_count;
-        const bool few = (long long)a.max_q_len * group <= 8;
+        const bool few = few_tile_rows(a.max_q_len, group) == 8;
         // <codes, dims, 8-row tiles, keys a block, blocks a step, warps, ring stages>
         // Two blocks a step where the registers allow it: one costs 68 us instead of 57 (64 ragged contexts, pages of
         // 16), 55 instead of 44 (the same at 64 dims), 41 instead of 34 (64 dims, pages of 64), 61 instead of 52 (24 x 5
