@@ -404,7 +404,11 @@ int w4a16_version(void);
  * word (its output is then meaningless); so does the attention over the
  * 8-bit cache, in all its CTAs (1) or in every vals[0]-th (2 and more); n = 0
  * turns it off;
- * n = 0 restores the built-in choice for which = 1, 2, 4 or 8.  An invalid
+ * which = 10: kernels of w4a16_kv_attention_shared, vals = {1: the few-rows
+ * kernel alone, 2: the tensor-core kernel for every group or sequence with
+ * more than 32 rows a kv head}, n = 1, whatever the sizes (which otherwise may
+ * also have w4a16_kv_attention called);
+ * n = 0 restores the built-in choice for which = 1, 2, 4, 8 or 10.  An invalid
  * configuration is rejected here or, for the decode shape limits, by the
  * next w4a16_gemm call with W4A16_ERR_ARG. */
 int w4a16_debug_set_config(int which, const int *vals, int n);
@@ -520,14 +524,15 @@ int w4a16_kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int 
  * first pages in common: samples or beams of one prompt (w4a16_kv_fork,
  * w4a16_kv_reorder), users of one system prompt.  Sequences [group_starts[g],
  * group_starts[g + 1]) are group g, and their first prefix_lens[g] positions
- * are in the same pages (group_starts [n_groups + 1], non-decreasing, within
- * [0, n_seqs]; prefix_lens [n_groups], 0 or more; device, read there like the
- * lengths; what is wrong in them is reported in the status word).  Sequences of
- * no group share nothing.  The whole pages among these positions that lie
- * before every new token of the group are read once for all of its tokens,
- * and from the row of its first sequence that brings any: with rows that do
- * name the same pages the result is w4a16_kv_attention's but for rounding
- * (sums over the shared keys and over the others are joined in fp32).
+ * are in the same pages: the rows of the table say so, entry by entry
+ * (group_starts [n_groups + 1], non-decreasing, within [0, n_seqs]; prefix_lens
+ * [n_groups], 0 or more; on the device, like the lengths; what is wrong in them
+ * is reported in the status word where they are looked at).  Sequences of no
+ * group share nothing.  The whole pages among these positions that lie before
+ * every new token of the group are read once for all of its tokens, through
+ * the row of one of its sequences, where that is worth it; the result is
+ * w4a16_kv_attention's but for rounding (sums over the shared keys and over
+ * the others are joined in fp32).
  * workspace: w4a16_kv_attention_shared_workspace bytes, as above. */
 int w4a16_kv_attention_shared(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
                               const w4a16_kv_batch_t *batch, int max_q_len, const int32_t *group_starts,

@@ -10,6 +10,24 @@ from kv_reference import Problem, attention, attention_tolerance
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(params=["few", "many"])
+def shared_kernels(request, cuda_lib):
+    """Those that look at the groups."""
+    cuda_lib.w4a16_debug_set_config(10, [1 if request.param == "few" else 2])
+    yield cuda_lib
+    cuda_lib.w4a16_debug_set_config(10, None)
+
+
+@pytest.fixture(params=["few", "many", "chosen"])
+def kernels(request, cuda_lib):
+    """The few-rows kernel alone, the tensor-core kernel where there are rows for it, or whichever the sizes call for
+    (with these small ones w4a16_kv_attention itself)."""
+    if request.param != "chosen":
+        cuda_lib.w4a16_debug_set_config(10, [1 if request.param == "few" else 2])
+    yield cuda_lib
+    cuda_lib.w4a16_debug_set_config(10, None)
+
+
 def grouped(groups, heads=8, kv_heads=2, dim=128, page=16, store="int8", layout="heads", act="bf16", seed=0, loose=()):
     """(problem, group starts, prefix lengths): groups of (prefix, [(past beyond the prefix, new tokens), ...]); `loose`
     sequences (past, new) come after them and are in no group."""
@@ -70,60 +88,60 @@ def check(w, p, starts, prefix, **kw):
 @pytest.mark.parametrize("store, act", [("int8", "bf16"), ("e4m3", "f16"), ("int8", "f16"), ("e4m3", "bf16")])
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("heads, kv_heads", [(4, 4), (8, 2), (14, 2), (8, 1), (40, 2)])
-def test_single_tokens(cuda_lib, store, act, dim, heads, kv_heads):
+def test_single_tokens(kernels, store, act, dim, heads, kv_heads):
     groups = [(100, [(0, 1), (3, 1), (40, 1)]), (16, [(0, 1), (200, 1)]), (333, [(5, 1)] * 4), (64, [(9, 1)])]
-    check(cuda_lib, *grouped(groups, heads, kv_heads, dim, 16, store, "heads", act, seed=heads + dim))
+    check(kernels, *grouped(groups, heads, kv_heads, dim, 16, store, "heads", act, seed=heads + dim))
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 @pytest.mark.parametrize("layout", ["heads", "tokens", "padded", "pairs"])
 @pytest.mark.parametrize("members", [2, 9, 40, 70])
-def test_pages_layouts_and_rows(cuda_lib, page, layout, members):
+def test_pages_layouts_and_rows(kernels, page, layout, members):
     """Rows a group and kv head from 8 to 280: both kernels, one and two halves of the large tile, several tiles."""
     groups = [(300, [(i * 7 % 50, 1) for i in range(members)]), (128, [(3, 1)] * 3)]
-    check(cuda_lib, *grouped(groups, page=page, layout=layout, seed=page + members))
-    check(cuda_lib, *grouped(groups, page=page, layout=layout, store="e4m3", dim=64, act="f16", seed=members))
+    check(kernels, *grouped(groups, page=page, layout=layout, seed=page + members))
+    check(kernels, *grouped(groups, page=page, layout=layout, store="e4m3", dim=64, act="f16", seed=members))
 
 
 @pytest.mark.parametrize("prefix", [0, 1, 15, 16, 17, 127, 128, 129, 255, 256, 1000])
 @pytest.mark.parametrize("members", [3, 40])
-def test_prefix_lengths(cuda_lib, prefix, members):
-    check(cuda_lib, *grouped([(prefix, [(i % 5, 1 + i % 2) for i in range(members)])], seed=prefix))
+def test_prefix_lengths(kernels, prefix, members):
+    check(kernels, *grouped([(prefix, [(i % 5, 1 + i % 2) for i in range(members)])], seed=prefix))
 
 
 @pytest.mark.parametrize("new", [1, 2, 5, 40, 200])
 @pytest.mark.parametrize("page", [16, 64])
-def test_several_tokens(cuda_lib, new, page):
+def test_several_tokens(kernels, new, page):
     """Sequences with many tokens, few and none; the rest of a sequence is causal."""
     groups = [(257, [(0, new), (30, 1), (0, 0), (7, new)]), (90, [(1, 3), (100, new)]), (50, [(2, 0), (3, 0)])]
-    check(cuda_lib, *grouped(groups, page=page, seed=new + page, loose=[(33, new), (0, 2)]))
+    check(kernels, *grouped(groups, page=page, seed=new + page, loose=[(33, new), (0, 2)]))
 
 
-def test_mixed_groups(cuda_lib):
+def test_mixed_groups(kernels):
     """Groups for either kernel and sequences for either kernel in one call."""
     groups = [(200, [(4, 1)] * 60), (500, [(1, 1), (2, 1)]), (77, [(9, 50), (8, 1)])] + [(64, [(3, 1)] * 2)] * 20
-    check(cuda_lib, *grouped(groups, page=32, seed=8, loose=[(400, 90)]))
-    check(cuda_lib, *grouped(groups, page=16, heads=16, kv_heads=2, seed=9, loose=[(5, 1)] * 3))
+    check(kernels, *grouped(groups, page=32, seed=8, loose=[(400, 90)]))
+    check(kernels, *grouped(groups, page=16, heads=16, kv_heads=2, seed=9, loose=[(5, 1)] * 3))
 
 
-def test_no_groups(cuda_lib):
+def test_no_groups(kernels):
     p, _, _ = grouped([], loose=[(100, 1), (0, 1), (40, 60)])
-    check(cuda_lib, p, [0], [])
-    check(cuda_lib, p, [1, 1, 3, 3], [10, 0, 20])                     # nothing in common that is a page
-    check(cuda_lib, p, [3, 3], [50])
+    check(kernels, p, [0], [])
+    check(kernels, p, [1, 1, 3, 3], [10, 0, 20])                     # nothing in common that is a page
+    check(kernels, p, [3, 3], [50])
 
 
 @pytest.mark.parametrize("prefix", [96, 97, 112, 400])
-def test_prefix_past_the_past(cuda_lib, prefix):
+def test_prefix_past_the_past(kernels, prefix):
     """A prefix that reaches into the new tokens counts as far as the shortest past of those that bring any."""
     p, starts, _ = grouped([(96, [(0, 3), (20, 1), (0, 0)])], seed=2)
     p.table[2, :6] = -1                                               # brings nothing: its row is not read
-    check(cuda_lib, p, starts, [prefix])
+    check(kernels, p, starts, [prefix])
 
 
-def test_pages_of_the_first_row_that_brings_tokens(cuda_lib):
+def test_pages_of_the_first_row_that_brings_tokens(shared_kernels):
     """Whatever the others' rows say for the shared part is not looked at."""
-    w = cuda_lib
+    w = shared_kernels
     for members in (4, 50):
         p, starts, prefix = grouped([(130, [(5, 0)] + [(7, 1)] * members)], seed=members)
         want = attention(p)
@@ -137,32 +155,32 @@ def test_pages_of_the_first_row_that_brings_tokens(cuda_lib):
 
 @pytest.mark.parametrize("scale", [0.0, -0.125, 1.5])
 @pytest.mark.parametrize("members", [3, 40])
-def test_scales(cuda_lib, scale, members):
-    check(cuda_lib, *grouped([(150, [(9, 1)] * members)], seed=4), scale=scale)
+def test_scales(kernels, scale, members):
+    check(kernels, *grouped([(150, [(9, 1)] * members)], seed=4), scale=scale)
 
 
 @pytest.mark.parametrize("members, max_new", [(5, 0), (5, 4), (40, 0), (40, 1), (5, 1000)])
-def test_any_longest(cuda_lib, members, max_new):
-    check(cuda_lib, *grouped([(150, [(9, 1 + i % 4) for i in range(members)])], seed=5), max_new=max_new)
+def test_any_longest(kernels, members, max_new):
+    check(kernels, *grouped([(150, [(9, 1 + i % 4) for i in range(members)])], seed=5), max_new=max_new)
 
 
-def test_long_prefix(cuda_lib):
+def test_long_prefix(kernels):
     groups = [(20000, [(3, 1), (700, 1), (20, 2)]), (9000, [(100, 1)] * 33)]
-    check(cuda_lib, *grouped(groups, kv_heads=2, page=64, store="e4m3", layout="tokens", seed=6))
-    check(cuda_lib, *grouped(groups, kv_heads=1, dim=64, page=16, seed=7))
+    check(kernels, *grouped(groups, kv_heads=2, page=64, store="e4m3", layout="tokens", seed=6))
+    check(kernels, *grouped(groups, kv_heads=1, dim=64, page=16, seed=7))
 
 
 @pytest.mark.parametrize("count", [513, 1100])
-def test_many_sequences_and_groups(cuda_lib, count):
+def test_many_sequences_and_groups(kernels, count):
     """More of them than one launch takes."""
     groups = [(33, [(i % 3, 1), (1, 1)]) for i in range(count // 2)]
-    check(cuda_lib, *grouped(groups, heads=2, kv_heads=1, dim=64, seed=9))
-    check(cuda_lib, *grouped([(40, [(i % 3, 1) for i in range(count)])], heads=2, kv_heads=1, dim=64, seed=10))
+    check(kernels, *grouped(groups, heads=2, kv_heads=1, dim=64, seed=9))
+    check(kernels, *grouped([(40, [(i % 3, 1) for i in range(count)])], heads=2, kv_heads=1, dim=64, seed=10))
 
 
-def test_rows_of_no_sequence(cuda_lib):
+def test_rows_of_no_sequence(kernels):
     """Rows before the first start and after the last: zeros and -inf."""
-    w = cuda_lib
+    w = kernels
     p, starts, prefix = grouped([(100, [(2, 1)] * 3), (40, [(1, 2)] * 2)], seed=11)
     cache, table, lens, q_starts, rows = p.to_cuda(w)
     rows = torch.cat([rows.new_full((2, rows.shape[1]), 9.0), rows, rows.new_full((3, rows.shape[1]), 9.0)])
@@ -179,9 +197,9 @@ def test_rows_of_no_sequence(cuda_lib):
 
 @pytest.mark.parametrize("starts, prefix", [([0, 3, 2, 5], [64, 64, 64]), ([-1, 2, 5], [64, 64]), ([0, 2, 6], [64, 64]),
                                              ([0, 2, 5], [64, -1]), ([4, 1, 2**31 - 1], [64, 64]), ([5, 0], [64])])
-def test_groups_that_cannot_be(cuda_lib, starts, prefix):
+def test_groups_that_cannot_be(shared_kernels, starts, prefix):
     """Reported; sequences of groups that are right are right, nothing out of range is read."""
-    w = cuda_lib
+    w = shared_kernels
     p, _, _ = grouped([(64, [(5, 1)] * 5)], seed=12)
     run(w, p, starts, prefix)
     assert w.w4a16_last_device_error() == -9
@@ -189,9 +207,9 @@ def test_groups_that_cannot_be(cuda_lib, starts, prefix):
     check(w, p, [0, 5], [64])
 
 
-def test_bad_pages(cuda_lib):
+def test_bad_pages(kernels):
     """A page id out of range among the shared ones: its keys are left out for all of the group, and it is reported."""
-    w = cuda_lib
+    w = kernels
     for members in (3, 45):
         p, starts, prefix = grouped([(96, [(5, 1)] * members)], seed=13)
         p.table[0, 2], p.table[1:, 2] = p.n_pages, -1
@@ -211,9 +229,9 @@ def test_bad_pages(cuda_lib):
                 assert bool(((out[b, a].cpu().double() - want).abs() <= attention_tolerance(p, want, spread)).all())
 
 
-def test_blocks_that_are_not_finite(cuda_lib):
+def test_blocks_that_are_not_finite(kernels):
     """Seen by the group: NaN for the group, nothing for the others."""
-    w = cuda_lib
+    w = kernels
     p, starts, prefix = grouped([(64, [(5, 1)] * 3), (64, [(5, 1)] * 40)], seed=14)
     p.vs[p.table[0, 1].long()] = math.inf
     p.v.view(torch.int8)[p.table[0, 1].long()] = 0
@@ -222,9 +240,9 @@ def test_blocks_that_are_not_finite(cuda_lib):
 
 
 @pytest.mark.parametrize("members", [4, 40])
-def test_captured(cuda_lib, members):
+def test_captured(kernels, members):
     """One captured call, replayed with other lengths, groups and prefixes."""
-    w = cuda_lib
+    w = kernels
     p, starts, prefix = grouped([(200, [(9, 1)] * members), (200, [(3, 1)] * members)], seed=15)
     cache, table, lens, q_starts, rows = p.to_cuda(w)
     q = rows[:, :p.heads * p.dim].unflatten(1, (p.heads, p.dim))
@@ -254,9 +272,9 @@ def test_captured(cuda_lib, members):
     assert w.w4a16_last_device_error() == 0
 
 
-def test_other_stream_and_workspace(cuda_lib):
+def test_other_stream_and_workspace(kernels):
     """A workspace of its own, used by one call after the other, with other sizes and with the plain attention."""
-    w = cuda_lib
+    w = kernels
     ws = torch.full((160 << 20,), 0xff, dtype=torch.uint8, device="cuda")
     for i, members in enumerate((3, 40, 5, 70)):
         p, starts, prefix = grouped([(300, [(9, 1 + i)] * members)], seed=16 + i)
@@ -274,8 +292,8 @@ def test_other_stream_and_workspace(cuda_lib):
 
 @pytest.mark.parametrize("groups", [[(9000, [(5, 1)] * 3)], [(3000, [(500, 1)] * 50)], [(400, [(0, 300)] * 2)]])
 @pytest.mark.parametrize("hold", [1, 2])
-def test_waits_run_out_and_the_next_call_is_right(cuda_lib, groups, hold):
-    w = cuda_lib
+def test_waits_run_out_and_the_next_call_is_right(kernels, groups, hold):
+    w = kernels
     p, starts, prefix = grouped(groups, seed=17)
     w.w4a16_clear_device_error()
     w.w4a16_debug_set_config(7, [hold])

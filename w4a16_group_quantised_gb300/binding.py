@@ -461,8 +461,9 @@ def w4a16_debug_set_config(which: int, vals=None) -> None:
     which=3 programmatic dependent launch {flag}; which=4 balanced decode
     kernel {on, ring depth}; which=7 timeout-path test {on} (decode kernels
     issue no weight copies, so their bounded waits run out); which=8 prefill
-    row split (fused and dense forms) at {n_split} (a multiple of 256).  vals=None
-    restores the built-in choice."""
+    row split (fused and dense forms) at {n_split} (a multiple of 256); which=10
+    kernels of w4a16_kv_attention_shared {1 few rows, 2 tensor cores where there are
+    more than 32 rows}.  vals=None restores the built-in choice."""
     lib = load_library()
     if vals is None:
         rc = lib.w4a16_debug_set_config(which, None, 0)

@@ -84,6 +84,7 @@ void log_selection(const char *line) {
 int g_sk_on = 0, g_sk_ns = 4;
 // test hook (w4a16_debug_set_config(7)): decode kernels issue no weight copies
 int g_hold_copies = 0;
+int g_shared_kernels = 0;
 // Streams whose last library launch wrote weights (w4a16_pack,
 // w4a16_pack_zeros): the next GEMM on such a stream is launched without
 // programmatic dependent launch, because the GEMM kernels read weights
@@ -484,6 +485,11 @@ int hold_copies() {
     return g_hold_copies;
 }
 
+int shared_kernels() {
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    return g_shared_kernels;
+}
+
 int device_info(const DeviceInfo **out) { return get_device(out); }
 
 bool kernel_log_on() {
@@ -827,6 +833,12 @@ int w4a16_debug_set_config(int which, const int *vals, int n) {
         if (n == 0) { g_prefill_split = 0; return W4A16_OK; }
         if (n != 1 || vals == nullptr || vals[0] <= 0 || vals[0] % 256 != 0) return W4A16_ERR_ARG;
         g_prefill_split = vals[0];
+        return W4A16_OK;
+    }
+    if (which == 10) {
+        if (n == 0) { g_shared_kernels = 0; return W4A16_OK; }
+        if (n != 1 || vals == nullptr || vals[0] < 1 || vals[0] > 2) return W4A16_ERR_ARG;
+        g_shared_kernels = vals[0];
         return W4A16_OK;
     }
     if (which == 7) {

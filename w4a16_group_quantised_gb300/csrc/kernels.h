@@ -108,29 +108,34 @@ struct KvAttentionArgs {
     int dtype;                            // 0 fp16, 1 bf16
     void *workspace;
 };
-// Attention of a batch whose sequences share pages (kv_attention_shared.cu): a
-// pass over the shared keys, an entry for each group, and one over the rest,
-// an entry for each sequence.  What a pass finds for a row (a token and query
-// head) is sums that are not yet divided, relative to 2^m with denominator l:
-// in its arrays, or as the parts of a tile that several CTAs share.
+// Attention of a batch whose sequences share pages (kv_attention_shared.cu).
+// An entry is a group's shared keys with the rows of all its tokens, or what is
+// left of a sequence.  What a kernel finds for a row (a token and query head) of
+// either kind is sums that are not yet divided, relative to 2^m with
+// denominator l: in arrays, or as the parts of a tile that several CTAs share.
 struct KvEntry {
     int q0, n;                            // rows of the token tensors
-    int len, pad;                         // keys, from position 0 of the first page on
+    int len;                              // keys, from position 0 of the first page on
+    int flags;                            // kKvOthers, kKvAlone, kKvBig
     long long pages;                      // where its page ids begin in the block table
-    long long pad2;
+    long long pad;
 };
+constexpr int kKvOthers = 1;              // a sequence: row t sees keys up to len - n + t; else every row sees all
+constexpr int kKvAlone = 2;               // a sequence that shares nothing: what is found is the result
+constexpr int kKvBig = 4;                 // kv_attention_tc.cu's, if that kernel is to run at all
 struct KvShare {
     const KvEntry *entries;
-    int step;                             // 0: the shared keys, which every row sees; 1: the others, row t up to len - n + t
+    const int *use_many;                  // whether kKvBig entries are kv_attention_tc.cu's
     int defer;                            // parts are left where they are; else the last CTA to come sums them
-    float *out;                           // [n_tokens, n_heads, head_dim] sums
-    float *ml;                            // [n_tokens, n_heads, 2] m and l
-    unsigned long long *where;            // [n_tokens, n_heads]: kv_where, 0 where the pass has nothing
+    // of shared keys, of others:
+    float *out[2];                        // [n_tokens, n_heads, head_dim] sums
+    float *ml[2];                         // [n_tokens, n_heads, 2] m and l
+    unsigned long long *where[2];         // [n_tokens, n_heads]: kv_where, 0 where there is nothing
 };
-enum { kKvNone = 0, kKvInArrays = 1, kKvFewParts = 2, kKvManyParts = 3 };
+enum { kKvNone = 0, kKvInArrays = 1, kKvFewParts = 2, kKvManyParts = 3, kKvDone = 4 };
 // Parts of row `row` of a tile, in slot 1 of CTA `from` and slot 0 of the CTAs after it up to `to`.
 __host__ __device__ inline unsigned long long kv_where(int kind, int row, int from, int to) {
-    return (unsigned long long)kind | (unsigned long long)row << 2 | (unsigned long long)from << 16 |
+    return (unsigned long long)kind | (unsigned long long)row << 3 | (unsigned long long)from << 16 |
            (unsigned long long)to << 32;
 }
 cudaError_t launch_kv_append(const KvCache &c, const KvBatch &b, const void *k_new, long long k_stride,
@@ -143,7 +148,7 @@ cudaError_t launch_kv_attention(const KvAttentionArgs &a, const KvCache &c, cons
 // sequences with more than row_limit rows (tokens * query heads of a kv head), in kv_attention_tc.cu; share: or null
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, int row_limit,
                                      const DeviceInfo &dev, cudaStream_t s, bool pdl, const KvShare *share = nullptr);
-int kv_attention_many_launches(const KvBatch &b, int group);   // kernels that a call of it runs
+bool kv_attention_many_at_once(const KvBatch &b, int group);   // whether one launch takes all entries of such a batch
 constexpr int kManyTileRows = 256;        // of a tile of kv_attention_tc.cu, and of its parts
 int kv_few_rows_most(const KvCache &c);   // rows up to which kv_few_rows.cuh's kernel is the faster one
 // sequences [group_starts[g], group_starts[g + 1]) have their first prefix_lens[g] positions in the same pages
@@ -200,6 +205,7 @@ long long beam_select_workspace(int n_groups, int width, int vocab, int n_out);
 int device_info(const DeviceInfo **out);
 bool pdl_enabled();
 int hold_copies();                        // test hook: see w4a16_debug_set_config(7)
+int shared_kernels();                     // w4a16_debug_set_config(10): 0 chosen, 1 few rows, 2 many rows where there are
 bool kernel_log_on();
 void log_kernel_selection(const char *line);
 

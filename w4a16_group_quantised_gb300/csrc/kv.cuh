@@ -36,12 +36,6 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvBatch &b, int page_shift, i
     return s;
 }
 
-// The same of an entry, which the kernel that wrote it has checked.
-__device__ __forceinline__ KvSeq kv_entry(const KvShare &sh, int i) {
-    const KvEntry e = sh.entries[i];
-    return KvSeq{e.q0, e.n, e.len};
-}
-
 // The page of position block `blk` (below the table's width) of sequence i, or -1 (reported).
 __device__ __forceinline__ int kv_page(const KvCache &c, const KvBatch &b, int i, int blk, int *status) {
     const int p = b.block_table[(long long)i * b.max_blocks + blk];
@@ -75,17 +69,29 @@ __device__ __forceinline__ uint16_t kv_to_act(float v) {
     return DT == 0 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// `count` dims from d0 on of a row's sums, to the pass's arrays.
+// `count` dims from d0 on of a row's sums, found for an entry with these flags.
 template <int D>
-__device__ __forceinline__ void kv_store_sums(const KvShare &sh, long long at, int d0, const float *v, int count, float l,
-                                              float m) {
-    float4 *dst = reinterpret_cast<float4 *>(sh.out + at * D + d0);
+__device__ __forceinline__ void kv_store_sums(const KvAttentionArgs &a, const KvShare &sh, int flags, long long at, int d0,
+                                              const float *v, int count, float l, float m) {
+    const int others = flags & kKvOthers;
+    if (flags & kKvAlone) {
+        const float r = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t *dst = static_cast<uint16_t *>(a.out) + at * D + d0;
 #pragma unroll
-    for (int i = 0; i < count; i += 4) dst[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-    if (d0 == 0) {
-        reinterpret_cast<float2 *>(sh.ml)[at] = make_float2(m, l);
-        sh.where[at] = kv_where(kKvInArrays, 0, 0, 0);
+        for (int i = 0; i < count; i += 4) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = a.dtype == 0 ? kv_to_act<0>(v[i + k] * r) : kv_to_act<1>(v[i + k] * r);
+            *reinterpret_cast<uint2 *>(dst + i) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+        }
+        if (a.lse && d0 == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    } else {
+        float4 *dst = reinterpret_cast<float4 *>(sh.out[others] + at * D + d0);
+#pragma unroll
+        for (int i = 0; i < count; i += 4) dst[i / 4] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        if (d0 == 0) reinterpret_cast<float2 *>(sh.ml[others])[at] = make_float2(m, l);
     }
+    if (d0 == 0) sh.where[others][at] = flags & kKvAlone ? kKvDone : kKvInArrays;
 }
 
 // ---- codes

@@ -211,7 +211,6 @@ int w4a16_kv_attention_shared(const void *q, long long q_stride, int n_heads, co
         kv_attention_shared_workspace(n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, n_groups, b.n_tokens, *dev))
         return W4A16_ERR_ARG;
     const KvAttentionArgs a{q, q_stride, n_heads, max_q_len, 0, 0, scale, out, lse_or_null, (int)dtype, workspace};
-    if (n_groups == 0) return done(launch_kv_attention(a, c, b, *dev, str(stream), pdl_enabled()));
     return done(launch_kv_attention_shared(a, c, b, KvGroups{group_starts, prefix_lens, n_groups}, *dev, str(stream),
                                            pdl_enabled()));
 }

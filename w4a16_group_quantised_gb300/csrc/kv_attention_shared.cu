@@ -7,18 +7,17 @@
 //     out = (2^(m_1 - m) o_1 + 2^(m_2 - m) o_2) / (2^(m_1 - m) l_1 + 2^(m_2 - m) l_2).
 // So the keys that a group's sequences have in common are read once, for the
 // tokens of all of them as the rows of one problem, and joined with every row's
-// sum over its own keys at the end.  Four kernels:
-//  * the plan: what a group shares (whole pages that lie before all of its new
+// sum over its own keys at the end.
+//  * The plan: what a group shares (whole pages that lie before all of its new
 //    tokens), as an entry of rows, keys and a place in the block table for
-//    each group and for the rest of each sequence;
-//  * the shared keys, all rows of a group seeing all of them;
-//  * the others;
-//  * the join, a warp or half of one a row.
-// The middle two are the kernels of kv_few_rows.cuh and kv_attention_tc.cu with
-// entries in place of sequences; which of them follows from the rows.  A group's
-// tile is long, and there are few of them, so that each is cut over many CTAs:
-// the parts that these leave are read by the join, by all SMs, where in
-// kv_attention the last CTA to come sums them alone.
+//    each group and for the rest of each sequence.
+//  * The kernels of kv_few_rows.cuh and, where it may pay, kv_attention_tc.cu,
+//    with entries in place of sequences: shared keys, which every row of a
+//    group sees, and the others at once.
+//  * The join, a warp or half of one a row.  A group's tile is long and there are
+//    few of them, so that each is cut over many CTAs: the parts that these
+//    leave are read here, by all SMs, where in kv_attention the last CTA to come
+//    sums them alone.
 #include <algorithm>
 #include <cstdio>
 
@@ -28,14 +27,34 @@ namespace w4a16 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kLeastShared = 64;          // positions that are worth an entry
+constexpr int kBigRows = 32;              // more rows a kv head may be kv_attention_tc.cu's
+
+// What an entry takes, in ns of the whole GPU at 152 SMs: kv_few_rows.cuh 16 keys of a tile of 8 or 16 rows, kv_attention_tc.cu
+// 128 keys of a tile of 256.  What that kernel takes more than the other to start and end: 25 us.  Measured, the one /
+// the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to 56,
+// over 20000 56 to 77 / 87 to 91; 16 groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126 at
+// 32, 163 / 130 at 40, 200 / 136 at 64.
+constexpr int kFewQuarterNs8 = 3, kFewQuarterNs16 = 4;
+constexpr int kManyNs = 16;
+constexpr long long kManyStartNs = 25000;
+__host__ __device__ inline long long few_cost(long long rows, int tile_rows, long long keys, int kv_heads) {
+    return (rows + tile_rows - 1) / tile_rows * ((keys + 15) / 16) * kv_heads *
+           (tile_rows == 16 ? kFewQuarterNs16 : kFewQuarterNs8) / 4;
+}
+__host__ __device__ inline long long many_cost(long long rows, long long keys, int kv_heads) {
+    return (rows + kManyTileRows - 1) / kManyTileRows * ((keys + 127) / 128) * kv_heads * kManyNs;
+}
 
 struct PlanParams {
     KvBatch b;
     KvGroups g;
-    int page_shift;
-    KvEntry *groups, *seqs;
+    int page_shift, kv_heads, group, tile_rows;
+    KvEntry *entries;                     // of groups, then of sequences
     int *shared;                          // positions that each group shares
-    uint4 *where;                         // of both passes, to be cleared
+    int *use_many;
+    long long many_start;                 // what the tensor-core kernel takes more to start and end
+    uint4 *where;                         // of both kinds, to be cleared
     long long where_vecs;
     int *status;
 };
@@ -49,6 +68,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
             p.where[i] = make_uint4(0, 0, 0, 0);
         return;
     }
+    __shared__ unsigned long long s_few, s_many;          // what the big entries take
+    if (threadIdx.x == 0) s_few = s_many = 0;
+    __syncthreads();
+    auto big = [&](int n, int keys) {
+        const long long rows = (long long)n * p.group;
+        if (rows <= kBigRows || keys <= 0) return 0;
+        atomicAdd(&s_few, (unsigned long long)few_cost(rows, p.tile_rows, keys, p.kv_heads));
+        atomicAdd(&s_many, (unsigned long long)many_cost(rows, keys, p.kv_heads));
+        return kKvBig;
+    };
     const int lane = threadIdx.x & 31, n_seqs = p.b.n_seqs, n_groups = p.g.n_groups;
     for (int g = threadIdx.x >> 5; g < n_groups; g += kPlanThreads / 32) {
         const int s0 = p.g.group_starts[g], s1 = p.g.group_starts[g + 1], said = p.g.prefix_lens[g];
@@ -68,10 +97,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
         first = __reduce_min_sync(0xffffffffu, first);
         q0 = __reduce_min_sync(0xffffffffu, q0), q1 = __reduce_max_sync(0xffffffffu, q1);
         past = __reduce_min_sync(0xffffffffu, past);
-        const int n = count > 1 ? min(max(said, 0), past) >> p.page_shift << p.page_shift : 0;
+        int n = count > 1 ? min(max(said, 0), past) >> p.page_shift << p.page_shift : 0;
+        if (n < kLeastShared) n = 0;
         if (lane == 0) {
             p.shared[g] = n;
-            p.groups[g] = n > 0 ? KvEntry{q0, q1 - q0, n, 0, (long long)first * p.b.max_blocks, 0} : KvEntry{};
+            p.entries[g] = n > 0 ? KvEntry{q0, q1 - q0, n, big(q1 - q0, n), (long long)first * p.b.max_blocks, 0} : KvEntry{};
         }
     }
     __syncthreads();
@@ -88,24 +118,23 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
         // starts that fall may find a sequence in a group that it was not counted with: never more than its past
         const int past = max(s.len - s.n, 0) >> p.page_shift << p.page_shift;
         const int skip = member && s.n > 0 ? min(p.shared[lo - 1], past) : 0;
-        p.seqs[i] = KvEntry{s.q0, s.n, s.len - skip, 0, (long long)i * p.b.max_blocks + (skip >> p.page_shift), 0};
+        const int flags = kKvOthers | (skip == 0 ? kKvAlone : 0) | big(s.n, s.len - skip);
+        p.entries[n_groups + i] =
+            KvEntry{s.q0, s.n, s.len - skip, flags, (long long)i * p.b.max_blocks + (skip >> p.page_shift), 0};
     }
+    __syncthreads();
+    if (threadIdx.x == 0) *p.use_many = (long long)s_few > (long long)s_many + p.many_start;
 }
 
-// What the join reads of a pass.
-struct PassSums {
-    const unsigned long long *where;
-    const float *out, *ml;
-    const float *few, *many;              // parts
-    int few_rows;                         // of a tile of kv_few_rows.cuh
-};
 struct JoinParams {
     KvAttentionArgs a;
-    PassSums pass[2];
+    KvShare share;
+    const float *few, *many;              // parts
+    int few_rows;                         // of a tile of kv_few_rows.cuh
     int rows;
 };
 
-// A row's sums of both passes, D / 4 lanes a row, four dims each.
+// A row's sums of both kinds, D / 4 lanes a row, four dims each.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     kv_begin();
@@ -123,21 +152,22 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
     };
     unsigned long long where[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) where[i] = p.pass[i].where[row];
+    for (int i = 0; i < 2; ++i) where[i] = p.share.where[i][row];
+    if ((where[1] & 7) == kKvDone) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const PassSums &s = p.pass[i];
-        const int kind = (int)(where[i] & 3), r = (int)(where[i] >> 2 & 511);
+        const int kind = (int)(where[i] & 7), r = (int)(where[i] >> 3 & 511);
         const int from = (int)(where[i] >> 16 & 0xffff), to = (int)(where[i] >> 32 & 0xffff);
         if (kind == kKvNone) continue;
         if (kind == kKvInArrays) {
-            add(reinterpret_cast<const float2 *>(s.ml)[row], *reinterpret_cast<const float4 *>(s.out + row * D + d));
+            add(reinterpret_cast<const float2 *>(p.share.ml[i])[row],
+                *reinterpret_cast<const float4 *>(p.share.out[i] + row * D + d));
             continue;
         }
         const bool few = kind == kKvFewParts;
-        const int tile = few ? s.few_rows : kManyTileRows, part = tile * (D + 2);
+        const int tile = few ? p.few_rows : kManyTileRows, part = tile * (D + 2);
         // where a part has the row's four dims, and its (m, l)
-        const float *base = few ? s.few : s.many;
+        const float *base = few ? p.few : p.many;
         const int at = few ? r * D + d : d * tile + 4 * r, ml_at = tile * D + 2 * r;
         constexpr int N = 8;                               // parts whose loads are on their way together
         for (int c = from; c <= to; c += N) {
@@ -164,9 +194,9 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 }
 
 struct Scratch {
-    void *few[2], *many[2];               // of the passes' kernels: tickets, parts
-    KvEntry *groups, *seqs;
-    int *shared;
+    void *few, *many;                     // of the two kernels: tickets, parts
+    KvEntry *entries;
+    int *shared, *use_many;
     unsigned long long *where[2];
     float *ml[2], *out[2];
     long long bytes;
@@ -184,15 +214,14 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     };
     Scratch s;
     const long long rows = (long long)n_tokens * n_heads;
-    const bool many = (long long)n_tokens * (n_heads / n_kv_heads) > kTileRows;
-    s.groups = reinterpret_cast<KvEntry *>(take((long long)n_groups * sizeof(KvEntry)));
-    s.seqs = reinterpret_cast<KvEntry *>(take((long long)n_seqs * sizeof(KvEntry)));
+    s.entries = reinterpret_cast<KvEntry *>(take(((long long)n_groups + n_seqs) * sizeof(KvEntry)));
     s.shared = reinterpret_cast<int *>(take((long long)n_groups * 4));
-    s.where[0] = reinterpret_cast<unsigned long long *>(take(2 * ((rows * 8 + 15) & ~15LL)));
-    s.where[1] = s.where[0] + ((rows + 1) & ~1LL);
+    s.use_many = reinterpret_cast<int *>(take(4));
+    s.where[0] = reinterpret_cast<unsigned long long *>(take((rows + 1) / 2 * 32));
+    s.where[1] = s.where[0] + (rows + 1) / 2 * 2;
+    s.few = take(tickets_bytes(dev) + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4);
+    s.many = (long long)n_tokens * (n_heads / n_kv_heads) > kBigRows ? take(kv_attention_many_workspace(head_dim, dev)) : nullptr;
     for (int i = 0; i < 2; ++i) {
-        s.few[i] = take(tickets_bytes(dev) + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4);
-        s.many[i] = many ? take(kv_attention_many_workspace(head_dim, dev)) : nullptr;
         s.ml[i] = reinterpret_cast<float *>(take(rows * 8));
         s.out[i] = reinterpret_cast<float *>(take(rows * head_dim * 4));
     }
@@ -200,59 +229,57 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     return s;
 }
 
+// Bytes of cache up to which kv_attention is called instead, should all sequences be as long as the table is wide: up to
+// there its one launch is the faster one.
+constexpr long long kLeastBytes = 32LL << 20;
+
 }  // namespace
 
 cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &c, const KvBatch &b, const KvGroups &g,
                                        const DeviceInfo &dev, cudaStream_t s, bool pdl) {
-    const Scratch w = scratch_of(a.workspace, a.n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, g.n_groups, b.n_tokens, dev);
-    const int group = a.n_heads / c.n_kv_heads, most = kv_few_rows_most(c), rows = b.n_tokens * a.n_heads;
-    const long long vecs = ((long long)rows + 1) / 2 * 2;
-    const PlanParams plan{b, g, c.page_shift, w.groups, w.seqs, w.shared, reinterpret_cast<uint4 *>(w.where[0]), vecs,
-                          dev.status};
-    const int fill = (int)std::min<long long>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
-    cudaError_t e = kv_launch(plan_shared_kernel, dim3(1 + fill), dim3(kPlanThreads), 0, s, pdl, plan);
-    if (e != cudaSuccess) return e;
-    // Shared keys: by the tokens that a group has in the mean when that decides, else each kernel those it is for.
-    const long long all = (long long)b.n_tokens * group;
-    const bool many_shared = all > most, all_many_shared = many_shared && all > (long long)most * g.n_groups;
-    // The others as in kv_attention.cu.
-    const bool many = (long long)a.max_q_len * group > most;
-    const bool all_many = many && (long long)a.max_q_len * b.n_seqs == b.n_tokens;
+    const int group = a.n_heads / c.n_kv_heads, rows = b.n_tokens * a.n_heads;
+    const long long longest = (long long)b.max_blocks << c.page_shift;
+    const int forced = shared_kernels();
+    const bool plain = forced ? g.n_groups == 0 : g.n_groups == 0 || longest * b.n_seqs * c.n_kv_heads * c.head_dim * 2 <= kLeastBytes;
+    // the tensor-core kernel is launched where the plan might ask for it
+    const int tile_rows = few_tile_rows(a.max_q_len, group);
+    const long long all = (long long)b.n_tokens * group, entries = (long long)g.n_groups + b.n_seqs;
+    const long long many_start = forced == 2 ? -(1LL << 60) : kManyStartNs;
+    const bool may_many = all > kBigRows && forced != 1 && few_cost(2 * (all + entries * tile_rows), tile_rows, longest, c.n_kv_heads) > many_start;
     if (kernel_log_on()) {
         char line[256];
         std::snprintf(line, sizeof line,
-                      "kv_attention_shared tokens=%d seqs=%d groups=%d longest=%d heads=%d/%d D=%d page=%d %s %s shared=%s "
-                      "others=%s rows<=%d grid=%d pdl=%d",
+                      "kv_attention_shared tokens=%d seqs=%d groups=%d longest=%d heads=%d/%d D=%d page=%d %s %s kernel=%s "
+                      "rows=%d grid=%d pdl=%d",
                       b.n_tokens, b.n_seqs, g.n_groups, a.max_q_len, a.n_heads, c.n_kv_heads, c.head_dim, 1 << c.page_shift,
                       c.kv_dtype == kKvInt8 ? "int8" : "e4m3", a.dtype == 0 ? "fp16" : "bf16",
-                      all_many_shared ? "many_rows" : many_shared ? "few_rows+many_rows" : "few_rows",
-                      all_many ? "many_rows" : many ? "few_rows+many_rows" : "few_rows", most, dev.sm_count, pdl ? 1 : 0);
+                      plain ? "kv_attention" : may_many ? "few_rows+many_rows" : "few_rows", tile_rows, dev.sm_count, pdl ? 1 : 0);
         log_kernel_selection(line);
     }
-    JoinParams join{a, {}, rows};
-    for (int i = 0; i < 2; ++i) {
-        KvBatch batch = b;
-        batch.n_seqs = i ? b.n_seqs : g.n_groups;
-        KvAttentionArgs args = a;
-        if (i == 0) args.max_q_len = b.n_tokens;           // picks tiles of 8 or 16 rows
-        const bool some_many = i ? many : many_shared, only_many = i ? all_many : all_many_shared;
-        KvShare share{i ? w.seqs : w.groups, i, 0, w.out[i], w.ml[i], w.where[i]};
-        if (!only_many) {
-            args.workspace = w.few[i];
-            share.defer = batch.n_seqs <= kMaxSeqs;        // one launch: its parts stay until the join
-            e = launch_few_rows<true>(args, c, batch, some_many ? most : 0, share, dev, s, pdl);
-            if (e != cudaSuccess) return e;
-        }
-        if (some_many) {
-            args.workspace = w.many[i];
-            share.defer = kv_attention_many_launches(batch, group) == 1;
-            e = launch_kv_attention_many(args, c, batch, only_many ? 0 : most, dev, s, pdl, &share);
-            if (e != cudaSuccess) return e;
-        }
-        auto parts = [&](void *ws) { return reinterpret_cast<const float *>(static_cast<char *>(ws) + tickets_bytes(dev)); };
-        join.pass[i] = PassSums{w.where[i], w.out[i], w.ml[i], parts(w.few[i]), w.many[i] ? parts(w.many[i]) : nullptr,
-                                few_tile_rows(args.max_q_len, group)};
+    if (plain) return launch_kv_attention(a, c, b, dev, s, pdl);
+    const Scratch w = scratch_of(a.workspace, a.n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, g.n_groups, b.n_tokens, dev);
+    const long long vecs = ((long long)rows + 1) / 2 * 2;
+    const PlanParams plan{b, g, c.page_shift, c.n_kv_heads, group, tile_rows, w.entries, w.shared, w.use_many, forced == 1 ? 1LL << 60 : many_start,
+                          reinterpret_cast<uint4 *>(w.where[0]), vecs, dev.status};
+    const int fill = (int)std::min<long long>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
+    cudaError_t e = kv_launch(plan_shared_kernel, dim3(1 + fill), dim3(kPlanThreads), 0, s, pdl, plan);
+    if (e != cudaSuccess) return e;
+    KvBatch batch = b;
+    batch.n_seqs = (int)entries;
+    KvAttentionArgs args = a;
+    KvShare share{w.entries, w.use_many, 0, {w.out[0], w.out[1]}, {w.ml[0], w.ml[1]}, {w.where[0], w.where[1]}};
+    args.workspace = w.few;
+    share.defer = entries <= kMaxSeqs;                     // one launch: its parts stay until the join
+    e = launch_few_rows<true>(args, c, batch, 0, share, dev, s, pdl);
+    if (e != cudaSuccess) return e;
+    if (may_many) {
+        args.workspace = w.many;
+        share.defer = kv_attention_many_at_once(batch, group);
+        e = launch_kv_attention_many(args, c, batch, 0, dev, s, pdl, &share);
+        if (e != cudaSuccess) return e;
     }
+    auto parts = [&](void *ws) { return reinterpret_cast<const float *>(static_cast<char *>(ws) + tickets_bytes(dev)); };
+    const JoinParams join{a, share, parts(w.few), may_many ? parts(w.many) : nullptr, tile_rows, rows};
     const dim3 grid((unsigned)(((long long)rows * (c.head_dim / 4) + 255) / 256));
     return c.head_dim == 128 ? kv_launch(join_kernel<128>, grid, dim3(256), 0, s, pdl, join)
                              : kv_launch(join_kernel<64>, grid, dim3(256), 0, s, pdl, join);
@@ -260,7 +287,9 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
 
 long long kv_attention_shared_workspace(int n_heads, int n_kv_heads, int head_dim, int n_seqs, int n_groups,
                                         int n_tokens, const DeviceInfo &dev) {
-    return scratch_of(nullptr, n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens, dev).bytes;
+    // what kv_attention needs where that is called
+    return std::max(scratch_of(nullptr, n_heads, n_kv_heads, head_dim, n_seqs, n_groups, n_tokens, dev).bytes,
+                    kv_attention_workspace(n_heads, n_kv_heads, head_dim, n_seqs, n_tokens, dev));
 }
 
 }  // namespace w4a16

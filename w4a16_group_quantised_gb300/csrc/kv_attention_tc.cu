@@ -57,6 +57,7 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = kManyTileRows, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
+constexpr int kFlagShift = 26;            // SHARED: an entry's flags above its first row, 2^24 at most
 constexpr int kMaxPairs = 1216;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
 constexpr int kCost = 3;                  // steps that a tile's start and end count for in the shares
@@ -90,6 +91,7 @@ struct ManyTile {
     int lo, hi;                           // its rows see positions below `sinks` and lo..hi
     long long begin;                      // on the line
     long long pages;                      // where its page ids begin in the block table (SHARED)
+    int flags;                            // of the entry (SHARED)
 };
 
 // A tile with this CTA's steps [s0, s1) of it; s1 == 0 ends the list.
@@ -426,15 +428,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     grid_dependency_wait();
 
-    // the position of a tile's tok-th token
-    auto position = [&](int first, int tok) { return SHARED ? first + tok * p.share.step : first + tok; };
+    // the position tok tokens after `first`: all the same where every row sees all keys
+    auto position = [](int flags, int first, int tok) { return flags & kKvOthers ? first + tok : first; };
     auto tile_of = [&](const int4 s, int b, int r) {
         ManyTile t;
         t.seq = b;
-        t.q0 = s.x, t.n = s.y, t.len = s.z, t.first = SHARED && p.share.step == 0 ? s.z - 1 : s.z - s.y;
+        t.flags = SHARED ? s.x >> kFlagShift : kKvOthers;
+        t.q0 = SHARED ? s.x & (1 << kFlagShift) - 1 : s.x, t.n = s.y, t.len = s.z;
+        t.first = t.flags & kKvOthers ? s.z - s.y : s.z - 1;
         t.row0 = r * 2 * half_rows;
         t.rows = min(2 * half_rows, s.y * group - t.row0);
-        const int lo_pos = position(t.first, t.row0 / group), hi_pos = position(t.first, (t.row0 + t.rows - 1) / group);
+        const int lo_pos = position(t.flags, t.first, t.row0 / group);
+        const int hi_pos = position(t.flags, t.first, (t.row0 + t.rows - 1) / group);
         const int lo = p.a.window > 0 ? max(0, lo_pos + 1 - p.a.window) : 0;
         t.lo = lo, t.hi = hi_pos;
         t.block0 = lo / kKeys;
@@ -472,10 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int4 s = make_int4(0, 0, 0, 0);
         int mine = 0;
         if (i < B) {
-            const KvSeq q = SHARED ? kv_entry(p.share, i) : kv_sequence(p.b, p.c.page_shift, i, p.status);
+            KvSeq q;
+            int flags = 0;                                         // above the bits of a row
+            if constexpr (SHARED) {
+                const KvEntry e = p.share.entries[i];
+                q = KvSeq{e.q0, (e.flags & kKvBig) && *p.share.use_many ? e.n : 0, e.len};
+                flags = e.flags << kFlagShift;
+            } else {
+                q = kv_sequence(p.b, p.c.page_shift, i, p.status);
+            }
             const int rows = q.n * group;
             mine = rows <= p.row_limit ? 0 : (rows + 2 * half_rows - 1) / (2 * half_rows);
-            s = make_int4(q.q0, q.n, q.len, 0);
+            s = make_int4(q.q0 | flags, q.n, q.len, 0);
         }
         long long all;
         s.w = (int)scan(mine, all) + pairs - p.pair_first;         // within this launch's range
@@ -543,7 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Parts cost a CTA about 8 steps, and an eighth of its time: prompts of 300 / 1920 / 8192 tokens dealt whole
         // take 18 / 50 / 549 us, in shares 23 / 68 / 578; five tokens each over 24 contexts, where a whole tile is
         // most of a CTA's share, take 76 us dealt and 51 in shares.
-        deal = most <= total / grid + 8 + total / grid / 8;
+        // Left for the join parts cost 2 or so: 16 groups of 100 to 1920 shared keys 97 us at 8 steps, 94 at 2.
+        deal = SHARED && p.share.defer ? most <= total / grid + 2 + total / grid / 16 : most <= total / grid + 8 + total / grid / 8;
     }
 
     auto tile_at = [&](int pair, int head) {
@@ -668,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = s0 == 0 && s1 == t.steps, opens = s0 == 0;
             const bool exists = r < half_rows && base_row + r < t.rows;
             const int tok0 = (t.row0 + base_row) / group;          // the half's first token
-            const int min_pos = position(t.first, tok0), pos = exists ? position(min_pos, r_tok) : -1;
-            const int max_pos = position(t.first, (t.row0 + min(base_row + half_rows, t.rows) - 1) / group);
+            const int flags = SHARED ? t.flags : kKvOthers;
+            const int min_pos = position(flags, t.first, tok0), pos = exists ? position(flags, min_pos, r_tok) : -1;
+            const int max_pos = position(flags, t.first, (t.row0 + min(base_row + half_rows, t.rows) - 1) / group);
             float ref = kRefStart, sum = 0.0f;
             const int first_st = twice ? s0 + half : s0;
             for (int st = first_st; st < s1 && runs; st += twice ? 2 : 1) {
@@ -843,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float f[32];
                     read_out(c, f);
                     if (has) {
-                        if constexpr (SHARED) kv_store_sums<D>(p.share, at, c, f, 32, sum, ref);
+                        if constexpr (SHARED) kv_store_sums<D>(p.a, p.share, t.flags, at, c, f, 32, sum, ref);
                         else store(at, c, f, inv);
                     }
                 }
@@ -878,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (has) __stcg(reinterpret_cast<float2 *>(mine + kTileRows * D) + row, make_float2(ref, sum));
                 const int from = first_cta(t, ctas, total), to = last_cta(t, ctas, total);
                 if (SHARED && p.share.defer) {                     // whoever reads the rows sums the parts
-                    if (has && opens) p.share.where[at] = kv_where(kKvManyParts, row, from, to);
+                    if (has && opens) p.share.where[t.flags & kKvOthers][at] = kv_where(kKvManyParts, row, from, to);
                     tc_fence_before();
                     close_tile(idx);
                     continue;
@@ -941,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 f[4 * k + 3] = fmaf(y[k].w, wb, fmaf(x[k].w, wa, f[4 * k + 3]));
                             }
                         }
-                        if constexpr (SHARED) kv_store_sums<D>(p.share, at, d, f, 32, l, m);
+                        if constexpr (SHARED) kv_store_sums<D>(p.a, p.share, t.flags, at, d, f, 32, l, m);
                         else store(at, d, f, inv);
                     }
                     if (!SHARED && p.a.lse) p.a.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
@@ -1331,7 +1346,7 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
         }
         b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
         // as many pairs as these sequences can have at most
-        const long long pairs = (long long)b.n_tokens * group / (2 * half_rows) + b.n_seqs;
+        const long long pairs = (SHARED ? 2LL : 1LL) * b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
             // with a row limit the other kernel has seen to the rows that no sequence owns
             const bool mine = !SHARED && row_limit == 0 && first == 0;
@@ -1356,14 +1371,9 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
 
 }  // namespace
 
-int kv_attention_many_launches(const KvBatch &batch, int group) {
-    const int half_rows = kHalfRows / group * group;
-    int n = 0;
-    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
-        const long long pairs = (long long)batch.n_tokens * group / (2 * half_rows) + std::min(kMaxSeqs, batch.n_seqs - b0);
-        n += (int)((pairs + kMaxPairs - 1) / kMaxPairs);
-    }
-    return n;
+bool kv_attention_many_at_once(const KvBatch &batch, int group) {
+    const long long rows = 2LL * batch.n_tokens * group;
+    return batch.n_seqs <= kMaxSeqs && rows / (2 * (kHalfRows / group * group)) + batch.n_seqs <= kMaxPairs;
 }
 
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,

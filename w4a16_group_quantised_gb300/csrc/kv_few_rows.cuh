@@ -76,6 +76,7 @@ constexpr int kLeast = 2;                 // fewest steps worth a CTA
 constexpr int kFewSeqs = 16;              // so many sequences may have their tiles cut alike ...
 constexpr int kManyHeads = 8;             // ... of so many kv heads
 constexpr int kTileCost = 32;             // keys that the start and end of a tile count for in the shares
+constexpr int kFlagShift = 26;            // SHARED: an entry's flags above its first row, 2^24 at most
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kTop = 15.9f;             // weights stay below 2^kTop, inside fp16 ...
 constexpr float kHead = 14.0f;            // ... and a moved reference puts the largest at 2^kHead
@@ -231,10 +232,18 @@ __global__ void __launch_bounds__(32 * NW, 1)
         long long v = 0;
         int tiles = 0;
         if (i < B) {
-            const KvSeq s = SHARED ? kv_entry(p.share, i) : kv_sequence(p.b, p.c.page_shift, i, p.status);
+            KvSeq s;
+            int flags = 0;                                         // above the bits of a row
+            if constexpr (SHARED) {
+                const KvEntry e = p.share.entries[i];
+                s = KvSeq{e.q0, (e.flags & kKvBig) && *p.share.use_many ? 0 : e.n, e.len};
+                flags = e.flags << kFlagShift;
+            } else {
+                s = kv_sequence(p.b, p.c.page_shift, i, p.status);
+            }
             const int rows = s.n * group;
             const int row_tiles = p.row_limit > 0 && rows > p.row_limit ? 0 : (rows + ROWS - 1) / ROWS;
-            seqs[i] = make_int4(s.q0, s.n, s.len, row_tiles);
+            seqs[i] = make_int4(s.q0 | flags, s.n, s.len, row_tiles);
             tiles = row_tiles * Hk;
             v = (long long)tiles * (span(s.n, s.len).steps + COST);
         }
@@ -409,8 +418,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
         int q0, n, row, head;                                      // the sequence's rows, the tile's first row, its kv head
         int first;                                                 // position of the sequence's first new token
     };
-    // the position of a tile's tok-th token
-    auto position = [&](int first, int tok) { return SHARED ? first + tok * p.share.step : first + tok; };
+    // an entry's flags, and the position of a tile's tok-th token
+    auto flags_of = [](int q0) { return SHARED ? q0 >> kFlagShift : kKvOthers; };
+    auto position = [&](const Tile &tl, int tok) { return flags_of(tl.q0) & kKvOthers ? tl.first + tok : tl.first; };
     uint32_t q[NR][KS][2];
     float o[NR][KS][4], ref[NR][2], sum[NR][2], fac[NR][2];
     int row_pos[NR][2], min_pos = 0, max_pos = 0;                  // position of each row's token; -1: no such row
@@ -424,7 +434,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
         const int r = tl.row + row;
         if (r >= tl.n * group) return false;
         const int tok = divide(r, group);
-        at = (long long)(tl.q0 + tok) * p.a.n_heads + tl.head * group + r - tok * group;
+        const int q0 = SHARED ? tl.q0 & (1 << kFlagShift) - 1 : tl.q0;
+        at = (long long)(q0 + tok) * p.a.n_heads + tl.head * group + r - tok * group;
         return true;
     };
     auto load_rows = [&](int at) {
@@ -440,12 +451,13 @@ __global__ void __launch_bounds__(32 * NW, 1)
         tl.head = divide(idx, s.w);
         tl.row = (idx - tl.head * s.w) * ROWS;
         tl.q0 = s.x, tl.n = s.y;
-        tl.first = SHARED && p.share.step == 0 ? s.z - 1 : s.z - s.y;
+        tl.first = flags_of(s.x) & kKvOthers ? s.z - s.y : s.z - 1;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const int r = tl.row + nr * 8 + g, tok = divide(r, group);
             const bool has = r < s.y * group;
-            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(s.x + tok) * p.a.q_stride +
+            const int q0 = SHARED ? s.x & (1 << kFlagShift) - 1 : s.x;
+            const uint16_t *src = static_cast<const uint16_t *>(p.a.q) + (long long)(q0 + tok) * p.a.q_stride +
                                   (tl.head * group + r - tok * group) * D;
 #pragma unroll
             for (int j = 0; j < KS / 4; ++j)
@@ -457,8 +469,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
     };
     auto start_tile = [&](const Tile &tl) {
         tile = tl;
-        min_pos = position(tl.first, divide(tl.row, group));
-        max_pos = position(tl.first, divide(min(tl.row + ROWS, tl.n * group) - 1, group));
+        min_pos = position(tl, divide(tl.row, group));
+        max_pos = position(tl, divide(min(tl.row + ROWS, tl.n * group) - 1, group));
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             // row g's dims as B: for a lane's chunk t (and t + 4), four words of four dims each
@@ -494,7 +506,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             for (int e = 0; e < 2; ++e) {
                 fac[nr][e] = __shfl_sync(0xffffffffu, back, (2 * t + e) * 4);
                 const int rr = tl.row + row_of(nr, e);
-                row_pos[nr][e] = rr < tl.n * group ? position(tl.first, divide(rr, group)) : -1;
+                row_pos[nr][e] = rr < tl.n * group ? position(tl, divide(rr, group)) : -1;
                 ref[nr][e] = kRefStart;
                 sum[nr][e] = 0.0f;
             }
@@ -504,9 +516,9 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 for (int i = 0; i < 4; ++i) o[nr][k][i] = 0.0f;
         }
     };
-    auto store_row = [&](long long at, int d0, const float *v, int count, float l, float m) {
+    auto store_row = [&](int q0, long long at, int d0, const float *v, int count, float l, float m) {
         if constexpr (SHARED) {
-            kv_store_sums<D>(p.share, at, d0, v, count, l, m);
+            kv_store_sums<D>(p.a, p.share, flags_of(q0), at, d0, v, count, l, m);
             return;
         }
         const float r = l == 0.0f ? 0.0f : 1.0f / l;
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 long long at;
                 if (!place(tile, row, at)) continue;
                 if (whole) {
-                    store_row(at, g * 2 * KS, v, 2 * KS, sum[nr][e], ref[nr][e]);
+                    store_row(tile.q0, at, g * 2 * KS, v, 2 * KS, sum[nr][e], ref[nr][e]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < KS; k += 2)
@@ -887,7 +899,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         const Tile tl = {sh.begin, sh.end, sh.q0, sh.n, sh.row, sh.head, 0};
         for (int row = lane; row < ROWS; row += 32) {
             long long at;
-            if (place(tl, row, at)) p.share.where[at] = kv_where(kKvFewParts, row, blockIdx.x, to);
+            if (place(tl, row, at)) p.share.where[flags_of(tl.q0) & kKvOthers][at] = kv_where(kKvFewParts, row, blockIdx.x, to);
         }
     }
     // those within the CTA: each by the warp that holds the first part
@@ -900,7 +912,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 float acc[4], l, m;
                 sum_parts(sh, true, row, d, acc, l, m);
                 long long at;
-                if (place(tile, row, at)) store_row(at, d, acc, 4, l, m);
+                if (place(tile, row, at)) store_row(tile.q0, at, d, acc, 4, l, m);
             }
         }
     }
@@ -946,7 +958,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
                 }
             }
             long long at;
-            if (place(tl, row, at)) store_row(at, d, acc, 4, l, m);
+            if (place(tl, row, at)) store_row(tl.q0, at, d, acc, 4, l, m);
         }
     }
 }
