@@ -125,7 +125,8 @@ constexpr int kKvAlone = 2;               // a sequence that shares nothing: wha
 constexpr int kKvBig = 4;                 // kv_attention_tc.cu's, if that kernel is to run at all
 struct KvShare {
     const KvEntry *entries;
-    const int *use_many;                  // whether kKvBig entries are kv_attention_tc.cu's
+    const int *use_many;                  // whether kKvBig entries are kv_attention_tc.cu's; CTAs of that kernel, of the other
+    int beside;                           // kv_few_rows.cuh's kernel runs beside the other, launched before it
     int defer;                            // parts are left where they are; else the last CTA to come sums them
     // of shared keys, of others:
     float *out[2];                        // [n_tokens, n_heads, head_dim] sums

@@ -28,32 +28,32 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kLeastShared = 64;          // positions that are worth an entry
-constexpr int kBigRows = 32;              // more rows a kv head may be kv_attention_tc.cu's
+constexpr int kBigRows = 16;              // more rows a kv head may be kv_attention_tc.cu's
 
-// What an entry takes, in ns of the whole GPU at 152 SMs: kv_few_rows.cuh 16 keys of a tile of 8 or 16 rows, kv_attention_tc.cu
-// 128 keys of a tile of 256.  What that kernel takes more than the other to start and end: 25 us.  Measured, the one /
-// the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to 56,
-// over 20000 56 to 77 / 87 to 91; 16 groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126 at
-// 32, 163 / 130 at 40, 200 / 136 at 64.
-constexpr int kFewQuarterNs8 = 3, kFewQuarterNs16 = 4;
-constexpr int kManyNs = 16;
-constexpr long long kManyStartNs = 25000;
-__host__ __device__ inline long long few_cost(long long rows, int tile_rows, long long keys, int kv_heads) {
-    return (rows + tile_rows - 1) / tile_rows * ((keys + 15) / 16) * kv_heads *
-           (tile_rows == 16 ? kFewQuarterNs16 : kFewQuarterNs8) / 4;
+// What entries take, in ns on kCostSms SMs: kv_few_rows.cuh 16 keys of a tile of 8 or 16 rows (and a tile's start and end as
+// much as 32), kv_attention_tc.cu 128 keys of a tile of 256; and what each kernel takes to start and end.  Measured, the
+// one / the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to
+// 56, over 20000 56 to 77 / 87 to 91; 16 groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126
+// at 32, 163 / 130 at 40, 200 / 136 at 64.
+constexpr float kFewNs8 = 0.75f, kFewNs16 = 1.05f, kManyNs = 16.0f;
+constexpr float kFewStartNs = 10000.0f, kManyStartNs = 30000.0f;
+constexpr int kCostSms = 152;
+__host__ __device__ inline unsigned long long few_steps(long long rows, int tile_shift, int keys) {
+    return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (unsigned)(((keys + 15) >> 4) + 2);
 }
-__host__ __device__ inline long long many_cost(long long rows, long long keys, int kv_heads) {
-    return (rows + kManyTileRows - 1) / kManyTileRows * ((keys + 127) / 128) * kv_heads * kManyNs;
+__host__ __device__ inline unsigned long long many_steps(long long rows, int keys) {
+    return (unsigned long long)((rows + kManyTileRows - 1) / kManyTileRows) * (unsigned)((keys + 127) >> 7);
 }
 
 struct PlanParams {
     KvBatch b;
     KvGroups g;
-    int page_shift, kv_heads, group, tile_rows;
+    int page_shift, kv_heads, group, tile_shift;
     KvEntry *entries;                     // of groups, then of sequences
     int *shared;                          // positions that each group shares
-    int *use_many;
-    long long many_start;                 // what the tensor-core kernel takes more to start and end
+    int *use_many;                        // KvShare
+    int choice;                           // w4a16_debug_set_config(10)
+    int sms, may_many, beside;
     uint4 *where;                         // of both kinds, to be cleared
     long long where_vecs;
     int *status;
@@ -68,14 +68,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
             p.where[i] = make_uint4(0, 0, 0, 0);
         return;
     }
-    __shared__ unsigned long long s_few, s_many;          // what the big entries take
-    if (threadIdx.x == 0) s_few = s_many = 0;
+    // steps of the big entries by either kernel, of the others; the best division of the SMs
+    __shared__ unsigned long long s_few, s_many, s_rest;
+    __shared__ unsigned s_best;
+    if (threadIdx.x == 0) s_few = s_many = s_rest = 0, s_best = 0xffffffffu;
     __syncthreads();
+    unsigned long long few = 0, many = 0, rest = 0;       // of this thread
     auto big = [&](int n, int keys) {
         const long long rows = (long long)n * p.group;
-        if (rows <= kBigRows || keys <= 0) return 0;
-        atomicAdd(&s_few, (unsigned long long)few_cost(rows, p.tile_rows, keys, p.kv_heads));
-        atomicAdd(&s_many, (unsigned long long)many_cost(rows, keys, p.kv_heads));
+        const unsigned long long steps = few_steps(rows, p.tile_shift, max(keys, 0));
+        if (rows <= kBigRows) {
+            rest += steps;
+            return 0;
+        }
+        few += steps;
+        many += many_steps(rows, max(keys, 0));
         return kKvBig;
     };
     const int lane = threadIdx.x & 31, n_seqs = p.b.n_seqs, n_groups = p.g.n_groups;
@@ -122,8 +129,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
         p.entries[n_groups + i] =
             KvEntry{s.q0, s.n, s.len - skip, flags, (long long)i * p.b.max_blocks + (skip >> p.page_shift), 0};
     }
+    auto sum = [&](unsigned long long v, unsigned long long &to) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (lane == 0 && v > 0) atomicAdd(&to, v);
+    };
+    sum(few, s_few), sum(many, s_many), sum(rest, s_rest);
     __syncthreads();
-    if (threadIdx.x == 0) *p.use_many = (long long)s_few > (long long)s_many + p.many_start;
+    // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.  On few
+    // SMs that one's tiles are the longer to wait for: twice what its work takes.
+    const float few_ns = p.tile_shift == 3 ? kFewNs8 : kFewNs16, heads = (float)p.kv_heads * kCostSms;
+    const float on_many = (float)s_many * kManyNs * heads, on_rest = (float)s_rest * few_ns * heads;
+    const bool some_rest = s_rest > 0;
+    if (p.may_many && p.choice != 1 && s_few > 0) {
+        for (int k = threadIdx.x + 1; k <= p.sms; k += kPlanThreads) {
+            float t;
+            if (k == p.sms) {
+                t = kManyStartNs + on_many / p.sms + (some_rest ? kFewStartNs + on_rest / p.sms : 0.0f);
+            } else {
+                if (!p.beside || !some_rest) continue;
+                t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + 2.0f * on_rest / (p.sms - k));
+            }
+            atomicMin(&s_best, (unsigned)fminf(t, 4.0e6f) << 10 | (unsigned)k);   // up to 4 ms, and k
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        const float alone = kFewStartNs + (on_rest + (float)s_few * few_ns * heads) / p.sms;
+        const bool use = s_best != 0xffffffffu && (p.choice == 2 || alone >= 4.0e6f || (float)(s_best >> 10) < alone);
+        const int k = use ? (int)(s_best & 1023) : 0;
+        p.use_many[0] = use;
+        p.use_many[1] = k;
+        p.use_many[2] = k == p.sms ? k : p.sms - k;
+    }
 }
 
 struct JoinParams {
@@ -216,7 +254,7 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     const long long rows = (long long)n_tokens * n_heads;
     s.entries = reinterpret_cast<KvEntry *>(take(((long long)n_groups + n_seqs) * sizeof(KvEntry)));
     s.shared = reinterpret_cast<int *>(take((long long)n_groups * 4));
-    s.use_many = reinterpret_cast<int *>(take(4));
+    s.use_many = reinterpret_cast<int *>(take(12));
     s.where[0] = reinterpret_cast<unsigned long long *>(take((rows + 1) / 2 * 32));
     s.where[1] = s.where[0] + (rows + 1) / 2 * 2;
     s.few = take(tickets_bytes(dev) + (long long)dev.sm_count * 2 * kTileRows * (head_dim + 2) * 4);
@@ -242,10 +280,11 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     const int forced = shared_kernels();
     const bool plain = forced ? g.n_groups == 0 : g.n_groups == 0 || longest * b.n_seqs * c.n_kv_heads * c.head_dim * 2 <= kLeastBytes;
     // the tensor-core kernel is launched where the plan might ask for it
-    const int tile_rows = few_tile_rows(a.max_q_len, group);
+    const int tile_rows = few_tile_rows(a.max_q_len, group), tile_shift = tile_rows == 16 ? 4 : 3;
     const long long all = (long long)b.n_tokens * group, entries = (long long)g.n_groups + b.n_seqs;
-    const long long many_start = forced == 2 ? -(1LL << 60) : kManyStartNs;
-    const bool may_many = all > kBigRows && forced != 1 && few_cost(2 * (all + entries * tile_rows), tile_rows, longest, c.n_kv_heads) > many_start;
+    const float most = (float)few_steps(2 * (all + entries * tile_rows), tile_shift, (int)longest) * c.n_kv_heads *
+                       (tile_rows == 16 ? kFewNs16 : kFewNs8);
+    const bool may_many = all > kBigRows && forced != 1 && (forced == 2 || most > kManyStartNs);
     if (kernel_log_on()) {
         char line[256];
         std::snprintf(line, sizeof line,
@@ -259,25 +298,26 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     if (plain) return launch_kv_attention(a, c, b, dev, s, pdl);
     const Scratch w = scratch_of(a.workspace, a.n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, g.n_groups, b.n_tokens, dev);
     const long long vecs = ((long long)rows + 1) / 2 * 2;
-    const PlanParams plan{b, g, c.page_shift, c.n_kv_heads, group, tile_rows, w.entries, w.shared, w.use_many, forced == 1 ? 1LL << 60 : many_start,
-                          reinterpret_cast<uint4 *>(w.where[0]), vecs, dev.status};
+    const PlanParams plan{b, g, c.page_shift, c.n_kv_heads, group, tile_shift, w.entries, w.shared, w.use_many, forced,
+                          dev.sm_count, may_many, pdl, reinterpret_cast<uint4 *>(w.where[0]), vecs, dev.status};
     const int fill = (int)std::min<long long>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
     cudaError_t e = kv_launch(plan_shared_kernel, dim3(1 + fill), dim3(kPlanThreads), 0, s, pdl, plan);
     if (e != cudaSuccess) return e;
     KvBatch batch = b;
     batch.n_seqs = (int)entries;
     KvAttentionArgs args = a;
-    KvShare share{w.entries, w.use_many, 0, {w.out[0], w.out[1]}, {w.ml[0], w.ml[1]}, {w.where[0], w.where[1]}};
-    args.workspace = w.few;
-    share.defer = entries <= kMaxSeqs;                     // one launch: its parts stay until the join
-    e = launch_few_rows<true>(args, c, batch, 0, share, dev, s, pdl);
-    if (e != cudaSuccess) return e;
+    KvShare share{w.entries, w.use_many, 0, 0, {w.out[0], w.out[1]}, {w.ml[0], w.ml[1]}, {w.where[0], w.where[1]}};
     if (may_many) {
         args.workspace = w.many;
         share.defer = kv_attention_many_at_once(batch, group);
         e = launch_kv_attention_many(args, c, batch, 0, dev, s, pdl, &share);
         if (e != cudaSuccess) return e;
     }
+    args.workspace = w.few;
+    share.defer = entries <= kMaxSeqs;                     // one launch: its parts stay until the join
+    share.beside = may_many && pdl;
+    e = launch_few_rows<true>(args, c, batch, 0, share, dev, s, pdl);
+    if (e != cudaSuccess) return e;
     auto parts = [&](void *ws) { return reinterpret_cast<const float *>(static_cast<char *>(ws) + tickets_bytes(dev)); };
     const JoinParams join{a, share, parts(w.few), may_many ? parts(w.many) : nullptr, tile_rows, rows};
     const dim3 grid((unsigned)(((long long)rows * (c.head_dim / 4) + 255) / 256));

@@ -526,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Whole tiles or equal shares?  With few tiles the longest first, dealt out to and fro, can come close to
     // equal shares without the parts that shared tiles leave; each thread adds up one CTA's hand.
     uint16_t *order = reinterpret_cast<uint16_t *>(smem + L::kOrder);
-    const int grid = gridDim.x;
+    const int grid = SHARED ? p.share.use_many[1] : gridDim.x;
+    if (SHARED && blockIdx.x >= grid) return;
     auto dealt = [&](int cta, int round) { return round * grid + (round & 1 ? grid - 1 - cta : cta); };
     bool deal = false;
     if (pairs <= kSorted) {
@@ -1284,7 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // launch, also for a replay, whose tag is the same.  All out of shared memory: the loops have no register to
         // spare for what is needed here.
         const int n = misc[5];
-        const long long all = pre[n] * Hk, shares = min((long long)gridDim.x, (all + kCost) / (1 + kCost));
+        const long long all = pre[n] * Hk, shares = min((long long)grid, (all + kCost) / (1 + kCost));
         const long long from = s_cut[0], to = s_cut[1];
         for (int i = 0; i < 2 && from < to; ++i) {
             const long long at = i ? to - 1 : from;

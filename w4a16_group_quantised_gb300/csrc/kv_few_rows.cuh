@@ -220,7 +220,14 @@ __global__ void __launch_bounds__(32 * NW, 1)
     if (lane < NS) mbar_init(bars + lane * 8, 1);
     if (tid <= NW) shared[tid].has = 0;
     fence_mbar_init();
-    kv_begin();
+    // Beside the kernel before it, which waited for the plan before it let this one start: its end is waited for at this
+    // one's, by all CTAs, so that whoever waits for this kernel has both.
+    const bool beside = SHARED && p.share.beside;
+    if (!beside) kv_begin();
+    else __threadfence();                                          // the plan's entries, not what a call before left in L1
+    auto leave = [&]() {
+        if (beside) grid_dependency_wait();
+    };
 
     // ---- the line: each sequence's steps and tiles, summed up
     constexpr int COST = (kTileCost + KB * BPS - 1) / (KB * BPS);
@@ -276,7 +283,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
     }
     __syncthreads();
     kv_empty_rows(p.a, p.b, D, p.before ? seqs[0].x : 0, p.after ? seqs[B - 1].x + seqs[B - 1].y : p.b.n_tokens);
-    if (total == 0) return;
+    if (total == 0) {
+        leave();
+        return;
+    }
 
     // the sequence, one of lo..hi, of a position of the line: of steps alone (cost = 0), or with the tiles' cost
     auto find = [&](long long at, int cost, int lo, int hi) {
@@ -287,8 +297,12 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
         return lo;
     };
-    const long long ctas = min((long long)gridDim.x, (total + kLeast + COST - 1) / (kLeast + COST));
-    if (blockIdx.x >= ctas) return;
+    const int grid = SHARED ? p.share.use_many[2] : gridDim.x;
+    const long long ctas = min((long long)grid, (total + kLeast + COST - 1) / (kLeast + COST));
+    if (blockIdx.x >= ctas) {
+        leave();
+        return;
+    }
     // The step where an equal share of the work begins: `at` steps and tiles' costs into the line.  In a
     // short tile, when `snap`, the tile's first; *moved is where that is with the costs.
     auto step_of = [&](long long at, bool snap, long long &moved, int lo, int hi, int &b) {
@@ -361,7 +375,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
     __syncthreads();
     const long long c0 = s_cut[0];
     const int mine = (int)(s_cut[NW] - c0);
-    if (mine <= 0) return;
+    if (mine <= 0) {
+        leave();
+        return;
+    }
     auto warp_start = [&](int w) { return (int)(s_cut[w] - c0); };
     const int w0 = warp_start(warp), w1 = warp_start(warp + 1), seq_lo = s_seq[warp], seq_hi = s_seq[warp + 1];
 
@@ -878,7 +895,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
             s_to[nth] = to;
         }
     }
-    if (gave_up) return;
+    if (gave_up) {
+        leave();
+        return;
+    }
     if (defer && out[1] && warp == NW - 1) {
         // the tile that begins here: the last CTA whose share begins by its last step
         const Shared sh = shared[s_out[1]];
@@ -916,7 +936,10 @@ __global__ void __launch_bounds__(32 * NW, 1)
             }
         }
     }
-    if (defer || (!out[0] && !out[1])) return;
+    if (defer || (!out[0] && !out[1])) {
+        leave();
+        return;
+    }
     __syncthreads();
     // ---- a tile that CTAs from..to share: the last of them to come sums it
 #pragma unroll
@@ -961,6 +984,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             if (place(tl, row, at)) store_row(tl.q0, at, d, acc, 4, l, m);
         }
     }
+    leave();
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
