@@ -116,6 +116,32 @@ def test_too_few_pages(cuda_lib, spare):
     check(cuda_lib, cache, table, n, ref, [1, 3, 1, 1, 17, 2])
 
 
+@pytest.mark.parametrize("rows, spare", [(1024, 100), (1024, 511), (1100, 0), (1100, 550), (1100, 2000)])
+def test_many_rows_and_too_few_pages(cuda_lib, rows, spare):
+    """Where rows or pages are too many for one launch, and just before."""
+    lens = [16 * (1 + b % 3) + (b % 5) for b in range(rows)]
+    cache, table, n, ref = pool(cuda_lib, lens, rows, kv_heads=1, dim=64, spare=spare)
+    table = torch.cat([table, torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
+    shared(table, n, ref, [[b, b + 1, b + 2] for b in range(0, rows - 3, 7)])
+    check(cuda_lib, cache, table, n, ref, [b % 4 for b in range(rows)])
+
+
+@pytest.mark.parametrize("pages", [32768, 32769])
+def test_pool_of_one_launch_and_one_more(cuda_lib, pages):
+    w = cuda_lib
+    g = torch.Generator().manual_seed(pages)
+    codes = [torch.randint(-127, 128, (pages, 1, 16, 64), generator=g, dtype=torch.int8).cuda() for _ in range(2)]
+    cache = w.KVCache(*codes, torch.ones((pages, 1), device="cuda"), torch.ones((pages, 1), device="cuda"))
+    ref = torch.randint(0, 2, (pages,), generator=g, dtype=torch.int32)
+    ref[-1], ref[:64] = 0, 1
+    table = torch.full((40, 700), -1, dtype=torch.int32)
+    table[:, 0] = torch.arange(40) // 2
+    ref[:20] = 2
+    lens = torch.full((40,), 5, dtype=torch.int32)
+    new = [7000 if b % 2 else 6500 for b in range(40)]                  # more than half of the pages: not enough
+    check(w, cache, table.cuda(), lens.cuda(), ref.cuda(), new)
+
+
 @pytest.mark.parametrize("n_tokens", [0, 1, 5, 11, 12, 40])
 def test_too_few_rows(cuda_lib, n_tokens):
     cache, table, n, ref = pool(cuda_lib, [16, 20, 3], 3, spare=9)

@@ -30,25 +30,29 @@ constexpr int kPlanThreads = 1024;
 constexpr int kLeastShared = 64;          // positions that are worth an entry
 constexpr int kBigRows = 16;              // more rows a kv head may be kv_attention_tc.cu's
 
-// What entries take, in ns on kCostSms SMs: kv_few_rows.cuh 16 keys of a tile of 8 or 16 rows (and a tile's start and end as
-// much as 32), kv_attention_tc.cu 128 keys of a tile of 256; and what each kernel takes to start and end.  Measured, the
-// one / the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to
+// What entries take, in ns on kCostSms SMs with 128 dims: kv_few_rows.cuh 16 keys of a tile of 8 rows, with pages of 16 or
+// more tokens, or of 16 rows (and a tile's start and end as
+// much as 80 or 192), kv_attention_tc.cu 128 keys of a tile of 256 (and a tile's start and end as much as 384); and what each
+// kernel takes to start and end.  Fitted to calls at ten divisions of the SMs (64 sequences on a prompt of 8192 tokens: 20 /
+// 40 / 60 / 80 / 100 / 120 / 140 of 152 SMs for shared keys take 128 / 94 / 81 / 77 / 91 / 122 / 261 us, all for one kernel
+// after the other 99).  Measured, the one / the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to
 // 56, over 20000 56 to 77 / 87 to 91; 16 groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126
 // at 32, 163 / 130 at 40, 200 / 136 at 64.
-constexpr float kFewNs8 = 0.75f, kFewNs16 = 1.05f, kManyNs = 16.0f;
-constexpr float kFewStartNs = 10000.0f, kManyStartNs = 30000.0f;
+constexpr float kFewNs8 = 0.75f, kFewNs8Wide = 0.6f, kFewNs16 = 1.05f, kManyNs = 16.0f, kOf64Dims = 0.6f;
+constexpr float kFewStartNs = 10000.0f, kManyStartNs = 45000.0f;
 constexpr int kCostSms = 152;
 __host__ __device__ inline unsigned long long few_steps(long long rows, int tile_shift, int keys) {
-    return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (unsigned)(((keys + 15) >> 4) + 2);
+    return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (unsigned)(((keys + 15) >> 4) + (tile_shift == 3 ? 5 : 12));
 }
 __host__ __device__ inline unsigned long long many_steps(long long rows, int keys) {
-    return (unsigned long long)((rows + kManyTileRows - 1) / kManyTileRows) * (unsigned)((keys + 127) >> 7);
+    return (unsigned long long)((rows + kManyTileRows - 1) / kManyTileRows) * (unsigned)(((keys + 127) >> 7) + 3);
 }
 
 struct PlanParams {
     KvBatch b;
     KvGroups g;
-    int page_shift, kv_heads, group, tile_shift;
+    int page_shift, group, tile_shift;
+    float few_ns, many_ns;                // of a step, all kv heads
     KvEntry *entries;                     // of groups, then of sequences
     int *shared;                          // positions that each group shares
     int *use_many;                        // KvShare
@@ -136,10 +140,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
     };
     sum(few, s_few), sum(many, s_many), sum(rest, s_rest);
     __syncthreads();
-    // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.  On few
-    // SMs that one's tiles are the longer to wait for: twice what its work takes.
-    const float few_ns = p.tile_shift == 3 ? kFewNs8 : kFewNs16, heads = (float)p.kv_heads * kCostSms;
-    const float on_many = (float)s_many * kManyNs * heads, on_rest = (float)s_rest * few_ns * heads;
+    // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.  Half as
+    // much again for that one's work beside the other: with too few SMs it is by far the last, with too many hardly earlier.
+    const float few_ns = p.few_ns * kCostSms, on_many = (float)s_many * p.many_ns * kCostSms, on_rest = (float)s_rest * few_ns;
     const bool some_rest = s_rest > 0;
     if (p.may_many && p.choice != 1 && s_few > 0) {
         for (int k = threadIdx.x + 1; k <= p.sms; k += kPlanThreads) {
@@ -148,14 +151,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
                 t = kManyStartNs + on_many / p.sms + (some_rest ? kFewStartNs + on_rest / p.sms : 0.0f);
             } else {
                 if (!p.beside || !some_rest) continue;
-                t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + 2.0f * on_rest / (p.sms - k));
+                t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + 1.5f * on_rest / (p.sms - k));
             }
             atomicMin(&s_best, (unsigned)fminf(t, 4.0e6f) << 10 | (unsigned)k);   // up to 4 ms, and k
         }
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        const float alone = kFewStartNs + (on_rest + (float)s_few * few_ns * heads) / p.sms;
+        const float alone = kFewStartNs + (on_rest + (float)s_few * few_ns) / p.sms;
         const bool use = s_best != 0xffffffffu && (p.choice == 2 || alone >= 4.0e6f || (float)(s_best >> 10) < alone);
         const int k = use ? (int)(s_best & 1023) : 0;
         p.use_many[0] = use;
@@ -282,8 +285,9 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     // the tensor-core kernel is launched where the plan might ask for it
     const int tile_rows = few_tile_rows(a.max_q_len, group), tile_shift = tile_rows == 16 ? 4 : 3;
     const long long all = (long long)b.n_tokens * group, entries = (long long)g.n_groups + b.n_seqs;
-    const float most = (float)few_steps(2 * (all + entries * tile_rows), tile_shift, (int)longest) * c.n_kv_heads *
-                       (tile_rows == 16 ? kFewNs16 : kFewNs8);
+    const float scale = c.n_kv_heads * (c.head_dim == 64 ? kOf64Dims : 1.0f);
+    const float few_ns = scale * (tile_rows == 16 ? kFewNs16 : c.page_shift > 4 ? kFewNs8Wide : kFewNs8);
+    const float most = (float)few_steps(2 * (all + entries * tile_rows), tile_shift, (int)longest) * few_ns;
     const bool may_many = all > kBigRows && forced != 1 && (forced == 2 || most > kManyStartNs);
     if (kernel_log_on()) {
         char line[256];
@@ -298,7 +302,7 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     if (plain) return launch_kv_attention(a, c, b, dev, s, pdl);
     const Scratch w = scratch_of(a.workspace, a.n_heads, c.n_kv_heads, c.head_dim, b.n_seqs, g.n_groups, b.n_tokens, dev);
     const long long vecs = ((long long)rows + 1) / 2 * 2;
-    const PlanParams plan{b, g, c.page_shift, c.n_kv_heads, group, tile_shift, w.entries, w.shared, w.use_many, forced,
+    const PlanParams plan{b, g, c.page_shift, group, tile_shift, few_ns, scale * kManyNs, w.entries, w.shared, w.use_many, forced,
                           dev.sm_count, may_many, pdl, reinterpret_cast<uint4 *>(w.where[0]), vecs, dev.status};
     const int fill = (int)std::min<long long>((vecs + 4 * kPlanThreads - 1) / (4 * kPlanThreads), dev.sm_count);
     cudaError_t e = kv_launch(plan_shared_kernel, dim3(1 + fill), dim3(kPlanThreads), 0, s, pdl, plan);
@@ -314,7 +318,7 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
         if (e != cudaSuccess) return e;
     }
     args.workspace = w.few;
-    share.defer = entries <= kMaxSeqs;                     // one launch: its parts stay until the join
+    share.defer = entries <= kMaxEntries;                     // one launch: its parts stay until the join
     share.beside = may_many && pdl;
     e = launch_few_rows<true>(args, c, batch, 0, share, dev, s, pdl);
     if (e != cudaSuccess) return e;

@@ -57,6 +57,7 @@ namespace {
 
 constexpr int kHalfRows = 128, kTileRows = kManyTileRows, kKeys = 128;
 constexpr int kMaxSeqs = 512;             // sequences of a launch
+constexpr int kMaxEntries = 640;          // entries of one (SHARED): 512 sequences and their groups
 constexpr int kFlagShift = 26;            // SHARED: an entry's flags above its first row, 2^24 at most
 constexpr int kMaxPairs = 1216;           // (sequence, row tile) pairs of a launch
 constexpr int kShortSteps = 2;            // tiles of up to so many steps stay in one CTA
@@ -111,7 +112,7 @@ struct ManySmem {
     static constexpr int kV = kK + kStages * kOperand;
     static constexpr int kPre = kV + kStages * kOperand;                // line position of each pair, of one kv head
     static constexpr int kSeq = kPre + (kMaxPairs + 1) * 8 + 8;   // int4 {q0, n, len, pairs before}
-    static constexpr int kPairSeq = kSeq + kMaxSeqs * 16;         // sequence of each pair
+    static constexpr int kPairSeq = kSeq + kMaxEntries * 16;         // sequence of each pair
     static constexpr int kOrder = kPairSeq + kMaxPairs * 2;       // pairs by falling steps
     static constexpr int kScale = kOrder + kSorted * 2;        // [4][8] float4 {ks, log2 vs, 1 / vs, -}
     static constexpr int kExchange = kScale + 4 * 8 * 16;                // (M, l) of the second half's rows
@@ -1336,7 +1337,8 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
     if (e != cudaSuccess) return e;
     static std::atomic<unsigned long long> launches{SHARED ? 0x7e57ab1f0000ull : 0x7e57ab1e0000ull};
     const KvEntry *entries = share.entries;
-    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
+    constexpr int kMost = SHARED ? kMaxEntries : kMaxSeqs;
+    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMost) {
         KvBatch b = batch;
         if constexpr (SHARED) {
             share.entries = entries + b0;
@@ -1345,7 +1347,7 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
             b.kv_lens += b0;
             b.q_starts += b0;
         }
-        b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
+        b.n_seqs = std::min(kMost, batch.n_seqs - b0);
         // as many pairs as these sequences can have at most
         const long long pairs = (SHARED ? 2LL : 1LL) * b.n_tokens * group / (2 * half_rows) + b.n_seqs;
         for (long long first = 0; first < pairs; first += kMaxPairs) {
@@ -1374,7 +1376,7 @@ cudaError_t launch_many(const KvAttentionArgs &a, const KvCache &c, const KvBatc
 
 bool kv_attention_many_at_once(const KvBatch &batch, int group) {
     const long long rows = 2LL * batch.n_tokens * group;
-    return batch.n_seqs <= kMaxSeqs && rows / (2 * (kHalfRows / group * group)) + batch.n_seqs <= kMaxPairs;
+    return batch.n_seqs <= kMaxEntries && rows / (2 * (kHalfRows / group * group)) + batch.n_seqs <= kMaxPairs;
 }
 
 cudaError_t launch_kv_attention_many(const KvAttentionArgs &a, const KvCache &c, const KvBatch &batch, int row_limit,

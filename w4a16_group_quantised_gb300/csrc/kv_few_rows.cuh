@@ -68,6 +68,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kMaxSeqs = 512;             // sequences of a launch
+constexpr int kMaxEntries = 640;          // entries of one (SHARED): 512 sequences and their groups
 // Tiles of up to so many keys stay in one CTA.  256 / never / 1024, us, contexts of 100 to 300 keys: 256 sequences 32.7 /
 // 33.4 / 31.4, 64 16.1 / 16.1 / 15.2, 8 12.2 / 11.7 / 11.6; 64 of 500 to 1000 28.5 / 28.4 / 30.5, one of 1000 14.4 / 14.4 /
 // 16.0: 1024 takes too long where there are few tiles, never costs some where there are many.
@@ -131,9 +132,9 @@ struct FewSmem {
     static constexpr int kPart = kRows * (D + 2);                  // floats: rows of out, then (M, l) of each row
     static constexpr int kPark = NW * NS * kStage;                 // a warp's first piece, if another began it
     static constexpr int kSeq = kPark + NW * kPart * 4;            // int4 {q0, n, len, row tiles}
-    static constexpr int kPre = kSeq + kMaxSeqs * 16;              // line position of each sequence
-    static constexpr int kTiles = kPre + kMaxSeqs * 8;             // tiles of the sequences before each
-    static constexpr int kBars = kTiles + kMaxSeqs * 4;
+    static constexpr int kPre = kSeq + kMaxEntries * 16;              // line position of each sequence
+    static constexpr int kTiles = kPre + kMaxEntries * 8;             // tiles of the sequences before each
+    static constexpr int kBars = kTiles + kMaxEntries * 4;
     static constexpr int kShared = kBars + NW * NS * 8;            // tiles that warps share: the CTA's first, then by warp
     static constexpr int kMisc = kShared + (NW + 1) * 32;
     static constexpr int kEnd = kMisc + (2 * NW + 1) * 8 + 32 + (NW + 2) * 4 + 1024;       // 1024: slack to align the base
@@ -1051,7 +1052,8 @@ cudaError_t launch_few_rows(const KvAttentionArgs &a, const KvCache &c, const Kv
     if (e != cudaSuccess) return e;
     if (merged) v = k;
     static std::atomic<unsigned long long> launches{SHARED ? 0x5ca1ab1f0000ull : 0x5ca1ab1e0000ull};
-    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMaxSeqs) {
+    constexpr int kMost = SHARED ? kMaxEntries : kMaxSeqs;
+    for (int b0 = 0; b0 < batch.n_seqs; b0 += kMost) {
         KvBatch b = batch;
         if constexpr (SHARED) {
             share.entries = entries + b0;
@@ -1060,7 +1062,7 @@ cudaError_t launch_few_rows(const KvAttentionArgs &a, const KvCache &c, const Kv
             b.kv_lens += b0;
             b.q_starts += b0;
         }
-        b.n_seqs = std::min(kMaxSeqs, batch.n_seqs - b0);
+        b.n_seqs = std::min(kMost, batch.n_seqs - b0);
         const bool owns = !SHARED;                              // rows that are no sequence's
         FewParams p{a, c, b, row_limit, token_first ? 1 : 0, merged ? 1 : 0, owns && b0 == 0,
                     owns && b0 + b.n_seqs == batch.n_seqs, merged && apart < 0 ? 1 : 0, merged && apart < 0 ? 0 : 1,

@@ -252,10 +252,8 @@ struct GrowRow {
 
 // What a call of grow works out on the way to its tables.
 struct GrowScratch {
-    int *total;          // [0] free pages
-    int *counts;         // of each chunk
+    int *counts;         // free pages of each chunk
     uint32_t *bits;      // free pages
-    int *list;           // free pages by rank
     GrowRow *rows;
 };
 
@@ -347,88 +345,134 @@ __global__ void __launch_bounds__(kChunk)
     }
 }
 
-// The free pages by rank: each CTA those of its chunk.
-__global__ void __launch_bounds__(kChunk) grow_list_kernel(GrowScratch w, int n_pages) {
-    kv_begin();
-    __shared__ int scratch[32];
-    const int n_chunks = (n_pages + kChunk - 1) / kChunk;
-    int before = 0, all = 0;
-    for (int i = threadIdx.x; i < n_chunks; i += blockDim.x) {
-        const int v = w.counts[i];
-        all += v;
-        before += i < (int)blockIdx.x ? v : 0;
+// The free page of rank r of each thread that asks (r >= 0), 1024 chunks at a
+// time: the chunk by the sums of the counts before it, then its words.  Every
+// thread of the CTA calls; the ranks are below the number of free pages.
+constexpr int kGrowThreads = 256, kWindow = 1024;
+__device__ int page_of_rank(const uint32_t *bits, const int *counts, int n_chunks, int r, int *before, int *scratch) {
+    int page = -1;
+    for (int base = 0; base < n_chunks; base += kWindow) {
+        int v[kWindow / kGrowThreads], sum = 0, all;
+#pragma unroll
+        for (int j = 0; j < kWindow / kGrowThreads; ++j) {
+            const int i = base + threadIdx.x * (kWindow / kGrowThreads) + j;
+            v[j] = i < n_chunks ? counts[i] : 0;
+            sum += v[j];
+        }
+        int ahead = block_before<int>(sum, scratch, &all);
+#pragma unroll
+        for (int j = 0; j < kWindow / kGrowThreads; ++j) {
+            before[threadIdx.x * (kWindow / kGrowThreads) + j] = ahead;
+            ahead += v[j];
+        }
+        __syncthreads();
+        if (r >= 0 && r < all) {
+            int lo = 0, hi = min(kWindow, n_chunks - base) - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (before[mid] <= r) lo = mid;
+                else hi = mid - 1;
+            }
+            int left = r - before[lo];
+            const uint4 *words = reinterpret_cast<const uint4 *>(bits + (long long)(base + lo) * (kChunk / 32));
+            uint32_t w[kChunk / 32];
+#pragma unroll
+            for (int j = 0; j < kChunk / 128; ++j) {
+                const uint4 x = words[j];
+                w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+            }
+            uint32_t word = 0;
+            int at = -1;
+#pragma unroll
+            for (int j = 0; j < kChunk / 32; ++j) {
+                const int n = __popc(w[j]);
+                if (at < 0 && left < n) at = j, word = w[j];
+                if (at < 0) left -= n;
+            }
+            for (; left > 0; --left) word &= word - 1;
+            page = (base + lo) * kChunk + at * 32 + __ffs(word) - 1;
+        }
+        r = r >= all ? r - all : -1;
+        if (!__syncthreads_or(r >= 0)) break;
     }
-    before = block_sum(before, scratch);
-    all = block_sum(all, scratch);
-    const int p = blockIdx.x * kChunk + threadIdx.x;
-    const bool is_free = w.bits[p >> 5] >> (threadIdx.x & 31) & 1;
-    int total;
-    const int at = before + block_before<int>(is_free, scratch, &total);
-    if (is_free) w.list[at] = p;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *w.total = all;
+    return page;
 }
 
-// `parts` CTAs a row: its entries, its tokens' positions and slots, the copy of
-// its last page.  From the first row on for which the free pages, or the rows
-// of the token tensors, do not suffice, none grows.
-__global__ void grow_fill_kernel(KvCache c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount,
-                                 GrowScratch w, int n_tokens, int *q_starts, int *positions, long long *slots,
-                                 int parts, int *status) {
+// `parts` CTAs a row, by blocks: its entries, its tokens' positions and slots,
+// the copy of its last page.  From the first row on for which the free pages,
+// or the rows of the token tensors, do not suffice, none grows.
+__global__ void __launch_bounds__(kGrowThreads)
+    grow_fill_kernel(KvCache c, int *table, int *lens, int n_seqs, int max_blocks, int *refcount, GrowScratch w,
+                     int n_tokens, int *q_starts, int *positions, long long *slots, int parts, int *status) {
     kv_begin();
-    __shared__ int s_total;
-    const int me = blockIdx.x / parts, part = blockIdx.x % parts, shift = c.page_shift;
-    const int free_pages = *w.total;
+    __shared__ int scratch[32], before[kWindow], s_page[kGrowThreads], s_total;
+    const int me = blockIdx.x / parts, part = blockIdx.x % parts, shift = c.page_shift, tid = threadIdx.x;
+    const int n_chunks = (c.n_pages + kChunk - 1) / kChunk;
+    GrowRow end = {}, g = {};
+    if (n_seqs > 0) end = w.rows[n_seqs - 1];
+    if (me < n_seqs) g = w.rows[me];
+    int free_pages = 0;
+    for (int i = tid; i < n_chunks; i += kGrowThreads) free_pages += w.counts[i];
+    free_pages = block_sum(free_pages, scratch);
     auto fits = [&](const GrowRow &r) { return r.tokens <= n_tokens && r.pages <= free_pages; };
-    int total = 0;                                       // tokens of the rows that grow
-    if (n_seqs > 0) {
-        const GrowRow end = w.rows[n_seqs - 1];
-        total = end.tokens;
-        if (!fits(end)) {
-            if (threadIdx.x == 0) s_total = 0;
-            __syncthreads();
-            for (int i = threadIdx.x; i + 1 < n_seqs; i += blockDim.x) {
-                const GrowRow r = w.rows[i];
-                if (fits(r) && !fits(w.rows[i + 1])) s_total = r.tokens;
-            }
-            __syncthreads();
-            total = s_total;
-            if (blockIdx.x == 0 && threadIdx.x == 0) kv_report(status);
+    int total = end.tokens;                              // tokens of the rows that grow
+    if (!fits(end)) {
+        if (tid == 0) s_total = 0;
+        __syncthreads();
+        for (int i = tid; i + 1 < n_seqs; i += kGrowThreads) {
+            const GrowRow r = w.rows[i];
+            if (fits(r) && !fits(w.rows[i + 1])) s_total = r.tokens;
         }
+        __syncthreads();
+        total = s_total;
+        if (blockIdx.x == 0 && tid == 0) kv_report(status);
     }
     // rows of the token tensors that are no sequence's
-    for (long long i = (long long)total + (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_tokens;
-         i += (long long)gridDim.x * blockDim.x) {
+    for (long long i = (long long)total + (long long)blockIdx.x * kGrowThreads + tid; i < n_tokens;
+         i += (long long)gridDim.x * kGrowThreads) {
         positions[i] = -1;
         slots[i] = -1;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) q_starts[0] = 0;
+    if (blockIdx.x == 0 && tid == 0) q_starts[0] = 0;
     if (me >= n_seqs) return;
-    const GrowRow g = w.rows[me];
     const bool ok = fits(g);
-    if (part == 0 && threadIdx.x == 0) q_starts[me + 1] = ok ? g.tokens : total;
+    if (part == 0 && tid == 0) q_starts[me + 1] = ok ? g.tokens : total;
     if (!ok || g.n == 0) return;
-    const int *list = w.list + (g.pages - g.need);
-    // the row's new pages are those of blocks `start` and on
-    const int start = ((g.len + (1 << shift) - 1) >> shift) - g.copies;
-    for (int t = part * blockDim.x + threadIdx.x; t < g.n; t += parts * blockDim.x) {
-        const int pos = g.len + t, blk = pos >> shift;
-        const int p = blk >= start ? list[blk - start] : g.last;
-        positions[g.tokens - g.n + t] = pos;
-        slots[g.tokens - g.n + t] = ((long long)p << shift) + (pos & ((1 << shift) - 1));
-    }
-    if (part == 0) {
-        int *to = table + (long long)me * max_blocks + start;
-        for (int k = threadIdx.x; k < g.need; k += blockDim.x) {
-            const int p = list[k];
-            to[k] = p;
-            refcount[p] = 1;
+    // its blocks from the one of the first new token on, some at a time; those from `start` on get new pages, the first of
+    // them the copy of the last page if there is one
+    const int first = g.len >> shift, start = ((g.len + (1 << shift) - 1) >> shift) - g.copies;
+    const int blocks = ((g.len + g.n - 1) >> shift) + 1 - first, rank = g.pages - g.need - start;
+    int *entries = table + (long long)me * max_blocks;
+    const int each = min(kGrowThreads, (blocks + parts - 1) / parts);
+    for (int b0 = part * each; b0 < blocks || (b0 == part * each && g.copies); b0 += parts * each) {
+        const int blk = first + b0 + tid;
+        const bool mine = tid < each && b0 + tid < blocks;
+        // the last thread finds the page of the copy, which every part has a hand in
+        const bool copy = g.copies && b0 == part * each && tid == kGrowThreads - 1;
+        const int r = mine && blk >= start ? rank + blk : copy ? rank + start : -1;
+        const int p = __syncthreads_or(r >= 0) ? page_of_rank(w.bits, w.counts, n_chunks, r, before, scratch) : -1;
+        if (mine) {
+            s_page[tid] = r >= 0 ? p : g.last;
+            if (r >= 0) {
+                entries[blk] = p;
+                refcount[p] = 1;
+            }
         }
-        if (threadIdx.x == 0) {
-            lens[me] = g.len + g.n;
-            if (g.copies) drop_page(g.last, refcount, c.n_pages, status);
+        if (copy) s_total = p;
+        __syncthreads();
+        const int t0 = max((first + b0) << shift, g.len), t1 = min((first + min(b0 + each, blocks)) << shift, g.len + g.n);
+        for (int pos = t0 + tid; pos < t1; pos += kGrowThreads) {
+            const int row = g.tokens - g.n + pos - g.len;
+            positions[row] = pos;
+            slots[row] = ((long long)s_page[(pos >> shift) - first - b0] << shift) + (pos & ((1 << shift) - 1));
         }
+        if (g.copies && b0 == part * each) copy_page(c, g.last, s_total, part, parts);
+        __syncthreads();
     }
-    if (g.copies) copy_page(c, g.last, list[0], part, parts);
+    if (part == 0 && tid == 0) {
+        lens[me] = g.len + g.n;
+        if (g.copies) drop_page(g.last, refcount, c.n_pages, status);
+    }
 }
 
 __global__ void free_kernel(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
@@ -468,14 +512,16 @@ __global__ void trim_kernel(int *table, const int *lens, int max_blocks, int *re
 // so beams that go on from one another cost counts for the pages since they
 // parted only.  Whoever takes a page id out of an entry lowers its count: the
 // counts are right whatever the lists say.
-__global__ void reorder_kernel(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
-                               const int *dst, const int *src, int n, int cols, int *status) {
+__global__ void __launch_bounds__(1024)
+    reorder_kernel(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages, const int *dst,
+                   const int *src, int n, int cols_shift, int *status) {
     kv_begin();
-    extern __shared__ int dyn[];
+    extern __shared__ int2 entries[];                    // what a row gets, what it had; then the lengths
     constexpr int kSkip = -2;                            // the row stays as it is
-    int *entries = dyn, *old_lens = dyn + n * cols;
+    const int cells = n << cols_shift, cols = 1 << cols_shift;
+    int *old_lens = reinterpret_cast<int *>(entries + cells);
     const bool first = blockIdx.x == 0;
-    const int col0 = blockIdx.x * cols, width = min(cols, max_blocks - col0);
+    const int col0 = blockIdx.x << cols_shift, width = min(cols, max_blocks - col0);
     auto row_to = [&](int i) { return dst ? dst[i] : i; };
     for (int i = threadIdx.x; first && i < n; i += blockDim.x) {
         const int s = src[i], d = row_to(i);
@@ -484,27 +530,26 @@ __global__ void reorder_kernel(int *table, int *lens, int n_seqs, int max_blocks
         old_lens[i] = bad ? kSkip : s < 0 ? 0 : lens[s];
     }
 #pragma unroll 4
-    for (int k = threadIdx.x; k < n * cols; k += blockDim.x) {
-        const int i = k / cols, at = k % cols, s = src[i], d = row_to(i);
-        int v = kSkip;
+    for (int k = threadIdx.x; k < cells; k += blockDim.x) {
+        const int i = k >> cols_shift, at = k & (cols - 1), s = src[i], d = row_to(i);
+        int2 e = make_int2(kSkip, kSkip);
         if (at < width && s < n_seqs && d >= 0 && d < n_seqs) {
-            v = s < 0 ? -1 : table[(long long)s * max_blocks + col0 + at];
-            if (v >= n_pages) kv_report(status);
-            if (v < 0 || v >= n_pages) v = -1;
+            e.y = table[(long long)d * max_blocks + col0 + at];
+            e.x = s < 0 ? -1 : table[(long long)s * max_blocks + col0 + at];
+            if (e.x >= n_pages) kv_report(status);
+            if (e.x < 0 || e.x >= n_pages) e.x = -1;
         }
-        entries[k] = v;
+        entries[k] = e;
     }
     __syncthreads();
     for (int i = threadIdx.x; first && i < n; i += blockDim.x)
         if (old_lens[i] != kSkip) lens[row_to(i)] = old_lens[i];
 #pragma unroll 4
-    for (int k = threadIdx.x; k < n * cols; k += blockDim.x) {
-        const int v = entries[k];
-        if (v == kSkip) continue;
-        int *e = table + (long long)row_to(k / cols) * max_blocks + col0 + k % cols;
-        if (*e == v) continue;
-        const int was = atomicExch(e, v);
-        if (v >= 0) atomicAdd(refcount + v, 1);
+    for (int k = threadIdx.x; k < cells; k += blockDim.x) {
+        const int2 e = entries[k];
+        if (e.x == kSkip || e.x == e.y) continue;
+        const int was = atomicExch(table + (long long)row_to(k >> cols_shift) * max_blocks + col0 + (k & (cols - 1)), e.x);
+        if (e.x >= 0) atomicAdd(refcount + e.x, 1);
         drop_page(was, refcount, n_pages, status);
     }
 }
@@ -648,10 +693,8 @@ GrowScratch grow_scratch(void *ws, int n_pages) {
         p += round16(bytes);
         return q;
     };
-    s.total = reinterpret_cast<int *>(take(16));
     s.counts = reinterpret_cast<int *>(take(chunks * 4));
     s.bits = reinterpret_cast<uint32_t *>(take(chunks * kChunk / 8));
-    s.list = reinterpret_cast<int *>(take((long long)n_pages * 4));
     s.rows = reinterpret_cast<GrowRow *>(p);
     return s;
 }
@@ -670,25 +713,26 @@ cudaError_t launch_kv_grow(const KvCache &c, int *table, int *lens, int n_seqs, 
     e = kv_launch(grow_plan_kernel, dim3(chunks + 1), dim3(kChunk), smem, s, pdl, c, table, lens, new_lens, n_seqs,
                   max_blocks, refcount, places, w, dev.status);
     if (e != cudaSuccess) return e;
-    e = kv_launch(grow_list_kernel, dim3(chunks), dim3(kChunk), 0, s, pdl, w, c.n_pages);
-    if (e != cudaSuccess) return e;
-    // CTAs a row: for the copy of a page, or for a few of an even share of the tokens
+    // CTAs a row: for the copy of a page, or for some 2048 of an even share of the tokens
     const int rows = std::max(n_seqs, 1);
-    const int parts = std::max(std::min(copy_parts(c), 4), std::min(n_tokens / rows / (4 * kCopyThreads) + 1, 16));
-    return kv_launch(grow_fill_kernel, dim3((unsigned)rows * parts), dim3(kCopyThreads), 0, s, pdl, c, table, lens, n_seqs,
+    const int parts = std::max(std::min(copy_parts(c), 4), std::min(n_tokens / rows / 2048 + 1, 16));
+    return kv_launch(grow_fill_kernel, dim3((unsigned)rows * parts), dim3(kGrowThreads), 0, s, pdl, c, table, lens, n_seqs,
                      max_blocks, refcount, w, n_tokens, q_starts, positions, slots, parts, dev.status);
 }
 
 cudaError_t launch_kv_reorder(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
                               const int *dst, const int *src, int n, const DeviceInfo &dev, cudaStream_t s, bool pdl) {
-    // a sector's columns a CTA, fewer where the rows would not fit
-    int cols = 8;
-    while (cols > 1 && (long long)n * cols * 4 > 64 << 10) cols /= 2;
-    const size_t smem = (size_t)n * (cols + 1) * 4;
+    // A sector's columns a CTA; fewer where the rows would not fit, or where there would be fewer CTAs than SMs: 1024 rows
+    // of up to 550 columns take 23 us with 8 columns a CTA, 7 with 4.
+    int shift = 3;
+    while (shift > 0 && ((long long)n << shift) * 8 > 64 << 10) --shift;
+    while (shift > 0 && (long long)n << shift > 2048 && (max_blocks >> shift) < dev.sm_count) --shift;
+    const size_t smem = ((size_t)n << shift) * 8 + (size_t)n * 4;
     const cudaError_t e = raise_smem_cap(reinterpret_cast<const void *>(reorder_kernel), smem);
     if (e != cudaSuccess) return e;
-    return kv_launch(reorder_kernel, dim3((max_blocks + cols - 1) / cols), dim3(512), smem, s, pdl, table, lens, n_seqs,
-                     max_blocks, refcount, n_pages, dst, src, n, cols, dev.status);
+    const int threads = std::min(1024, std::max(128, (n << shift) + 31 & ~31));
+    return kv_launch(reorder_kernel, dim3((max_blocks + (1 << shift) - 1) >> shift), dim3(threads), smem, s, pdl, table, lens,
+                     n_seqs, max_blocks, refcount, n_pages, dst, src, n, shift, dev.status);
 }
 
 cudaError_t launch_kv_free(int *table, int *lens, int n_seqs, int max_blocks, int *refcount, int n_pages,
@@ -723,8 +767,7 @@ cudaError_t launch_kv_compact(const KvCache &c, int *table, int n_seqs, int max_
 
 long long kv_grow_workspace(int n_pages, int n_seqs) {
     const long long chunks = (n_pages + kChunk - 1) / kChunk;
-    return 16 + round16(chunks * 4) + round16(chunks * kChunk / 8) + round16((long long)n_pages * 4) +
-           (long long)n_seqs * sizeof(GrowRow);
+    return round16(chunks * 4) + round16(chunks * kChunk / 8) + (long long)n_seqs * sizeof(GrowRow);
 }
 
 long long kv_pool_workspace(int n_pages) {
