@@ -111,6 +111,22 @@ def test_many_requests(cuda_lib, groups):
     check(cuda_lib, x, s, 4, 8)
 
 
+@pytest.mark.parametrize("rows, width", [(2048, 4), (2052, 4), (5000, 1), (3200, 64)])
+def test_very_many_beams(cuda_lib, rows, width):
+    """Up to 2048 those that go on are looked up first; of more, the others are passed over one by one."""
+    x, s, g = problem(rows, 300, "bf16", rows)
+    done = torch.rand(rows, generator=g) < 0.3
+    s[torch.rand(rows, generator=g) < 0.2] = -math.inf
+    x[done] = math.nan                                                 # never read
+    check(cuda_lib, x, s, width, 4, finished=done, end=299)
+
+
+@pytest.mark.parametrize("act", ["f16", "f32"])
+def test_the_largest_vocabulary(cuda_lib, act):
+    x, s, _ = problem(2, 1 << 24, act, 12, spread=2.0)
+    check(cuda_lib, x, s, 2, 5)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("n_out", [1, 5, 64])
 def test_ties(cuda_lib, act, n_out):

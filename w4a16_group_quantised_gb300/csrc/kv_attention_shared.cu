@@ -272,7 +272,7 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
 
 // Bytes of cache up to which kv_attention is called instead, should all sequences be as long as the table is wide: up to
 // there its one launch is the faster one.
-constexpr long long kLeastBytes = 32LL << 20;
+constexpr double kLeastBytes = 32 << 20;
 
 }  // namespace
 
@@ -281,7 +281,7 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     const int group = a.n_heads / c.n_kv_heads, rows = b.n_tokens * a.n_heads;
     const long long longest = (long long)b.max_blocks << c.page_shift;
     const int forced = shared_kernels();
-    const bool plain = forced ? g.n_groups == 0 : g.n_groups == 0 || longest * b.n_seqs * c.n_kv_heads * c.head_dim * 2 <= kLeastBytes;
+    const bool plain = forced ? g.n_groups == 0 : g.n_groups == 0 || 2.0 * longest * b.n_seqs * c.n_kv_heads * c.head_dim <= kLeastBytes;
     // the tensor-core kernel is launched where the plan might ask for it
     const int tile_rows = few_tile_rows(a.max_q_len, group), tile_shift = tile_rows == 16 ? 4 : 3;
     const long long all = (long long)b.n_tokens * group, entries = (long long)g.n_groups + b.n_seqs;
