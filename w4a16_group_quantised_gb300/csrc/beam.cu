@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
     grid_dependency_wait();
 
     // ---- the beams that go on, in order (all of them where there are too many to look)
-    int alive = rows;
+    unsigned alive = rows;
     if (rows <= kMaxRows) {
         alive = 0;
         for (int base = 0; base < rows; base += kThreads) {
@@ -220,20 +220,20 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
     if (alive == 0) return;
     // Pieces of a beam: as many as fill the grid once, twice and so on, whichever takes least with the cost of a piece's
     // start and end.  Lane i tries i + 1 rounds.
-    const int T = cut.row_tiles, grid = gridDim.x;
-    int q;
+    // (32-bit numbers: 2^20 beams with 1024 / width pieces each at most, and a division of 64 bits is a hundred instructions.)
+    const unsigned T = cut.row_tiles, grid = gridDim.x;
+    unsigned q;
     {
-        const long long fits = (long long)(lane + 1) * grid / alive;
-        q = (int)max(1LL, min(fits, (long long)cut.slots));
-        const long long rounds = ((long long)alive * q + grid - 1) / grid;
-        long long cost = rounds * ((T + q - 1) / q + kPieceCost) << 5 | lane;
-        long long least_cost = cost;
+        q = max(1u, min((lane + 1) * grid / alive, (unsigned)cut.slots));
+        const unsigned rounds = (alive * q + grid - 1) / grid;
+        const float cost = (float)rounds * (float)((T + q - 1) / q + kPieceCost);
+        float least_cost = cost;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) least_cost = min(least_cost, __shfl_xor_sync(0xffffffffu, least_cost, d));
-        q = __shfl_sync(0xffffffffu, q, (int)(least_cost & 31));
+        for (int d = 16; d > 0; d >>= 1) least_cost = fminf(least_cost, __shfl_xor_sync(0xffffffffu, least_cost, d));
+        q = __shfl_sync(0xffffffffu, q, __ffs(__ballot_sync(0xffffffffu, cost == least_cost)) - 1);
     }
-    const long long units = (long long)alive * q;
-    const long long u0 = blockIdx.x * units / grid, u1 = (blockIdx.x + 1) * units / grid;
+    const unsigned units = alive * q, each = units / grid, more = units % grid;   // the first `more` CTAs have one more
+    const unsigned u0 = blockIdx.x * each + min(blockIdx.x, more), u1 = u0 + each + (blockIdx.x < more);
     if (u0 == u1) return;
 
     float m = -INFINITY, hi = 0.0f, lo = 0.0f;             // of this thread and piece
@@ -300,21 +300,21 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
 
     Raw<DT> next[NV];
     int row = 0, piece = 0, tile = 0, last = 0;            // what is being loaded: a beam's piece, up to tile `last`
-    auto open = [&](long long u) {
-        const int o = (int)(u / q);
-        piece = (int)(u - (long long)o * q);
-        row = rows <= kMaxRows ? (int)s_rows[o] : o;
-        tile = (int)((long long)piece * T / q), last = (int)((long long)(piece + 1) * T / q) - 1;
+    auto open = [&](unsigned u) {
+        const unsigned o = u / q;
+        piece = u - o * q;
+        row = rows <= kMaxRows ? (int)s_rows[o] : (int)o;
+        tile = piece * T / q, last = (piece + 1) * T / q - 1;
     };
     int first = 0;                                         // of the tiles whose candidates are not in the list
-    long long u = u0 - 1;
+    unsigned u = u0 - 1;                                   // + 1 is u0, also where that is 0
     for (bool started = false, fresh = true;;) {
         const int here = row, here_piece = piece, this_tile = tile, base = tile * TILE;
         const bool ends = !started || tile == last;
         Raw<DT> x[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) x[j] = next[j];
-        if (!ends || u + 1 < u1) {
+        if (!ends || u + 1 != u1) {
             if (ends) open(++u);
             else ++tile;
             const int end = rows <= kMaxRows || goes_on(a, row) ? a.vocab : 0;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
                 add_to(hi, lo, s_hi[w]);
                 lo += s_lo[w];
             }
-            sums[slot] = PartSum{(double)hi + (double)lo, all, q};
+            sums[slot] = PartSum{(double)hi + (double)lo, all, (int)q};
         }
         if (u == u1) return;
         m = -INFINITY, hi = lo = 0.0f, least = -INFINITY;
