@@ -170,6 +170,32 @@ def test_long_prefix(kernels):
     check(kernels, *grouped(groups, kv_heads=1, dim=64, page=16, seed=7))
 
 
+@pytest.mark.parametrize("groups", [[(12000, [(9000, 1), (11000, 1)])], [(30000, [(3, 1)] * 2)],
+                                    [(12000, [(9000, 1), (11000, 1)]), (10000, [(8000, 2), (9000, 1)])]])
+@pytest.mark.parametrize("dim, page", [(128, 64), (64, 16)])
+def test_few_long_tiles_token_first(kernels, groups, dim, page):
+    """Tiles of one entry cut into the same number of pieces, or not where that would be uneven."""
+    check(kernels, *grouped(groups, heads=16, kv_heads=8, dim=dim, page=page, store="e4m3", layout="tokens", act="f16", seed=dim))
+
+
+@pytest.mark.parametrize("members", [3, 60])
+def test_without_early_start(kernels, members):
+    """One kernel after the other, each waiting for the one before it."""
+    kernels.w4a16_debug_set_config(3, [0])
+    try:
+        check(kernels, *grouped([(500, [(i % 9, 1) for i in range(members)]), (80, [(1, 40), (2, 1)])], seed=21))
+    finally:
+        kernels.w4a16_debug_set_config(3, [1])
+
+
+@pytest.mark.parametrize("members, prefix", [(160, 4000), (64, 6000)])
+@pytest.mark.parametrize("heads, kv_heads", [(32, 8), (32, 4)])
+def test_as_the_sizes_call_for(cuda_lib, members, prefix, heads, kv_heads):
+    """Large enough for the tensor-core kernel to be chosen, with the other beside it."""
+    groups = [(prefix, [(i * 37 % 300, 1) for i in range(members)]), (60, [(1000, 1)] * 3)]
+    check(cuda_lib, *grouped(groups, heads=heads, kv_heads=kv_heads, seed=members))
+
+
 @pytest.mark.parametrize("count", [513, 1100])
 def test_many_sequences_and_groups(kernels, count):
     """More of them than one launch takes."""

@@ -36,6 +36,15 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvBatch &b, int page_shift, i
     return s;
 }
 
+// An entry, the place of its page ids and the plan's division, from L2: the
+// kernel that reads them may have started before the one in front of it ended.
+__device__ __forceinline__ KvEntry kv_entry(const KvShare &sh, int i) {
+    const int4 v = __ldcg(reinterpret_cast<const int4 *>(sh.entries + i));
+    return KvEntry{v.x, v.y, v.z, v.w, 0, 0};
+}
+__device__ __forceinline__ long long kv_entry_pages(const KvShare &sh, int i) { return __ldcg(&sh.entries[i].pages); }
+__device__ __forceinline__ int kv_division(const KvShare &sh, int i) { return __ldcg(sh.use_many + i); }
+
 // The page of position block `blk` (below the table's width) of sequence i, or -1 (reported).
 __device__ __forceinline__ int kv_page(const KvCache &c, const KvBatch &b, int i, int blk, int *status) {
     const int p = b.block_table[(long long)i * b.max_blocks + blk];

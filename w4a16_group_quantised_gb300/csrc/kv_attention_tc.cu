@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             KvSeq q;
             int flags = 0;                                         // above the bits of a row
             if constexpr (SHARED) {
-                const KvEntry e = p.share.entries[i];
-                q = KvSeq{e.q0, (e.flags & kKvBig) && *p.share.use_many ? e.n : 0, e.len};
+                const KvEntry e = kv_entry(p.share, i);
+                q = KvSeq{e.q0, (e.flags & kKvBig) && kv_division(p.share, 0) ? e.n : 0, e.len};
                 flags = e.flags << kFlagShift;
             } else {
                 q = kv_sequence(p.b, p.c.page_shift, i, p.status);
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Whole tiles or equal shares?  With few tiles the longest first, dealt out to and fro, can come close to
     // equal shares without the parts that shared tiles leave; each thread adds up one CTA's hand.
     uint16_t *order = reinterpret_cast<uint16_t *>(smem + L::kOrder);
-    const int grid = SHARED ? p.share.use_many[1] : gridDim.x;
+    const int grid = SHARED ? kv_division(p.share, 1) : gridDim.x;
     if (SHARED && blockIdx.x >= grid) return;
     auto dealt = [&](int cta, int round) { return round * grid + (round & 1 ? grid - 1 - cta : cta); };
     bool deal = false;
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ManyTile t = tile_of(s, b, pair - s.w);
         t.pair = pair, t.head = head;
         t.begin = pre[pair] * Hk + (long long)head * (t.steps + kCost);
-        if (SHARED) t.pages = p.share.entries[b].pages;
+        if (SHARED) t.pages = kv_entry_pages(p.share, b);
         return t;
     };
     auto find_pair = [&](long long at) {                           // the pair of a position of the line

@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(32 * NW, 1)
             KvSeq s;
             int flags = 0;                                         // above the bits of a row
             if constexpr (SHARED) {
-                const KvEntry e = p.share.entries[i];
-                s = KvSeq{e.q0, (e.flags & kKvBig) && *p.share.use_many ? 0 : e.n, e.len};
+                const KvEntry e = kv_entry(p.share, i);
+                s = KvSeq{e.q0, (e.flags & kKvBig) && kv_division(p.share, 0) ? 0 : e.n, e.len};
                 flags = e.flags << kFlagShift;
             } else {
                 s = kv_sequence(p.b, p.c.page_shift, i, p.status);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
         }
         return lo;
     };
-    const int grid = SHARED ? p.share.use_many[2] : gridDim.x;
+    const int grid = SHARED ? kv_division(p.share, 2) : gridDim.x;
     const long long ctas = min((long long)grid, (total + kLeast + COST - 1) / (kLeast + COST));
     if (blockIdx.x >= ctas) {
         leave();
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(32 * NW, 1)
             m.where = (blk * KB & ((1 << p.c.page_shift) - 1)) | head << 8;
             if (blk * KB < s.z) {
                 m.pos = blk * KB;
-                const long long row = SHARED ? p.share.entries[b].pages : (long long)b * p.b.max_blocks;
+                const long long row = SHARED ? kv_entry_pages(p.share, b) : (long long)b * p.b.max_blocks;
                 m.page = p.b.block_table[row + (blk * KB >> p.c.page_shift)];
             }
         }
