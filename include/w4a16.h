@@ -406,7 +406,7 @@ int w4a16_version(void);
  * turns it off;
  * which = 10: kernels of w4a16_kv_attention_shared, vals = {1: the few-rows
  * kernel alone, 2: the tensor-core kernel for every group or sequence with
- * more than 32 rows a kv head}, n = 1, whatever the sizes (which otherwise may
+ * more than 16 rows a kv head}, n = 1, whatever the sizes (which otherwise may
  * also have w4a16_kv_attention called);
  * n = 0 restores the built-in choice for which = 1, 2, 4, 8 or 10.  An invalid
  * configuration is rejected here or, for the decode shape limits, by the

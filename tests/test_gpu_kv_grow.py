@@ -203,6 +203,35 @@ def test_large_pool(cuda_lib):
     check(w, cache, table, lens, ref, [33, 1, 40])
 
 
+def test_pool_of_more_than_a_million_pages(cuda_lib):
+    """Counts of more chunks than are looked at together, codes past 2^31 bytes."""
+    w = cuda_lib
+    pages = 2_200_001
+    codes = [torch.zeros((pages, 1, 16, 64), dtype=torch.int8, device="cuda") for _ in range(2)]
+    cache = w.KVCache(*codes, torch.ones((pages, 1), device="cuda"), torch.ones((pages, 1), device="cuda"))
+    ref = torch.ones(pages, dtype=torch.int32, device="cuda")
+    free = [70, 1_048_575, 1_048_576, 1_500_000, 2_097_151, 2_097_152, 2_200_000]
+    ref[free] = 0
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    table[1, 0], table[2, 0] = 2_199_998, 2_199_998
+    ref[2_199_998] = 2
+    codes[0][2_199_998], codes[1][2_199_998] = 5, -7
+    lens = torch.tensor([0, 9, 9], dtype=torch.int32, device="cuda")
+    new = torch.tensor([48, 24, 8], dtype=torch.int32, device="cuda")
+    starts, positions, slots = w.w4a16_kv_grow(cache, table, lens, ref, new, 80)
+    torch.cuda.synchronize()
+    # three blocks; a copy and two blocks; the last row that names it keeps its page, and begins a block
+    assert table.tolist() == [free[:3] + [-1], free[3:6] + [-1], [2_199_998, free[6], -1, -1]]
+    assert lens.tolist() == [48, 33, 17] and starts.tolist() == [0, 48, 72, 80]
+    assert bool((ref == 1).all()) and w.w4a16_last_device_error() == 0
+    want = [16 * p + i for p in free[:3] for i in range(16)]
+    want += [16 * free[3] + i for i in range(9, 16)] + [16 * free[4] + i for i in range(16)] + [16 * free[5]]
+    want += [16 * 2_199_998 + i for i in range(9, 16)] + [16 * free[6]]
+    assert slots.tolist() == want
+    for c, v in zip(codes, (5, -7)):
+        assert bool((c[free[3]] == v).all()) and int((c != 0).any(-1).any(-1).sum()) == 2
+
+
 def test_other_stream_outputs_and_workspace(cuda_lib):
     w = cuda_lib
     cache, table, n, ref = pool(w, [20, 31, 0], 3, spare=20)

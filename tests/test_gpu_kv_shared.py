@@ -93,6 +93,30 @@ def test_single_tokens(kernels, store, act, dim, heads, kv_heads):
     check(kernels, *grouped(groups, heads, kv_heads, dim, 16, store, "heads", act, seed=heads + dim))
 
 
+@pytest.mark.parametrize("heads, kv_heads, dim", [(128, 1, 128), (256, 2, 64), (64, 64, 64), (33, 11, 128)])
+def test_many_heads(kernels, heads, kv_heads, dim):
+    groups = [(150, [(0, 1), (3, 1), (40, 2)]), (16, [(0, 1), (100, 3)]), (90, [(9, 1)])]
+    check(kernels, *grouped(groups, heads, kv_heads, dim, seed=heads))
+
+
+@pytest.mark.parametrize("members", [4, 40])
+def test_tokens_without_keys(kernels, members):
+    """Lengths of zero, and shorter than the tokens that the sequence brings: these see nothing, and nothing is shared."""
+    w = kernels
+    p, starts, prefix = grouped([(100, [(7, 3)] * members), (100, [(7, 3)] * members)], seed=3)
+    p.lens[1], p.lens[members], p.lens[members + 1] = 0, 2, 1
+    out, lse = run(w, p, starts, prefix)
+    assert int((lse == -math.inf).sum()) == (3 + 1 + 2) * p.heads
+    assert w.w4a16_last_device_error() == -9             # a sequence shorter than what it brings, as everywhere
+    w.w4a16_clear_device_error()
+    # the definition wants a key at least: with one the second sequence's last token has it
+    assert bool((out[5] == 0).all())
+    p.lens[1] = 1
+    want, want_lse, _ = attention(p)
+    out[5], lse[5] = want[5].to(out), want_lse[5].to(lse)
+    compare(p, out, lse)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 @pytest.mark.parametrize("layout", ["heads", "tokens", "padded", "pairs"])
 @pytest.mark.parametrize("members", [2, 9, 40, 70])

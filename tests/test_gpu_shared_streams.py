@@ -104,6 +104,44 @@ def test_growth_on_two_streams_at_once(cuda_lib):
     assert w.w4a16_last_device_error() == 0
 
 
+def test_two_graphs_share_a_workspace(kernels):
+    """Captured calls of different sizes with one workspace between them, replayed in turn on a stream."""
+    w = kernels
+    ws = torch.full((160 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    calls, check = [], []
+    for seed, members in ((4, 40), (5, 7)):
+        p, starts, prefix = grouped([(300 + seed, [(i % 30, 1) for i in range(members)])] * 2, seed=seed)
+        cache, table, lens, q_starts, rows = p.to_cuda(w)
+        q, a, b = rows[:, :p.heads * p.dim].unflatten(1, (p.heads, p.dim)), put(starts), put(prefix)
+        lse = torch.empty((p.T, p.heads), device="cuda")
+        calls.append(lambda args=(q, cache, table, lens, q_starts, 1, a, b), lse=lse: w.w4a16_kv_attention_shared(
+            *args, lse=lse, workspace=ws))
+        check.append(lambda out, p=p, lse=lse: compare(p, out, lse))
+    for seed, rows in ((1, 8), (2, 300)):
+        x, s, _ = problem(rows, 20000 + seed, "f16", seed)
+        x, s = x.cuda(), s.cuda()
+        want = w.w4a16_beam_select(x, s, 4, 4)
+        calls.append(lambda x=x, s=s: w.w4a16_beam_select(x, s, 4, 4, workspace=ws))
+        check.append(lambda out, want=want: [torch.testing.assert_close(o, v, rtol=0, atol=0) for o, v in zip(out, want)])
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in calls], []
+    for g, call in zip(graphs, calls):
+        with torch.cuda.graph(g):
+            outs.append(call())
+    for out in outs:
+        for o in out if isinstance(out, tuple) else [out]:
+            o.fill_(1)
+    for _ in range(5):
+        for i in (0, 2, 1, 3, 0, 1, 2, 3):
+            graphs[i].replay()
+    torch.cuda.synchronize()
+    for c, out in zip(check, outs):
+        c(out)
+    assert w.w4a16_last_device_error() == 0
+
+
 @pytest.mark.parametrize("name", ["shared", "select", "grow"])
 def test_a_dropped_result_is_not_handed_out_while_its_stream_works(cuda_lib, name):
     from test_gpu_kv_pages import pool

@@ -463,7 +463,7 @@ def w4a16_debug_set_config(which: int, vals=None) -> None:
     issue no weight copies, so their bounded waits run out); which=8 prefill
     row split (fused and dense forms) at {n_split} (a multiple of 256); which=10
     kernels of w4a16_kv_attention_shared {1 few rows, 2 tensor cores where there are
-    more than 32 rows}.  vals=None restores the built-in choice."""
+    more than 16 rows a kv head}.  vals=None restores the built-in choice."""
     lib = load_library()
     if vals is None:
         rc = lib.w4a16_debug_set_config(which, None, 0)

@@ -13,14 +13,16 @@
 //  * Each thread keeps a sum of its own, so nothing but the candidates is
 //    exchanged: 2^(x log2 e - R) with R the integer next to its largest x log2 e,
 //    so that sums with other references differ by a power of two, exactly.
-//    log2 e is two fp32 numbers; a tile is summed in fp32, tiles in two fp32
-//    numbers, threads in 64 bits: the continuations of different beams, a few
-//    1e-2 apart in earnest, are told apart down to about 1e-8.  Which thread
-//    sums what goes by the token alone, so that equal beams have equal sums.
+//    log2 e is two fp32 numbers; a thread's part of a tile is summed in fp32, tiles
+//    and threads in two fp32 numbers, pieces in 64 bits: the continuations of
+//    different beams, a few 1e-2 apart in earnest, are told apart down to about
+//    1e-8.  Which thread sums what goes by the token alone, so that equal beams
+//    have equal sums.
 //  * Within a beam c rises with x: candidates are logits, kept as 64-bit keys
-//    (the value's order, then the lower token).  Threads whose largest logit of
-//    a tile is above the n-th best so far append theirs to a list, which is cut
-//    to its n best when it has grown.  A piece's first tile gets its threshold
+//    (the value's order, then the lower token).  Threads note the vectors of 8 whose
+//    largest logit is above the n-th best so far; every 8 tiles, and at a piece's
+//    end, these are looked at again (they are in L2 still), their candidates join
+//    a list, and it is cut to its n best.  A piece's first tile gets its threshold
 //    from the least of the maxima of n groups of threads: n logits at least reach
 //    it, a few times n in earnest.  Where more do than the list holds (many equal
 //    ones), the n threads with the best maxima are found out, of which at most
@@ -53,6 +55,7 @@ constexpr float kHuge = 536870912.0f;                  // 2^29: from here on log
 
 // Logits of a tile per thread, in vectors of 8: as many as 16 registers hold.
 template <int DT> constexpr int kPer = DT == 2 ? 16 : 32;
+
 // The sum of a piece of a beam's logits: l = sum 2^(x log2 e - reference(m)), m the
 // largest x.  Where |m| >= 2^29 nothing but the logits that equal m counts, and l is their number.
 struct PartSum {
