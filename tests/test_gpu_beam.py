@@ -105,6 +105,31 @@ def test_widths(cuda_lib, width, n_out, groups):
     check(cuda_lib, x, s, width, n_out)
 
 
+@pytest.mark.parametrize("width, n_out, vocab, act", [(64, 64, 70001, "f32"), (16, 32, 131072, "bf16"), (40, 64, 66001, "f16"),
+                                                      (16, 1, 131071, "f32"), (16, 32, 60, "f32"), (3, 64, 9000, "bf16")])
+def test_many_candidates(cuda_lib, width, n_out, vocab, act):
+    """More pieces, and more candidates of the best ones, than are compared with one another at once."""
+    x, s, _ = problem(width, vocab, act, width + vocab)
+    check(cuda_lib, x, s, width, n_out)
+    check(cuda_lib, x, s * 0.001, width, n_out)                        # nearly even
+
+
+@pytest.mark.parametrize("width, n_out", [(64, 64), (16, 32), (64, 1), (5, 64)])
+def test_ties_of_many_beams(cuda_lib, width, n_out):
+    """All beams alike, the pieces of each too."""
+    x, s, g = problem(2 * width, 70000, "f32", width)
+    x[:] = torch.arange(70000).remainder(7).float()
+    s[:] = -2.0
+    check(cuda_lib, x, s, width, n_out)
+    x[:] = 0.0
+    check(cuda_lib, x, s, width, n_out)
+    x[:] = torch.randn(70000, generator=g)
+    got = check(cuda_lib, x, s, width, n_out)
+    # the best token of every beam, then the second
+    rows = [i % width for i in range(n_out)]
+    assert got[1] == [rows, [width + i for i in rows]]
+
+
 @pytest.mark.parametrize("groups", [40, 200])
 def test_many_requests(cuda_lib, groups):
     x, s, _ = problem(groups * 4, 9000, "bf16", groups)

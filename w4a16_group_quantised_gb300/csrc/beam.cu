@@ -29,7 +29,9 @@
 //    n times a thread's share can come.
 //  * The second kernel, a CTA per request, joins the pieces' sums, scores the
 //    candidates in 64 bits and picks the n best by counting who is better.
-//    Of sorted lists only the n with the best heads can hold any.
+//    Of sorted lists only the n with the best heads can hold any, and of these
+//    lists' l-th candidates only the n / l best: 32 of 16 beams with 60 logits took
+//    67 us with all candidates counted, 16 so.
 //
 // Measured on the GPU: 256 beams of 64 requests, a fifth of them ended, over
 // 131072 bf16 logits, 54 MB: 23 us, 2.3 TB/s of logits; 40 beams over 50001 fp16
@@ -48,8 +50,9 @@ constexpr int kPieceCost = 3;                          // tiles that a piece's s
 constexpr int kBatch = 8;                              // tiles between two cuts of a list
 constexpr int kList = 33 * kBeamMost;                  // its room: n candidates, and n threads' logits of a tile
 constexpr int kVectors = 1024;                         // vectors with candidates between two cuts
-constexpr int kMergeThreads = 256;
+constexpr int kSmallMerge = 256;                       // candidates for which the second kernel has 256 threads, not 1024
 constexpr int kMaxLists = 1024;                        // (beam, piece) pairs of a request
+constexpr int kFewCandidates = 128, kFewHeads = 128;   // so many are compared with one another at once
 constexpr int kMaxRows = 2048;                         // beams among which those that go on are looked up first
 constexpr float kHuge = 536870912.0f;                  // 2^29: from here on logits are 32 and more apart
 
@@ -135,9 +138,12 @@ struct Raw {
     uint32_t w[DT == 2 ? 8 : 4];
 };
 // A thread's vectors of a tile, at `at` and every kThreads vectors, of a row
-// aligned to `align` bytes; -inf from `end` on.
+// aligned to `align` bytes; -inf from `end` on.  Returns whether a warp's vectors
+// are a half word late, the words that they begin in, where a row begins in the
+// middle of one: shift_tile then.  (256 beams over 131071 bf16 logits: 52 us with
+// loads of 2 bytes, 30 so; 24 over 131072 and loads of 16.)
 template <int DT, int NV>
-__device__ __forceinline__ void load_tile(Raw<DT> (&x)[NV], const char *row, int align, int at, int end) {
+__device__ __forceinline__ bool load_tile(Raw<DT> (&x)[NV], const char *row, int align, int at, int end, bool first_row) {
     constexpr int N = DT == 2 ? 8 : 4, SIZE = DT == 2 ? 4 : 2;
     const char *p = row + (long long)at * SIZE;
     constexpr int STEP = kThreads * 8;
@@ -149,7 +155,16 @@ __device__ __forceinline__ void load_tile(Raw<DT> (&x)[NV], const char *row, int
                 const uint4 v = ldg_stream_v4(p + j * STEP * SIZE + 4 * i);
                 x[j].w[i] = v.x, x[j].w[i + 1] = v.y, x[j].w[i + 2] = v.z, x[j].w[i + 3] = v.w;
             }
-        return;
+        return false;
+    }
+    const int lane = threadIdx.x & 31;
+    if (DT != 2 && align == 2 && at + (31 - lane) * 8 + (NV - 1) * STEP + 9 <= end && (at > lane * 8 || !first_row)) {
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(p - 2);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[j].w[i] = __ldg(words + j * (STEP * SIZE / 4) + i);
+        return true;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j, p += STEP * SIZE, at += STEP) {
@@ -166,6 +181,19 @@ __device__ __forceinline__ void load_tile(Raw<DT> (&x)[NV], const char *row, int
                 x[j].w[i] = (at + 2 * i < end ? __ldg(halves + 2 * i) : none) |
                             (at + 2 * i + 1 < end ? (uint32_t)__ldg(halves + 2 * i + 1) : none) << 16;
         }
+    }
+    return false;
+}
+// What load_tile left half a word late.  A vector's last value is in the next
+// thread's first word.
+template <int DT, int NV>
+__device__ __forceinline__ void shift_tile(Raw<DT> (&x)[NV], const char *row, int at) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        uint32_t beyond = __shfl_down_sync(0xffffffffu, x[j].w[0], 1);
+        if ((threadIdx.x & 31) == 31) beyond = __ldg(reinterpret_cast<const uint32_t *>(row + 2LL * (at + j * kThreads * 8) + 14));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[j].w[i] = __funnelshift_r(x[j].w[i], i < 3 ? x[j].w[(i + 1) & 3] : beyond, 16);
     }
 }
 template <int DT>
@@ -308,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
     };
 
     Raw<DT> next[NV];
+    bool next_late = false;
     int row = 0, piece = 0, tile = 0, last = 0;            // what is being loaded: a beam's piece, up to tile `last`
     auto open = [&](unsigned u) {
         const unsigned o = u / q;
@@ -323,13 +352,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
         Raw<DT> x[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) x[j] = next[j];
+        if constexpr (DT != 2)
+            if (next_late) shift_tile<DT>(x, start_of(here), base + tid * 8);
         if (!ends || u + 1 != u1) {
             if (ends) open(++u);
             else ++tile;
             const int end = rows <= kMaxRows || goes_on(a, row) ? a.vocab : 0;
             const char *p = start_of(row);
             const int low = (int)(reinterpret_cast<uintptr_t>(p) & 15), align = low == 0 ? 16 : low & 3 ? 2 : 4;
-            load_tile<DT>(next, p, align, tile * TILE + tid * 8, end);
+            next_late = load_tile<DT>(next, p, align, tile * TILE + tid * 8, end, row == 0);
         } else {
             ++u;
         }
@@ -498,7 +529,8 @@ __device__ __forceinline__ double log_of(double l) {
 }
 
 // A CTA per request: its beams' sums, then the best of the candidates.
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, const Cut cut, const PartSum *sums,
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const Cut cut, const PartSum *sums,
                                                               const unsigned long long *lists, int *status) {
     // One is better than another when it is greater.  The order of its score, 0 for none; among equal ones the lower
     // beam, the greater logit, the lower token.  Integers: comparing 64-bit numbers is slow here.
@@ -512,48 +544,52 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
     double *s_top = dyn, *s_cum = s_top + kBeamMost;       // of each beam: its largest logit; its score less log sum
                                                            // e^(x - largest)
     Candidate *s_least = reinterpret_cast<Candidate *>(s_cum + kBeamMost);
-    Candidate *s_heads = s_least + 1, *s_cand = s_heads + kMaxLists;
-    int *s_parts = reinterpret_cast<int *>(s_cand + K * K);   // of each beam: lists it has, -1 where it has finished
-    int &s_n = s_parts[kBeamMost];
+    Candidate *s_heads = s_least + 1, *s_best = s_heads, *s_cand = s_heads + kMaxLists;
+    int *s_which = reinterpret_cast<int *>(s_cand + K * K), *s_list = s_which + kMaxLists;
+    int *s_parts = s_list + kBeamMost;                     // of each beam: lists it has, -1 where it has finished
+    int *s_count = s_parts + kBeamMost;
     const int row0 = blockIdx.x * W;
-    if (tid == 0) s_n = 0, *s_least = Candidate{0, 0};
+    if (tid < 4) s_count[tid] = 0;
+    if (tid == 0) *s_least = Candidate{0, 0};
     kv_begin();
     const unsigned long long *mine = lists + (long long)row0 * slots * K;
     // all loads at once: what a beam has no part for is not looked at
     unsigned long long head = 0;
     if (tid < n_lists) head = mine[(long long)tid * K];
-    for (int b = tid >> 5; b < W; b += kMergeThreads / 32) {
-        const PartSum *p = sums + (long long)(row0 + b) * slots;
-        const float score = a.scores[row0 + b];
-        const bool ended = a.finished && a.finished[row0 + b];
+    // `across` lanes a beam: as many as it may have pieces, a warp at most
+    const int across = slots > 16 ? 32 : slots > 8 ? 16 : slots > 4 ? 8 : slots > 2 ? 4 : slots;
+    for (int base = 0; base < W; base += THREADS / across) {
+        const int b = base + tid / across, part0 = tid % across;
+        const bool real = b < W;
+        const PartSum *p = sums + (long long)(row0 + (real ? b : 0)) * slots;
+        const float score = real ? a.scores[row0 + b] : 0.0f;
+        const bool ended = real && a.finished && a.finished[row0 + b];
         PartSum part = {0.0, 0.0f, 0};
-        if (lane < slots) part = p[lane];
+        if (part0 < slots) part = p[part0];
         double largest = 0.0, log_sum = 0.0;
-        int parts = __shfl_sync(0xffffffffu, part.parts, 0);
-        if (ended || !isfinite(score)) {
-            parts = isfinite(score) ? -1 : 0;
+        int parts = __shfl_sync(0xffffffffu, part.parts, lane - part0);
+        if (!real || ended || !isfinite(score)) parts = 0;
+        float top = part0 < parts ? part.m : -INFINITY;
+        for (int i = part0 + 32; i < parts; i += 32) top = fmaxf(top, p[i].m);
+        for (int d = across / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        double l = part0 < parts ? part.l * carried(part.m, top) : 0.0;
+        for (int i = part0 + 32; i < parts; i += 32) l += p[i].l * carried(p[i].m, top);
+        for (int d = across / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        // the row of a NaN or +inf has no probabilities, one without any token but -inf has no continuations
+        if (parts == 0) {
+            if (ended && isfinite(score)) parts = -1;
+        } else if (top == INFINITY || l != l) {
+            if (part0 == 0) kv_report(status);
+            parts = 0;
+        } else if (top == -INFINITY) {
+            parts = 0;
         } else {
-            float top = lane < parts ? part.m : -INFINITY;
-            for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, p[i].m);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            double l = lane < parts ? part.l * carried(part.m, top) : 0.0;
-            for (int i = lane + 32; i < parts; i += 32) l += p[i].l * carried(p[i].m, top);
-            for (int d = parts > 8 ? 16 : parts > 2 ? 4 : 1; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-            // the row of a NaN or +inf has no probabilities, one without any token but -inf has no continuations
-            if (top == INFINITY || l != l) {
-                if (lane == 0) kv_report(status);
-                parts = 0;
-            } else if (top == -INFINITY) {
-                parts = 0;
-            } else {
-                largest = top;
-                // relative to the largest, which may be far larger than the sum's logarithm
-                log_sum = log_of(l);
-                if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
-            }
+            largest = top;
+            // relative to the largest, which may be far larger than the sum's logarithm
+            log_sum = log_of(l);
+            if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
         }
-        if (lane == 0) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
+        if (real && part0 == 0) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
     }
     __syncthreads();
     // a list's i-th candidate
@@ -566,34 +602,83 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
         return Candidate{ordered64(s_cum[b] + ((double)key_value(key) - s_top[b])),
                          beam | key >> 32 << 24 | (0xffffffu - key_token(key))};
     };
-    // of so many sorted lists only the n with the best heads matter
-    if (n_lists >= K) {
-        for (int i = tid; i < n_lists; i += kMergeThreads) s_heads[i] = candidate(i, 0, i == tid ? head : mine[(long long)i * K]);
-        __syncthreads();
-        for (int i = tid; i < n_lists; i += kMergeThreads) {
-            const Candidate c = s_heads[i];
-            if (c.score == 0) continue;
-            int place = 0;
-#pragma unroll 4
-            for (int j = 0; j < n_lists; ++j) place += s_heads[j] > c;
-            if (place == K - 1) *s_least = c;
-        }
-        __syncthreads();
-    }
-    const Candidate least = *s_least;
-    for (int i = tid; i < n_lists * K; i += kMergeThreads) {
-        const int list = i / K, at = i - list * K;
-        if (n_lists >= K && least > s_heads[list]) continue;
-        const Candidate c = candidate(list, at, mine[i]);
-        if (c.score != 0 && !(least > c)) s_cand[atomicAdd(&s_n, 1)] = c;
+    // places for those threads of a warp that want one
+    auto place_for = [&](bool want, int *count) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, want);
+        int at = 0;
+        if (lane == 0 && bits) at = atomicAdd(count, __popc(bits));
+        return __shfl_sync(0xffffffffu, at, 0) + __popc(bits & ((1u << lane) - 1));
+    };
+    // the lists by their heads; only the n best of them matter
+    for (int base = 0; base < n_lists; base += THREADS) {
+        const int i = base + tid;
+        Candidate c = {0, 0};
+        if (i < n_lists) c = candidate(i, 0, base == 0 ? head : mine[(long long)i * K]);
+        const int at = place_for(c.score != 0, s_count);
+        if (c.score != 0) s_heads[at] = c, s_which[at] = i;
     }
     __syncthreads();
-    const int n = s_n;
-    for (int i = tid; i < n; i += kMergeThreads) {
-        const Candidate c = s_cand[i];
+    int heads = s_count[0];
+    if (heads > kFewHeads) {
+        // those from the n-th best score on, by the 32 bits that say most, which are found bit by bit
+        Candidate c = {0, 0};
+        int which = 0;
+        if (tid < heads) c = s_heads[tid], which = s_which[tid];
+        const uint32_t mine32 = (uint32_t)(c.score >> 32);
+        uint32_t low = 0;
+        for (int bit = 31; bit >= 0; --bit)
+            if (__syncthreads_count(mine32 >= (low | 1u << bit)) >= K) low |= 1u << bit;
+        const bool stays = tid < heads && mine32 >= low;
+        const int at = place_for(stays, s_count + 3);
+        if (stays) s_heads[at] = c, s_which[at] = which;
+        __syncthreads();
+        heads = s_count[3];
+    }
+    const int L = min(heads, K);
+    for (int i = tid; i < heads; i += THREADS) {
+        const Candidate c = s_heads[i];
         int place = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) place += s_cand[j] > c;
+        for (int j = 0; j < heads; ++j) place += s_heads[j] > c;
+        if (place < K) s_list[place] = s_which[i];
+        if (place == K - 1) *s_least = c;
+    }
+    __syncthreads();
+    // their candidates, the first ones of all lists, the second ones and so on.  The l-th of the list with the j-th best head
+    // has j + l better ones, one below n heads has n.
+    const Candidate least = *s_least;
+    for (int base = 0; base < L * K; base += THREADS) {
+        const int i = base + tid, l = i / L, j = i - l * L;
+        Candidate c = {0, 0};
+        if (i < L * K && j + l < K) c = candidate(s_list[j], l, mine[(long long)s_list[j] * K + l]);
+        if (least > c) c = {0, 0};
+        if (i < L * K) s_cand[i] = c;
+        const int at = place_for(c.score != 0, s_count + 1);
+        if (c.score != 0 && at < kFewCandidates) s_best[at] = c;
+    }
+    __syncthreads();
+    int n = s_count[1];
+    if (n > kFewCandidates) {
+        // where b lists have a better l-th one, (b + 1) (l + 1) - 1 are better: some n log n may be among the n best
+        for (int base = 0; base < L * K; base += THREADS) {
+            const int i = base + tid, l = i / L;
+            const Candidate c = i < L * K ? s_cand[i] : Candidate{0, 0};
+            int better = c.score != 0 ? 1 : K + 1;
+            if (c.score != 0)
+#pragma unroll 4
+                for (int j = l * L; j < (l + 1) * L; ++j) better += s_cand[j] > c;
+            const bool may = better * (l + 1) <= K;
+            const int at = place_for(may, s_count + 2);
+            if (may) s_best[at] = c;
+        }
+        __syncthreads();
+        n = s_count[2];
+    }
+    for (int i = tid; i < n; i += THREADS) {
+        const Candidate c = s_best[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place += s_best[j] > c;
         if (place >= K) continue;
         const int b = 63 - (int)(c.key >> 56), token = 0xffffff - (int)(c.key & 0xffffffu);
         const long long at = (long long)blockIdx.x * K + place;
@@ -602,7 +687,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const BeamArgs a, 
         a.out_tokens[at] = token;
         if (a.out_finished) a.out_finished[at] = s_parts[b] < 0 || token == a.end_token;
     }
-    for (int i = n + tid; i < K; i += kMergeThreads) {
+    for (int i = n + tid; i < K; i += THREADS) {
         const long long at = (long long)blockIdx.x * K + i;
         a.out_scores[at] = -INFINITY;
         a.out_rows[at] = a.out_tokens[at] = -1;
@@ -629,10 +714,14 @@ cudaError_t launch_beam_select(const BeamArgs &a, void *workspace, const DeviceI
                     : a.dtype == 1 ? kv_launch(scan_kernel<1>, grid, block, 0, s, pdl, a, cut, sums, lists)
                                    : kv_launch(scan_kernel<2>, grid, block, 0, s, pdl, a, cut, sums, lists);
     if (e != cudaSuccess) return e;
-    const size_t smem = 2 * kBeamMost * 8 + (1 + kMaxLists + (size_t)a.n_out * a.n_out) * 16 + (kBeamMost + 1) * 4;
-    e = raise_smem_cap(reinterpret_cast<const void *>(merge_kernel), smem);
+    const size_t smem = 2 * kBeamMost * 8 + (1 + kMaxLists + (size_t)a.n_out * a.n_out) * 16 + (kMaxLists + 2 * kBeamMost + 4) * 4;
+    // few candidates are in order sooner in a small CTA, many in a large one
+    const int n_lists = a.width * cut.slots;
+    const bool large = n_lists > 256 || std::min(n_lists, a.n_out) * a.n_out > kSmallMerge;   // no more heads than threads
+    const auto merge = large ? merge_kernel<1024> : merge_kernel<256>;
+    e = raise_smem_cap(reinterpret_cast<const void *>(merge), smem);
     if (e != cudaSuccess) return e;
-    return kv_launch(merge_kernel, dim3(a.n_groups), dim3(kMergeThreads), smem, s, pdl, a, cut, sums, lists, dev.status);
+    return kv_launch(merge, dim3(a.n_groups), dim3(large ? 1024 : 256), smem, s, pdl, a, cut, sums, lists, dev.status);
 }
 
 long long beam_select_workspace(int n_groups, int width, int vocab, int n_out) {
