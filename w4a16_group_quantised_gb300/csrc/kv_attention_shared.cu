@@ -21,9 +21,9 @@
 //
 // Measured on the GPU (32 query heads of 128 dims; w4a16_kv_attention in
 // brackets): 64 sequences on a system prompt of 8192 tokens with 1 to 2000 of
-// their own, e4m3, 164 MB: 62 us (159), 2.7 TB/s; 24 and 40 sequences of 1 to 5
+// their own, e4m3, 164 MB: 63 us (159), 2.6 TB/s; 24 and 40 sequences of 1 to 5
 // tokens on documents of 20 and 32 thousand, 109 GFLOP: 212 us (760), 510
-// TFLOP/s; 16 prompts of 100 to 1920 tokens in 3 to 8 samples: 52 us (55).  Bound
+// TFLOP/s; 16 prompts of 100 to 1920 tokens in 3 to 8 samples: 51 us (55).  Bound
 // by the two kernels' own ways: what they take to start and end (the plan 5 us,
 // the join 4 to 8 beside), their tiles' chains, and the codes' conversion, which
 // comes again for every 8 or 256 rows.
@@ -41,20 +41,21 @@ constexpr int kBigRows = 16;              // more rows a kv head may be kv_atten
 
 // What entries take, in ns on kCostSms SMs with 128 dims: kv_few_rows.cuh 16 keys of
 // a tile of 8 rows, with pages of 16 or of more tokens, or of 16 rows (a tile's start
-// and end count for 80 or 192 keys); kv_attention_tc.cu 128 keys of a tile of 256 (384
-// keys); and what each kernel takes to start and end.  Fitted to calls at ten
-// divisions of the SMs: 64 sequences on a prompt of 8192 tokens take 128 / 94 / 81 /
-// 77 / 91 / 122 / 261 us with 20 / 40 / 60 / 80 / 100 / 120 / 140 of 152 SMs for the
-// shared keys, 99 with one kernel after the other.
-// Few rows / tensor cores for the shared keys, us a call with 8 kv heads: 1 group of 24
-// to 64 rows over 500 keys 32 to 34 / 54 to 56, over 20000 56 to 77 / 87 to 91; 16
-// groups over 500 keys 56 / 58 at 32 rows, 69 / 65 at 64, over 4000 keys 126 / 126 at
-// 32, 163 / 130 at 40, 200 / 136 at 64.
-constexpr float kFewNs8 = 0.75f, kFewNs8Wide = 0.6f, kFewNs16 = 1.05f, kManyNs = 16.0f, kOf64Dims = 0.6f;
-constexpr float kFewStartNs = 10000.0f, kManyStartNs = 45000.0f;
+// and end count for 192 or 288 keys); kv_attention_tc.cu 128 keys of a tile of 256 (384
+// keys); and what each kernel takes to start and end.  Fitted to 170 calls of 8 to 256
+// sequences in 1 to 16 groups that read 190 to 840 MB unshared: all 170 take 10.2 ms
+// so, 9.9 with the better choice for each, 11.1 with starts of 10 and 45 us and 80 keys
+// a tile, and 64 sequences on a prompt of 8192 tokens 64 us (73 with 1.5 of the
+// others' time, which most like as well).
+// Few rows / tensor cores for the shared keys, us a call with 8 heads to each of 4 kv
+// heads, 64 keys of each sequence's own: one group of 8 sequences over 25000 keys
+// 47 / 42, over 51000 82 / 53; of 32 over 6000 48 / 40, over 13000 83 / 46; 16 groups of
+// 16 over 700 keys 57 / 61, over 1500 89 / 65; 4 groups of 4 over 12000 48 / 49.
+constexpr float kFewNs8 = 0.75f, kFewNs8Wide = 0.66f, kFewNs16 = 1.05f, kManyNs = 16.0f, kOf64Dims = 0.55f;
+constexpr float kFewStartNs = 16000.0f, kManyStartNs = 40000.0f;
 constexpr int kCostSms = 152;
 __host__ __device__ inline unsigned long long few_steps(long long rows, int tile_shift, int keys) {
-    const unsigned ends = tile_shift == 3 ? 5 : 12;
+    const unsigned ends = tile_shift == 3 ? 12 : 18;
     return (unsigned long long)((rows + (1 << tile_shift) - 1) >> tile_shift) * (((keys + 15) >> 4) + ends);
 }
 __host__ __device__ inline unsigned long long many_steps(long long rows, int keys) {
@@ -153,8 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
     };
     sum(few, s_few), sum(many, s_many), sum(rest, s_rest);
     __syncthreads();
-    // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.  Half as
-    // much again for that one's work beside the other: with too few SMs it is by far the last, with too many hardly earlier.
+    // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.
     const float few_ns = p.few_ns * kCostSms, on_many = (float)s_many * p.many_ns * kCostSms, on_rest = (float)s_rest * few_ns;
     const bool some_rest = s_rest > 0;
     if (p.may_many && p.choice != 1 && s_few > 0) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
                 t = kManyStartNs + on_many / p.sms + (some_rest ? kFewStartNs + on_rest / p.sms : 0.0f);
             } else {
                 if (!p.beside || !some_rest) continue;
-                t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + 1.5f * on_rest / (p.sms - k));
+                t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + on_rest / (p.sms - k));
             }
             atomicMin(&s_best, (unsigned)fminf(t, 4.0e6f) << 10 | (unsigned)k);   // up to 4 ms, and k
         }
@@ -283,10 +283,20 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     return s;
 }
 
-// Bytes of cache up to which kv_attention is called instead, should all sequences be as long as the table is wide: its one
-// launch is the faster one there, this / that in us: 4 beams on 901 tokens (8 MB) 33 / 20, 8 x 4 sequences on 200 (17 MB) 48 /
-// 22, 8 x 2 on 1000 (34 MB) 28 / 26, 16 on 4000 (133 MB) 38 / 40, 8 x 8 on 4000 (532 MB) 76 / 102.
-constexpr double kLeastBytes = 32 << 20;
+// Whether kv_attention is called instead, by what there is at most: sequences as long as the table is wide.  Its one launch
+// is the faster one for few bytes of cache, and where sequences fill tiles by themselves: what sharing saves are tiles, of 8
+// rows (which one sequence with 8 rows fills), or of the 256 of kv_attention_tc.cu, which take as long as some 3.6 of 8.
+// This / that in us, bytes as all sequences read them:
+//    1 row a sequence (query heads of a kv head, times tokens): 48 MB 16 / 18, 96 MB 17 to 27 / 24, 192 MB 19 to 36 / 38
+//    4 rows: 48 MB 18 to 26 / 18, 96 MB 25 to 33 / 25, 192 MB 33 to 41 / 38, 400 MB 50 to 62 / 67
+//    8 rows: 96 MB 32 to 40 / 26 to 29, 192 MB 42 to 59 / 40, 400 MB 45 to 68 / 67 (16 sequences in 4 groups 86)
+//    16 rows: 62 MB 43 / 30, 125 MB 50 / 52, 188 MB 43 / 53.  32 rows: 31 MB 37 / 30, 62 MB 45 / 52, 94 MB 40 / 52
+//    64 rows: 62 MB 56 / 45, 94 MB 47 / 66, 125 MB 82 / 81, 188 MB 65 / 101
+//    128 rows: 62 MB 75 / 45, 125 MB 122 / 82, 188 MB 91 / 102, 375 MB 156 / 196.  256 rows: 375 MB 303 / 226
+bool kv_attention_instead(double bytes, int rows) {
+    const double tiles = std::min((double)((rows + 7) / 8), 3.6);
+    return rows > 96 || bytes * tiles <= (40 << 20) * (double)std::min(std::max(rows, 2), 8);
+}
 
 }  // namespace
 
@@ -295,7 +305,10 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &a, const KvCache &
     const int group = a.n_heads / c.n_kv_heads, rows = b.n_tokens * a.n_heads;
     const long long longest = (long long)b.max_blocks << c.page_shift;
     const int forced = shared_kernels();
-    const bool plain = forced ? g.n_groups == 0 : g.n_groups == 0 || 2.0 * longest * b.n_seqs * c.n_kv_heads * c.head_dim <= kLeastBytes;
+    const int seqs = std::min(b.n_seqs, b.n_tokens);          // that bring tokens, at most
+    const int seq_rows = (int)(((long long)b.n_tokens * group + seqs - 1) / seqs);
+    const bool plain = g.n_groups == 0 ||
+                       (!forced && kv_attention_instead(2.0 * longest * seqs * c.n_kv_heads * c.head_dim, seq_rows));
     // the tensor-core kernel is launched where the plan might ask for it
     const int tile_rows = few_tile_rows(a.max_q_len, group), tile_shift = tile_rows == 16 ? 4 : 3;
     const long long all = (long long)b.n_tokens * group, entries = (long long)g.n_groups + b.n_seqs;
