@@ -34,8 +34,8 @@
 //    67 us with all candidates counted, 16 so.
 //
 // Measured on the GPU: 256 beams of 64 requests, a fifth of them ended, over
-// 131072 bf16 logits, 54 MB: 23 us, 2.3 TB/s of logits; 40 beams over 50001 fp16
-// logits 14 us; one beam over 32000 fp32 logits 9.5 us.  Of the 23, 7 are the second
+// 131072 bf16 logits, 54 MB: 21 us, 2.5 TB/s of logits; 40 beams over 50001 fp16
+// logits 13 us; one beam over 32000 fp32 logits 8.5 us.  Of the 21, 6 are the second
 // kernel; the first issues 11 instructions a logit (6 of them arithmetic of the sum)
 // at 0.55 a cycle and scheduler, 2.7 CTAs an SM, each with 16 KB on their way.
 #include <algorithm>
