@@ -30,15 +30,16 @@
 //  * The second kernel, a CTA per request, joins the pieces' sums, scores the
 //    candidates in 64 bits and picks the n best by counting who is better.
 //    Of sorted lists only the n with the best heads can hold any, and of these
-//    lists' l-th candidates only the n / l best: 32 of 16 beams with 60 logits took
-//    67 us with all candidates counted, 16 so.
+//    lists' l-th candidates only the n / l best: 32 of 16 beams with 79 logits took
+//    67 us with all candidates counted, 12 so.
 //
 // Measured on the GPU: 256 beams of 64 requests, a fifth of them ended, over
-// 131072 bf16 logits, 54 MB: 21 us, 2.5 TB/s of logits; 40 beams over 50001 fp16
-// logits 13 us; one beam over 32000 fp32 logits 8.5 us.  Of the 21, 6 are the second
+// 131072 bf16 logits, 54 MB: 21 us, 2.6 TB/s of logits; 40 beams over 50001 fp16
+// logits 11.5 us; one beam over 32000 fp32 logits 8 us.  Of the 21, 6 are the second
 // kernel; the first issues 11 instructions a logit (6 of them arithmetic of the sum)
 // at 0.55 a cycle and scheduler, 2.7 CTAs an SM, each with 16 KB on their way.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.cuh"
 
@@ -132,6 +133,26 @@ __device__ __forceinline__ double from_ordered64(unsigned long long u) {
     return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
 }
 
+// How many of `list`'s first n keys are above `mine`, 8 of them looked at together: one by one takes 23 cycles a key,
+// 3200 of the 11000 of a piece of 2000 tokens of which 32 are kept.  The list's room is a multiple of 8, and it is 16-byte aligned.
+__device__ __forceinline__ int better_than(unsigned long long mine, const unsigned long long *list, int n) {
+    int better = 0, j = 0;
+    auto look = [&](auto whole) {
+        ulonglong2 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = reinterpret_cast<const ulonglong2 *>(list + j)[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            better += v[k].x > mine && (decltype(whole)::value || j + 2 * k < n);
+            better += v[k].y > mine && (decltype(whole)::value || j + 2 * k + 1 < n);
+        }
+    };
+#pragma unroll 1
+    for (; j + 8 <= n; j += 8) look(std::true_type{});
+    if (j < n) look(std::false_type{});
+    return better;
+}
+
 // A vector of 8 logits as it is in memory.
 template <int DT>
 struct Raw {
@@ -171,6 +192,14 @@ __device__ __forceinline__ bool load_tile(Raw<DT> (&x)[NV], const char *row, int
         const uint32_t *words = reinterpret_cast<const uint32_t *>(p);
         const uint16_t *halves = reinterpret_cast<const uint16_t *>(p);
         const uint32_t none = DT == 0 ? 0xfc00u : 0xff80u;
+        if (align == 16 && at + 8 <= end) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                const uint4 v = ldg_stream_v4(p + 4 * i);
+                x[j].w[i] = v.x, x[j].w[i + 1] = v.y, x[j].w[i + 2] = v.z, x[j].w[i + 3] = v.w;
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (DT == 2)
@@ -219,8 +248,8 @@ template <int DT>
 __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, const Cut cut, PartSum *sums,
                                                            unsigned long long *lists) {
     constexpr int PER = kPer<DT>, NV = PER / 8, TILE = kThreads * PER;
-    __shared__ unsigned long long list[kList];
-    __shared__ unsigned long long s_best[kBeamMost], s_maxima[kThreads];
+    __shared__ __align__(16) unsigned long long list[kList];
+    __shared__ __align__(16) unsigned long long s_best[kBeamMost], s_maxima[kThreads];
     __shared__ float s_group[kThreads];
     __shared__ unsigned long long s_least;
     __shared__ float s_hi[kWarps], s_lo[kWarps], s_max[kWarps];
@@ -281,9 +310,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
 #pragma unroll 1
         for (int i = tid; i < n; i += kThreads) {
             const unsigned long long mine = list[i];
-            int better = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) better += list[j] > mine;
+            const int better = better_than(mine, list, n);
             if (better < K) s_best[better] = mine;
         }
         __syncthreads();
@@ -317,9 +344,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
         s_maxima[tid] = best;
         if (tid == 0) s_least = 0;
         __syncthreads();
-        int better = 0;
-#pragma unroll 4
-        for (int j = 0; j < kThreads; ++j) better += s_maxima[j] > best;
+        const int better = better_than(best, s_maxima, kThreads);
         if (best != 0 && better == K - 1) s_least = best;
         __syncthreads();
         if (best >= max(s_least, 1ull))
@@ -528,16 +553,42 @@ __device__ __forceinline__ double log_of(double l) {
     return fma((double)e, 0.693147180559945309417, (double)(2.0f * q) + (double)rest);
 }
 
+// One is better than another when it is greater.  The order of its score, 0 for none; among equal ones the lower
+// beam, the greater logit, the lower token.  Integers: comparing 64-bit numbers is slow here.
+struct __align__(16) Candidate {
+    unsigned long long score, key;                         // key: 63 - beam, the logit's order, 2^24 - 1 - token
+    __device__ bool operator>(const Candidate &o) const {
+        // whether o less this borrows, as 128-bit numbers: with branches a comparison takes 100 cycles, with both words'
+        // comparisons 30
+        uint32_t borrow;
+        asm("{ .reg .u64 t; sub.cc.u64 t, %1, %2; subc.cc.u64 t, %3, %4; subc.u32 %0, 0, 0; }"
+            : "=r"(borrow) : "l"(o.key), "l"(key), "l"(o.score), "l"(score));
+        return borrow != 0;
+    }
+};
+// How many of the n from `list` on are better, eight of them looked at together.
+__device__ __forceinline__ int better_than(const Candidate &c, const Candidate *list, int n) {
+    int better = 0, j = 0;
+#pragma unroll 1
+    for (; j + 8 <= n; j += 8) {
+        Candidate o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = list[j + k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) better += o[k] > c;
+    }
+#pragma unroll 1
+    for (; j < n; j += 2) {
+        const Candidate o0 = list[j], o1 = list[min(j + 1, n - 1)];
+        better += (o0 > c) + (j + 1 < n && o1 > c);
+    }
+    return better;
+}
+
 // A CTA per request: its beams' sums, then the best of the candidates.
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const Cut cut, const PartSum *sums,
+__global__ void __launch_bounds__(THREADS, 1) merge_kernel(const BeamArgs a, const Cut cut, const PartSum *sums,
                                                               const unsigned long long *lists, int *status) {
-    // One is better than another when it is greater.  The order of its score, 0 for none; among equal ones the lower
-    // beam, the greater logit, the lower token.  Integers: comparing 64-bit numbers is slow here.
-    struct Candidate {
-        unsigned long long score, key;                     // key: 63 - beam, the logit's order, 2^24 - 1 - token
-        __device__ bool operator>(const Candidate &o) const { return score > o.score || (score == o.score && key > o.key); }
-    };
     // no static shared memory: raise_smem_cap
     extern __shared__ double dyn[];
     const int tid = threadIdx.x, lane = tid & 31, K = a.n_out, W = a.width, slots = cut.slots, n_lists = W * slots;
@@ -556,8 +607,29 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
     // all loads at once: what a beam has no part for is not looked at
     unsigned long long head = 0;
     if (tid < n_lists) head = mine[(long long)tid * K];
-    // `across` lanes a beam: as many as it may have pieces, a warp at most
+    const float own_score = tid < W ? a.scores[row0 + tid] : 0.0f;
+    // a beam's sum l and largest logit, and what they come to
+    auto finish = [&](int b, float score, double l, float top, int parts, bool writes) {
+        double largest = 0.0, log_sum = 0.0;
+        // the row of a NaN or +inf has no probabilities, one without any token but -inf has no continuations
+        if (parts > 0 && (top == INFINITY || l != l)) {
+            if (writes) kv_report(status);
+            parts = 0;
+        } else if (parts > 0 && top == -INFINITY) {
+            parts = 0;
+        } else if (parts > 0) {
+            largest = top;
+            // relative to the largest, which may be far larger than the sum's logarithm
+            log_sum = log_of(l);
+            if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
+        }
+        if (writes) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
+    };
+    // `across` lanes a beam: as many as it may have pieces, a warp at most.  Of more than a few warps the logarithms come
+    // afterwards, a lane a beam: 64-bit instructions take a warp 16 cycles and more each (16 beams of 32 pieces: 10400
+    // cycles, 7900 so; 4 beams of 8 3300, 4200 so).
     const int across = slots > 16 ? 32 : slots > 8 ? 16 : slots > 4 ? 8 : slots > 2 ? 4 : slots;
+    const bool afterwards = W * across > 128;
     for (int base = 0; base < W; base += THREADS / across) {
         const int b = base + tid / across, part0 = tid % across;
         const bool real = b < W;
@@ -566,7 +638,6 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
         const bool ended = real && a.finished && a.finished[row0 + b];
         PartSum part = {0.0, 0.0f, 0};
         if (part0 < slots) part = p[part0];
-        double largest = 0.0, log_sum = 0.0;
         int parts = __shfl_sync(0xffffffffu, part.parts, lane - part0);
         if (!real || ended || !isfinite(score)) parts = 0;
         float top = part0 < parts ? part.m : -INFINITY;
@@ -575,23 +646,16 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
         double l = part0 < parts ? part.l * carried(part.m, top) : 0.0;
         for (int i = part0 + 32; i < parts; i += 32) l += p[i].l * carried(p[i].m, top);
         for (int d = across / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        // the row of a NaN or +inf has no probabilities, one without any token but -inf has no continuations
-        if (parts == 0) {
-            if (ended && isfinite(score)) parts = -1;
-        } else if (top == INFINITY || l != l) {
-            if (part0 == 0) kv_report(status);
-            parts = 0;
-        } else if (top == -INFINITY) {
-            parts = 0;
-        } else {
-            largest = top;
-            // relative to the largest, which may be far larger than the sum's logarithm
-            log_sum = log_of(l);
-            if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
-        }
-        if (real && part0 == 0) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
+        if (ended && isfinite(score)) parts = -1;
+        const bool writes = real && part0 == 0;
+        if (!afterwards) finish(b, score, l, top, parts, writes);
+        else if (writes) s_top[b] = top, s_cum[b] = l, s_parts[b] = parts;
     }
     __syncthreads();
+    if (afterwards) {
+        if (tid < W) finish(tid, own_score, s_cum[tid], (float)s_top[tid], s_parts[tid], true);
+        __syncthreads();
+    }
     // a list's i-th candidate
     auto candidate = [&](int list, int i, unsigned long long key) {
         const int b = list / slots, part = list - b * slots, parts = s_parts[b];
@@ -637,9 +701,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
     const int L = min(heads, K);
     for (int i = tid; i < heads; i += THREADS) {
         const Candidate c = s_heads[i];
-        int place = 0;
-#pragma unroll 4
-        for (int j = 0; j < heads; ++j) place += s_heads[j] > c;
+        const int place = better_than(c, s_heads, heads);
         if (place < K) s_list[place] = s_which[i];
         if (place == K - 1) *s_least = c;
     }
@@ -663,11 +725,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
         for (int base = 0; base < L * K; base += THREADS) {
             const int i = base + tid, l = i / L;
             const Candidate c = i < L * K ? s_cand[i] : Candidate{0, 0};
-            int better = c.score != 0 ? 1 : K + 1;
-            if (c.score != 0)
-#pragma unroll 4
-                for (int j = l * L; j < (l + 1) * L; ++j) better += s_cand[j] > c;
-            const bool may = better * (l + 1) <= K;
+            const bool may = c.score != 0 && (better_than(c, s_cand + l * L, L) + 1) * (l + 1) <= K;
             const int at = place_for(may, s_count + 2);
             if (may) s_best[at] = c;
         }
@@ -676,9 +734,7 @@ __global__ void __launch_bounds__(THREADS) merge_kernel(const BeamArgs a, const 
     }
     for (int i = tid; i < n; i += THREADS) {
         const Candidate c = s_best[i];
-        int place = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) place += s_best[j] > c;
+        const int place = better_than(c, s_best, n);
         if (place >= K) continue;
         const int b = 63 - (int)(c.key >> 56), token = 0xffffff - (int)(c.key & 0xffffffu);
         const long long at = (long long)blockIdx.x * K + place;
