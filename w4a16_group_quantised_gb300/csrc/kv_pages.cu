@@ -446,11 +446,11 @@ __global__ void __launch_bounds__(kGrowThreads)
     const int first = g.len >> shift, start = ((g.len + (1 << shift) - 1) >> shift) - g.copies;
     const int blocks = ((g.len + g.n - 1) >> shift) + 1 - first, rank = g.pages - g.need - start;
     int *entries = table + (long long)me * max_blocks;
-    const int each = min(kGrowThreads, (blocks + parts - 1) / parts);
+    // the last thread has no block of its own: it finds the page of the copy, which every part has a hand in
+    const int each = min(kGrowThreads - 1, (blocks + parts - 1) / parts);
     for (int b0 = part * each; b0 < blocks || (b0 == part * each && g.copies); b0 += parts * each) {
         const int blk = first + b0 + tid;
         const bool mine = tid < each && b0 + tid < blocks;
-        // the last thread finds the page of the copy, which every part has a hand in
         const bool copy = g.copies && b0 == part * each && tid == kGrowThreads - 1;
         const int r = mine && blk >= start ? rank + blk : copy ? rank + start : -1;
         const int p = __syncthreads_or(r >= 0) ? page_of_rank(w.bits, w.counts, n_chunks, r, before, scratch) : -1;
