@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
     // Both kernels side by side, on some SMs each, or one after the other on all; or the few-rows kernel alone.
     const float few_ns = p.few_ns * kCostSms, on_many = (float)s_many * p.many_ns * kCostSms, on_rest = (float)s_rest * few_ns;
     const bool some_rest = s_rest > 0;
+    // The least time t and its k in one word: t is above 0, so that its bits are in its order, and of the 23 of its fraction
+    // 13 do; the 10 below them are k.  (A cut t would be the same for every k from the cut on, and k = 1 the least.)
     if (p.may_many && p.choice != 1 && s_few > 0) {
         for (int k = threadIdx.x + 1; k <= p.sms; k += kPlanThreads) {
             float t;
@@ -166,13 +168,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_shared_kernel(const PlanPar
                 if (!p.beside || !some_rest) continue;
                 t = fmaxf(kManyStartNs + on_many / k, kFewStartNs + on_rest / (p.sms - k));
             }
-            atomicMin(&s_best, (unsigned)fminf(t, 4.0e6f) << 10 | (unsigned)k);   // up to 4 ms, and k
+            atomicMin(&s_best, (__float_as_uint(t) & ~1023u) | (unsigned)k);
         }
         __syncthreads();
     }
     if (threadIdx.x == 0) {
         const float alone = kFewStartNs + (on_rest + (float)s_few * few_ns) / p.sms;
-        const bool use = s_best != 0xffffffffu && (p.choice == 2 || alone >= 4.0e6f || (float)(s_best >> 10) < alone);
+        const bool use = s_best != 0xffffffffu && (p.choice == 2 || __uint_as_float(s_best & ~1023u) < alone);
         const int k = use ? (int)(s_best & 1023) : 0;
         p.use_many[0] = use;
         p.use_many[1] = k;
