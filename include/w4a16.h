@@ -634,8 +634,10 @@ int w4a16_kv_pool_workspace(int n_pages, long long *bytes);
  * request's n_out best: c, the beam's row in [0, n_groups * width) and the
  * token, in falling order: tokens of one beam as their logits are, equal ones in
  * the order of (row, token).  Beams are compared in 64 bits; what is off in c
- * is its beam's logarithm, by 2^-18 at most and some 2^-26 in earnest (sums of
- * exponentials in 32 bits).  c is rounded once.
+ * is its beam's logarithm (exponentials and sums in 32 bits), by 2^-18 at most,
+ * 2^-20 where one token has nearly all of the probability; some 2^-24 to 2^-22
+ * in earnest.  Continuations of different beams that are closer than that may
+ * come in either order; no c is above its beam's score.  c is rounded once.
  *   - A token of logit -inf, a beam whose score is not finite, and one whose
  *     logits are all -inf give nothing.  Where too few are left the rest of the
  *     n_out places are empty: -inf, row -1, token -1.

@@ -14,10 +14,14 @@
 //    exchanged: 2^(x log2 e - R) with R the integer next to its largest x log2 e,
 //    so that sums with other references differ by a power of two, exactly.
 //    log2 e is two fp32 numbers; a thread's part of a tile is summed in fp32, tiles
-//    and threads in two fp32 numbers, pieces in 64 bits: the continuations of
-//    different beams, a few 1e-2 apart in earnest, are told apart down to about
-//    1e-8.  Which thread sums what goes by the token alone, so that equal beams
-//    have equal sums.
+//    and threads in two fp32 numbers, pieces in 64 bits.  What is off in a beam's
+//    logarithm: where one token has nearly all of the probability, its own
+//    exponential, 2^-22, its exponent's two roundings, 2^-25, and the additions
+//    of its tile, 2^-24 each of up to 10: 2^-20 together, 3e-7 the most and 7e-8 as a
+//    root mean square over 512 rows each of 30 to 131072 logits; 8e-8 the most where
+//    many of 32000 and more share it.  The continuations of different beams are a few
+//    1e-2 apart in earnest; those closer than that may change places.  Which thread
+//    sums what goes by the token alone, so that equal beams have equal sums.
 //  * Within a beam c rises with x: candidates are logits, kept as 64-bit keys
 //    (the value's order, then the lower token).  Threads note the vectors of 8 whose
 //    largest logit is above the n-th best so far; every 8 tiles, and at a piece's
@@ -622,6 +626,8 @@ __global__ void __launch_bounds__(THREADS, 1) merge_kernel(const BeamArgs a, con
             // relative to the largest, which may be far larger than the sum's logarithm
             log_sum = log_of(l);
             if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
+            // the largest counts for 1: a sum that rounding has below that would give its token more than its beam has
+            if (__double2hiint(log_sum) < 0) log_sum = 0.0;
         }
         if (writes) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
     };
