@@ -533,6 +533,14 @@ int w4a16_kv_attention_workspace(int n_heads, int n_kv_heads, int head_dim, int 
  * the row of one of its sequences, where that is worth it; the result is
  * w4a16_kv_attention's but for rounding (sums over the shared keys and over
  * the others are joined in fp32).
+ *   - The shortest past of a group's sequences that bring tokens is where its
+ *     shared pages end: one sequence with little cached (an empty row that gets
+ *     its first token) has the others read what they have in common each for
+ *     itself.  Leave it out of the group, or have it bring no token.
+ *   - Whether it is worth it goes by the call's sizes, every sequence taken to be
+ *     as long as the table is wide; w4a16_kv_attention is called where that is
+ *     little.  In a table much wider than its sequences little cache is taken
+ *     for much: a call of a few us may take a third more.
  * workspace: w4a16_kv_attention_shared_workspace bytes, as above. */
 int w4a16_kv_attention_shared(const void *q, long long q_stride, int n_heads, const w4a16_kv_cache_t *cache,
                               const w4a16_kv_batch_t *batch, int max_q_len, const int32_t *group_starts,

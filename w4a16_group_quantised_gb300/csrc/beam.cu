@@ -5,7 +5,8 @@
 // is worth
 //     c(b, t) = s_b + x_bt - log sum_t' e^x_bt'
 // and the n best of a request's beams come out in order, ties to the lower
-// beam, then the lower token.  Bound by reading the logits once.
+// beam, then the lower token.  It cannot do without reading the logits once; few
+// of them take two launches' chains of loads, many what is worked out for each.
 //
 //  * The logits of each beam that goes on are tiles, cut into as many pieces as
 //    fill the GPU; a second kernel joins a beam's pieces.  The next tile is on its

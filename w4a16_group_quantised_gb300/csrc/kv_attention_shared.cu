@@ -21,9 +21,9 @@
 //
 // Measured on the GPU (32 query heads of 128 dims; w4a16_kv_attention in
 // brackets): 64 sequences on a system prompt of 8192 tokens with 1 to 2000 of
-// their own, e4m3, 164 MB: 63 us (159), 2.6 TB/s; 24 and 40 sequences of 1 to 5
-// tokens on documents of 20 and 32 thousand, 109 GFLOP: 212 us (760), 510
-// TFLOP/s; 16 prompts of 100 to 1920 tokens in 3 to 8 samples: 51 us (55).  Bound
+// their own, e4m3, 164 MB: 62 us (154), 2.6 TB/s; 31 and 40 sequences of 1 to 5
+// tokens on documents of 32 thousand, 109 GFLOP: 211 us (759), 515
+// TFLOP/s; 16 prompts of 100 to 1920 tokens in 3 to 8 samples: 52 us (52).  Bound
 // by the two kernels' own ways: what they take to start and end (the plan 5 us,
 // the join 4 to 8 beside), their tiles' chains, and the codes' conversion, which
 // comes again for every 8 or 256 rows.
@@ -285,7 +285,8 @@ Scratch scratch_of(void *ws, int n_heads, int n_kv_heads, int head_dim, int n_se
     return s;
 }
 
-// Whether kv_attention is called instead, by what there is at most: sequences as long as the table is wide.  Its one launch
+// Whether kv_attention is called instead, by what there is at most: sequences as long as the table is wide, the lengths
+// being on the device (in a table of 2048 columns four beams of 901 tokens take 16.7 us, in one of 61 12.8).  Its one launch
 // is the faster one for few bytes of cache, and where sequences fill tiles by themselves: what sharing saves are tiles, of 8
 // rows (which one sequence with 8 rows fills), or of the 256 of kv_attention_tc.cu, which take as long as some 3.6 of 8.
 // This / that in us, bytes as all sequences read them:
