@@ -643,8 +643,8 @@ int w4a16_kv_pool_workspace(int n_pages, long long *bytes);
  * token, in falling order: tokens of one beam as their logits are, equal ones in
  * the order of (row, token).  Beams are compared in 64 bits; what is off in c
  * is its beam's logarithm (exponentials and sums in 32 bits), by 2^-18 at most,
- * 2^-20 where one token has nearly all of the probability; some 2^-24 to 2^-22
- * in earnest.  Continuations of different beams that are closer than that may
+ * some 2^-24 to 2^-22 in earnest, and nothing where one token has all of the
+ * probability.  Continuations of different beams that are closer than that may
  * come in either order; no c is above its beam's score.  c is rounded once.
  *   - A token of logit -inf, a beam whose score is not finite, and one whose
  *     logits are all -inf give nothing.  Where too few are left the rest of the

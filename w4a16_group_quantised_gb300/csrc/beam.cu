@@ -15,14 +15,14 @@
 //    exchanged: 2^(x log2 e - R) with R the integer next to its largest x log2 e,
 //    so that sums with other references differ by a power of two, exactly.
 //    log2 e is two fp32 numbers; a thread's part of a tile is summed in fp32, tiles
-//    and threads in two fp32 numbers, pieces in 64 bits.  What is off in a beam's
-//    logarithm: where one token has nearly all of the probability, its own
-//    exponential, 2^-22, its exponent's two roundings, 2^-25, and the additions
-//    of its tile, 2^-24 each of up to 10: 2^-20 together, 3e-7 the most and 7e-8 as a
-//    root mean square over 512 rows each of 30 to 131072 logits; 8e-8 the most where
-//    many of 32000 and more share it.  The continuations of different beams are a few
-//    1e-2 apart in earnest; those closer than that may change places.  Which thread
-//    sums what goes by the token alone, so that equal beams have equal sums.
+//    and threads in two fp32 numbers, pieces in 64 bits, and the logarithm is of the
+//    sum over the largest weight as it was added up, whose error cancels: where one
+//    token has all of the probability nothing is off.  Else what is: the others'
+//    exponentials and the largest's, 2^-22 each, their exponents' roundings, and the
+//    additions of a tile, 2^-24 each of up to 10: 2e-7 the most and 6e-8 as a root mean
+//    square over 512 rows each of 30 to 131072 logits.  The continuations of different
+//    beams are a few 1e-2 apart in earnest; those closer than that may change places.
+//    Which thread sums what goes by the token alone, so that equal beams have equal sums.
 //  * Within a beam c rises with x: candidates are logits, kept as 64-bit keys
 //    (the value's order, then the lower token).  Threads note the vectors of 8 whose
 //    largest logit is above the n-th best so far; every 8 tiles, and at a piece's
@@ -40,7 +40,7 @@
 //
 // Measured on the GPU: 256 beams of 64 requests, a fifth of them ended, over
 // 131072 bf16 logits, 54 MB: 21 us, 2.6 TB/s of logits; 40 beams over 50001 fp16
-// logits 11.5 us; one beam over 32000 fp32 logits 8 us.  Of the 21, 6 are the second
+// logits 11.3 us; one beam over 32000 fp32 logits 8 us.  Of the 21, 6 are the second
 // kernel; the first issues 11 instructions a logit (6 of them arithmetic of the sum)
 // at 0.55 a cycle and scheduler, 2.7 CTAs an SM, each with 16 KB on their way.
 #include <algorithm>
@@ -537,17 +537,18 @@ __global__ void __launch_bounds__(kThreads, 3) scan_kernel(const BeamArgs a, con
     }
 }
 
-// The logarithm of a sum of 0.25 and more, to 2^-29: of its fraction f in
+// The logarithm of a sum l over one of its weights w, the largest, to 2^-29: of the quotient's fraction f in
 // [0.7, 1.4] as 2 atanh(q), q = (f - 1) / (f + 1), in two fp32 numbers and a
 // series in q^2.  64-bit arithmetic is slow here: log() takes 1.5 us.
-__device__ __forceinline__ double log_of(double l) {
-    const long long bits = __double_as_longlong(l);
-    int e = (int)(bits >> 52) - 1023;
-    double f = __longlong_as_double((bits & 0xfffffffffffffLL) | 0x3ff0000000000000LL);
-    if (f > 1.41421356) f *= 0.5, ++e;
-    const float fh = (float)f, fl = (float)(f - fh);
+__device__ __forceinline__ double log_over(double l, float w) {
+    const float h = (float)l, over = h / w;            // the quotient: this and `left`
+    const float left = __fdividef(fmaf(-over, w, h) + (float)(l - (double)h), w);
+    int e = (int)(__float_as_uint(over) >> 23) - 127;
+    float scale = __uint_as_float((uint32_t)(127 - e) << 23);
+    if (over * scale > 1.41421356f) scale *= 0.5f, ++e;
+    const float fh = over * scale, fl = left * scale;
     const float n = fh - 1.0f, d = fh + 1.0f, dl = (fh - (d - 1.0f)) + fl;   // n exactly, d to its rounding, which dl holds
-    const float q = n / d, ql = (fmaf(-q, d, n) + fl - q * dl) / d, z = q * fmaf(2.0f, ql, q);
+    const float q = n / d, ql = __fdividef(fmaf(-q, d, n) + fl - q * dl, d), z = q * fmaf(2.0f, ql, q);
     float s = 1.0f / 13.0f;                            // z^6 / 13 < 6e-11
     s = fmaf(s, z, 1.0f / 11.0f);
     s = fmaf(s, z, 1.0f / 9.0f);
@@ -556,6 +557,10 @@ __device__ __forceinline__ double log_of(double l) {
     s = fmaf(s, z, 1.0f / 3.0f);
     const float rest = 2.0f * fmaf(q * z, s, ql);
     return fma((double)e, 0.693147180559945309417, (double)(2.0f * q) + (double)rest);
+}
+// What a beam's largest logit counts for in its sum, as scan_kernel has it, bit for bit.
+__device__ __forceinline__ float largest_weight(float m) {
+    return fabsf(m) >= kHuge ? 1.0f : ex2(__fmaf_rn(m, kLog2eLow, __fmaf_rn(m, kLog2e, -reference(m))));
 }
 
 // One is better than another when it is greater.  The order of its score, 0 for none; among equal ones the lower
@@ -624,10 +629,9 @@ __global__ void __launch_bounds__(THREADS, 1) merge_kernel(const BeamArgs a, con
             parts = 0;
         } else if (parts > 0) {
             largest = top;
-            // relative to the largest, which may be far larger than the sum's logarithm
-            log_sum = log_of(l);
-            if (fabsf(top) < kHuge) log_sum += (double)reference(top) * 0.693147180559945309417 - largest;
-            // the largest counts for 1: a sum that rounding has below that would give its token more than its beam has
+            // relative to the largest, whose own weight as it was added up counts for 1: its exponential's error cancels, and
+            // one token, or equal ones, come to their number.  No token may get more than its beam has.
+            log_sum = log_over(l, largest_weight(top));
             if (__double2hiint(log_sum) < 0) log_sum = 0.0;
         }
         if (writes) s_top[b] = largest, s_cum[b] = score - log_sum, s_parts[b] = parts;
